@@ -10,6 +10,10 @@ Storage convention (raw storage tensors, as the C ABI sees memory):
   * A: (batch, n, n); row-major holds A itself, column-major holds A^T in memory;
   * B: (batch, n, nrhs) row-major, (batch, nrhs, n) column-major;
   * bdsv strips: (batch, nbr, bs, 3*bs), padded vector: (batch, (nbr + 2)*bs).
+
+The row operators (gated linear recurrence, norms around a block) take rows of contiguous
+elements, (rows, width) or (batch, length, width), that may be column windows of a wider
+tensor: the last stride is 1, the rows lie at one distance.
 """
 from __future__ import annotations
 
@@ -21,10 +25,11 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libbsolve.so")
 
 BS_OK, BS_ERR_INVALID_ARG, BS_ERR_UNSUPPORTED, BS_ERR_CUDA = 0, 1, 2, 3
-BS_FP32, BS_FP64 = 0, 1
+BS_FP32, BS_FP64, BS_BF16, BS_FP16 = 0, 1, 2, 3
 BS_ROW_MAJOR, BS_COL_MAJOR = 0, 1
 BS_LOWER, BS_UPPER = 0, 1
 BS_CONTRACT_DEFAULT, BS_CONTRACT_RUDA = 0, 1
+BS_GATE_SILU, BS_GATE_SIGMOID, BS_GATE_LINEAR = 0, 1, 2
 
 
 class Options(ctypes.Structure):
@@ -46,6 +51,10 @@ EXPORTED = (
     "bs_getrf_getrs_host_workspace", "bs_getrf_getrs_batched_host",
     "bs_potrf_potrs_host_workspace", "bs_potrf_potrs_batched_host",
     "bs_bdsv_host_workspace", "bs_bdsv_batched_host", "bs_getrf_getrs_batched_host_static",
+    "bs_grec_batched", "bs_grec_backward_batched", "bs_grec_step_batched",
+    "bs_grec_tape_rows", "bs_grec_backward_workspace", "bs_grec_supported",
+    "bs_gnorm_batched", "bs_gnorm_backward_batched", "bs_gnorm_backward_workspace",
+    "bs_gnorm_supported",
     "bs_status_string", "bs_last_cuda_error", "bs_getrf_getrs_supported",
     "bs_potrf_potrs_supported", "bs_bdsv_supported", "bs_version",
 )
@@ -124,6 +133,32 @@ def lib() -> ctypes.CDLL:
             for name in ("bs_getrf_getrs_batched_host", "bs_potrf_potrs_batched_host",
                          "bs_bdsv_batched_host", "bs_getrf_getrs_batched_host_static"):
                 getattr(L, name).restype = i32
+            f64 = ctypes.c_double
+            L.bs_grec_batched.argtypes = [i32, i32, i64, i64, vp, vp, i64, vp, i64, vp, i64, vp,
+                                          f64, vp, vp, i64, vp, vp, vp]
+            L.bs_grec_backward_batched.argtypes = [i32, i32, i64, i64, vp, vp, i64, vp, i64, vp,
+                                                   i64, vp, f64, vp, vp, i64, vp, vp, i64, vp,
+                                                   i64, vp, i64, vp, vp, vp, sz, vp]
+            L.bs_grec_step_batched.argtypes = [i32, i32, i64, vp, i64, vp, i64, vp, i64, vp, f64,
+                                               vp, i64, vp, vp, i64, vp]
+            L.bs_gnorm_batched.argtypes = [i32, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp,
+                                           f64, i32, vp, i64, vp, i64, vp]
+            L.bs_gnorm_backward_batched.argtypes = [i32, i64, i32, vp, i64, vp, i64, vp, i64, vp,
+                                                    vp, vp, f64, i32, vp, i64, vp, i64, vp, i64,
+                                                    vp, i64, vp, i64, vp, vp, vp, vp, sz, vp]
+            for name in ("bs_grec_batched", "bs_grec_backward_batched", "bs_grec_step_batched",
+                         "bs_gnorm_batched", "bs_gnorm_backward_batched"):
+                getattr(L, name).restype = i32
+            L.bs_grec_tape_rows.argtypes = [i64, i64]
+            L.bs_grec_tape_rows.restype = i64
+            L.bs_grec_backward_workspace.argtypes = [i32, i64, i64]
+            L.bs_grec_backward_workspace.restype = sz
+            L.bs_gnorm_backward_workspace.argtypes = [i32, i64]
+            L.bs_gnorm_backward_workspace.restype = sz
+            L.bs_grec_supported.argtypes = [i32, i32]
+            L.bs_grec_supported.restype = i32
+            L.bs_gnorm_supported.argtypes = [i32, i32]
+            L.bs_gnorm_supported.restype = i32
             L.bs_status_string.argtypes = [i32]
             L.bs_status_string.restype = ctypes.c_char_p
             L.bs_last_cuda_error.argtypes = []
@@ -530,3 +565,220 @@ def bs_getrf_getrs_batched_host_static(A, B, ipiv, info, layout: int = ROW_MAJOR
         for s_ in streams:
             s_.synchronize()
     return streams
+
+
+# --------------------------------------------------------------- row operators
+_ROW_CODES = {}
+
+
+def _row_code(dtype) -> int:
+    if not _ROW_CODES:
+        import torch
+        _ROW_CODES.update({torch.float32: BS_FP32, torch.bfloat16: BS_BF16,
+                           torch.float16: BS_FP16})
+    code = _ROW_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}: float32, bfloat16 or float16")
+    return code
+
+
+def _row(t, name: str, like):
+    """(pointer, ld) of a row operand: of like's shape and dtype, on its device, the last stride 1
+    and the rows at one distance (ld elements). None: (0, 0)."""
+    if t is None:
+        return 0, 0
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {like.dtype}")
+    shape, st = t.shape, t.stride()
+    if shape != like.shape:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected {tuple(like.shape)}")
+    if t.device != like.device or not t.is_cuda:
+        raise ValueError(f"{name}: bsolve operands are device tensors of one device")
+    width = shape[-1]
+    if width > 1 and st[-1] != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if len(shape) == 2:
+        ld = st[0] if shape[0] > 1 else width
+    else:
+        b, n = shape[0], shape[1]
+        ld = st[1] if n > 1 else (st[0] if b > 1 else width)
+        if b > 1 and n > 1 and st[0] != n * ld:
+            raise ValueError(f"{name}: the rows of all sequences must lie at one distance")
+    if ld < width and t.numel():
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), max(ld, width)
+
+
+def _vec(t, name: str, like, numel: int, dtype=None) -> int:
+    """The pointer of a contiguous operand of numel elements (FP32 unless dtype says otherwise)
+    on like's device. None: 0."""
+    if t is None:
+        return 0
+    if dtype is None:
+        import torch
+        dtype = torch.float32
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{name}: {t.numel()} elements, expected {numel}")
+    if t.device != like.device or not t.is_cuda:
+        raise ValueError(f"{name}: bsolve operands are device tensors of one device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _work(work, like):
+    import torch
+    if work is None:
+        return 0, 0
+    return _vec(work, "work", like, work.numel(), torch.uint8), work.numel()
+
+
+def _sequences(x, offsets):
+    """(batch, rows, channels, pointer of offsets) of a recurrence call."""
+    if offsets is None:
+        if x.dim() != 3:
+            raise ValueError(f"x: shape {tuple(x.shape)}, expected (batch, length, channels), or "
+                             "(rows, channels) with offsets")
+        batch, length, channels = x.shape
+        return batch, batch * length, channels, 0
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected (rows, channels) with offsets")
+    if offsets.numel() < 1:
+        raise ValueError("offsets: batch + 1 row numbers expected")
+    at = _vec(offsets, "offsets", x, offsets.numel(), torch.int64)
+    return offsets.numel() - 1, x.shape[0], x.shape[1], at
+
+
+def bs_grec_tape_rows(batch: int, rows: int) -> int:
+    """Rows of the tape of a recurrence call over batch sequences of rows rows in all."""
+    return lib().bs_grec_tape_rows(batch, rows)
+
+
+def bs_grec_backward_workspace(channels: int, batch: int, rows: int) -> int:
+    """Bytes of bs_grec_backward_batched's workspace."""
+    return lib().bs_grec_backward_workspace(channels, batch, rows)
+
+
+def bs_grec_batched(x, r, i, lam, h, h0=None, hT=None, offsets=None, tape=None,
+                    kappa: float = 8.0, stream=None) -> None:
+    """Gated linear recurrence over whole sequences: h <- the states (see bsolve.h). x, r, i, h:
+    (batch, length, channels), or (rows, channels) with offsets, batch + 1 int64 row numbers;
+    h0, hT: (batch, channels) float32; tape: (bs_grec_tape_rows(...), channels) float32, for
+    the backward call."""
+    batch, rows, channels, at = _sequences(x, offsets)
+    code = _row_code(x.dtype)
+    px, ldx = _row(x, "x", x)
+    pr, ldr = _row(r, "r", x)
+    pi, ldi = _row(i, "i", x)
+    ph, ldh = _row(h, "h", x)
+    L = lib()
+    st = L.bs_grec_batched(
+        code, channels, batch, rows, at, px, ldx, pr, ldr, pi, ldi,
+        _vec(lam, "lam", x, channels), kappa, _vec(h0, "h0", x, batch * channels), ph, ldh,
+        _vec(hT, "hT", x, batch * channels),
+        0 if tape is None else _vec(tape, "tape", x, L.bs_grec_tape_rows(batch, rows) * channels),
+        _stream(stream))
+    _check(st, "bs_grec_batched")
+
+
+def bs_grec_backward_batched(x, r, i, lam, tape, dh, dx, dr, di, dlam, work, dhT=None, dh0=None,
+                             offsets=None, kappa: float = 8.0, stream=None) -> None:
+    """Gradients of bs_grec_batched from its inputs, its tape and the gradients of h (and hT):
+    dx, dr, di, dlam (and dh0) are written (see bsolve.h). work: uint8, at least
+    bs_grec_backward_workspace(...) elements."""
+    batch, rows, channels, at = _sequences(x, offsets)
+    code = _row_code(x.dtype)
+    px, ldx = _row(x, "x", x)
+    pr, ldr = _row(r, "r", x)
+    pi, ldi = _row(i, "i", x)
+    pdh, lddh = _row(dh, "dh", x)
+    pdx, lddx = _row(dx, "dx", x)
+    pdr, lddr = _row(dr, "dr", x)
+    pdi, lddi = _row(di, "di", x)
+    pw, nw = _work(work, x)
+    L = lib()
+    st = L.bs_grec_backward_batched(
+        code, channels, batch, rows, at, px, ldx, pr, ldr, pi, ldi,
+        _vec(lam, "lam", x, channels), kappa,
+        _vec(tape, "tape", x, L.bs_grec_tape_rows(batch, rows) * channels), pdh, lddh,
+        _vec(dhT, "dhT", x, batch * channels), pdx, lddx, pdr, lddr, pdi, lddi,
+        _vec(dlam, "dlam", x, channels), _vec(dh0, "dh0", x, batch * channels), pw, nw,
+        _stream(stream))
+    _check(st, "bs_grec_backward_batched")
+
+
+def bs_grec_step_batched(x, r, i, lam, state, y, slots=None, kappa: float = 8.0,
+                         stream=None) -> None:
+    """One row of the recurrence for each of a batch of sequences: state, (num_slots, channels)
+    float32, advances in place and y <- the new states (see bsolve.h). x, r, i, y: (batch,
+    channels); slots: batch int32 rows of state, None: row j for sequence j."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected (batch, channels)")
+    batch, channels = x.shape
+    if state.dim() != 2 or state.shape[1] != channels:
+        raise ValueError(f"state: shape {tuple(state.shape)}, expected (num_slots, {channels})")
+    code = _row_code(x.dtype)
+    px, ldx = _row(x, "x", x)
+    pr, ldr = _row(r, "r", x)
+    pi, ldi = _row(i, "i", x)
+    py, ldy = _row(y, "y", x)
+    st = lib().bs_grec_step_batched(
+        code, channels, batch, px, ldx, pr, ldr, pi, ldi, _vec(lam, "lam", x, channels), kappa,
+        _vec(state, "state", x, state.numel()), state.shape[0],
+        _vec(slots, "slots", x, batch, torch.int32), py, ldy, _stream(stream))
+    _check(st, "bs_grec_step_batched")
+
+
+def bs_gnorm_backward_workspace(width: int, rows: int) -> int:
+    """Bytes of bs_gnorm_backward_batched's workspace."""
+    return lib().bs_gnorm_backward_workspace(width, rows)
+
+
+def bs_gnorm_batched(f, y=None, z=None, x=None, w_post=None, scale=None, w_pre=None, u=None,
+                     eps: float = 1e-6, gate: int = BS_GATE_SILU, stream=None) -> None:
+    """y <- x + scale * (f / rms(f) * w_post * act(z)), u <- y / rms(y) * w_pre; every part but f
+    and one output optional (see bsolve.h). f, z, x, y, u: (rows, width) or (batch, length,
+    width); w_post, scale, w_pre: width float32 elements."""
+    width = f.shape[-1]
+    code = _row_code(f.dtype)
+    pf, ldf = _row(f, "f", f)
+    pz, ldz = _row(z, "z", f)
+    px, ldx = _row(x, "x", f)
+    py, ldy = _row(y, "y", f)
+    pu, ldu = _row(u, "u", f)
+    st = lib().bs_gnorm_batched(
+        code, f.numel() // width if width else 0, width, pf, ldf, pz, ldz, px, ldx,
+        _vec(w_post, "w_post", f, width), _vec(scale, "scale", f, width),
+        _vec(w_pre, "w_pre", f, width), eps, gate, py, ldy, pu, ldu, _stream(stream))
+    _check(st, "bs_gnorm_batched")
+
+
+def bs_gnorm_backward_batched(f, dy, df, work=None, z=None, x=None, w_post=None, scale=None,
+                              w_pre=None, du=None, dz=None, dx=None, dw_post=None, dscale=None,
+                              dw_pre=None, eps: float = 1e-6, gate: int = BS_GATE_SILU,
+                              stream=None) -> None:
+    """Gradients of bs_gnorm_batched from its inputs and the gradients of y and u (either may be
+    None): df and, where given, dz, dx, dw_post, dscale, dw_pre are written (see bsolve.h).
+    work: uint8, at least bs_gnorm_backward_workspace(...) elements, for the last three."""
+    width = f.shape[-1]
+    code = _row_code(f.dtype)
+    pf, ldf = _row(f, "f", f)
+    pz, ldz = _row(z, "z", f)
+    px, ldx = _row(x, "x", f)
+    pdy, lddy = _row(dy, "dy", f)
+    pdu, lddu = _row(du, "du", f)
+    pdf, lddf = _row(df, "df", f)
+    pdz, lddz = _row(dz, "dz", f)
+    pdx, lddx = _row(dx, "dx", f)
+    pw, nw = _work(work, f)
+    st = lib().bs_gnorm_backward_batched(
+        code, f.numel() // width if width else 0, width, pf, ldf, pz, ldz, px, ldx,
+        _vec(w_post, "w_post", f, width), _vec(scale, "scale", f, width),
+        _vec(w_pre, "w_pre", f, width), eps, gate, pdy, lddy, pdu, lddu, pdf, lddf, pdz, lddz,
+        pdx, lddx, _vec(dw_post, "dw_post", f, width), _vec(dscale, "dscale", f, width),
+        _vec(dw_pre, "dw_pre", f, width), pw, nw, _stream(stream))
+    _check(st, "bs_gnorm_backward_batched")

@@ -343,6 +343,10 @@ bs_status split_opts(const bs_options* opts, SplitOpts* o) {
 
 }  // namespace
 
+namespace bsolve {
+void record_cuda_error(cudaError_t e) { g_last_cuda_error = static_cast<int>(e); }
+}  // namespace bsolve
+
 extern "C" {
 
 size_t bs_getrf_getrs_host_workspace(bs_dtype dtype, int n, int nrhs, int64_t chunk) {

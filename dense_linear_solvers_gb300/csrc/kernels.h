@@ -112,4 +112,63 @@ size_t lu_cta_bytes(int n, int nrhs, int elem_size);
 size_t chol_smem_bytes(int n, int nrhs, int elem_size);
 size_t chol_sys_bytes(int n, int nrhs, int elem_size);
 
+// The row operators (bs_grec and bs_gnorm calls): operands of T (float, __nv_bfloat16 or
+// __half) as rows of contiguous elements, row j at j * ld of its base.
+
+// The inputs of a gated linear recurrence. offsets == nullptr: sequences of `length` rows.
+template <typename T>
+struct GrecRows {
+  int channels;
+  int64_t batch, rows, length;
+  const int64_t* offsets;
+  const T *x, *r, *i;
+  int64_t ldx, ldr, ldi;
+};
+
+template <typename T>
+cudaError_t launch_grec(const GrecRows<T>& p, const float* lam, float kappa, const float* h0,
+                        T* h, int64_t ldh, float* hT, float* tape, cudaStream_t stream);
+template <typename T>
+cudaError_t launch_grec_backward(const GrecRows<T>& p, const float* lam, float kappa,
+                                 const float* tape, const T* dh, int64_t lddh, const float* dhT,
+                                 T* dx, int64_t lddx, T* dr, int64_t lddr, T* di, int64_t lddi,
+                                 float* dlam, float* dh0, void* work, cudaStream_t stream);
+size_t grec_backward_workspace(int channels, int64_t batch, int64_t rows);
+template <typename T>
+cudaError_t launch_grec_step(const GrecRows<T>& p, const float* lam, float kappa, float* state,
+                             int64_t num_slots, const int32_t* slots, T* y, int64_t ldy,
+                             cudaStream_t stream);
+
+// The operands of the norms around a block; null: absent (see bsolve.h).
+template <typename T>
+struct GnormRows {
+  int64_t rows;
+  int width;
+  const T *f, *z, *x;
+  int64_t ldf, ldz, ldx;
+  const float *w_post, *scale, *w_pre;
+  float eps;
+  int gate;
+};
+
+template <typename T>
+struct GnormGrads {
+  const T *dy, *du;
+  int64_t lddy, lddu;
+  T *df, *dz, *dx;
+  int64_t lddf, lddz, lddx;
+  float *dw_post, *dscale, *dw_pre;
+};
+
+template <typename T>
+cudaError_t launch_gnorm(const GnormRows<T>& p, T* y, int64_t ldy, T* u, int64_t ldu,
+                         cudaStream_t stream);
+template <typename T>
+cudaError_t launch_gnorm_backward(const GnormRows<T>& p, const GnormGrads<T>& g, void* work,
+                                  cudaStream_t stream);
+size_t gnorm_backward_workspace(int width, int64_t rows);
+
+// Records a launch error as the one bs_last_cuda_error() returns.
+void record_cuda_error(cudaError_t e);
+
 }  // namespace bsolve

@@ -51,7 +51,9 @@ typedef enum {
   BS_ERR_CUDA = 3
 } bs_status;
 
-typedef enum { BS_FP32 = 0, BS_FP64 = 1 } bs_dtype;
+/* The solvers take BS_FP32 and BS_FP64; the bs_grec and bs_gnorm calls BS_FP32, BS_BF16 and
+ * BS_FP16. */
+typedef enum { BS_FP32 = 0, BS_FP64 = 1, BS_BF16 = 2, BS_FP16 = 3 } bs_dtype;
 
 /* Element (r, c) of an n x m operand lives at r*m + c (row-major) or c*n + r
  * (column-major) within its system. */
@@ -345,6 +347,131 @@ BS_API bs_status bs_bdmv_batched(bs_dtype dtype, int num_block_rows, int block_s
 BS_API bs_status bs_bdmv2_batched(bs_dtype dtype, int num_block_rows, int block_size,
                                   int64_t batch, const void* strips, const void* x_padded,
                                   void* y_padded, void* y2_padded, void* stream);
+
+/*
+ * Gated linear recurrence over long sequences: one unit lower bidiagonal system per sequence
+ * and channel, (I - Z diag(a)) h = u with Z the shift by one row, solved by a scan; its
+ * backward pass (the transposed, upper bidiagonal system); and one row of it from a kept
+ * state. With l the log of the decay and sigma the logistic function, row t of channel c is
+ *   l_t = -kappa softplus(lam_c) sigma(r_t),        a_t = exp(l_t),
+ *   u_t = sqrt(1 - a_t^2) sigma(i_t) x_t,           h_t = a_t h_{t-1} + u_t.
+ *
+ * dtype (BS_FP32, BS_BF16, BS_FP16) is the type of the row operands x, r, i, h and their
+ * gradients; lam, every state (h0, hT, tape, the step's states), dhT, dh0 and dlam are
+ * FP32. All arithmetic and every state is FP32; each row output is rounded once.
+ *
+ * Rows: an operand holds `rows` rows of `channels` contiguous elements, row j at element
+ * j * ld of its base (ld >= channels; 64-bit offsets), so that operands may be column windows
+ * of a wider matrix. offsets == NULL: `batch` sequences of rows / batch rows each, one after
+ * another (rows a multiple of batch). Otherwise offsets holds batch + 1 increasing int64 row
+ * numbers in device memory and sequence s is rows offsets[s] .. offsets[s+1] - 1; rows of no
+ * sequence are neither read nor written. A sequence may be empty: its final state is its
+ * initial one. (The kernels clamp offsets to 0 .. rows; decreasing offsets give unspecified
+ * results in the outputs, no access outside the operands.)
+ *
+ * Base addresses are aligned to their element type only (8 bytes for offsets). Wider aligned operands
+ * are read in wider pieces (16-byte aligned bases and ld a multiple of 16 bytes serve best).
+ * Inputs may overlap each other; an output may not overlap any other operand, except that
+ * row operands of equal ld may interleave as disjoint column windows of one matrix and that
+ * hT may be h0 itself. Infinities and NaN stay in their sequence and channel.
+ *
+ * bs_grec_batched:
+ *   h0    batch x channels initial states, or NULL for zeros.
+ *   h     the states of every row.
+ *   hT    batch x channels final states, or NULL.
+ *   tape  bs_grec_tape_rows(batch, rows) x channels, or NULL: the states that
+ *         bs_grec_backward_batched restarts from (the state before rows 0, 64, 128, ... of
+ *         each sequence).
+ * bs_grec_backward_batched: x, r, i, lam, kappa, offsets and tape as in the forward call;
+ *   dh    the gradient of h;  dhT  batch x channels, the gradient of hT, or NULL for zeros.
+ *   dx, dr, di    the gradients of x, r, i.
+ *   dlam  channels: the gradient of lam, summed over all rows in a fixed order.
+ *   dh0   batch x channels: the gradient of h0, or NULL.
+ *   work  device workspace of bs_grec_backward_workspace(...) bytes, 16-byte aligned. Holds
+ *         nothing between calls.
+ * bs_grec_step_batched: one row for each of `batch` sequences:
+ *   state    num_slots x channels, in and out.
+ *   slots    batch int32: the row of `state` that row j advances; NULL: row j. Row j with a
+ *            slot outside 0 .. num_slots - 1 changes no state and gets y = 0. Two rows with
+ *            one slot: unspecified states.
+ *   y        the new states, in dtype.
+ * Results do not depend on the stream or the run: no atomics, a fixed order of every sum.
+ * Supported: 1 <= channels <= 2^20, batch <= 2^31 - 1, kappa finite and > 0.
+ */
+BS_API bs_status bs_grec_batched(bs_dtype dtype, int channels, int64_t batch, int64_t rows,
+                                 const int64_t* offsets, const void* x, int64_t ldx,
+                                 const void* r, int64_t ldr, const void* i, int64_t ldi,
+                                 const float* lam, double kappa, const float* h0, void* h,
+                                 int64_t ldh, float* hT, float* tape, void* stream);
+BS_API bs_status bs_grec_backward_batched(bs_dtype dtype, int channels, int64_t batch,
+                                          int64_t rows, const int64_t* offsets, const void* x,
+                                          int64_t ldx, const void* r, int64_t ldr, const void* i,
+                                          int64_t ldi, const float* lam, double kappa,
+                                          const float* tape, const void* dh, int64_t lddh,
+                                          const float* dhT, void* dx, int64_t lddx, void* dr,
+                                          int64_t lddr, void* di, int64_t lddi, float* dlam,
+                                          float* dh0, void* work, size_t work_bytes,
+                                          void* stream);
+BS_API bs_status bs_grec_step_batched(bs_dtype dtype, int channels, int64_t batch, const void* x,
+                                      int64_t ldx, const void* r, int64_t ldr, const void* i,
+                                      int64_t ldi, const float* lam, double kappa, float* state,
+                                      int64_t num_slots, const int32_t* slots, void* y,
+                                      int64_t ldy, void* stream);
+/* Rows of the tape, and bytes of the backward call's workspace (0 for invalid sizes). */
+BS_API int64_t bs_grec_tape_rows(int64_t batch, int64_t rows);
+BS_API size_t bs_grec_backward_workspace(int channels, int64_t batch, int64_t rows);
+
+/*
+ * The norms around a block, fused with the block's gate and residual scale: from the block's
+ * output f, its gate z and the residual x of each row,
+ *   n = f / sqrt(mean(f^2) + eps) * w_post,   t = n * act(z),   y = x + scale * t,
+ *   u = y / sqrt(mean(y^2) + eps) * w_pre,
+ * the means over the row's `width` elements; y is the new residual, u the next block's input.
+ * Optional parts (NULL): z (t = n), x (y = scale * t), w_post (no norm after the block:
+ * n = f), scale (1), u with w_pre (no norm before the next block), y (not stored; u is still
+ * that of y unrounded). One of y and u must be given, u and w_pre together.
+ *
+ * dtype (BS_FP32, BS_BF16, BS_FP16) is the type of f, z, x, y, u and their gradients, rows of
+ * `width` contiguous elements at ld as in the bs_grec calls; w_post, scale and w_pre are
+ * FP32 vectors of width elements, their gradients too. All arithmetic is FP32, each row
+ * output rounded once. Alignment and overlap as in the bs_grec calls.
+ *   gate  the activation of z: BS_GATE_SILU z sigma(z), BS_GATE_SIGMOID sigma(z),
+ *         BS_GATE_LINEAR z. Read whether or not z is given.
+ *   eps   finite and > 0.
+ * bs_gnorm_backward_batched: f, z, x, w_post, scale, w_pre, eps, gate as in the forward call
+ *   (du stands for u: w_pre and du together); dy and du the gradients of y and u, either may
+ *   be NULL (zeros), not both.
+ *   df           the gradient of f.
+ *   dz, dx       those of z and x; NULL: not stored. dz needs z, dx needs x.
+ *   dw_post, dscale, dw_pre   width elements each, summed over all rows in a fixed order;
+ *                NULL: not stored. Each needs its parameter (dw_pre: du too).
+ *   work         device workspace of bs_gnorm_backward_workspace(width, rows) bytes, 16-byte
+ *                aligned. Holds nothing between calls; may be NULL where none of the three
+ *                sums is stored.
+ * rows == 0 launches nothing but the three sums' zeros.
+ * Supported: 1 <= width <= 65536.
+ */
+typedef enum { BS_GATE_SILU = 0, BS_GATE_SIGMOID = 1, BS_GATE_LINEAR = 2 } bs_gate;
+
+BS_API bs_status bs_gnorm_batched(bs_dtype dtype, int64_t rows, int width, const void* f,
+                                  int64_t ldf, const void* z, int64_t ldz, const void* x,
+                                  int64_t ldx, const float* w_post, const float* scale,
+                                  const float* w_pre, double eps, bs_gate gate, void* y,
+                                  int64_t ldy, void* u, int64_t ldu, void* stream);
+BS_API bs_status bs_gnorm_backward_batched(bs_dtype dtype, int64_t rows, int width, const void* f,
+                                           int64_t ldf, const void* z, int64_t ldz, const void* x,
+                                           int64_t ldx, const float* w_post, const float* scale,
+                                           const float* w_pre, double eps, bs_gate gate,
+                                           const void* dy, int64_t lddy, const void* du,
+                                           int64_t lddu, void* df, int64_t lddf, void* dz,
+                                           int64_t lddz, void* dx, int64_t lddx, float* dw_post,
+                                           float* dscale, float* dw_pre, void* work,
+                                           size_t work_bytes, void* stream);
+BS_API size_t bs_gnorm_backward_workspace(int width, int64_t rows);
+
+/* 1 if the calls with this type and row length have a kernel instance, else 0 (no launch). */
+BS_API int bs_grec_supported(bs_dtype dtype, int channels);
+BS_API int bs_gnorm_supported(bs_dtype dtype, int width);
 
 /* Human-readable name of a status code (a static string). */
 BS_API const char* bs_status_string(bs_status status);
