@@ -86,34 +86,49 @@ __device__ __forceinline__ float grec_rate_slope(float lam) {
 //     2^-40 of full scale.
 // The approximate exponential, reciprocal and root are within 2 ulp of FP32 (2^-22), two
 // orders below a 16-bit output's rounding and near that of one FP32 operation.
+// Two neighbouring channels at a time: the products and sums are FP32 pair instructions.
 struct Gates {
-  float a, s, sr, si, er, ei, l, rs;
+  float2 a, s, sr, si, er, ei, l, rs;
 };
 
-__device__ __forceinline__ Gates grec_gates(float r, float i, float rate) {
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 operator*(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 operator+(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  return __ffma2_rn(a, b, c);
+}
+
+// neg_rate: -K of the two channels.
+__device__ __forceinline__ Gates grec_gates(float2 r, float2 i, float2 neg_rate) {
   Gates g;
-  g.er = ex2(min_nan(r * -kLog2e, 60.f));
-  g.ei = ex2(min_nan(i * -kLog2e, 60.f));
-  const float p = 1.f + g.er, q = 1.f + g.ei;
-  const float d = rcp(p * q);
-  g.sr = fmaf(q, d, -0x1p-60f);
+  r = r * both(-kLog2e);
+  i = i * both(-kLog2e);
+  g.er = make_float2(ex2(min_nan(r.x, 60.f)), ex2(min_nan(r.y, 60.f)));
+  g.ei = make_float2(ex2(min_nan(i.x, 60.f)), ex2(min_nan(i.y, 60.f)));
+  const float2 p = g.er + both(1.f), q = g.ei + both(1.f);
+  float2 d = p * q;
+  d = make_float2(rcp(d.x), rcp(d.y));
+  g.sr = fma2(q, d, both(-0x1p-60f));
   g.si = p * d;
-  g.l = max_nan(-rate * g.sr, -80.f);
-  const float t = fmaf(g.l, kLog2e, 12582912.f);  // 1.5 * 2^23: n in the low bits
-  const float n = t - 12582912.f;
-  float f = fmaf(n, -0.693359375f, g.l);          // ln 2 in two parts, the first exact * n
-  f = fmaf(n, 2.12194440e-4f, f);
-  float e = fmaf(f, 1.f / 5040.f, 1.f / 720.f);
-  e = fmaf(f, e, 1.f / 120.f);
-  e = fmaf(f, e, 1.f / 24.f);
-  e = fmaf(f, e, 1.f / 6.f);
-  e = fmaf(f, e, 0.5f);
-  e = fmaf(f * f, e, f);
-  const float two_n = __int_as_float((__float_as_int(t) << 23) + 0x3f800000);
-  const float E = fmaf(two_n, e, two_n - 1.f);
-  g.a = 1.f + E;
-  const float w = max_nan(-E * (1.f + g.a), 0x1p-80f);
-  g.rs = rsqrt_fast(w);
+  g.l = neg_rate * g.sr;
+  g.l = make_float2(max_nan(g.l.x, -80.f), max_nan(g.l.y, -80.f));
+  const float2 t = fma2(g.l, both(kLog2e), both(12582912.f));  // 1.5 * 2^23: n in the low bits
+  const float2 n = t + both(-12582912.f);
+  float2 f = fma2(n, both(-0.693359375f), g.l);  // ln 2 in two parts, the first exact * n
+  f = fma2(n, both(2.12194440e-4f), f);
+  float2 e = fma2(f, both(1.f / 5040.f), both(1.f / 720.f));
+  e = fma2(f, e, both(1.f / 120.f));
+  e = fma2(f, e, both(1.f / 24.f));
+  e = fma2(f, e, both(1.f / 6.f));
+  e = fma2(f, e, both(0.5f));
+  e = fma2(f * f, e, f);
+  const float2 two_n = make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
+                                   __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000));
+  const float2 E = fma2(two_n, e, two_n + both(-1.f));
+  g.a = E + both(1.f);
+  float2 w = fma2(E, g.a, E);  // E (1 + a) = a^2 - 1
+  w = make_float2(max_nan(-w.x, 0x1p-80f), max_nan(-w.y, 0x1p-80f));
+  g.rs = make_float2(rsqrt_fast(w.x), rsqrt_fast(w.y));
   g.s = w * g.rs;
   return g;
 }

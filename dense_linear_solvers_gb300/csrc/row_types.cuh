@@ -24,4 +24,37 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
+// Two neighbouring elements: as one value of twice the size, and in FP32.
+template <typename T>
+struct Pair;
+template <>
+struct Pair<float> {
+  using type = float2;
+};
+template <>
+struct Pair<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+};
+template <>
+struct Pair<__half> {
+  using type = __half2;
+};
+
+__device__ __forceinline__ float2 to_f32(float2 v) { return v; }
+__device__ __forceinline__ float2 to_f32(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+__device__ __forceinline__ float2 to_f32(__half2 v) { return __half22float2(v); }
+
+template <typename T>
+__device__ __forceinline__ typename Pair<T>::type pair_from_f32(float2 v);
+template <>
+__device__ __forceinline__ float2 pair_from_f32<float>(float2 v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat162 pair_from_f32<__nv_bfloat16>(float2 v) {
+  return __float22bfloat162_rn(v);
+}
+template <>
+__device__ __forceinline__ __half2 pair_from_f32<__half>(float2 v) {
+  return __float22half2_rn(v);
+}
+
 }  // namespace bsolve
