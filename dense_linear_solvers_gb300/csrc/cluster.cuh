@@ -69,10 +69,12 @@ bool pair_stores(const T* p, int64_t ld) {
 
 // Blocks of a cluster that share one sequence and channel tile: `units` such pairs are at hand, of
 // `length` rows each (packed sequences: on average), `rows` rows a block at a time. As many as
-// fill the GPU's 152 SMs twice, but no more than the sequence has pieces for.
+// the GPU's 152 SMs hold at once, two blocks each, and no more than the sequence has pieces
+// for: a second wave of few blocks costs more than idle slots.
 inline int grec_cluster(int64_t units, int64_t length, int rows) {
   int n = 1;
-  while (n < kMaxCluster && units * n < 2 * 152 && length > static_cast<int64_t>(n) * rows) n *= 2;
+  while (n < kMaxCluster && units * 2 * n <= 2 * 152 && length > static_cast<int64_t>(n) * rows)
+    n *= 2;
   return n;
 }
 

@@ -1,0 +1,340 @@
+// Backward pass of the gated linear recurrence (bs_grec_backward_batched of bsolve.h).
+//
+// The gradient g_t of the state after row t solves the transposed system,
+//   g_t = dh_t + a_{t+1} g_{t+1},
+// a scan from the last row to the first; every input's gradient is a product of g_t with factors
+// of row t and of the state h_{t-1} before it. The states are not read back (h was rounded when it
+// was stored) but solved again in FP32 from the tape, in the same pass over x, r and i that
+// the gradients need: four reads and three writes an element.
+//
+// The mapping is the forward pass's: 64 channels a block, two a lane, R rows a warp, pieces of
+// kWarps * R = 64 rows, one tape state each, so that the states need no exchange between blocks;
+// consecutive pieces lie on the blocks of a cluster, which walk the sequence from its end.
+// One step:
+//   each warp turns its rows into a_t, the gates and the three compositions' parts: A the product
+//     of the a_t, H the state from zero (forward), P the gradient a_t g_t handed on from
+//     zero (backward);
+//   the warps meet in shared memory, the blocks' (A, P) in every block's over the cluster;
+//   each warp runs its rows forward from its true state, then backward from its true gradient,
+//     writing the three gradients.
+// The gradient of lam: every lane sums D = dL/dl * l over its rows, the block's warps are added at
+// the end and each block writes one partial sum a channel; a second kernel adds those in order.
+#include "cluster.cuh"
+#include "grec_math.cuh"
+#include "grec_tile.cuh"
+#include "kernels.h"
+#include "row_types.cuh"
+
+namespace bsolve {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kR = 8;
+static_assert(kWarps * kR == kTapeRows, "a block's piece starts at a state on the tape");
+
+struct Exchange {  // of two channels
+  float2 A, P;
+};
+
+template <typename T, bool ALIGNED, int STAGES>
+struct GrecBackwardShared {
+  static constexpr int kOperand = kR * Tile<T, ALIGNED>::kRowBytes;  // one warp's rows
+  static constexpr int kStage = 4 * kOperand;
+  static constexpr int kWarp = STAGES * kStage;
+  static constexpr int kSegments = 2 * kWarps * 32 * sizeof(Exchange);
+  static constexpr int kStates = 2 * kWarps * 32 * sizeof(float2);
+  static constexpr int kBlocks = 2 * kMaxCluster * 32 * sizeof(Exchange);
+  static constexpr int kBytes = kSegments + kStates + kBlocks + kWarps * kWarp;
+};
+
+template <typename T>
+struct GrecGradRows {
+  const T* dh;
+  T *dx, *dr, *di;
+  int64_t lddh, lddx, lddr, lddi;
+  bool px, pr, pi;  // pairs of elements stored as one value
+};
+
+template <typename T, bool ALIGNED, int STAGES>
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1)
+grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__ lam, float kappa,
+                     const float* __restrict__ tape, const float* dhT, float* dh0,
+                     float* __restrict__ partial) {
+  using S = GrecBackwardShared<T, ALIGNED, STAGES>;
+  extern __shared__ __align__(16) char shared[];
+  Exchange* segments = reinterpret_cast<Exchange*>(shared);
+  Exchange* blocks = reinterpret_cast<Exchange*>(shared + S::kSegments);
+  float2* states = reinterpret_cast<float2*>(shared + S::kSegments + S::kBlocks);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  char* mine = shared + S::kSegments + S::kBlocks + S::kStates + warp * S::kWarp;
+  const int peers = cluster_size(), rank = cluster_rank();
+  const int c0 = static_cast<int>(blockIdx.x) / peers * kTileC;
+  const int valid = p.channels - c0 < kTileC ? p.channels - c0 : kTileC;
+  const int c = c0 + 2 * lane;
+  const bool first = c < p.channels, second = c + 1 < p.channels;
+  const float2 rate = make_float2(first ? -grec_rate(lam[c], kappa) : 0.f,
+                                  second ? -grec_rate(lam[c + 1], kappa) : 0.f);
+  const int64_t es = sizeof(T);
+  const int step_rows = peers * kTapeRows;
+  float2 dlam = make_float2(0.f, 0.f);
+  int parity = 0;
+  if (peers > 1) cluster_sync();  // every block runs before one writes to another
+
+  for (int64_t s = blockIdx.y; s < p.batch; s += gridDim.y) {
+    int64_t start, end;
+    sequence_rows(p.offsets, s, p.length, p.rows, &start, &end);
+    float2 carry = make_float2(0.f, 0.f);  // a_{t+1} g_{t+1} at the end of the step's rows
+    if (dhT) {
+      if (first) carry.x = dhT[s * p.channels + c];
+      if (second) carry.y = dhT[s * p.channels + c + 1];
+    }
+    const int64_t tb = tape_base(start, s);
+    const int64_t steps = (end - start + step_rows - 1) / step_rows;
+    // the warp's first row of this step; the last step first
+    int64_t row = start + (steps - 1) * step_rows + rank * kTapeRows + warp * kR;
+
+    auto stage = [&](int64_t at, int slot) {
+      const int n = at < start || at >= end ? 0 : (end - at < kR ? static_cast<int>(end - at) : kR);
+      char* to = mine + slot * S::kStage;
+      if (n > 0) {
+        stage_rows<T, ALIGNED, kR>(to, p.x + at * p.ldx + c0, p.ldx * es, n, valid, p.x);
+        stage_rows<T, ALIGNED, kR>(to + S::kOperand, p.r + at * p.ldr + c0, p.ldr * es, n, valid,
+                                   p.r);
+        stage_rows<T, ALIGNED, kR>(to + 2 * S::kOperand, p.i + at * p.ldi + c0, p.ldi * es, n,
+                                   valid, p.i);
+        stage_rows<T, ALIGNED, kR>(to + 3 * S::kOperand, g.dh + at * g.lddh + c0, g.lddh * es, n,
+                                   valid, g.dh);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < STAGES; ++k) stage(row - static_cast<int64_t>(k) * step_rows, k);
+
+    int slot = 0;
+    for (int64_t step = steps - 1; step >= 0; --step, row -= step_rows) {
+      const int n = row >= end ? 0 : (end - row < kR ? static_cast<int>(end - row) : kR);
+      const int64_t piece = row - warp * kR - start;  // the block's first row of the sequence
+      float2 before = make_float2(0.f, 0.f);          // the state in front of the block's rows
+      if (start + piece < end) {
+        const float* at = tape + (tb + piece / kTapeRows) * p.channels + c;
+        if (first) before.x = at[0];
+        if (second) before.y = at[1];
+      }
+      cp_async_wait_group<STAGES - 1>();
+      __syncwarp();
+      const char* in = mine + slot * S::kStage;
+      const unsigned lx = low_bits(p.x + row * p.ldx), lr = low_bits(p.r + row * p.ldr),
+                     li = low_bits(p.i + row * p.ldi), lh = low_bits(g.dh + row * g.lddh);
+      auto read = [&](int operand, int j, unsigned low, int64_t ld) {
+        return staged_pair<T, ALIGNED>(in + operand * S::kOperand, j, low,
+                                       static_cast<unsigned>(ld * es));
+      };
+
+      float2 a[kR], er[kR], ei[kR], hb[kR];
+      Exchange m{both(1.f), both(0.f)};
+      float2 H = both(0.f);
+      auto element = [&](int j) {
+        const Gates q = grec_gates(read(1, j, lr, p.ldr), read(2, j, li, p.ldi), rate);
+        a[j] = q.a;
+        er[j] = q.er;
+        ei[j] = q.ei;
+        hb[j] = q.s * q.si * read(0, j, lx, p.ldx);  // u, until the states are known
+        H = fma2(a[j], H, hb[j]);
+        m.A = m.A * a[j];
+      };
+      auto back = [&](int j) { m.P = a[j] * (m.P + read(3, j, lh, g.lddh)); };
+      if (n == kR) {
+#pragma unroll
+        for (int j = 0; j < kR; ++j) element(j);
+#pragma unroll
+        for (int j = kR - 1; j >= 0; --j) back(j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kR; ++j)
+          if (j < n) element(j);
+#pragma unroll
+        for (int j = kR - 1; j >= 0; --j)
+          if (j < n) back(j);
+      }
+
+      Exchange* seg = segments + parity * kWarps * 32;
+      float2* st = states + parity * kWarps * 32;
+      seg[warp * 32 + lane] = m;
+      st[warp * 32 + lane] = H;
+      __syncthreads();
+      float2 after = carry;  // what comes from behind the warp's rows
+      if (peers > 1) {
+        Exchange* blk = blocks + parity * kMaxCluster * 32;
+        if (warp < peers) {  // warp w tells block w
+          Exchange all = seg[(kWarps - 1) * 32 + lane];
+#pragma unroll
+          for (int w = kWarps - 2; w >= 0; --w) {
+            const Exchange q = seg[w * 32 + lane];
+            all = {q.A * all.A, fma2(q.A, all.P, q.P)};
+          }
+          store_remote(blk + rank * 32 + lane, warp, all);
+        }
+        cluster_sync();
+        for (int q = peers - 1; q >= 0; --q) {
+          if (q == rank) after = carry;
+          const Exchange e = blk[q * 32 + lane];
+          carry = fma2(e.A, carry, e.P);
+        }
+      } else {
+#pragma unroll
+        for (int w = kWarps - 1; w >= 0; --w) {
+          const Exchange e = seg[w * 32 + lane];
+          carry = fma2(e.A, carry, e.P);
+        }
+      }
+      for (int w = kWarps - 1; w > warp; --w) {
+        const Exchange e = seg[w * 32 + lane];
+        after = fma2(e.A, after, e.P);
+      }
+      for (int w = 0; w < warp; ++w) before = fma2(seg[w * 32 + lane].A, before, st[w * 32 + lane]);
+      parity ^= 1;
+
+      T* dx = g.dx + row * g.lddx + c;
+      T* dr = g.dr + row * g.lddr + c;
+      T* di = g.di + row * g.lddi + c;
+      auto forth = [&](int j) {
+        const float2 u = hb[j];
+        hb[j] = before;
+        before = fma2(a[j], before, u);
+      };
+      auto emit = [&](int j) {
+        const float2 x = read(0, j, lx, p.ldx);
+        const float2 gt = read(3, j, lh, g.lddh) + after;
+        after = a[j] * gt;
+        // the gates again from their exponentials: fewer registers than keeping them all
+        const Gates q = grec_gates_from(er[j], ei[j], rate);
+        const float2 y = q.si * x, gs = gt * q.s;
+        const float2 d = after * (q.l * hb[j] + both(-1.f) * (y * a[j] * (q.l * q.rs)));
+        dlam = dlam + d;
+        store_pair<T>(dx + j * g.lddx, gs * q.si, g.px, first, second);
+        store_pair<T>(di + j * g.lddi, gs * y * (q.ei * q.si), g.pi, first, second);
+        store_pair<T>(dr + j * g.lddr, d * (q.er * q.sr), g.pr, first, second);
+      };
+      if (n == kR) {
+#pragma unroll
+        for (int j = 0; j < kR; ++j) forth(j);
+#pragma unroll
+        for (int j = kR - 1; j >= 0; --j) emit(j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kR; ++j)
+          if (j < n) forth(j);
+#pragma unroll
+        for (int j = kR - 1; j >= 0; --j)
+          if (j < n) emit(j);
+      }
+      __syncwarp();
+      stage(row - static_cast<int64_t>(STAGES) * step_rows, slot);
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
+    }
+    cp_async_wait_all();
+    if (dh0 && rank == 0 && warp == 0) {
+      if (first) dh0[s * p.channels + c] = carry.x;
+      if (second) dh0[s * p.channels + c + 1] = carry.y;
+    }
+  }
+
+  // the block's sum of D a channel, warps in order
+  float2* sums = reinterpret_cast<float2*>(mine - warp * S::kWarp);
+  __syncthreads();
+  sums[warp * 32 + lane] = dlam;
+  __syncthreads();
+  if (warp == 0) {
+    float2 sum = sums[lane];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) sum = sum + sums[w * 32 + lane];
+    float* at = partial + (static_cast<int64_t>(blockIdx.y) * peers + rank) * p.channels + c;
+    if (first) at[0] = sum.x;
+    if (second) at[1] = sum.y;
+  }
+  if (peers > 1) cluster_sync();  // no block leaves while another may still write to it
+}
+
+// dlam[c] = slope(lam_c) * the sum of the blocks' parts: 32 channels a block, each of its 16
+// warps every sixteenth part in order, then the warps' sums in order.
+constexpr int kSumWarps = 16;
+
+__global__ void __launch_bounds__(32 * kSumWarps)
+grec_dlam_kernel(int channels, int64_t parts, const float* __restrict__ lam,
+                 const float* __restrict__ partial, float* __restrict__ dlam) {
+  __shared__ float sums[kSumWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x * 32 + lane;
+  float sum = 0.f;
+  if (c < channels)
+    for (int64_t k = warp; k < parts; k += kSumWarps) sum += partial[k * channels + c];
+  sums[warp][lane] = sum;
+  __syncthreads();
+  if (warp != 0 || c >= channels) return;
+  sum = 0.f;
+  for (int w = 0; w < kSumWarps; ++w) sum += sums[w][lane];
+  dlam[c] = sum * grec_rate_slope(lam[c]);
+}
+
+int64_t tiles_of(int channels) { return (channels + kTileC - 1) / kTileC; }
+int64_t grid_y(int64_t batch) { return batch < 65535 ? batch : 65535; }
+
+template <typename T, bool ALIGNED, int STAGES>
+cudaError_t launch_backward(const GrecRows<T>& p, const GrecGradRows<T>& g, const float* lam,
+                            float kappa, const float* tape, const float* dhT, float* dh0,
+                            float* partial, int cluster, cudaStream_t stream) {
+  using S = GrecBackwardShared<T, ALIGNED, STAGES>;
+  return launch_clusters(grec_backward_kernel<T, ALIGNED, STAGES>,
+                         dim3(static_cast<unsigned>(tiles_of(p.channels) * cluster),
+                              static_cast<unsigned>(grid_y(p.batch))),
+                         32 * kWarps, S::kBytes, cluster, stream, p, g, lam, kappa, tape, dhT, dh0,
+                         partial);
+}
+
+}  // namespace
+
+size_t grec_backward_workspace(int channels, int64_t batch, int64_t rows) {
+  if (batch == 0) return 0;
+  // packed sequences may take a smaller cluster than this; never a larger one
+  const int64_t parts = grid_y(batch) * grec_cluster(tiles_of(channels) * batch, rows, kTapeRows);
+  return static_cast<size_t>(parts) * channels * sizeof(float);
+}
+
+template <typename T>
+cudaError_t launch_grec_backward(const GrecRows<T>& p, const float* lam, float kappa,
+                                 const float* tape, const T* dh, int64_t lddh, const float* dhT,
+                                 T* dx, int64_t lddx, T* dr, int64_t lddr, T* di, int64_t lddi,
+                                 float* dlam, float* dh0, void* work, cudaStream_t stream) {
+  float* partial = static_cast<float*>(work);
+  int64_t parts = 0;
+  if (p.batch > 0) {
+    const GrecGradRows<T> g{dh, dx, dr, di, lddh, lddx, lddr, lddi,
+                            pair_stores(dx, lddx), pair_stores(dr, lddr), pair_stores(di, lddi)};
+    const int64_t length = p.offsets ? p.rows / p.batch + 1 : p.length;
+    const int cluster = grec_cluster(tiles_of(p.channels) * p.batch,
+                                     length < p.rows ? length : p.rows, kTapeRows);
+    parts = grid_y(p.batch) * cluster;
+    const bool aligned = rows_aligned(p.x, p.ldx) && rows_aligned(p.r, p.ldr) &&
+                         rows_aligned(p.i, p.ldi) && rows_aligned(dh, lddh);
+    const cudaError_t e =
+        aligned ? launch_backward<T, true, 2>(p, g, lam, kappa, tape, dhT, dh0, partial, cluster,
+                                              stream)
+                : launch_backward<T, false, 2>(p, g, lam, kappa, tape, dhT, dh0, partial, cluster,
+                                               stream);
+    if (e != cudaSuccess) return e;
+  }
+  grec_dlam_kernel<<<(p.channels + 31) / 32, 32 * kSumWarps, 0, stream>>>(p.channels, parts, lam,
+                                                                         partial, dlam);
+  return cudaGetLastError();
+}
+
+#define BSOLVE_GREC_BACKWARD(T)                                                                 \
+  template cudaError_t launch_grec_backward<T>(                                                 \
+      const GrecRows<T>&, const float*, float, const float*, const T*, int64_t, const float*,   \
+      T*, int64_t, T*, int64_t, T*, int64_t, float*, float*, void*, cudaStream_t);
+BSOLVE_GREC_BACKWARD(float)
+BSOLVE_GREC_BACKWARD(__nv_bfloat16)
+BSOLVE_GREC_BACKWARD(__half)
+#undef BSOLVE_GREC_BACKWARD
+
+}  // namespace bsolve

@@ -98,13 +98,17 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return __ffma2_rn(a, b, c);
 }
 
-// neg_rate: -K of the two channels.
-__device__ __forceinline__ Gates grec_gates(float2 r, float2 i, float2 neg_rate) {
+// e^-v, at most 2^60.
+__device__ __forceinline__ float2 bounded_exp_neg(float2 v) {
+  v = v * both(-kLog2e);
+  return make_float2(ex2(min_nan(v.x, 60.f)), ex2(min_nan(v.y, 60.f)));
+}
+
+// From er and ei; neg_rate: -K of the two channels.
+__device__ __forceinline__ Gates grec_gates_from(float2 er, float2 ei, float2 neg_rate) {
   Gates g;
-  r = r * both(-kLog2e);
-  i = i * both(-kLog2e);
-  g.er = make_float2(ex2(min_nan(r.x, 60.f)), ex2(min_nan(r.y, 60.f)));
-  g.ei = make_float2(ex2(min_nan(i.x, 60.f)), ex2(min_nan(i.y, 60.f)));
+  g.er = er;
+  g.ei = ei;
   const float2 p = g.er + both(1.f), q = g.ei + both(1.f);
   float2 d = p * q;
   d = make_float2(rcp(d.x), rcp(d.y));
@@ -131,6 +135,10 @@ __device__ __forceinline__ Gates grec_gates(float2 r, float2 i, float2 neg_rate)
   g.rs = make_float2(rsqrt_fast(w.x), rsqrt_fast(w.y));
   g.s = w * g.rs;
   return g;
+}
+
+__device__ __forceinline__ Gates grec_gates(float2 r, float2 i, float2 neg_rate) {
+  return grec_gates_from(bounded_exp_neg(r), bounded_exp_neg(i), neg_rate);
 }
 
 }  // namespace bsolve
