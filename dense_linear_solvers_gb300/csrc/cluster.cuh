@@ -21,9 +21,14 @@ __device__ __forceinline__ int cluster_size() {
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
   return static_cast<int>(n);
 }
-// Every thread of every block of the cluster arrives; what was written before is seen after.
+// Every thread of every block of the cluster arrives. The barrier itself orders no memory on
+// arrival: a warp that has stored to its peers publishes that with cluster_publish() first, so
+// that the others need not wait for their own stores to global memory.
+__device__ __forceinline__ void cluster_publish() {
+  asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
@@ -45,15 +50,20 @@ __device__ __forceinline__ unsigned low_bits(const void* p) {
 }
 
 // Stores two neighbouring elements, as one value where `pairs` says that they are aligned.
-template <typename T>
+// WHOLE: both are there and aligned.
+template <typename T, bool WHOLE>
 __device__ __forceinline__ void store_pair(T* at, float2 v, bool pairs, bool first, bool second) {
   const typename Pair<T>::type q = pair_from_f32<T>(v);
-  if (pairs && second) {
+  if (WHOLE || (pairs && second)) {
     *reinterpret_cast<typename Pair<T>::type*>(at) = q;
   } else {
     if (first) at[0] = q.x;
     if (second) at[1] = q.y;
   }
+}
+template <typename T>
+__device__ __forceinline__ T* row_at(T* base, int row, unsigned pitch) {
+  return reinterpret_cast<T*>(reinterpret_cast<char*>(base) + row * static_cast<uint64_t>(pitch));
 }
 
 // Whether every row of an operand starts on a 16-byte boundary, or on one of two elements.

@@ -1,5 +1,7 @@
 // Gated linear recurrence (bs_grec calls of bsolve.h): forward over sequences, and one row from kept
 // states.
+#include <type_traits>
+
 #include "cluster.cuh"
 #include "grec_math.cuh"
 #include "grec_tile.cuh"
@@ -8,14 +10,6 @@
 
 namespace bsolve {
 namespace {
-
-struct Gate1 {
-  float a, s, sr, si, er, ei, l, rs;
-};
-__device__ __forceinline__ Gate1 gates1(float r, float i, float rate) {
-  const Gates g = grec_gates(both(r), both(i), both(-rate));
-  return {g.a.x, g.s.x, g.sr.x, g.si.x, g.er.x, g.ei.x, g.l.x, g.rs.x};
-}
 
 // ------------------------------------------------------------------ forward
 //
@@ -36,6 +30,11 @@ struct Composition {  // of two channels
 };
 
 __device__ __forceinline__ float2 apply(const Composition& m, float2 h) { return fma2(m.A, h, m.H); }
+
+// `second` after `first`.
+__device__ __forceinline__ Composition compose(const Composition& second, const Composition& first) {
+  return {second.A * first.A, apply(second, first.H)};
+}
 
 template <typename T, int R, bool ALIGNED, int STAGES>
 struct GrecForwardShared {
@@ -63,11 +62,14 @@ grec_forward_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa, c
   const int valid = p.channels - c0 < kTileC ? p.channels - c0 : kTileC;
   const int c = c0 + 2 * lane;
   const bool first = c < p.channels, second = c + 1 < p.channels;
-  const float2 rate = make_float2(first ? -grec_rate(lam[c], kappa) : 0.f,
-                                  second ? -grec_rate(lam[c + 1], kappa) : 0.f);
-  const int64_t px = p.ldx * static_cast<int64_t>(sizeof(T)),
-                pr = p.ldr * static_cast<int64_t>(sizeof(T)),
-                pi = p.ldi * static_cast<int64_t>(sizeof(T));
+  const float2 rate = make_float2(first ? grec_rate(lam[c], kappa) : 0.f,
+                                  second ? grec_rate(lam[c + 1], kappa) : 0.f);
+  const bool small = __all_sync(0xFFFFFFFFu, rate.x <= kSmallRate && rate.y <= kSmallRate);
+  const unsigned px = static_cast<unsigned>(p.ldx * sizeof(T)),
+                 pr = static_cast<unsigned>(p.ldr * sizeof(T)),
+                 pi = static_cast<unsigned>(p.ldi * sizeof(T)),
+                 ph = static_cast<unsigned>(ldh * sizeof(T));
+  const bool whole = pairs && valid == kTileC;
   const int step_rows = peers * kWarps * R;
   int parity = 0;
   if (peers > 1) cluster_sync();  // every block runs before one writes to another
@@ -107,42 +109,49 @@ grec_forward_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa, c
                      li = low_bits(p.i + row * p.ldi);
       float2 a[R], u[R];
       Composition m{both(1.f), both(0.f)};
-      auto element = [&](int j) {
-        const float2 x = staged_pair<T, ALIGNED>(in, j, lx, static_cast<unsigned>(px));
-        const Gates g = grec_gates(
-            staged_pair<T, ALIGNED>(in + S::kOperand, j, lr, static_cast<unsigned>(pr)),
-            staged_pair<T, ALIGNED>(in + 2 * S::kOperand, j, li, static_cast<unsigned>(pi)), rate);
+      auto element = [&](int j, auto kind) {
+        const float2 x = staged_pair<T, ALIGNED>(in, j, lx, px);
+        const float2 r =
+            staged_pair<T, ALIGNED>(in + S::kOperand, j, lr, pr);
+        const float2 i =
+            staged_pair<T, ALIGNED>(in + 2 * S::kOperand, j, li, pi);
+        const Gates g =
+            grec_gates<decltype(kind)::value>(grec_exp_neg<false>(r), grec_exp_neg<false>(i), rate);
         a[j] = g.a;
         u[j] = g.s * g.si * x;
         m.A = m.A * a[j];
         m.H = fma2(a[j], m.H, u[j]);
       };
-      if (n == R) {  // no branch between the rows: their instructions interleave
+      if (n == R && small) {  // no branch between the rows: their instructions interleave
 #pragma unroll
-        for (int j = 0; j < R; ++j) element(j);
+        for (int j = 0; j < R; ++j) element(j, std::true_type());
+      } else if (n == R) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) element(j, std::false_type());
       } else {
 #pragma unroll
         for (int j = 0; j < R; ++j)
-          if (j < n) element(j);
+          if (j < n) element(j, std::false_type());
       }
       __syncwarp();
       stage(row + static_cast<int64_t>(STAGES) * step_rows, slot);
       slot = slot + 1 == STAGES ? 0 : slot + 1;
 
+      // the composition of the block's rows in front of the warp's
       Composition* seg = segments + parity * kWarps * 32;
       seg[warp * 32 + lane] = m;
       __syncthreads();
-      float2 before = state;  // the state in front of the warp's rows
+      Composition front{both(1.f), both(0.f)};
+#pragma unroll
+      for (int w = 0; w < kWarps - 1; ++w)
+        if (w < warp) front = compose(seg[w * 32 + lane], front);
+      float2 before = state;  // the state in front of the block's, then of the warp's rows
       if (peers > 1) {
         Composition* blk = blocks + parity * kMaxCluster * 32;
-        if (warp < peers) {  // warp w tells block w
-          Composition all = seg[lane];
-#pragma unroll
-          for (int w = 1; w < kWarps; ++w) {
-            const Composition q = seg[w * 32 + lane];
-            all = {q.A * all.A, apply(q, all.H)};
-          }
-          for (int w = warp; w < peers; w += kWarps) store_remote(blk + rank * 32 + lane, w, all);
+        if (warp == kWarps - 1) {
+          const Composition all = compose(m, front);
+          for (int q = 0; q < peers; ++q) store_remote(blk + rank * 32 + lane, q, all);
+          cluster_publish();
         }
         cluster_sync();
         for (int q = 0; q < peers; ++q) {
@@ -153,7 +162,7 @@ grec_forward_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa, c
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) state = apply(seg[w * 32 + lane], state);
       }
-      for (int w = 0; w < warp; ++w) before = apply(seg[w * 32 + lane], before);
+      before = apply(front, before);
       parity ^= 1;
 
       if (tape && n > 0 && (row - start) % kTapeRows == 0) {
@@ -162,17 +171,17 @@ grec_forward_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa, c
         if (second) at[1] = before.y;
       }
       T* out = h + row * ldh + c;
-      auto emit = [&](int j) {
+      auto emit = [&](int j, auto kind) {
         before = fma2(a[j], before, u[j]);
-        store_pair<T>(out + j * ldh, before, pairs, first, second);
+        store_pair<T, decltype(kind)::value>(row_at(out, j, ph), before, pairs, first, second);
       };
-      if (n == R) {
+      if (n == R && whole) {
 #pragma unroll
-        for (int j = 0; j < R; ++j) emit(j);
+        for (int j = 0; j < R; ++j) emit(j, std::true_type());
       } else {
 #pragma unroll
         for (int j = 0; j < R; ++j)
-          if (j < n) emit(j);
+          if (j < n) emit(j, std::false_type());
       }
     }
     cp_async_wait_all();
@@ -196,9 +205,11 @@ grec_step_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa,
     const int64_t slot = slots ? slots[j] : j;
     float h = 0.f;
     if (slot >= 0 && slot < num_slots) {
-      const Gate1 g = gates1(to_f32(p.r[j * p.ldr + c]), to_f32(p.i[j * p.ldi + c]), rate);
+      const Gates g = grec_gates<false>(grec_exp_neg<false>(both(to_f32(p.r[j * p.ldr + c]))),
+                                        grec_exp_neg<false>(both(to_f32(p.i[j * p.ldi + c]))),
+                                        both(rate));
       float* at = state + slot * p.channels + c;
-      h = fmaf(g.a, *at, g.s * g.si * to_f32(p.x[j * p.ldx + c]));
+      h = fmaf(g.a.x, *at, g.s.x * g.si.x * to_f32(p.x[j * p.ldx + c]));
       *at = h;
     }
     y[j * ldy + c] = from_f32<T>(h);

@@ -19,6 +19,8 @@
 //     writing the three gradients.
 // The gradient of lam: every lane sums D = dL/dl * l over its rows, the block's warps are added at
 // the end and each block writes one partial sum a channel; a second kernel adds those in order.
+#include <type_traits>
+
 #include "cluster.cuh"
 #include "grec_math.cuh"
 #include "grec_tile.cuh"
@@ -35,6 +37,11 @@ static_assert(kWarps * kR == kTapeRows, "a block's piece starts at a state on th
 struct Exchange {  // of two channels
   float2 A, P;
 };
+__device__ __forceinline__ float2 apply(const Exchange& m, float2 g) { return fma2(m.A, g, m.P); }
+// `second` after `first`, towards the sequence's start.
+__device__ __forceinline__ Exchange compose(const Exchange& second, const Exchange& first) {
+  return {second.A * first.A, apply(second, first.P)};
+}
 
 template <typename T, bool ALIGNED, int STAGES>
 struct GrecBackwardShared {
@@ -72,9 +79,13 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
   const int valid = p.channels - c0 < kTileC ? p.channels - c0 : kTileC;
   const int c = c0 + 2 * lane;
   const bool first = c < p.channels, second = c + 1 < p.channels;
-  const float2 rate = make_float2(first ? -grec_rate(lam[c], kappa) : 0.f,
-                                  second ? -grec_rate(lam[c + 1], kappa) : 0.f);
-  const int64_t es = sizeof(T);
+  const float2 rate = make_float2(first ? grec_rate(lam[c], kappa) : 0.f,
+                                  second ? grec_rate(lam[c + 1], kappa) : 0.f);
+  const bool small = __all_sync(0xFFFFFFFFu, rate.x <= kSmallRate && rate.y <= kSmallRate);
+  const unsigned es = sizeof(T);
+  const unsigned px = p.ldx * es, pr = p.ldr * es, pi = p.ldi * es, ph = g.lddh * es,
+                 pdx = g.lddx * es, pdr = g.lddr * es, pdi = g.lddi * es;
+  const bool whole = g.px && g.pr && g.pi && valid == kTileC;
   const int step_rows = peers * kTapeRows;
   float2 dlam = make_float2(0.f, 0.f);
   int parity = 0;
@@ -97,13 +108,10 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
       const int n = at < start || at >= end ? 0 : (end - at < kR ? static_cast<int>(end - at) : kR);
       char* to = mine + slot * S::kStage;
       if (n > 0) {
-        stage_rows<T, ALIGNED, kR>(to, p.x + at * p.ldx + c0, p.ldx * es, n, valid, p.x);
-        stage_rows<T, ALIGNED, kR>(to + S::kOperand, p.r + at * p.ldr + c0, p.ldr * es, n, valid,
-                                   p.r);
-        stage_rows<T, ALIGNED, kR>(to + 2 * S::kOperand, p.i + at * p.ldi + c0, p.ldi * es, n,
-                                   valid, p.i);
-        stage_rows<T, ALIGNED, kR>(to + 3 * S::kOperand, g.dh + at * g.lddh + c0, g.lddh * es, n,
-                                   valid, g.dh);
+        stage_rows<T, ALIGNED, kR>(to, p.x + at * p.ldx + c0, px, n, valid, p.x);
+        stage_rows<T, ALIGNED, kR>(to + S::kOperand, p.r + at * p.ldr + c0, pr, n, valid, p.r);
+        stage_rows<T, ALIGNED, kR>(to + 2 * S::kOperand, p.i + at * p.ldi + c0, pi, n, valid, p.i);
+        stage_rows<T, ALIGNED, kR>(to + 3 * S::kOperand, g.dh + at * g.lddh + c0, ph, n, valid, g.dh);
       }
       cp_async_commit();
     };
@@ -125,33 +133,37 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
       const char* in = mine + slot * S::kStage;
       const unsigned lx = low_bits(p.x + row * p.ldx), lr = low_bits(p.r + row * p.ldr),
                      li = low_bits(p.i + row * p.ldi), lh = low_bits(g.dh + row * g.lddh);
-      auto read = [&](int operand, int j, unsigned low, int64_t ld) {
-        return staged_pair<T, ALIGNED>(in + operand * S::kOperand, j, low,
-                                       static_cast<unsigned>(ld * es));
+      auto read = [&](int operand, int j, unsigned low, unsigned pitch) {
+        return staged_pair<T, ALIGNED>(in + operand * S::kOperand, j, low, pitch);
       };
 
       float2 a[kR], er[kR], ei[kR], hb[kR];
       Exchange m{both(1.f), both(0.f)};
       float2 H = both(0.f);
-      auto element = [&](int j) {
-        const Gates q = grec_gates(read(1, j, lr, p.ldr), read(2, j, li, p.ldi), rate);
+      auto element = [&](int j, auto kind) {
+        er[j] = grec_exp_neg<true>(read(1, j, lr, pr));
+        ei[j] = grec_exp_neg<true>(read(2, j, li, pi));
+        const Gates q = grec_gates<decltype(kind)::value>(er[j], ei[j], rate);
         a[j] = q.a;
-        er[j] = q.er;
-        ei[j] = q.ei;
-        hb[j] = q.s * q.si * read(0, j, lx, p.ldx);  // u, until the states are known
+        hb[j] = q.s * q.si * read(0, j, lx, px);  // u, until the states are known
         H = fma2(a[j], H, hb[j]);
         m.A = m.A * a[j];
       };
-      auto back = [&](int j) { m.P = a[j] * (m.P + read(3, j, lh, g.lddh)); };
+      auto back = [&](int j) { m.P = a[j] * (m.P + read(3, j, lh, ph)); };
       if (n == kR) {
+        if (small) {
 #pragma unroll
-        for (int j = 0; j < kR; ++j) element(j);
+          for (int j = 0; j < kR; ++j) element(j, std::true_type());
+        } else {
+#pragma unroll
+          for (int j = 0; j < kR; ++j) element(j, std::false_type());
+        }
 #pragma unroll
         for (int j = kR - 1; j >= 0; --j) back(j);
       } else {
 #pragma unroll
         for (int j = 0; j < kR; ++j)
-          if (j < n) element(j);
+          if (j < n) element(j, std::false_type());
 #pragma unroll
         for (int j = kR - 1; j >= 0; --j)
           if (j < n) back(j);
@@ -162,36 +174,31 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
       seg[warp * 32 + lane] = m;
       st[warp * 32 + lane] = H;
       __syncthreads();
-      float2 after = carry;  // what comes from behind the warp's rows
+      Exchange behind{both(1.f), both(0.f)};  // the block's rows behind the warp's
+#pragma unroll
+      for (int w = kWarps - 1; w > 0; --w)
+        if (w > warp) behind = compose(seg[w * 32 + lane], behind);
+      float2 after = carry;  // what comes from behind the block's, then the warp's rows
       if (peers > 1) {
         Exchange* blk = blocks + parity * kMaxCluster * 32;
-        if (warp < peers) {  // warp w tells block w
-          Exchange all = seg[(kWarps - 1) * 32 + lane];
-#pragma unroll
-          for (int w = kWarps - 2; w >= 0; --w) {
-            const Exchange q = seg[w * 32 + lane];
-            all = {q.A * all.A, fma2(q.A, all.P, q.P)};
-          }
-          store_remote(blk + rank * 32 + lane, warp, all);
+        if (warp == 0) {
+          const Exchange all = compose(m, behind);
+          for (int q = 0; q < peers; ++q) store_remote(blk + rank * 32 + lane, q, all);
+          cluster_publish();
         }
         cluster_sync();
         for (int q = peers - 1; q >= 0; --q) {
           if (q == rank) after = carry;
-          const Exchange e = blk[q * 32 + lane];
-          carry = fma2(e.A, carry, e.P);
+          carry = apply(blk[q * 32 + lane], carry);
         }
       } else {
 #pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
-          const Exchange e = seg[w * 32 + lane];
-          carry = fma2(e.A, carry, e.P);
-        }
+        for (int w = kWarps - 1; w >= 0; --w) carry = apply(seg[w * 32 + lane], carry);
       }
-      for (int w = kWarps - 1; w > warp; --w) {
-        const Exchange e = seg[w * 32 + lane];
-        after = fma2(e.A, after, e.P);
-      }
-      for (int w = 0; w < warp; ++w) before = fma2(seg[w * 32 + lane].A, before, st[w * 32 + lane]);
+      after = apply(behind, after);
+#pragma unroll
+      for (int w = 0; w < kWarps - 1; ++w)
+        if (w < warp) before = fma2(seg[w * 32 + lane].A, before, st[w * 32 + lane]);
       parity ^= 1;
 
       T* dx = g.dx + row * g.lddx + c;
@@ -202,31 +209,40 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
         hb[j] = before;
         before = fma2(a[j], before, u);
       };
-      auto emit = [&](int j) {
-        const float2 x = read(0, j, lx, p.ldx);
-        const float2 gt = read(3, j, lh, g.lddh) + after;
+      auto emit = [&](int j, auto kind, auto all) {
+        constexpr bool kWhole = decltype(all)::value;
+        const float2 x = read(0, j, lx, px);
+        const float2 gt = read(3, j, lh, ph) + after;
         after = a[j] * gt;
         // the gates again from their exponentials: fewer registers than keeping them all
-        const Gates q = grec_gates_from(er[j], ei[j], rate);
+        const Gates q = grec_gates<decltype(kind)::value>(er[j], ei[j], rate);
         const float2 y = q.si * x, gs = gt * q.s;
-        const float2 d = after * (q.l * hb[j] + both(-1.f) * (y * a[j] * (q.l * q.rs)));
+        const float2 d = after * (y * a[j] * (q.t * q.rs) + both(-1.f) * (q.t * hb[j]));
         dlam = dlam + d;
-        store_pair<T>(dx + j * g.lddx, gs * q.si, g.px, first, second);
-        store_pair<T>(di + j * g.lddi, gs * y * (q.ei * q.si), g.pi, first, second);
-        store_pair<T>(dr + j * g.lddr, d * (q.er * q.sr), g.pr, first, second);
+        store_pair<T, kWhole>(row_at(dx, j, pdx), gs * q.si, g.px, first, second);
+        store_pair<T, kWhole>(row_at(di, j, pdi), gs * y * (ei[j] * q.si), g.pi, first, second);
+        store_pair<T, kWhole>(row_at(dr, j, pdr), d * (er[j] * q.sr), g.pr, first, second);
       };
       if (n == kR) {
 #pragma unroll
         for (int j = 0; j < kR; ++j) forth(j);
+        if (small && whole) {
 #pragma unroll
-        for (int j = kR - 1; j >= 0; --j) emit(j);
+          for (int j = kR - 1; j >= 0; --j) emit(j, std::true_type(), std::true_type());
+        } else if (whole) {
+#pragma unroll
+          for (int j = kR - 1; j >= 0; --j) emit(j, std::false_type(), std::true_type());
+        } else {
+#pragma unroll
+          for (int j = kR - 1; j >= 0; --j) emit(j, std::false_type(), std::false_type());
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < kR; ++j)
           if (j < n) forth(j);
 #pragma unroll
         for (int j = kR - 1; j >= 0; --j)
-          if (j < n) emit(j);
+          if (j < n) emit(j, std::false_type(), std::false_type());
       }
       __syncwarp();
       stage(row - static_cast<int64_t>(STAGES) * step_rows, slot);

@@ -72,23 +72,24 @@ __device__ __forceinline__ float grec_rate_slope(float lam) {
   return (lam >= 0.f ? 1.f : e) / ((1.f + e) * sp);
 }
 
-// What one element's gates give.
-//   er = e^-r, ei = e^-i, each at most 2^60, share one reciprocal of (1 + er)(1 + ei):
-//     sigma(r) = (1 + ei) d,  1 - sigma(r) = er sigma(r), without cancellation. The bound keeps
-//     the product finite; sigma(r) is taken 2^-60 lower, so that a gate of -inf closes (a = 1,
-//     s = 0 up to 2^-40: the row hands its state on).
-//   a = exp(l) and 1 - a^2 both come from E = exp(l) - 1, since near a = 1 (long memory)
-//     1 - a^2 = -E (1 + a) keeps its digits while 1 - a*a loses them: l = n ln 2 + f with
-//     |f| <= ln 2 / 2, E = 2^n (e^f - 1) + (2^n - 1), e^f - 1 by its Taylor sum to f^7 (the
-//     next term is f^8 / 40320, 2e-8 of f at the end of the range). l is bounded at -80, where
-//     a is 2e-35.
-//   s = sqrt(1 - a^2) = w rsqrt(w), l / s = l rsqrt(w) with w >= 2^-80, where both are below
-//     2^-40 of full scale.
+// What one element's gates give, with l = -t:
+//   sigma(r) = 1 / (1 + e^-r); 1 - sigma(r) = e^-r sigma(r), without cancellation where e^-r is
+//     kept finite (grec_exp_neg<true>, at most 2^100: the sigma below is then 2^-100, not 0).
+//   a = e^-t and 1 - a^2 both come from m = 1 - e^-t, since near a = 1 (long memory) 1 - a^2 =
+//     m (1 + a) keeps its digits while 1 - a*a loses them. SMALL (rate at most kSmallRate, so that
+//     a >= 0.6): m = t - t^2 q(t), q the polynomial of degree 3 with the least relative error
+//     of m on [0, 0.5], 2^-24. Otherwise t = n ln 2 + f with |f| <= ln 2 / 2,
+//     m = (1 - 2^-n) + 2^-n (f - f^2 q(f)), q of degree 4 (2^-27), t bounded at 80, where a is 2e-35.
+//     On 16,384 x 4,096 BF16 rows the two take 26 and 32 instructions an element.
+//   2^-124 more in t, which no other value notices, keeps the root below away from 0 / 0:
+//   s = sqrt(1 - a^2) = w rsqrt(w), t / s = t rsqrt(w).
 // The approximate exponential, reciprocal and root are within 2 ulp of FP32 (2^-22), two
 // orders below a 16-bit output's rounding and near that of one FP32 operation.
+constexpr float kSmallRate = 0.5f;
+
 // Two neighbouring channels at a time: the products and sums are FP32 pair instructions.
 struct Gates {
-  float2 a, s, sr, si, er, ei, l, rs;
+  float2 a, s, sr, si, t, rs;  // decay, root, sigma(r), sigma(i), -l, 1 / root
 };
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
@@ -98,47 +99,49 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return __ffma2_rn(a, b, c);
 }
 
-// e^-v, at most 2^60.
-__device__ __forceinline__ float2 bounded_exp_neg(float2 v) {
+// e^-v; BOUNDED: at most 2^100.
+template <bool BOUNDED>
+__device__ __forceinline__ float2 grec_exp_neg(float2 v) {
   v = v * both(-kLog2e);
-  return make_float2(ex2(min_nan(v.x, 60.f)), ex2(min_nan(v.y, 60.f)));
+  if (BOUNDED) v = make_float2(min_nan(v.x, 100.f), min_nan(v.y, 100.f));
+  return make_float2(ex2(v.x), ex2(v.y));
 }
 
-// From er and ei; neg_rate: -K of the two channels.
-__device__ __forceinline__ Gates grec_gates_from(float2 er, float2 ei, float2 neg_rate) {
+// From e^-r, e^-i and the rates K of the two channels.
+template <bool SMALL>
+__device__ __forceinline__ Gates grec_gates(float2 er, float2 ei, float2 rate) {
   Gates g;
-  g.er = er;
-  g.ei = ei;
-  const float2 p = g.er + both(1.f), q = g.ei + both(1.f);
-  float2 d = p * q;
-  d = make_float2(rcp(d.x), rcp(d.y));
-  g.sr = fma2(q, d, both(-0x1p-60f));
-  g.si = p * d;
-  g.l = neg_rate * g.sr;
-  g.l = make_float2(max_nan(g.l.x, -80.f), max_nan(g.l.y, -80.f));
-  const float2 t = fma2(g.l, both(kLog2e), both(12582912.f));  // 1.5 * 2^23: n in the low bits
-  const float2 n = t + both(-12582912.f);
-  float2 f = fma2(n, both(-0.693359375f), g.l);  // ln 2 in two parts, the first exact * n
-  f = fma2(n, both(2.12194440e-4f), f);
-  float2 e = fma2(f, both(1.f / 5040.f), both(1.f / 720.f));
-  e = fma2(f, e, both(1.f / 120.f));
-  e = fma2(f, e, both(1.f / 24.f));
-  e = fma2(f, e, both(1.f / 6.f));
-  e = fma2(f, e, both(0.5f));
-  e = fma2(f * f, e, f);
-  const float2 two_n = make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
-                                   __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000));
-  const float2 E = fma2(two_n, e, two_n + both(-1.f));
-  g.a = E + both(1.f);
-  float2 w = fma2(E, g.a, E);  // E (1 + a) = a^2 - 1
-  w = make_float2(max_nan(-w.x, 0x1p-80f), max_nan(-w.y, 0x1p-80f));
+  const float2 p = er + both(1.f), q = ei + both(1.f);
+  g.sr = make_float2(rcp(p.x), rcp(p.y));
+  g.si = make_float2(rcp(q.x), rcp(q.y));
+  g.t = fma2(rate, g.sr, both(0x1p-124f));
+  float2 m;
+  if constexpr (SMALL) {
+    const float2 t = g.t;
+    float2 c = fma2(t, both(6.7512975e-3f), both(-4.0983321e-2f));  // -q(t)
+    c = fma2(t, c, both(1.6654362e-1f));
+    c = fma2(t, c, both(-4.9999245e-1f));
+    m = fma2(t * t, c, t);
+  } else {
+    g.t = make_float2(min_nan(g.t.x, 80.f), min_nan(g.t.y, 80.f));
+    const float2 k = fma2(g.t, both(-kLog2e), both(12582912.f));  // 1.5 * 2^23: -n in the low bits
+    const float2 n = k + both(-12582912.f);
+    float2 f = fma2(n, both(0.693359375f), g.t);  // ln 2 in two parts, the first exact * n
+    f = fma2(n, both(-2.12194440e-4f), f);
+    float2 c = fma2(f, both(-1.3459974e-3f), both(8.3572877e-3f));  // -q(f)
+    c = fma2(f, c, both(-4.1672192e-2f));
+    c = fma2(f, c, both(1.6666666e-1f));
+    c = fma2(f, c, both(-0.5f));
+    const float2 e = fma2(f * f, c, f);
+    const float2 two_n = make_float2(__int_as_float((__float_as_int(k.x) << 23) + 0x3f800000),
+                                     __int_as_float((__float_as_int(k.y) << 23) + 0x3f800000));
+    m = fma2(two_n, e, fma2(two_n, both(-1.f), both(1.f)));
+  }
+  g.a = fma2(m, both(-1.f), both(1.f));
+  const float2 w = fma2(m, g.a, m);
   g.rs = make_float2(rsqrt_fast(w.x), rsqrt_fast(w.y));
   g.s = w * g.rs;
   return g;
-}
-
-__device__ __forceinline__ Gates grec_gates(float2 r, float2 i, float2 neg_rate) {
-  return grec_gates_from(bounded_exp_neg(r), bounded_exp_neg(i), neg_rate);
 }
 
 }  // namespace bsolve

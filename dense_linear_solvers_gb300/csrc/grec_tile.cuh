@@ -34,7 +34,7 @@ __device__ __forceinline__ void cp_async_16(void* smem, const void* gmem, int by
 // the warp take part. Nothing outside the operand is read; what lies behind a row's valid
 // elements in shared memory is unspecified.
 template <typename T, bool ALIGNED, int R>
-__device__ __forceinline__ void stage_rows(char* smem, const T* first, int64_t pitch, int rows,
+__device__ __forceinline__ void stage_rows(char* smem, const T* first, unsigned pitch, int rows,
                                            int valid, const T* base) {
   using G = Tile<T, ALIGNED>;
   const int lane = threadIdx.x & 31;
@@ -45,19 +45,21 @@ __device__ __forceinline__ void stage_rows(char* smem, const T* first, int64_t p
     static_assert(R % kPer == 0, "whole copies");
     const int piece = lane % G::kPieces, sub = lane / G::kPieces;
     const int left = bytes - piece * 16;
-    if (left > 0) {
-      const char* src = row0 + sub * pitch + piece * 16;
-      char* to = smem + sub * G::kRowBytes + piece * 16;
+    const char* src = row0 + sub * static_cast<uint64_t>(pitch) + piece * 16;
+    char* to = smem + sub * G::kRowBytes + piece * 16;
+    if (rows == R && valid == kTileC) {
 #pragma unroll
-      for (int j = 0; j < R; j += kPer) {
-        if (j + sub < rows) cp_async_16(to + j * G::kRowBytes, src, left < 16 ? left : 16);
-        src += kPer * pitch;
-      }
+      for (int j = 0; j < R; j += kPer)
+        cp_async_16(to + j * G::kRowBytes, src + j * static_cast<uint64_t>(pitch), 16);
+    } else if (left > 0) {
+      for (int j = 0; j + sub < rows; j += kPer)
+        cp_async_16(to + j * G::kRowBytes, src + j * static_cast<uint64_t>(pitch),
+                    left < 16 ? left : 16);
     }
   } else {
     for (int q = lane; q < rows * G::kPieces; q += 32) {
       const int k = q / G::kPieces, piece = q - k * G::kPieces;
-      const char* src = row0 + k * pitch;
+      const char* src = row0 + k * static_cast<uint64_t>(pitch);
       const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
       const char* from = src - shift + piece * 16;
       const int left = bytes + shift - piece * 16;
