@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kMaxChannels = 1 << 20;
 constexpr int kMaxWidth = 65536;
-constexpr int64_t kMaxRows = int64_t(1) << 40;  // rows * ld stays far inside 64 bits
+constexpr int64_t kMaxRows = int64_t(1) << 30;  // a row's number, and a step beyond, fits 32 bits
 constexpr int64_t kMaxLd = int64_t(1) << 21;
 
 int element_size(bs_dtype dtype) {

@@ -27,9 +27,15 @@ __device__ __forceinline__ int cluster_size() {
 __device__ __forceinline__ void cluster_publish() {
   asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
 }
 
 // Stores 16 bytes at `at` (an address in this block's shared memory) in block `rank`'s.
@@ -77,34 +83,71 @@ bool pair_stores(const T* p, int64_t ld) {
           (2 * sizeof(T) - 1)) == 0;
 }
 
-// Blocks of a cluster that share one sequence and channel tile: `units` such pairs are at hand, of
-// `length` rows each (packed sequences: on average), `rows` rows a block at a time. As many as
-// the GPU's 152 SMs hold at once, two blocks each, and no more than the sequence has pieces
-// for: a second wave of few blocks costs more than idle slots.
-inline int grec_cluster(int64_t units, int64_t length, int rows) {
-  int n = 1;
-  while (n < kMaxCluster && units * 2 * n <= 2 * 152 && length > static_cast<int64_t>(n) * rows)
-    n *= 2;
-  return n;
-}
-
-template <typename... P, typename... A>
-cudaError_t launch_clusters(void (*kernel)(P...), dim3 grid, int threads, int shared, int cluster,
-                            cudaStream_t stream, A... args) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cluster;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
+inline cudaLaunchConfig_t cluster_config(cudaLaunchAttribute* attr, dim3 grid, int threads, int shared,
+                                  int cluster, cudaStream_t stream) {
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = cluster;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
   cudaLaunchConfig_t config{};
   config.gridDim = grid;
   config.blockDim = dim3(threads);
   config.dynamicSmemBytes = shared;
   config.stream = stream;
-  config.attrs = &attr;
+  config.attrs = attr;
   config.numAttrs = 1;
+  return config;
+}
+
+// How many clusters of 1 .. kMaxCluster blocks of a kernel the GPU holds at once; asked of the
+// driver at the kernel's first launch.
+struct Held {
+  int clusters[kMaxCluster + 1];
+  cudaError_t status;
+};
+
+template <typename... P>
+Held held_clusters(void (*kernel)(P...), int threads, int shared) {
+  Held h{};
+  h.status = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+  for (int n = 1; n <= kMaxCluster && h.status == cudaSuccess; ++n) {
+    cudaLaunchAttribute attr{};
+    const cudaLaunchConfig_t config =
+        cluster_config(&attr, dim3(n), threads, shared, n, nullptr);
+    h.status = cudaOccupancyMaxActiveClusters(&h.clusters[n], kernel, &config);
+  }
+  return h;
+}
+
+// Above so many pairs of a sequence and a channel tile, a block takes each alone.
+constexpr int64_t kManyUnits = 8192;
+
+// Blocks of a cluster that share one sequence and channel tile: `units` such pairs are at hand, of
+// `length` rows each (packed sequences: on average), a block takes `rows` of them in a
+// step. The clusters run in waves of what the GPU holds at once; a wave costs its steps and about
+// two more to fill and drain. The least such cost, the smaller cluster where two are alike.
+inline int grec_cluster(const Held& held, int64_t units, int64_t length, int rows) {
+  if (units > kManyUnits) return 1;
+  int best = 1;
+  double least = 0;
+  for (int n = 1; n <= kMaxCluster; ++n) {
+    if (held.clusters[n] < 1 || (n > 1 && length <= static_cast<int64_t>(n - 1) * rows)) break;
+    const int64_t waves = (units + held.clusters[n] - 1) / held.clusters[n];
+    const int64_t steps = (length + static_cast<int64_t>(n) * rows - 1) / (static_cast<int64_t>(n) * rows);
+    const double cost = static_cast<double>(waves) * static_cast<double>(steps + 2);
+    if (n == 1 || cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_clusters(void (*kernel)(P...), dim3 grid, int threads, int shared, int cluster,
+                            cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr{};
+  const cudaLaunchConfig_t config = cluster_config(&attr, grid, threads, shared, cluster, stream);
   return cudaLaunchKernelEx(&config, kernel, static_cast<P>(args)...);
 }
 

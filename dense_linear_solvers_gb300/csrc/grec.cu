@@ -13,17 +13,19 @@ namespace {
 
 // ------------------------------------------------------------------ forward
 //
-// A block takes a tile of 64 channels, a lane two of them, and 8 * R consecutive rows at a time,
-// a warp R of them; a cluster of blocks takes consecutive such pieces of one sequence. One step:
-//   every warp turns its rows into (a_t, u_t), kept in registers, and their composition
-//     h_out = A h_in + H (A the product of the a_t, H the state from zero);
-//   the warps' compositions meet in shared memory, the blocks' in every block's shared memory
-//     over the cluster; each warp composes those in front of it, in order, with the state
-//     at the step's start, which every block carries along;
-//   every warp runs its rows again from its own true state, one product-sum an element, and
-//     stores them.
+// A block takes a tile of 64 channels, a lane two of them, and W * 16 consecutive rows at a time,
+// a warp 16 of them; a cluster of blocks takes consecutive such pieces of one sequence. One step:
+//   every warp turns its rows into compositions h_j = A_j h_in + H_j from its first row on (A the
+//     product of the a_t, H the state from zero), kept in registers;
+//   the warps' last compositions meet in shared memory, the blocks' in every block's shared
+//     memory over the cluster, while the copies of a later step are issued; each warp composes
+//     those in front of it, in order, with the state at the step's start, which every block
+//     carries along;
+//   every warp applies its compositions to its own true state, one product-sum an element, and
+//     stores the states.
 // Each element is read and written once. The order of every sum follows from the sizes alone.
-constexpr int kWarps = 8;
+constexpr int kR = 16;      // rows a warp keeps in registers
+constexpr int kStages = 2;  // steps staged ahead
 
 struct Composition {  // of two channels
   float2 A, H;
@@ -36,22 +38,22 @@ __device__ __forceinline__ Composition compose(const Composition& second, const 
   return {second.A * first.A, apply(second, first.H)};
 }
 
-template <typename T, int R, bool ALIGNED, int STAGES>
+template <typename T, int W, bool ALIGNED>
 struct GrecForwardShared {
-  static constexpr int kOperand = R * Tile<T, ALIGNED>::kRowBytes;  // one warp's rows
+  static constexpr int kOperand = kR * Tile<T, ALIGNED>::kRowBytes;  // one warp's rows
   static constexpr int kStage = 3 * kOperand;
-  static constexpr int kWarp = STAGES * kStage;
-  static constexpr int kSegments = 2 * kWarps * 32 * sizeof(Composition);
+  static constexpr int kWarp = kStages * kStage;
+  static constexpr int kSegments = 2 * W * 32 * sizeof(Composition);
   static constexpr int kBlocks = 2 * kMaxCluster * 32 * sizeof(Composition);
-  static constexpr int kBytes = kSegments + kBlocks + kWarps * kWarp;
+  static constexpr int kBytes = kSegments + kBlocks + W * kWarp;
 };
 
-template <typename T, int R, bool ALIGNED, int STAGES>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1)
+template <typename T, int W, bool ALIGNED>
+__global__ void __launch_bounds__(32 * W, (sizeof(T) == 2 ? 16 : 8) / W)
 grec_forward_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa, const float* h0,
                     T* __restrict__ h, int64_t ldh, bool pairs, float* hT,
                     float* __restrict__ tape) {
-  using S = GrecForwardShared<T, R, ALIGNED, STAGES>;
+  using S = GrecForwardShared<T, W, ALIGNED>;
   extern __shared__ __align__(16) char shared[];
   Composition* segments = reinterpret_cast<Composition*>(shared);
   Composition* blocks = reinterpret_cast<Composition*>(shared + S::kSegments);
@@ -65,12 +67,10 @@ grec_forward_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa, c
   const float2 rate = make_float2(first ? grec_rate(lam[c], kappa) : 0.f,
                                   second ? grec_rate(lam[c + 1], kappa) : 0.f);
   const bool small = __all_sync(0xFFFFFFFFu, rate.x <= kSmallRate && rate.y <= kSmallRate);
-  const unsigned px = static_cast<unsigned>(p.ldx * sizeof(T)),
-                 pr = static_cast<unsigned>(p.ldr * sizeof(T)),
-                 pi = static_cast<unsigned>(p.ldi * sizeof(T)),
-                 ph = static_cast<unsigned>(ldh * sizeof(T));
-  const bool whole = pairs && valid == kTileC;
-  const int step_rows = peers * kWarps * R;
+  const unsigned ph = static_cast<unsigned>(ldh * sizeof(T));
+  const bool wide = valid == kTileC, whole = pairs && wide;
+  const int step_rows = peers * W * kR;
+  const int ahead = (rank * W + warp) * kR;  // the warp's first row of a step
   int parity = 0;
   if (peers > 1) cluster_sync();  // every block runs before one writes to another
 
@@ -82,105 +82,121 @@ grec_forward_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa, c
       if (first) state.x = h0[s * p.channels + c];
       if (second) state.y = h0[s * p.channels + c + 1];
     }
-    const int64_t tb = tape_base(start, s);
-    const int64_t steps = (end - start + step_rows - 1) / step_rows;
-    int64_t row = start + (rank * kWarps + warp) * R;  // the warp's first row of this step
+    const int length = static_cast<int>(end - start);
+    unsigned row = static_cast<unsigned>(start) + ahead;  // the warp's first row of this step
+    int left = length - ahead;                            // from there to the sequence's end
+    // a warp whose rows start at a multiple of 64 puts its state on the tape
+    float* tape_at = tape == nullptr || ahead % kTapeRows != 0
+                         ? nullptr
+                         : tape + (tape_base(start, s) + ahead / kTapeRows) * p.channels + c;
 
-    auto stage = [&](int64_t at, int slot) {
-      const int n = at >= end ? 0 : (end - at < R ? static_cast<int>(end - at) : R);
-      char* to = mine + slot * S::kStage;
+    auto stage = [&](int slot, int k) {  // the rows of the k-th step from this one
+      const int n = left - k * step_rows;
       if (n > 0) {
-        stage_rows<T, ALIGNED, R>(to, p.x + at * p.ldx + c0, px, n, valid, p.x);
-        stage_rows<T, ALIGNED, R>(to + S::kOperand, p.r + at * p.ldr + c0, pr, n, valid, p.r);
-        stage_rows<T, ALIGNED, R>(to + 2 * S::kOperand, p.i + at * p.ldi + c0, pi, n, valid, p.i);
+        const bool all = n >= kR && wide;
+        const unsigned at = row + k * step_rows;
+        char* to = mine + slot * S::kStage;
+        stage_tile<T, ALIGNED, kR>(to, p.x, at, p.ldx, c0, n < kR ? n : kR, all, valid);
+        stage_tile<T, ALIGNED, kR>(to + S::kOperand, p.r, at, p.ldr, c0, n < kR ? n : kR, all, valid);
+        stage_tile<T, ALIGNED, kR>(to + 2 * S::kOperand, p.i, at, p.ldi, c0, n < kR ? n : kR, all,
+                                  valid);
       }
       cp_async_commit();
     };
 #pragma unroll
-    for (int k = 0; k < STAGES; ++k) stage(row + static_cast<int64_t>(k) * step_rows, k);
+    for (int k = 0; k < kStages; ++k) stage(k, k);
 
     int slot = 0;
-    for (int64_t step = 0; step < steps; ++step, row += step_rows) {
-      const int n = row >= end ? 0 : (end - row < R ? static_cast<int>(end - row) : R);
-      cp_async_wait_group<STAGES - 1>();
+    for (int done = 0; done < length; done += step_rows, left -= step_rows, row += step_rows) {
+      const int n = left < kR ? left : kR;  // may be negative: none
+      cp_async_wait_group<kStages - 1>();
       __syncwarp();
       const char* in = mine + slot * S::kStage;
-      const unsigned lx = low_bits(p.x + row * p.ldx), lr = low_bits(p.r + row * p.ldr),
-                     li = low_bits(p.i + row * p.ldi);
-      float2 a[R], u[R];
-      Composition m{both(1.f), both(0.f)};
+      const Shift lx = shift_of<T, ALIGNED>(p.x, row, p.ldx),
+                  lr = shift_of<T, ALIGNED>(p.r, row, p.ldr),
+                  li = shift_of<T, ALIGNED>(p.i, row, p.ldi);
+      // of row j: the product of a up to it and the state from zero, in the end h_j = A_j h + H_j
+      Composition m[kR];
       auto element = [&](int j, auto kind) {
-        const float2 x = staged_pair<T, ALIGNED>(in, j, lx, px);
-        const float2 r =
-            staged_pair<T, ALIGNED>(in + S::kOperand, j, lr, pr);
-        const float2 i =
-            staged_pair<T, ALIGNED>(in + 2 * S::kOperand, j, li, pi);
+        const float2 x = staged_pair<T, ALIGNED>(in, j, lx);
+        const float2 r = staged_pair<T, ALIGNED>(in + S::kOperand, j, lr);
+        const float2 i = staged_pair<T, ALIGNED>(in + 2 * S::kOperand, j, li);
         const Gates g =
             grec_gates<decltype(kind)::value>(grec_exp_neg<false>(r), grec_exp_neg<false>(i), rate);
-        a[j] = g.a;
-        u[j] = g.s * g.si * x;
-        m.A = m.A * a[j];
-        m.H = fma2(a[j], m.H, u[j]);
+        const float2 u = g.s * g.si * x;
+        const Composition own{g.a, u};
+        m[j] = j == 0 ? own : compose(own, m[j > 0 ? j - 1 : 0]);
       };
-      if (n == R && small) {  // no branch between the rows: their instructions interleave
+      if (n == kR && small) {  // no branch between the rows: their instructions interleave
 #pragma unroll
-        for (int j = 0; j < R; ++j) element(j, std::true_type());
-      } else if (n == R) {
+        for (int j = 0; j < kR; ++j) element(j, std::true_type());
+      } else if (n == kR) {
 #pragma unroll
-        for (int j = 0; j < R; ++j) element(j, std::false_type());
+        for (int j = 0; j < kR; ++j) element(j, std::false_type());
       } else {
 #pragma unroll
-        for (int j = 0; j < R; ++j)
-          if (j < n) element(j, std::false_type());
+        for (int j = 0; j < kR; ++j) {
+          if (j < n) {
+            element(j, std::false_type());
+          } else {  // past the sequence's end a row hands on what it gets
+            m[j] = j == 0 ? Composition{both(1.f), both(0.f)} : m[j > 0 ? j - 1 : 0];
+          }
+        }
       }
-      __syncwarp();
-      stage(row + static_cast<int64_t>(STAGES) * step_rows, slot);
-      slot = slot + 1 == STAGES ? 0 : slot + 1;
-
-      // the composition of the block's rows in front of the warp's
-      Composition* seg = segments + parity * kWarps * 32;
-      seg[warp * 32 + lane] = m;
+      Composition* seg = segments + parity * W * 32 + lane;
+      seg[warp * 32] = m[kR - 1];
       __syncthreads();
+      // the composition of the block's rows in front of the warp's
       Composition front{both(1.f), both(0.f)};
 #pragma unroll
-      for (int w = 0; w < kWarps - 1; ++w)
-        if (w < warp) front = compose(seg[w * 32 + lane], front);
-      float2 before = state;  // the state in front of the block's, then of the warp's rows
+      for (int w = 0; w < W - 1; ++w)
+        if (w < warp) front = compose(seg[w * 32], front);
+      Composition* blk = blocks + parity * kMaxCluster * 32 + lane;
       if (peers > 1) {
-        Composition* blk = blocks + parity * kMaxCluster * 32;
-        if (warp == kWarps - 1) {
-          const Composition all = compose(m, front);
-          for (int q = 0; q < peers; ++q) store_remote(blk + rank * 32 + lane, q, all);
+        if (warp == W - 1) {
+          const Composition all = compose(m[kR - 1], front);
+          for (int q = 0; q < peers; ++q) store_remote(blk + rank * 32, q, all);
           cluster_publish();
         }
-        cluster_sync();
-        for (int q = 0; q < peers; ++q) {
+        cluster_arrive();
+      }
+      stage(slot, kStages);
+      slot = slot + 1 == kStages ? 0 : slot + 1;
+
+      float2 before = state;  // the state in front of the block's, then of the warp's rows
+      if (peers > 1) {
+        cluster_wait();
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) {
+          if (q == peers) break;
           if (q == rank) before = state;
-          state = apply(blk[q * 32 + lane], state);
+          state = apply(blk[q * 32], state);
         }
       } else {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) state = apply(seg[w * 32 + lane], state);
+        for (int w = 0; w < W; ++w) state = apply(seg[w * 32], state);
       }
       before = apply(front, before);
       parity ^= 1;
 
-      if (tape && n > 0 && (row - start) % kTapeRows == 0) {
-        float* at = tape + (tb + (row - start) / kTapeRows) * p.channels + c;
-        if (first) at[0] = before.x;
-        if (second) at[1] = before.y;
+      if (tape_at != nullptr) {
+        if (n > 0) {
+          if (first) tape_at[0] = before.x;
+          if (second) tape_at[1] = before.y;
+        }
+        tape_at += step_rows / kTapeRows * static_cast<int64_t>(p.channels);
       }
-      T* out = h + row * ldh + c;
+      T* out = h + c + row * ldh;
       auto emit = [&](int j, auto kind) {
-        before = fma2(a[j], before, u[j]);
-        store_pair<T, decltype(kind)::value>(row_at(out, j, ph), before, pairs, first, second);
+        store_pair<T, decltype(kind)::value>(row_at(out, j, ph), apply(m[j], before), pairs, first,
+                                             second);
       };
-      if (n == R && whole) {
+      if (n == kR && whole) {
 #pragma unroll
-        for (int j = 0; j < R; ++j) emit(j, std::true_type());
+        for (int j = 0; j < kR; ++j) emit(j, std::true_type());
       } else {
 #pragma unroll
-        for (int j = 0; j < R; ++j)
+        for (int j = 0; j < kR; ++j)
           if (j < n) emit(j, std::false_type());
       }
     }
@@ -224,19 +240,27 @@ dim3 grid_of(int channels, int64_t batch) {
 
 namespace {
 
-template <typename T, int R, bool ALIGNED, int STAGES>
+template <typename T, int W, bool ALIGNED>
 cudaError_t launch_forward(const GrecRows<T>& p, const float* lam, float kappa, const float* h0,
                            T* h, int64_t ldh, float* hT, float* tape, cudaStream_t stream) {
-  using S = GrecForwardShared<T, R, ALIGNED, STAGES>;
-  auto* kernel = grec_forward_kernel<T, R, ALIGNED, STAGES>;
+  using S = GrecForwardShared<T, W, ALIGNED>;
+  auto* kernel = grec_forward_kernel<T, W, ALIGNED>;
+  static const Held held = held_clusters(kernel, 32 * W, S::kBytes);
+  if (held.status != cudaSuccess) return held.status;
   const int64_t tiles = (p.channels + kTileC - 1) / kTileC;
   const int64_t length = p.offsets ? p.rows / p.batch + 1 : p.length;
-  const int cluster = grec_cluster(tiles * p.batch, length, kWarps * R);
+  const int cluster = grec_cluster(held, tiles * p.batch, length, W * kR);
   return launch_clusters(kernel, dim3(static_cast<unsigned>(tiles * cluster),
                                       static_cast<unsigned>(p.batch < 65535 ? p.batch : 65535)),
-                         32 * kWarps, S::kBytes, cluster, stream, p, lam, kappa, h0, h, ldh,
+                         32 * W, S::kBytes, cluster, stream, p, lam, kappa, h0, h, ldh,
                          pair_stores(h, ldh), hT, tape);
 }
+
+// Blocks of four warps while the pairs of a sequence and a tile fill the GPU by themselves (152 SMs
+// with three blocks): 64 x 512 rows x 2,048 channels BF16 take 96 us, with eight warps 106.
+// Otherwise eight, which meet less often: one sequence of 65,536 x 4,096 takes 457 us, with
+// four warps 501.
+constexpr int64_t kFourWarpUnits = 3 * 152;
 
 }  // namespace
 
@@ -245,8 +269,10 @@ cudaError_t launch_grec(const GrecRows<T>& p, const float* lam, float kappa, con
                         T* h, int64_t ldh, float* hT, float* tape, cudaStream_t stream) {
   const bool aligned = rows_aligned(p.x, p.ldx) && rows_aligned(p.r, p.ldr) &&
                        rows_aligned(p.i, p.ldi);
-  return aligned ? launch_forward<T, 16, true, 2>(p, lam, kappa, h0, h, ldh, hT, tape, stream)
-                 : launch_forward<T, 16, false, 2>(p, lam, kappa, h0, h, ldh, hT, tape, stream);
+  const bool four = (p.channels + kTileC - 1) / kTileC * p.batch >= kFourWarpUnits;
+  auto* launch = four ? (aligned ? launch_forward<T, 4, true> : launch_forward<T, 4, false>)
+                      : (aligned ? launch_forward<T, 8, true> : launch_forward<T, 8, false>);
+  return launch(p, lam, kappa, h0, h, ldh, hT, tape, stream);
 }
 
 template <typename T>

@@ -83,9 +83,8 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
                                   second ? grec_rate(lam[c + 1], kappa) : 0.f);
   const bool small = __all_sync(0xFFFFFFFFu, rate.x <= kSmallRate && rate.y <= kSmallRate);
   const unsigned es = sizeof(T);
-  const unsigned px = p.ldx * es, pr = p.ldr * es, pi = p.ldi * es, ph = g.lddh * es,
-                 pdx = g.lddx * es, pdr = g.lddr * es, pdi = g.lddi * es;
-  const bool whole = g.px && g.pr && g.pi && valid == kTileC;
+  const unsigned pdx = g.lddx * es, pdr = g.lddr * es, pdi = g.lddi * es;
+  const bool wide = valid == kTileC, whole = g.px && g.pr && g.pi && wide;
   const int step_rows = peers * kTapeRows;
   float2 dlam = make_float2(0.f, 0.f);
   int parity = 0;
@@ -99,57 +98,64 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
       if (first) carry.x = dhT[s * p.channels + c];
       if (second) carry.y = dhT[s * p.channels + c + 1];
     }
-    const int64_t tb = tape_base(start, s);
-    const int64_t steps = (end - start + step_rows - 1) / step_rows;
-    // the warp's first row of this step; the last step first
-    int64_t row = start + (steps - 1) * step_rows + rank * kTapeRows + warp * kR;
+    const int length = static_cast<int>(end - start);
+    const int steps = (length + step_rows - 1) / step_rows;
+    // the block's first row of this step, counted from the sequence's; the last step first
+    int piece = (steps - 1) * step_rows + rank * kTapeRows;
+    unsigned row = static_cast<unsigned>(start) + piece + warp * kR;  // the warp's first
+    const float* tape_at = tape + (tape_base(start, s) + piece / kTapeRows) * p.channels + c;
 
-    auto stage = [&](int64_t at, int slot) {
-      const int n = at < start || at >= end ? 0 : (end - at < kR ? static_cast<int>(end - at) : kR);
-      char* to = mine + slot * S::kStage;
-      if (n > 0) {
-        stage_rows<T, ALIGNED, kR>(to, p.x + at * p.ldx + c0, px, n, valid, p.x);
-        stage_rows<T, ALIGNED, kR>(to + S::kOperand, p.r + at * p.ldr + c0, pr, n, valid, p.r);
-        stage_rows<T, ALIGNED, kR>(to + 2 * S::kOperand, p.i + at * p.ldi + c0, pi, n, valid, p.i);
-        stage_rows<T, ALIGNED, kR>(to + 3 * S::kOperand, g.dh + at * g.lddh + c0, ph, n, valid, g.dh);
+    auto stage = [&](int slot, int k) {  // the rows of the k-th step from this one
+      const int ahead = piece + warp * kR - k * step_rows;  // counted from the sequence's first row
+      if (ahead >= 0) {
+        const int n = length - ahead < kR ? length - ahead : kR;
+        const bool all = n == kR && wide;
+        const unsigned at = row - k * step_rows;
+        char* to = mine + slot * S::kStage;
+        stage_tile<T, ALIGNED, kR>(to, p.x, at, p.ldx, c0, n, all, valid);
+        stage_tile<T, ALIGNED, kR>(to + S::kOperand, p.r, at, p.ldr, c0, n, all, valid);
+        stage_tile<T, ALIGNED, kR>(to + 2 * S::kOperand, p.i, at, p.ldi, c0, n, all, valid);
+        stage_tile<T, ALIGNED, kR>(to + 3 * S::kOperand, g.dh, at, g.lddh, c0, n, all, valid);
       }
       cp_async_commit();
     };
 #pragma unroll
-    for (int k = 0; k < STAGES; ++k) stage(row - static_cast<int64_t>(k) * step_rows, k);
+    for (int k = 0; k < STAGES; ++k) stage(k, k);
 
     int slot = 0;
-    for (int64_t step = steps - 1; step >= 0; --step, row -= step_rows) {
-      const int n = row >= end ? 0 : (end - row < kR ? static_cast<int>(end - row) : kR);
-      const int64_t piece = row - warp * kR - start;  // the block's first row of the sequence
-      float2 before = make_float2(0.f, 0.f);          // the state in front of the block's rows
-      if (start + piece < end) {
-        const float* at = tape + (tb + piece / kTapeRows) * p.channels + c;
-        if (first) before.x = at[0];
-        if (second) before.y = at[1];
+    for (; piece >= 0; piece -= step_rows, row -= step_rows) {
+      const int left = length - piece - warp * kR;
+      const int n = left < kR ? left : kR;    // may be negative: none
+      float2 before = make_float2(0.f, 0.f);  // the state in front of the block's rows
+      if (piece < length) {
+        if (first) before.x = tape_at[0];
+        if (second) before.y = tape_at[1];
       }
+      tape_at -= peers * static_cast<int64_t>(p.channels);
       cp_async_wait_group<STAGES - 1>();
       __syncwarp();
       const char* in = mine + slot * S::kStage;
-      const unsigned lx = low_bits(p.x + row * p.ldx), lr = low_bits(p.r + row * p.ldr),
-                     li = low_bits(p.i + row * p.ldi), lh = low_bits(g.dh + row * g.lddh);
-      auto read = [&](int operand, int j, unsigned low, unsigned pitch) {
-        return staged_pair<T, ALIGNED>(in + operand * S::kOperand, j, low, pitch);
+      const Shift lx = shift_of<T, ALIGNED>(p.x, row, p.ldx),
+                  lr = shift_of<T, ALIGNED>(p.r, row, p.ldr),
+                  li = shift_of<T, ALIGNED>(p.i, row, p.ldi),
+                  lh = shift_of<T, ALIGNED>(g.dh, row, g.lddh);
+      auto read = [&](int operand, int j, Shift at) {
+        return staged_pair<T, ALIGNED>(in + operand * S::kOperand, j, at);
       };
 
       float2 a[kR], er[kR], ei[kR], hb[kR];
       Exchange m{both(1.f), both(0.f)};
       float2 H = both(0.f);
       auto element = [&](int j, auto kind) {
-        er[j] = grec_exp_neg<true>(read(1, j, lr, pr));
-        ei[j] = grec_exp_neg<true>(read(2, j, li, pi));
+        er[j] = grec_exp_neg<true>(read(1, j, lr));
+        ei[j] = grec_exp_neg<true>(read(2, j, li));
         const Gates q = grec_gates<decltype(kind)::value>(er[j], ei[j], rate);
         a[j] = q.a;
-        hb[j] = q.s * q.si * read(0, j, lx, px);  // u, until the states are known
+        hb[j] = q.s * q.si * read(0, j, lx);  // u, until the states are known
         H = fma2(a[j], H, hb[j]);
         m.A = m.A * a[j];
       };
-      auto back = [&](int j) { m.P = a[j] * (m.P + read(3, j, lh, ph)); };
+      auto back = [&](int j) { m.P = a[j] * (m.P + read(3, j, lh)); };
       if (n == kR) {
         if (small) {
 #pragma unroll
@@ -169,41 +175,43 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
           if (j < n) back(j);
       }
 
-      Exchange* seg = segments + parity * kWarps * 32;
-      float2* st = states + parity * kWarps * 32;
-      seg[warp * 32 + lane] = m;
-      st[warp * 32 + lane] = H;
+      Exchange* seg = segments + parity * kWarps * 32 + lane;
+      float2* st = states + parity * kWarps * 32 + lane;
+      seg[warp * 32] = m;
+      st[warp * 32] = H;
       __syncthreads();
       Exchange behind{both(1.f), both(0.f)};  // the block's rows behind the warp's
 #pragma unroll
       for (int w = kWarps - 1; w > 0; --w)
-        if (w > warp) behind = compose(seg[w * 32 + lane], behind);
+        if (w > warp) behind = compose(seg[w * 32], behind);
       float2 after = carry;  // what comes from behind the block's, then the warp's rows
       if (peers > 1) {
-        Exchange* blk = blocks + parity * kMaxCluster * 32;
+        Exchange* blk = blocks + parity * kMaxCluster * 32 + lane;
         if (warp == 0) {
           const Exchange all = compose(m, behind);
-          for (int q = 0; q < peers; ++q) store_remote(blk + rank * 32 + lane, q, all);
+          for (int q = 0; q < peers; ++q) store_remote(blk + rank * 32, q, all);
           cluster_publish();
         }
         cluster_sync();
-        for (int q = peers - 1; q >= 0; --q) {
+#pragma unroll
+        for (int q = kMaxCluster - 1; q >= 0; --q) {
+          if (q >= peers) continue;
           if (q == rank) after = carry;
-          carry = apply(blk[q * 32 + lane], carry);
+          carry = apply(blk[q * 32], carry);
         }
       } else {
 #pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) carry = apply(seg[w * 32 + lane], carry);
+        for (int w = kWarps - 1; w >= 0; --w) carry = apply(seg[w * 32], carry);
       }
       after = apply(behind, after);
 #pragma unroll
       for (int w = 0; w < kWarps - 1; ++w)
-        if (w < warp) before = fma2(seg[w * 32 + lane].A, before, st[w * 32 + lane]);
+        if (w < warp) before = fma2(seg[w * 32].A, before, st[w * 32]);
       parity ^= 1;
 
-      T* dx = g.dx + row * g.lddx + c;
-      T* dr = g.dr + row * g.lddr + c;
-      T* di = g.di + row * g.lddi + c;
+      T* dx = g.dx + c + row * g.lddx;
+      T* dr = g.dr + c + row * g.lddr;
+      T* di = g.di + c + row * g.lddi;
       auto forth = [&](int j) {
         const float2 u = hb[j];
         hb[j] = before;
@@ -211,8 +219,8 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
       };
       auto emit = [&](int j, auto kind, auto all) {
         constexpr bool kWhole = decltype(all)::value;
-        const float2 x = read(0, j, lx, px);
-        const float2 gt = read(3, j, lh, ph) + after;
+        const float2 x = read(0, j, lx);
+        const float2 gt = read(3, j, lh) + after;
         after = a[j] * gt;
         // the gates again from their exponentials: fewer registers than keeping them all
         const Gates q = grec_gates<decltype(kind)::value>(er[j], ei[j], rate);
@@ -245,7 +253,7 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
           if (j < n) emit(j, std::false_type(), std::false_type());
       }
       __syncwarp();
-      stage(row - static_cast<int64_t>(STAGES) * step_rows, slot);
+      stage(slot, STAGES);
       slot = slot + 1 == STAGES ? 0 : slot + 1;
     }
     cp_async_wait_all();
@@ -298,9 +306,15 @@ int64_t grid_y(int64_t batch) { return batch < 65535 ? batch : 65535; }
 template <typename T, bool ALIGNED, int STAGES>
 cudaError_t launch_backward(const GrecRows<T>& p, const GrecGradRows<T>& g, const float* lam,
                             float kappa, const float* tape, const float* dhT, float* dh0,
-                            float* partial, int cluster, cudaStream_t stream) {
+                            float* partial, int64_t* parts, cudaStream_t stream) {
   using S = GrecBackwardShared<T, ALIGNED, STAGES>;
-  return launch_clusters(grec_backward_kernel<T, ALIGNED, STAGES>,
+  auto* kernel = grec_backward_kernel<T, ALIGNED, STAGES>;
+  static const Held held = held_clusters(kernel, 32 * kWarps, S::kBytes);
+  if (held.status != cudaSuccess) return held.status;
+  const int64_t length = p.offsets ? p.rows / p.batch + 1 : p.length;
+  const int cluster = grec_cluster(held, tiles_of(p.channels) * p.batch, length, kTapeRows);
+  *parts = grid_y(p.batch) * cluster;
+  return launch_clusters(kernel,
                          dim3(static_cast<unsigned>(tiles_of(p.channels) * cluster),
                               static_cast<unsigned>(grid_y(p.batch))),
                          32 * kWarps, S::kBytes, cluster, stream, p, g, lam, kappa, tape, dhT, dh0,
@@ -309,10 +323,10 @@ cudaError_t launch_backward(const GrecRows<T>& p, const GrecGradRows<T>& g, cons
 
 }  // namespace
 
-size_t grec_backward_workspace(int channels, int64_t batch, int64_t rows) {
+size_t grec_backward_workspace(int channels, int64_t batch, int64_t) {
   if (batch == 0) return 0;
-  // packed sequences may take a smaller cluster than this; never a larger one
-  const int64_t parts = grid_y(batch) * grec_cluster(tiles_of(channels) * batch, rows, kTapeRows);
+  const bool many = tiles_of(channels) * batch > kManyUnits;
+  const int64_t parts = grid_y(batch) * (many ? 1 : kMaxCluster);
   return static_cast<size_t>(parts) * channels * sizeof(float);
 }
 
@@ -326,16 +340,12 @@ cudaError_t launch_grec_backward(const GrecRows<T>& p, const float* lam, float k
   if (p.batch > 0) {
     const GrecGradRows<T> g{dh, dx, dr, di, lddh, lddx, lddr, lddi,
                             pair_stores(dx, lddx), pair_stores(dr, lddr), pair_stores(di, lddi)};
-    const int64_t length = p.offsets ? p.rows / p.batch + 1 : p.length;
-    const int cluster = grec_cluster(tiles_of(p.channels) * p.batch,
-                                     length < p.rows ? length : p.rows, kTapeRows);
-    parts = grid_y(p.batch) * cluster;
     const bool aligned = rows_aligned(p.x, p.ldx) && rows_aligned(p.r, p.ldr) &&
                          rows_aligned(p.i, p.ldi) && rows_aligned(dh, lddh);
     const cudaError_t e =
-        aligned ? launch_backward<T, true, 2>(p, g, lam, kappa, tape, dhT, dh0, partial, cluster,
+        aligned ? launch_backward<T, true, 2>(p, g, lam, kappa, tape, dhT, dh0, partial, &parts,
                                               stream)
-                : launch_backward<T, false, 2>(p, g, lam, kappa, tape, dhT, dh0, partial, cluster,
+                : launch_backward<T, false, 2>(p, g, lam, kappa, tape, dhT, dh0, partial, &parts,
                                                stream);
     if (e != cudaSuccess) return e;
   }

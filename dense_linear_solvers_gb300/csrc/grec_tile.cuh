@@ -29,63 +29,87 @@ __device__ __forceinline__ void cp_async_16(void* smem, const void* gmem, int by
                : "memory");
 }
 
-// Copies `rows` rows of `valid` elements (valid <= 64) into smem; `first` the first row's first
+// Copies `rows` rows of `valid` elements (valid <= 64) into smem; `row0` the first row's first
 // element, `pitch` the rows' distance in bytes, `base` the operand's first byte. All lanes of
 // the warp take part. Nothing outside the operand is read; what lies behind a row's valid
 // elements in shared memory is unspecified.
-template <typename T, bool ALIGNED, int R>
-__device__ __forceinline__ void stage_rows(char* smem, const T* first, unsigned pitch, int rows,
-                                           int valid, const T* base) {
-  using G = Tile<T, ALIGNED>;
+template <typename T>
+__device__ __forceinline__ void stage_rows_unaligned(char* smem, const char* row0, unsigned pitch,
+                                                     int rows, int valid, const char* base) {
+  using G = Tile<T, false>;
   const int lane = threadIdx.x & 31;
-  const char* row0 = reinterpret_cast<const char*>(first);
   const int bytes = valid * static_cast<int>(sizeof(T));
-  if constexpr (ALIGNED) {
-    constexpr int kPer = 32 / G::kPieces;  // rows the warp copies at once
-    static_assert(R % kPer == 0, "whole copies");
-    const int piece = lane % G::kPieces, sub = lane / G::kPieces;
-    const int left = bytes - piece * 16;
-    const char* src = row0 + sub * static_cast<uint64_t>(pitch) + piece * 16;
-    char* to = smem + sub * G::kRowBytes + piece * 16;
-    if (rows == R && valid == kTileC) {
-#pragma unroll
-      for (int j = 0; j < R; j += kPer)
-        cp_async_16(to + j * G::kRowBytes, src + j * static_cast<uint64_t>(pitch), 16);
-    } else if (left > 0) {
-      for (int j = 0; j + sub < rows; j += kPer)
-        cp_async_16(to + j * G::kRowBytes, src + j * static_cast<uint64_t>(pitch),
-                    left < 16 ? left : 16);
-    }
-  } else {
-    for (int q = lane; q < rows * G::kPieces; q += 32) {
-      const int k = q / G::kPieces, piece = q - k * G::kPieces;
-      const char* src = row0 + k * static_cast<uint64_t>(pitch);
-      const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
-      const char* from = src - shift + piece * 16;
-      const int left = bytes + shift - piece * 16;
-      if (left <= 0) continue;
-      char* to = smem + k * G::kRowBytes + piece * 16;
-      if (from >= reinterpret_cast<const char*>(base)) {
-        cp_async_16(to, from, left < 16 ? left : 16);
-      } else {  // the boundary lies in front of the operand: its first elements one by one
-        for (int b = shift; b < 16 && b < shift + bytes; b += static_cast<int>(sizeof(T)))
-          *reinterpret_cast<T*>(to + b) = *reinterpret_cast<const T*>(from + b);
-      }
+  for (int q = lane; q < rows * G::kPieces; q += 32) {
+    const int k = q / G::kPieces, piece = q - k * G::kPieces;
+    const char* src = row0 + k * static_cast<uint64_t>(pitch);
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
+    const char* from = src - shift + piece * 16;
+    const int left = bytes + shift - piece * 16;
+    if (left <= 0) continue;
+    char* to = smem + k * G::kRowBytes + piece * 16;
+    if (from >= base) {
+      cp_async_16(to, from, left < 16 ? left : 16);
+    } else {  // the boundary lies in front of the operand: its first elements one by one
+      for (int b = shift; b < 16 && b < shift + bytes; b += static_cast<int>(sizeof(T)))
+        *reinterpret_cast<T*>(to + b) = *reinterpret_cast<const T*>(from + b);
     }
   }
 }
 
-// The lane's two channels of staged row k; `low` the low address bits of the first row.
+// Copies `rows` rows from row `row` of an operand, columns from c0, into smem (whole: R rows of 64
+// elements). Addresses are worked out anew each time: a few instructions a step instead of registers
+// over all of it.
+template <typename T, bool ALIGNED, int R>
+__device__ __forceinline__ void stage_tile(char* smem, const T* base, unsigned row, int64_t ld,
+                                           int c0, int rows, bool whole, int valid) {
+  const unsigned pitch = static_cast<unsigned>(ld) * static_cast<unsigned>(sizeof(T));
+  if constexpr (ALIGNED) {
+    constexpr int kPieces = Tile<T, true>::kPieces, kPer = 32 / kPieces;  // rows copied at once
+    static_assert(R % kPer == 0, "whole copies");
+    const int lane = threadIdx.x & 31, piece = lane % kPieces, sub = lane / kPieces;
+    char* to = smem + sub * Tile<T, true>::kRowBytes + piece * 16;
+    const char* from = reinterpret_cast<const char*>(base + c0) + piece * 16 +
+                       static_cast<uint64_t>(row + sub) * pitch;
+    if (whole) {
+#pragma unroll
+      for (int j = 0; j < R; j += kPer)
+        cp_async_16(to + j * Tile<T, true>::kRowBytes, from + j * static_cast<uint64_t>(pitch), 16);
+    } else {
+      const int left = valid * static_cast<int>(sizeof(T)) - piece * 16;
+      if (left > 0)
+        for (int j = 0; j + sub < rows; j += kPer)
+          cp_async_16(to + j * Tile<T, true>::kRowBytes, from + j * static_cast<uint64_t>(pitch),
+                      left < 16 ? left : 16);
+    }
+  } else {
+    stage_rows_unaligned<T>(
+        smem, reinterpret_cast<const char*>(base + c0) + static_cast<uint64_t>(row) * pitch, pitch,
+        rows, valid, reinterpret_cast<const char*>(base));
+  }
+}
+
+// What staged_pair() needs to know of an operand's rows from row `row` where they are not aligned.
+struct Shift {
+  unsigned low, pitch;
+};
 template <typename T, bool ALIGNED>
-__device__ __forceinline__ float2 staged_pair(const char* smem, int k, unsigned low,
-                                              unsigned pitch) {
+__device__ __forceinline__ Shift shift_of(const T* base, unsigned row, int64_t ld) {
+  if (ALIGNED) return {0, 0};
+  const unsigned pitch = static_cast<unsigned>(ld) * static_cast<unsigned>(sizeof(T));
+  return {static_cast<unsigned>(reinterpret_cast<uintptr_t>(base)) + row * pitch, pitch};
+}
+
+// The lane's two channels of staged row k (a tile's column 0 lies on a multiple of 64 elements, so
+// that the shift of a row is that of its operand's row).
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ float2 staged_pair(const char* smem, int k, Shift at_row) {
   using G = Tile<T, ALIGNED>;
   const int lane = threadIdx.x & 31;
   if constexpr (ALIGNED) {
     return to_f32(*reinterpret_cast<const typename Pair<T>::type*>(
         smem + k * G::kRowBytes + lane * 2 * static_cast<int>(sizeof(T))));
   } else {
-    const unsigned shift = (low + k * pitch) & 15u;
+    const unsigned shift = (at_row.low + k * at_row.pitch) & 15u;
     const T* at = reinterpret_cast<const T*>(smem + k * G::kRowBytes + shift) + 2 * lane;
     return make_float2(to_f32(at[0]), to_f32(at[1]));
   }

@@ -396,7 +396,8 @@ BS_API bs_status bs_bdmv2_batched(bs_dtype dtype, int num_block_rows, int block_
  *            one slot: unspecified states.
  *   y        the new states, in dtype.
  * Results do not depend on the stream or the run: no atomics, a fixed order of every sum.
- * Supported: 1 <= channels <= 2^20, batch <= 2^31 - 1, kappa finite and > 0.
+ * Supported: 1 <= channels <= 2^20, batch <= 2^31 - 1, rows <= 2^30, ld <= 2^21, kappa finite
+ * and > 0.
  */
 BS_API bs_status bs_grec_batched(bs_dtype dtype, int channels, int64_t batch, int64_t rows,
                                  const int64_t* offsets, const void* x, int64_t ldx,
@@ -449,7 +450,7 @@ BS_API size_t bs_grec_backward_workspace(int channels, int64_t batch, int64_t ro
  *                aligned. Holds nothing between calls; may be NULL where none of the three
  *                sums is stored.
  * rows == 0 launches nothing but the three sums' zeros.
- * Supported: 1 <= width <= 65536.
+ * Supported: 1 <= width <= 65536, rows <= 2^30, ld <= 2^21.
  */
 typedef enum { BS_GATE_SILU = 0, BS_GATE_SIGMOID = 1, BS_GATE_LINEAR = 2 } bs_gate;
 
