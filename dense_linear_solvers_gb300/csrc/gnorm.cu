@@ -1,14 +1,17 @@
 // The norms around a block with its gate and residual scale (bs_gnorm calls of bsolve.h).
 //
-// A row is read once into registers, by one warp where it is short and by one block of 4 to 32
-// warps where it is long, reduced once for each mean, and its outputs are written once. Blocks
-// walk the rows at the grid's distance, so that the parameters stay in the first cache level and
-// the backward pass keeps its three sums over rows on the chip: each block adds them up in
-// shared memory, every thread its own columns, and writes one part of them at its end; a
-// second kernel adds the parts in order. Rows too long for a block's registers run the
-// looped kernels at the end, which read a row once for each mean and once for the outputs.
+// A row belongs to a group of 8 to 1024 threads, each with K 16-byte vectors of it; a group takes
+// ROWS rows at a time, and persistent blocks walk all of them. Each thread copies its own vectors of
+// the rows of the next turn into shared memory with cp.async while it works on these, so that
+// the loads need no registers and no barrier, and reads them as often as it needs them; the rows'
+// sums go through shuffles and, for groups of several warps, one barrier for all rows of the
+// turn. The parameters stay in the first cache level. The backward pass keeps its three sums over rows in
+// registers, every thread those of its own columns, and each block writes one part of them at
+// its end; a second kernel adds the parts in order. Rows too long for that run the looped kernels at
+// the end, which read a row once for each mean and once for the outputs.
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "gnorm_math.cuh"
 #include "kernels.h"
 #include "row_types.cuh"
@@ -17,15 +20,17 @@ namespace bsolve {
 namespace {
 
 constexpr int kSms = 152;
+constexpr int kTurns = 2;  // turns of rows in shared memory: this one and the next
 
-// Sums of N values over a row's warps, the same bits in every thread. Consecutive calls take
+// Sums of N values over a group's threads, the same bits in all of them. Consecutive calls take
 // the two halves of `red` in turn, so that one barrier a call is enough.
-template <int N, int WARPS>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N][32], int& turn) {
+template <int N, int THREADS>
+__device__ __forceinline__ void group_sums(float (&v)[N], float (*red)[N][32], int& turn) {
+  constexpr int LANES = THREADS < 32 ? THREADS : 32, WARPS = THREADS / LANES;
 #pragma unroll
   for (int k = 0; k < N; ++k)
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], m);
+    for (int m = LANES / 2; m > 0; m >>= 1) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], m);
   if constexpr (WARPS > 1) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0)
@@ -42,82 +47,148 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N][32], int
   }
 }
 
-// Row number and thread of the row, of the calling thread: WARPS == 1: four rows a block.
-template <int WARPS>
-struct Place {
-  static constexpr int kThreads = 32 * WARPS;
-  static constexpr int kBlock = WARPS == 1 ? 128 : kThreads;
-  static constexpr int kRows = kBlock / kThreads;
-  static __device__ __forceinline__ int thread() {
-    return WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
-  }
-  static __device__ __forceinline__ int64_t first() {
-    return WARPS == 1 ? blockIdx.x * int64_t(kRows) + (threadIdx.x >> 5) : blockIdx.x;
-  }
-  static __device__ __forceinline__ int64_t stride() { return gridDim.x * int64_t(kRows); }
+template <int THREADS>
+struct Group {
+  static constexpr int kBlock = THREADS < 128 && THREADS <= 32 ? 128 : THREADS;
+  static constexpr int kGroups = kBlock / THREADS;
 };
 
 // ------------------------------------------------------------------ forward
-template <typename T, int K, int WARPS, bool ALIGNED>
-__global__ void __launch_bounds__(Place<WARPS>::kBlock, WARPS == 1 ? 8 : 32 / WARPS)
+template <typename T, int K, int THREADS, int ROWS, bool ALIGNED>
+__global__ void __launch_bounds__(Group<THREADS>::kBlock, 1024 / Group<THREADS>::kBlock)
 gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, int64_t ldu) {
-  using P = Place<WARPS>;
-  constexpr int VE = kVecElements<T>, N = P::kThreads;
-  __shared__ float red[2][1][32];
-  int turn = 0;
-  const int t = P::thread();
+  using G = Group<THREADS>;
+  constexpr int H = kVecElements<T> / 2;  // pairs of a vector
+  constexpr int kRow = kStagedRow<THREADS, K, ALIGNED>;
+  __shared__ float red[2][ROWS][32];
+  extern __shared__ __align__(16) char shared[];
+  const int t = threadIdx.x % THREADS, group = threadIdx.x / THREADS;
+  char* mine = shared + group * (kTurns * ROWS * 3 * kRow);
   const float inv = 1.f / p.width;
-  for (int64_t row = P::first(); row < p.rows; row += P::stride()) {
-    RowVec<T> f[K], z[K], x[K];
-    const T* zr = p.z ? p.z + row * p.ldz : nullptr;
-    const T* xr = p.x ? p.x + row * p.ldx : nullptr;
+  const int bytes = p.width * static_cast<int>(sizeof(T));
+  const int64_t turn_rows = static_cast<int64_t>(gridDim.x) * G::kGroups * ROWS;
+  int64_t row0 = (static_cast<int64_t>(blockIdx.x) * G::kGroups + group) * ROWS;
+  int turn = 0;
+
+  auto stage = [&](int64_t from, int slot) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      f[k] = load_row<T, N, ALIGNED>(p.f + row * p.ldf, t, k, p.width);
-      z[k] = load_row<T, N, ALIGNED>(zr, t, k, p.width);
-      x[k] = load_row<T, N, ALIGNED>(xr, t, k, p.width);
-    }
-    float r1 = 1.f;
-    if (p.w_post) {
-      float sum[1] = {0.f};
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int e = 0; e < VE; ++e) sum[0] = fmaf(to_f32(f[k].e[e]), to_f32(f[k].e[e]), sum[0]);
-      row_sums<1, WARPS>(sum, red, turn);
-      r1 = 1.f / sqrtf(fmaf(sum[0], inv, p.eps));
-    }
-    float v[K][VE], sum[1] = {0.f};
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float w[VE];
-      load_params<T, N, ALIGNED>(p.w_post, 1.f, t, k, p.width, w);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) v[k][e] = to_f32(f[k].e[e]) * r1 * w[e];
+    for (int i = 0; i < ROWS; ++i) {
+      const int64_t row = from + i;
+      char* to = mine + (slot * ROWS + i) * 3 * kRow;
+      const bool in = row < p.rows;
+      stage_row<T, THREADS, K, ALIGNED>(
+          to, in ? reinterpret_cast<const char*>(p.f + row * p.ldf) : nullptr,
+          reinterpret_cast<const char*>(p.f), bytes, t);
       if (p.z)
-#pragma unroll
-        for (int e = 0; e < VE; ++e) v[k][e] *= gate_of(to_f32(z[k].e[e]), p.gate).act;
-      load_params<T, N, ALIGNED>(p.scale, 1.f, t, k, p.width, w);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        v[k][e] = fmaf(v[k][e], w[e], to_f32(x[k].e[e]));
-        sum[0] = fmaf(v[k][e], v[k][e], sum[0]);
-      }
-      if (y) store_row<T, N, ALIGNED>(y + row * ldy, t, k, p.width, v[k]);
+        stage_row<T, THREADS, K, ALIGNED>(
+            to + kRow, in ? reinterpret_cast<const char*>(p.z + row * p.ldz) : nullptr,
+            reinterpret_cast<const char*>(p.z), bytes, t);
+      if (p.x)
+        stage_row<T, THREADS, K, ALIGNED>(
+            to + 2 * kRow, in ? reinterpret_cast<const char*>(p.x + row * p.ldx) : nullptr,
+            reinterpret_cast<const char*>(p.x), bytes, t);
     }
-    if (u) {
-      row_sums<1, WARPS>(sum, red, turn);
-      const float r2 = 1.f / sqrtf(fmaf(sum[0], inv, p.eps));
+    cp_async_commit();
+  };
+  stage(row0, 0);
+  int slot = 0;
+  // the same number of turns for all groups of a block: the shuffles take whole warps
+  const int64_t block0 = static_cast<int64_t>(blockIdx.x) * G::kGroups * ROWS;
+  for (int64_t at = block0; at < p.rows; at += turn_rows, row0 += turn_rows) {
+    stage(row0 + turn_rows, slot ^ 1);
+    cp_async_wait_group<1>();
+    if (!ALIGNED) {
+      if (THREADS > 32) __syncthreads(); else __syncwarp();
+    }
+    const char* in = mine + slot * ROWS * 3 * kRow;
+    slot ^= 1;
+    float r1[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) r1[i] = 1.f;
+    if (p.w_post) {
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        float2 sum = both(0.f);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          float2 f[H];
+          staged_vector<T, THREADS, ALIGNED>(in + i * 3 * kRow, low_bits(p.f + (row0 + i) * p.ldf),
+                                             t, k, f);
+#pragma unroll
+          for (int e = 0; e < H; ++e) sum = fma2(f[e], f[e], sum);
+        }
+        r1[i] = sum.x + sum.y;
+      }
+      group_sums<ROWS, THREADS>(r1, red, turn);
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) r1[i] = 1.f / sqrtf(fmaf(r1[i], inv, p.eps));
+    }
+    float2 v[ROWS][K][H];
+    float r2[ROWS];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float2 w[H], c[H];
+      load_params<T, THREADS, ALIGNED>(p.w_post, 1.f, t, k, p.width, w);
+      load_params<T, THREADS, ALIGNED>(p.scale, 1.f, t, k, p.width, c);
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        const char* at_row = in + i * 3 * kRow;
+        float2 q[H];
+        staged_vector<T, THREADS, ALIGNED>(at_row, low_bits(p.f + (row0 + i) * p.ldf), t, k, q);
+#pragma unroll
+        for (int e = 0; e < H; ++e) v[i][k][e] = q[e] * both(r1[i]) * w[e];
+        if (p.z) {
+          staged_vector<T, THREADS, ALIGNED>(at_row + kRow, low_bits(p.z + (row0 + i) * p.ldz), t,
+                                             k, q);
+#pragma unroll
+          for (int e = 0; e < H; ++e) v[i][k][e] = v[i][k][e] * gate_of<false>(q[e], p.gate).act;
+        }
+        if (p.x) {
+          staged_vector<T, THREADS, ALIGNED>(at_row + 2 * kRow, low_bits(p.x + (row0 + i) * p.ldx),
+                                             t, k, q);
+#pragma unroll
+          for (int e = 0; e < H; ++e) v[i][k][e] = fma2(v[i][k][e], c[e], q[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < H; ++e) v[i][k][e] = v[i][k][e] * c[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      float2 sum = both(0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        float w[VE];
-        load_params<T, N, ALIGNED>(p.w_pre, 1.f, t, k, p.width, w);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) v[k][e] *= r2 * w[e];
-        store_row<T, N, ALIGNED>(u + row * ldu, t, k, p.width, v[k]);
+        for (int e = 0; e < H; ++e) sum = fma2(v[i][k][e], v[i][k][e], sum);
+        if (y && row0 + i < p.rows)
+          store_vector<T, THREADS, ALIGNED>(y + (row0 + i) * ldy, t, k, p.width, v[i][k]);
+      }
+      r2[i] = sum.x + sum.y;
+    }
+    if (!u) {
+      // every thread has read its rows before they are overwritten (a barrier of the sums else)
+      if (!ALIGNED && THREADS > 32) __syncthreads();
+      if (!ALIGNED && THREADS <= 32) __syncwarp();
+      continue;
+    }
+    group_sums<ROWS, THREADS>(r2, red, turn);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float2 w[H];
+      load_params<T, THREADS, ALIGNED>(p.w_pre, 1.f, t, k, p.width, w);
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        const float r = 1.f / sqrtf(fmaf(r2[i], inv, p.eps));
+        float2 q[H];
+#pragma unroll
+        for (int e = 0; e < H; ++e) q[e] = v[i][k][e] * (both(r) * w[e]);
+        if (row0 + i < p.rows)
+          store_vector<T, THREADS, ALIGNED>(u + (row0 + i) * ldu, t, k, p.width, q);
       }
     }
   }
+  cp_async_wait_all();
 }
 
 // ------------------------------------------------------------------ backward
@@ -126,129 +197,248 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
 //   dx = dy + q du w_pre - y q^3 mean(du w_pre y),     dt = dx scale,
 //   dz = dt n w_post act'(z),  dn = dt act(z) w_post,  df = r1 (dn - n mean(dn n)),
 //   dw_pre = sum du y q,  dscale = sum dx t,  dw_post = sum dt act(z) n.
-template <typename T, int K, int WARPS, bool ALIGNED>
-__global__ void __launch_bounds__(Place<WARPS>::kBlock,
-                                  WARPS == 1 ? 4 : (WARPS <= 16 && K == 1 ? 32 / WARPS : 1))
+template <typename T, int K, int THREADS, int ROWS, bool ALIGNED>
+__global__ void __launch_bounds__(Group<THREADS>::kBlock,
+                                  THREADS >= 512 ? 1 : 512 / Group<THREADS>::kBlock)
 gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ partial) {
-  using P = Place<WARPS>;
-  constexpr int VE = kVecElements<T>, N = P::kThreads;
-  __shared__ float red[2][2][32];
-  __shared__ float red1[2][1][32];
-  // [row of the block][3][K][VE][thread]: a warp's accesses fall into 32 banks
-  extern __shared__ float sums[];
-  int turn = 0, turn1 = 0;
-  const int t = P::thread();
+  using G = Group<THREADS>;
+  constexpr int H = kVecElements<T> / 2;
+  constexpr int kRow = kStagedRow<THREADS, K, ALIGNED>;
+  __shared__ float red[2][ROWS][32];
+  __shared__ float red2[2][2 * ROWS][32];
+  extern __shared__ __align__(16) char shared[];
+  const int t = threadIdx.x % THREADS, group = threadIdx.x / THREADS;
+  char* mine = shared + group * (kTurns * ROWS * 5 * kRow);
   const float inv = 1.f / p.width;
-  float* mine = sums + (WARPS == 1 ? (threadIdx.x >> 5) * 3 * K * VE * N : 0) + t;
-  if (partial)
+  const int bytes = p.width * static_cast<int>(sizeof(T));
+  const int64_t turn_rows = static_cast<int64_t>(gridDim.x) * G::kGroups * ROWS;
+  int64_t row0 = (static_cast<int64_t>(blockIdx.x) * G::kGroups + group) * ROWS;
+  int turn = 0, turn2 = 0;
+  float2 sw[K][H], sc[K][H], sp[K][H];  // the sums dw_post, dscale, dw_pre
 #pragma unroll
-    for (int j = 0; j < 3 * K * VE; ++j) mine[j * N] = 0.f;
-  for (int64_t row = P::first(); row < p.rows; row += P::stride()) {
-    RowVec<T> f[K], z[K], x[K], dy[K], du[K];
-    const T* zr = p.z ? p.z + row * p.ldz : nullptr;
-    const T* xr = p.x ? p.x + row * p.ldx : nullptr;
-    const T* yr = g.dy ? g.dy + row * g.lddy : nullptr;
-    const T* ur = g.du ? g.du + row * g.lddu : nullptr;
+  for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      f[k] = load_row<T, N, ALIGNED>(p.f + row * p.ldf, t, k, p.width);
-      z[k] = load_row<T, N, ALIGNED>(zr, t, k, p.width);
-      x[k] = load_row<T, N, ALIGNED>(xr, t, k, p.width);
-      du[k] = load_row<T, N, ALIGNED>(ur, t, k, p.width);
-      dy[k] = load_row<T, N, ALIGNED>(yr, t, k, p.width);
+    for (int e = 0; e < H; ++e) sw[k][e] = sc[k][e] = sp[k][e] = both(0.f);
+
+  auto one = [&](char* to, const T* base, int64_t ld, int64_t row) {
+    if (base)
+      stage_row<T, THREADS, K, ALIGNED>(
+          to, row < p.rows ? reinterpret_cast<const char*>(base + row * ld) : nullptr,
+          reinterpret_cast<const char*>(base), bytes, t);
+  };
+  auto stage = [&](int64_t from, int slot) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      char* to = mine + (slot * ROWS + i) * 5 * kRow;
+      one(to, p.f, p.ldf, from + i);
+      one(to + kRow, p.z, p.ldz, from + i);
+      one(to + 2 * kRow, p.x, p.ldx, from + i);
+      one(to + 3 * kRow, g.dy, g.lddy, from + i);
+      one(to + 4 * kRow, g.du, g.lddu, from + i);
     }
-    float r1 = 1.f;
+    cp_async_commit();
+  };
+  stage(row0, 0);
+  int slot = 0;
+  const int64_t block0 = static_cast<int64_t>(blockIdx.x) * G::kGroups * ROWS;
+  for (int64_t at = block0; at < p.rows; at += turn_rows, row0 += turn_rows) {
+    stage(row0 + turn_rows, slot ^ 1);
+    cp_async_wait_group<1>();
+    if (!ALIGNED) {
+      if (THREADS > 32) __syncthreads(); else __syncwarp();
+    }
+    const char* in = mine + slot * ROWS * 5 * kRow;
+    slot ^= 1;
+    auto read = [&](int operand, const T* base, int64_t ld, int i, int k, float2* v) {
+      staged_vector<T, THREADS, ALIGNED>(in + (i * 5 + operand) * kRow,
+                                         low_bits(base + (row0 + i) * ld), t, k, v);
+    };
+    float r1[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) r1[i] = 1.f;
     if (p.w_post) {
-      float sum[1] = {0.f};
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+      for (int i = 0; i < ROWS; ++i) {
+        float2 sum = both(0.f);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) sum[0] = fmaf(to_f32(f[k].e[e]), to_f32(f[k].e[e]), sum[0]);
-      row_sums<1, WARPS>(sum, red1, turn1);
-      r1 = 1.f / sqrtf(fmaf(sum[0], inv, p.eps));
-    }
-    float y[K][VE], both_sums[2] = {0.f, 0.f};
+        for (int k = 0; k < K; ++k) {
+          float2 f[H];
+          read(0, p.f, p.ldf, i, k, f);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float w[VE], c[VE];
-      load_params<T, N, ALIGNED>(p.w_post, 1.f, t, k, p.width, w);
-      load_params<T, N, ALIGNED>(p.scale, 1.f, t, k, p.width, c);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        float v = to_f32(f[k].e[e]) * r1 * w[e];
-        if (p.z) v *= gate_of(to_f32(z[k].e[e]), p.gate).act;
-        y[k][e] = fmaf(v, c[e], to_f32(x[k].e[e]));
+          for (int e = 0; e < H; ++e) sum = fma2(f[e], f[e], sum);
+        }
+        r1[i] = sum.x + sum.y;
       }
-      if (g.du) {
-        load_params<T, N, ALIGNED>(p.w_pre, 1.f, t, k, p.width, w);
+      group_sums<ROWS, THREADS>(r1, red, turn);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          both_sums[0] = fmaf(y[k][e], y[k][e], both_sums[0]);
-          both_sums[1] = fmaf(to_f32(du[k].e[e]) * w[e], y[k][e], both_sums[1]);
+      for (int i = 0; i < ROWS; ++i) r1[i] = 1.f / sqrtf(fmaf(r1[i], inv, p.eps));
+    }
+    float2 y[ROWS][K][H];
+    float r2[ROWS], back[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) r2[i] = back[i] = 0.f;
+    if (g.du) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float2 w[H], c[H];
+        load_params<T, THREADS, ALIGNED>(p.w_post, 1.f, t, k, p.width, w);
+        load_params<T, THREADS, ALIGNED>(p.scale, 1.f, t, k, p.width, c);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+          float2 q[H];
+          read(0, p.f, p.ldf, i, k, q);
+#pragma unroll
+          for (int e = 0; e < H; ++e) y[i][k][e] = q[e] * both(r1[i]) * w[e];
+          if (p.z) {
+            read(1, p.z, p.ldz, i, k, q);
+#pragma unroll
+            for (int e = 0; e < H; ++e) y[i][k][e] = y[i][k][e] * gate_of<false>(q[e], p.gate).act;
+          }
+          if (p.x) {
+            read(2, p.x, p.ldx, i, k, q);
+#pragma unroll
+            for (int e = 0; e < H; ++e) y[i][k][e] = fma2(y[i][k][e], c[e], q[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < H; ++e) y[i][k][e] = y[i][k][e] * c[e];
+          }
         }
       }
+      float sums[2 * ROWS];
+      float2 sq[ROWS], dot[ROWS];
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) sq[i] = dot[i] = both(0.f);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float2 w[H];
+        load_params<T, THREADS, ALIGNED>(p.w_pre, 0.f, t, k, p.width, w);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+          float2 q[H];
+          read(4, g.du, g.lddu, i, k, q);
+#pragma unroll
+          for (int e = 0; e < H; ++e) {
+            sq[i] = fma2(y[i][k][e], y[i][k][e], sq[i]);
+            dot[i] = fma2(q[e] * w[e], y[i][k][e], dot[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        sums[2 * i] = sq[i].x + sq[i].y;
+        sums[2 * i + 1] = dot[i].x + dot[i].y;
+      }
+      group_sums<2 * ROWS, THREADS>(sums, red2, turn2);
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        r2[i] = 1.f / sqrtf(fmaf(sums[2 * i], inv, p.eps));
+        back[i] = sums[2 * i + 1] * inv * r2[i] * r2[i] * r2[i];
+      }
     }
-    float r2 = 0.f, back = 0.f;
-    if (g.du) {
-      row_sums<2, WARPS>(both_sums, red, turn);
-      r2 = 1.f / sqrtf(fmaf(both_sums[0], inv, p.eps));
-      back = both_sums[1] * inv * r2 * r2 * r2;
-    }
-    float dn[K][VE], sum[1] = {0.f};
+    float2 dn[ROWS][K][H];
+    float mean[ROWS];
+    float2 dot[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) dot[i] = both(0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float w[VE], c[VE], d[VE], dz[VE];
-      load_params<T, N, ALIGNED>(p.w_pre, 0.f, t, k, p.width, w);
+      float2 w[H];
+      load_params<T, THREADS, ALIGNED>(p.w_pre, 0.f, t, k, p.width, w);
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const float u = to_f32(du[k].e[e]);
-        d[e] = fmaf(-y[k][e], back, fmaf(u * w[e], r2, to_f32(dy[k].e[e])));
-        if (g.dw_pre) mine[((2 * K + k) * VE + e) * N] += u * y[k][e] * r2;
-      }
-      if (g.dx) store_row<T, N, ALIGNED>(g.dx + row * g.lddx, t, k, p.width, d);
-      load_params<T, N, ALIGNED>(p.w_post, 1.f, t, k, p.width, w);
-      load_params<T, N, ALIGNED>(p.scale, 1.f, t, k, p.width, c);
+      for (int i = 0; i < ROWS; ++i) {  // dn holds dx for now
+        if (g.dy) {
+          read(3, g.dy, g.lddy, i, k, dn[i][k]);
+        } else {
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const Gate q = p.z ? gate_of(to_f32(z[k].e[e]), p.gate) : Gate{1.f, 0.f};
-        const float n = to_f32(f[k].e[e]) * r1, nw = n * w[e];
-        if (g.dscale) mine[((K + k) * VE + e) * N] += d[e] * nw * q.act;
-        const float dt = d[e] * c[e];
-        dz[e] = dt * nw * q.slope;
-        const float da = dt * q.act;
-        if (g.dw_post) mine[(k * VE + e) * N] += da * n;
-        dn[k][e] = da * w[e];
-        sum[0] = fmaf(dn[k][e], n, sum[0]);
+          for (int e = 0; e < H; ++e) dn[i][k][e] = both(0.f);
+        }
+        if (g.du) {
+          float2 q[H];
+          read(4, g.du, g.lddu, i, k, q);
+#pragma unroll
+          for (int e = 0; e < H; ++e) {
+            const float2 ur = q[e] * both(r2[i]);
+            dn[i][k][e] = fma2(ur, w[e], fma2(y[i][k][e], both(-back[i]), dn[i][k][e]));
+            sp[k][e] = fma2(ur, y[i][k][e], sp[k][e]);
+          }
+        }
+        if (g.dx && row0 + i < p.rows)
+          store_vector<T, THREADS, ALIGNED>(g.dx + (row0 + i) * g.lddx, t, k, p.width, dn[i][k]);
       }
-      if (g.dz) store_row<T, N, ALIGNED>(g.dz + row * g.lddz, t, k, p.width, dz);
+      float2 c[H];
+      load_params<T, THREADS, ALIGNED>(p.w_post, 1.f, t, k, p.width, w);
+      load_params<T, THREADS, ALIGNED>(p.scale, 1.f, t, k, p.width, c);
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        float2 f[H], z[H], dz[H];
+        read(0, p.f, p.ldf, i, k, f);
+        if (p.z) read(1, p.z, p.ldz, i, k, z);
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+          const Gate q = p.z ? gate_of<true>(z[e], p.gate) : Gate{both(1.f), both(0.f)};
+          const float2 n = f[e] * both(r1[i]), nw = n * w[e];
+          const float2 d = dn[i][k][e];
+          sc[k][e] = fma2(d * nw, q.act, sc[k][e]);
+          const float2 dt = d * c[e], da = dt * q.act;
+          dz[e] = dt * nw * q.slope;
+          sw[k][e] = fma2(da, n, sw[k][e]);
+          dn[i][k][e] = da * w[e];
+          dot[i] = fma2(dn[i][k][e], n, dot[i]);
+        }
+        if (g.dz && row0 + i < p.rows)
+          store_vector<T, THREADS, ALIGNED>(g.dz + (row0 + i) * g.lddz, t, k, p.width, dz);
+      }
     }
-    float mean = 0.f;
     if (p.w_post) {
-      row_sums<1, WARPS>(sum, red1, turn1);
-      mean = sum[0] * inv;
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) mean[i] = dot[i].x + dot[i].y;
+      group_sums<ROWS, THREADS>(mean, red, turn);
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (p.w_post)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < VE; ++e)
-          dn[k][e] = r1 * fmaf(-(to_f32(f[k].e[e]) * r1), mean, dn[k][e]);
-      store_row<T, N, ALIGNED>(g.df + row * g.lddf, t, k, p.width, dn[k]);
+      for (int i = 0; i < ROWS; ++i) {
+        if (p.w_post) {  // r1 (dn - f r1 mean)
+          float2 f[H];
+          read(0, p.f, p.ldf, i, k, f);
+          const float m = -r1[i] * (mean[i] * inv);
+#pragma unroll
+          for (int e = 0; e < H; ++e)
+            dn[i][k][e] = both(r1[i]) * fma2(f[e], both(m), dn[i][k][e]);
+        }
+        if (row0 + i < p.rows)
+          store_vector<T, THREADS, ALIGNED>(g.df + (row0 + i) * g.lddf, t, k, p.width, dn[i][k]);
+      }
+    if (!ALIGNED) {  // every thread has read its rows before they are overwritten
+      if (THREADS > 32) __syncthreads(); else __syncwarp();
     }
   }
+  cp_async_wait_all();
   if (!partial) return;
-  // the block's part: [3][width]; the four warps of short rows in order
-  if constexpr (WARPS == 1) __syncthreads();
-  for (int j = WARPS == 1 ? threadIdx.x >> 5 : 0; j < 3 * K; j += P::kRows)
+  // the block's part, [3][width]; the sums of several groups in order
+  float* sums = reinterpret_cast<float*>(shared);
+  auto put = [&](int which, float2 (&v)[K][H]) {
+    float* part = partial + (static_cast<int64_t>(blockIdx.x) * 3 + which) * p.width;
 #pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const int c = row_element<T, N, ALIGNED>(t, j % K, e);
-      if (c >= p.width) continue;
-      float v = 0.f;
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int r = 0; r < P::kRows; ++r) v += sums[(r * 3 * K * VE + j * VE + e) * N + t];
-      partial[(blockIdx.x * int64_t(3) + j / K) * p.width + c] = v;
-    }
+      for (int e = 0; e < 2 * H; ++e) {
+        const int c = row_element<T, THREADS, ALIGNED>(t, k, e);
+        float sum = e % 2 ? v[k][e / 2].y : v[k][e / 2].x;
+        if constexpr (G::kGroups > 1) {
+          __syncthreads();
+          sums[threadIdx.x] = sum;
+          __syncthreads();
+          if (group == 0)
+            for (int q = 1; q < G::kGroups; ++q) sum += sums[q * THREADS + t];
+        }
+        if (group == 0 && c < p.width) part[c] = sum;
+      }
+  };
+  __syncthreads();
+  put(0, sw);
+  put(1, sc);
+  put(2, sp);
 }
 
 // The three sums over rows: 32 columns a block, each of its 16 warps every sixteenth part in
@@ -280,7 +470,7 @@ constexpr int kLong = 1024;
 
 __device__ __forceinline__ float block_sum(float v, float (*red)[1][32], int& turn) {
   float s[1] = {v};
-  row_sums<1, kLong / 32>(s, red, turn);
+  group_sums<1, kLong>(s, red, turn);
   return s[0];
 }
 
@@ -288,7 +478,7 @@ template <typename T>
 __device__ __forceinline__ float new_residual(const GnormRows<T>& p, int64_t row, int c, float r1) {
   float t = to_f32(p.f[row * p.ldf + c]);
   if (p.w_post) t = t * r1 * p.w_post[c];
-  if (p.z) t *= gate_of(to_f32(p.z[row * p.ldz + c]), p.gate).act;
+  if (p.z) t *= gate_of<false>(both(to_f32(p.z[row * p.ldz + c])), p.gate).act.x;
   return fmaf(t, p.scale ? p.scale[c] : 1.f, p.x ? to_f32(p.x[row * p.ldx + c]) : 0.f);
 }
 
@@ -363,11 +553,12 @@ gnorm_long_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ 
       if (g.dx) g.dx[row * g.lddx + c] = from_f32<T>(d);
       const float n = to_f32(p.f[row * p.ldf + c]) * r1;
       const float w = p.w_post ? p.w_post[c] : 1.f;
-      const Gate q = p.z ? gate_of(to_f32(p.z[row * p.ldz + c]), p.gate) : Gate{1.f, 0.f};
-      if (g.dscale) part[p.width + c] += d * (n * w) * q.act;
+      const Gate q = p.z ? gate_of<true>(both(to_f32(p.z[row * p.ldz + c])), p.gate)
+                         : Gate{both(1.f), both(0.f)};
+      if (g.dscale) part[p.width + c] += d * (n * w) * q.act.x;
       const float dt = p.scale ? d * p.scale[c] : d;
-      if (g.dz) g.dz[row * g.lddz + c] = from_f32<T>(dt * (n * w) * q.slope);
-      const float da = dt * q.act;
+      if (g.dz) g.dz[row * g.lddz + c] = from_f32<T>(dt * (n * w) * q.slope.x);
+      const float da = dt * q.act.x;
       if (g.dw_post) part[c] += da * n;
       dot = fmaf(da * w, n, dot);
     }
@@ -378,7 +569,7 @@ gnorm_long_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ 
         d = fmaf(-new_residual(p, row, c, r1), back,
                  fmaf(to_f32(g.du[row * g.lddu + c]) * p.w_pre[c], r2, d));
       if (p.scale) d *= p.scale[c];
-      if (p.z) d *= gate_of(to_f32(p.z[row * p.ldz + c]), p.gate).act;
+      if (p.z) d *= gate_of<false>(both(to_f32(p.z[row * p.ldz + c])), p.gate).act.x;
       if (p.w_post)
         d = r1 * fmaf(-(to_f32(p.f[row * p.ldf + c]) * r1), mean, d * p.w_post[c]);
       g.df[row * g.lddf + c] = from_f32<T>(d);
@@ -388,60 +579,76 @@ gnorm_long_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ 
 
 // ------------------------------------------------------------------ launches
 
-// Warps a row and vectors a thread, from the vectors a row has: a warp while it holds them in two
-// vectors a lane, then the fewest warps with one vector a thread (two for the longest).
+// Threads of a row, from the 16-byte vectors it has: the fewest with one vector each, 8 at least; two
+// vectors each for the longest; 0: the looped kernels.
 struct Shape {
-  int warps, vectors;
+  int threads, vectors;
 };
 
 Shape shape_of(int width, int vec) {
   const int n = (width + vec - 1) / vec;
-  if (n <= 32) return {1, 1};
-  if (n <= 64) return {1, 2};
-  if (n <= 128) return {4, 1};
-  if (n <= 256) return {8, 1};
-  if (n <= 512) return {16, 1};
-  if (n <= 1024) return {32, 1};
-  if (n <= 2048) return {32, 2};
-  return {0, 0};  // long rows
+  for (int threads = 8; threads <= 1024; threads *= 2)
+    if (n <= threads) return {threads, 1};
+  return n <= 2048 ? Shape{1024, 2} : Shape{0, 0};
 }
 
-// Blocks that walk the rows: what the GPU holds at once.
-int blocks_for(const Shape& s, int64_t rows, int held) {
-  const int64_t need = s.warps == 1 ? (rows + 3) / 4 : rows;
+int block_of(const Shape& s) { return s.threads == 0 ? kLong : (s.threads <= 32 ? 128 : s.threads); }
+
+// Rows a block takes in a turn: two a group, one where a block has 1024 threads and 64 registers
+// each (or, looping, none to spare).
+int turn_rows(const Shape& s) {
+  return s.threads == 0 || s.threads == 1024 ? 1 : 2 * block_of(s) / s.threads;
+}
+
+// Persistent blocks: what the GPU holds of `threads` threads an SM, or what the rows need.
+int blocks_for(const Shape& s, int64_t rows, int threads) {
+  const int64_t need = (rows + turn_rows(s) - 1) / turn_rows(s);
+  const int64_t held = kSms * (threads > block_of(s) ? threads / block_of(s) : 1);
   return static_cast<int>(need < held ? need : held);
 }
 
+constexpr int kForwardThreads = 1024, kBackwardThreads = 512;  // of an SM
+
 int backward_blocks(int width, int vec, int64_t rows) {
-  const Shape s = shape_of(width, vec);
-  const int held = s.warps == 0 ? kSms : kSms * (s.warps == 1 ? 4 : s.vectors == 1 ? 32 / s.warps : 1);
-  return blocks_for(s, rows, held);
+  return blocks_for(shape_of(width, vec), rows, kBackwardThreads);
 }
 
 bool vec16(const void* p, int64_t bytes) {
   return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(bytes)) & 15) == 0;
 }
 
-// Calls f with (vectors, warps) as compile-time values.
+// Calls f with (vectors, threads, rows of a group) as compile-time values.
+template <int K, int THREADS, int ROWS>
+struct Config {
+  static constexpr int vectors = K, threads = THREADS, rows = ROWS;
+};
 template <typename F>
 cudaError_t with_shape(const Shape& s, F&& f) {
-  using std::integral_constant;
-  if (s.warps == 1 && s.vectors == 1) return f(integral_constant<int, 1>(), integral_constant<int, 1>());
-  if (s.warps == 1) return f(integral_constant<int, 2>(), integral_constant<int, 1>());
-  if (s.warps == 4) return f(integral_constant<int, 1>(), integral_constant<int, 4>());
-  if (s.warps == 8) return f(integral_constant<int, 1>(), integral_constant<int, 8>());
-  if (s.warps == 16) return f(integral_constant<int, 1>(), integral_constant<int, 16>());
-  if (s.vectors == 1) return f(integral_constant<int, 1>(), integral_constant<int, 32>());
-  return f(integral_constant<int, 2>(), integral_constant<int, 32>());
+  switch (s.threads) {
+    case 8: return f(Config<1, 8, 2>());
+    case 16: return f(Config<1, 16, 2>());
+    case 32: return f(Config<1, 32, 2>());
+    case 64: return f(Config<1, 64, 2>());
+    case 128: return f(Config<1, 128, 2>());
+    case 256: return f(Config<1, 256, 2>());
+    case 512: return f(Config<1, 512, 2>());
+    default: return s.vectors == 1 ? f(Config<1, 1024, 1>()) : f(Config<2, 1024, 1>());
+  }
 }
 
 template <typename T, bool ALIGNED>
 cudaError_t launch_forward(const Shape& s, const GnormRows<T>& p, T* y, int64_t ldy, T* u,
                            int64_t ldu, cudaStream_t stream) {
-  return with_shape(s, [&](auto k, auto warps) {
-    constexpr int K = decltype(k)::value, WARPS = decltype(warps)::value;
-    const int grid = blocks_for(s, p.rows, kSms * (WARPS == 1 ? 8 : 64 / WARPS));
-    gnorm_kernel<T, K, WARPS, ALIGNED><<<grid, Place<WARPS>::kBlock, 0, stream>>>(p, y, ldy, u, ldu);
+  return with_shape(s, [&](auto c) {
+    using C = decltype(c);
+    constexpr int kShared = Group<C::threads>::kGroups * kTurns * C::rows * 3 *
+                            kStagedRow<C::threads, C::vectors, ALIGNED>;
+    auto* kernel = gnorm_kernel<T, C::vectors, C::threads, C::rows, ALIGNED>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+    if (e != cudaSuccess) return e;
+    kernel<<<blocks_for(s, p.rows, kForwardThreads), Group<C::threads>::kBlock, kShared, stream>>>(
+        p, y, ldy, u, ldu);
     return cudaGetLastError();
   });
 }
@@ -449,14 +656,20 @@ cudaError_t launch_forward(const Shape& s, const GnormRows<T>& p, T* y, int64_t 
 template <typename T, bool ALIGNED>
 cudaError_t launch_backward(const Shape& s, const GnormRows<T>& p, const GnormGrads<T>& g,
                             float* partial, int parts, cudaStream_t stream) {
-  return with_shape(s, [&](auto k, auto warps) {
-    constexpr int K = decltype(k)::value, WARPS = decltype(warps)::value;
-    constexpr int kShared = 3 * K * kVecElements<T> * Place<WARPS>::kBlock * 4;
-    auto* kernel = gnorm_backward_kernel<T, K, WARPS, ALIGNED>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
-    if (e != cudaSuccess) return e;
-    kernel<<<parts, Place<WARPS>::kBlock, partial ? kShared : 0, stream>>>(p, g, partial);
+  return with_shape(s, [&](auto c) {
+    using C = decltype(c);
+    constexpr int kShared = Group<C::threads>::kGroups * kTurns * C::rows * 5 *
+                            kStagedRow<C::threads, C::vectors, ALIGNED>;
+    if constexpr (kShared > 227 * 1024 - 4096) {
+      // two vectors a thread and five operands do not fit: the looped kernel takes those rows
+      gnorm_long_backward_kernel<T><<<parts, kLong, 0, stream>>>(p, g, partial);
+    } else {
+      auto* kernel = gnorm_backward_kernel<T, C::vectors, C::threads, C::rows, ALIGNED>;
+      const cudaError_t e =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+      if (e != cudaSuccess) return e;
+      kernel<<<parts, Group<C::threads>::kBlock, kShared, stream>>>(p, g, partial);
+    }
     return cudaGetLastError();
   });
 }
@@ -474,8 +687,8 @@ cudaError_t launch_gnorm(const GnormRows<T>& p, T* y, int64_t ldy, T* u, int64_t
                          cudaStream_t stream) {
   const Shape s = shape_of(p.width, kVecElements<T>);
   const int64_t es = sizeof(T);
-  if (s.warps == 0) {
-    gnorm_long_kernel<T><<<blocks_for(s, p.rows, 2 * kSms), kLong, 0, stream>>>(p, y, ldy, u, ldu);
+  if (s.threads == 0) {
+    gnorm_long_kernel<T><<<blocks_for(s, p.rows, 2 * kLong), kLong, 0, stream>>>(p, y, ldy, u, ldu);
     return cudaGetLastError();
   }
   const bool aligned = vec16(p.f, p.ldf * es) && vec16(p.z, p.ldz * es) && vec16(p.x, p.ldx * es) &&
@@ -495,7 +708,7 @@ cudaError_t launch_gnorm_backward(const GnormRows<T>& p, const GnormGrads<T>& g,
   const int64_t es = sizeof(T);
   if (parts > 0) {
     cudaError_t e;
-    if (s.warps == 0) {
+    if (s.threads == 0) {
       gnorm_long_backward_kernel<T><<<parts, kLong, 0, stream>>>(p, g, partial);
       e = cudaGetLastError();
     } else {

@@ -1,110 +1,155 @@
-// The gate of the norms around a block and the rows' register layout (bs_gnorm calls).
+// The gate of the norms around a block and the staging of their rows (bs_gnorm calls).
 #pragma once
 
 #include <cstdint>
 #include <cuda_runtime.h>
 
 #include "grec_math.cuh"
+#include "grec_tile.cuh"
 #include "row_types.cuh"
 
 namespace bsolve {
 
+// act(z) and its derivative, for two elements; kind: a bs_gate. sigma(z) = 1 / (1 + e^-z),
+// 1 - sigma(z) = e^-z sigma(z) with e^-z kept finite there. The approximate exponential and
+// reciprocal are within 2 ulp.
 struct Gate {
-  float act, slope;  // act(z) and its derivative
+  float2 act, slope;
 };
 
-// kind: a bs_gate. sigma(z) = 1 / (1 + e^-z); 1 - sigma(z) = e^-z sigma(z), and 1 where e^-z
-// is beyond FP32. The approximate exponential and reciprocal are within 2 ulp.
-__device__ __forceinline__ Gate gate_of(float z, int kind) {
-  if (kind == 2) return {z, 1.f};
-  const float e = ex2(z * -kLog2e);
-  const float s = rcp(1.f + e);
-  const float c = z < -80.f ? 1.f : e * s;
+template <bool SLOPE>
+__device__ __forceinline__ Gate gate_of(float2 z, int kind) {
+  if (kind == 2) return {z, both(1.f)};
+  float2 e = z * both(-kLog2e);
+  e = make_float2(ex2(e.x), ex2(e.y));
+  float2 s = e + both(1.f);
+  s = make_float2(rcp(s.x), rcp(s.y));
+  const float2 zs = z * s;
+  if (!SLOPE) return {kind == 1 ? s : zs, s};
+  const float2 c = make_float2(fminf(e.x, 0x1p126f), fminf(e.y, 0x1p126f)) * s;
   if (kind == 1) return {s, s * c};
-  return {z * s, fmaf(z * s, c, s)};
+  return {zs, fma2(zs, c, s)};
 }
 
-// A thread's elements of a row in registers: VE of them, K times, as stored. ALIGNED: 16-byte
-// vectors, thread t the vectors t, t + threads, ...; otherwise single elements, thread t the
-// elements t, t + threads, ..., so that a warp's loads are still one stretch.
+// A thread's elements of a row, VE of them a vector. ALIGNED: 16-byte vectors, thread t the vectors t,
+// t + threads, ...; otherwise single elements, t, t + threads, ..., so that a warp's stores are
+// still one stretch.
 template <typename T>
 constexpr int kVecElements = 16 / static_cast<int>(sizeof(T));
 
-template <typename T>
-struct alignas(16) RowVec {
-  T e[kVecElements<T>];
-};
-
-__device__ __forceinline__ uint4 load_streamed(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
-// The element of the row that slot e of the thread's vector k holds.
 template <typename T, int THREADS, bool ALIGNED>
 __device__ __forceinline__ int row_element(int t, int k, int e) {
   constexpr int VE = kVecElements<T>;
   return ALIGNED ? (k * THREADS + t) * VE + e : (k * VE + e) * THREADS + t;
 }
 
-// Zeros where the row is absent or ends.
-template <typename T, int THREADS, bool ALIGNED>
-__device__ __forceinline__ RowVec<T> load_row(const T* row, int t, int k, int width) {
-  constexpr int VE = kVecElements<T>;
-  RowVec<T> v;
-  const int at = row_element<T, THREADS, ALIGNED>(t, k, 0);
-  if (ALIGNED && row != nullptr && at + VE <= width) {
-    *reinterpret_cast<uint4*>(&v) = load_streamed(row + at);
-    return v;
-  }
+// Bytes that a row takes in shared memory. Where it is not aligned it is staged from the 16-byte
+// boundary at or below its first element, one piece more.
+template <int THREADS, int K, bool ALIGNED>
+constexpr int kStagedRow = (THREADS * K + (ALIGNED ? 0 : 1)) * 16;
+
+// Copies a row into smem, zeros behind its `bytes`. ALIGNED: every thread what it will itself read.
+// row == nullptr: a row of zeros. `base` the operand's first byte: nothing in front is read.
+template <typename T, int THREADS, int K, bool ALIGNED>
+__device__ __forceinline__ void stage_row(char* smem, const char* row, const char* base, int bytes,
+                                          int t) {
+  if constexpr (ALIGNED) {
 #pragma unroll
-  for (int e = 0; e < VE; ++e) {
-    const int c = row_element<T, THREADS, ALIGNED>(t, k, e);
-    v.e[e] = row != nullptr && c < width ? row[c] : from_f32<T>(0.f);
+    for (int k = 0; k < K; ++k) {
+      const int at = (k * THREADS + t) * 16;
+      int left = row == nullptr ? 0 : bytes - at;
+      left = left < 0 ? 0 : (left > 16 ? 16 : left);
+      cp_async_16(smem + at, left ? row + at : base, left);
+    }
+  } else {
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+    const char* zero = reinterpret_cast<const char*>(
+        (reinterpret_cast<uintptr_t>(base) + 15) & ~static_cast<uintptr_t>(15));
+#pragma unroll
+    for (int k = 0; k <= K; ++k) {
+      if (k == K && t != 0) break;
+      const int piece = k == K ? K * THREADS : k * THREADS + t;
+      const char* from = row - shift + piece * 16;
+      int left = row == nullptr ? 0 : bytes + shift - piece * 16;
+      left = left < 0 ? 0 : (left > 16 ? 16 : left);
+      if (left == 0 || from >= base) {
+        cp_async_16(smem + piece * 16, left ? from : zero, left);
+      } else {  // the boundary lies in front of the operand: its first elements one by one
+        for (int b = shift; b < 16; b += static_cast<int>(sizeof(T)))
+          *reinterpret_cast<T*>(smem + b) =
+              b < shift + bytes ? *reinterpret_cast<const T*>(from + b) : from_f32<T>(0.f);
+      }
+    }
   }
-  return v;
+}
+
+// The thread's vector k of a staged row in FP32; `row` the row's address (its low bits are used).
+template <typename T, int THREADS, bool ALIGNED>
+__device__ __forceinline__ void staged_vector(const char* smem, unsigned row, int t, int k,
+                                              float2* v) {
+  constexpr int VE = kVecElements<T>;
+  using P = typename Pair<T>::type;
+  if constexpr (ALIGNED) {
+    struct alignas(16) Vec {
+      P p[VE / 2];
+    };
+    const Vec q = *reinterpret_cast<const Vec*>(smem + (k * THREADS + t) * 16);
+#pragma unroll
+    for (int e = 0; e < VE / 2; ++e) v[e] = to_f32(q.p[e]);
+  } else {
+    const T* at = reinterpret_cast<const T*>(smem + (row & 15u));
+#pragma unroll
+    for (int e = 0; e < VE / 2; ++e)
+      v[e] = make_float2(to_f32(at[row_element<T, THREADS, false>(t, k, 2 * e)]),
+                         to_f32(at[row_element<T, THREADS, false>(t, k, 2 * e + 1)]));
+  }
 }
 
 template <typename T, int THREADS, bool ALIGNED>
-__device__ __forceinline__ void store_row(T* row, int t, int k, int width, const float* v) {
+__device__ __forceinline__ void store_vector(T* row, int t, int k, int width, const float2* v) {
   constexpr int VE = kVecElements<T>;
+  using P = typename Pair<T>::type;
   const int at = row_element<T, THREADS, ALIGNED>(t, k, 0);
-  RowVec<T> q;
+  struct alignas(16) Vec {
+    P p[VE / 2];
+  } q;
 #pragma unroll
-  for (int e = 0; e < VE; ++e) q.e[e] = from_f32<T>(v[e]);
+  for (int e = 0; e < VE / 2; ++e) q.p[e] = pair_from_f32<T>(v[e]);
   if (ALIGNED && at + VE <= width) {
-    *reinterpret_cast<uint4*>(row + at) = *reinterpret_cast<const uint4*>(&q);
+    *reinterpret_cast<Vec*>(row + at) = q;
     return;
   }
 #pragma unroll
-  for (int e = 0; e < VE; ++e) {
-    const int c = row_element<T, THREADS, ALIGNED>(t, k, e);
-    if (c < width) row[c] = q.e[e];
+  for (int e = 0; e < VE / 2; ++e) {
+    const int c = row_element<T, THREADS, ALIGNED>(t, k, 2 * e),
+              d = row_element<T, THREADS, ALIGNED>(t, k, 2 * e + 1);
+    if (c < width) row[c] = q.p[e].x;
+    if (d < width) row[d] = q.p[e].y;
   }
 }
 
-// The vector's parameters (`fill` where the vector is absent, 0 behind the row's end); they stay
-// in the first cache level over the rows that a block walks.
+// The vector's parameters (`fill` where they are absent, 0 behind the row's end); they stay in the
+// first cache level over the rows that a block walks.
 template <typename T, int THREADS, bool ALIGNED>
 __device__ __forceinline__ void load_params(const float* w, float fill, int t, int k, int width,
-                                            float* v) {
+                                            float2* v) {
   constexpr int VE = kVecElements<T>;
   const int at = row_element<T, THREADS, ALIGNED>(t, k, 0);
   if (ALIGNED && w != nullptr && at + VE <= width) {
 #pragma unroll
-    for (int e = 0; e < VE; e += 4) {
-      const float4 q = __ldg(reinterpret_cast<const float4*>(w + at + e));
-      v[e] = q.x, v[e + 1] = q.y, v[e + 2] = q.z, v[e + 3] = q.w;
+    for (int e = 0; e < VE / 2; e += 2) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(w + at + 2 * e));
+      v[e] = make_float2(q.x, q.y);
+      v[e + 1] = make_float2(q.z, q.w);
     }
     return;
   }
 #pragma unroll
-  for (int e = 0; e < VE; ++e) {
-    const int c = row_element<T, THREADS, ALIGNED>(t, k, e);
-    v[e] = w == nullptr ? fill : (c < width ? __ldg(w + c) : 0.f);
+  for (int e = 0; e < VE / 2; ++e) {
+    const int c = row_element<T, THREADS, ALIGNED>(t, k, 2 * e),
+              d = row_element<T, THREADS, ALIGNED>(t, k, 2 * e + 1);
+    v[e].x = w == nullptr ? fill : (c < width ? __ldg(w + c) : 0.f);
+    v[e].y = w == nullptr ? fill : (d < width ? __ldg(w + d) : 0.f);
   }
 }
 
