@@ -22,29 +22,61 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kTurns = 2;  // turns of rows in shared memory: this one and the next
 
-// Sums of N values over a group's threads, the same bits in all of them. Consecutive calls take
-// the two halves of `red` in turn, so that one barrier a call is enough.
+// Sums of N (1, 2 or 4) values over a group's threads, the same bits in all of them. While lanes hold
+// several values, a step hands half of them to the lanes across and keeps the other half, so that N
+// values take little more than one value's shuffles. Consecutive calls take the two halves of
+// `red` in turn, so that one barrier a call is enough.
 template <int N, int THREADS>
-__device__ __forceinline__ void group_sums(float (&v)[N], float (*red)[N][32], int& turn) {
+__device__ __forceinline__ void group_sums(float (&v)[N], float (*red)[N * 32], int& turn) {
   constexpr int LANES = THREADS < 32 ? THREADS : 32, WARPS = THREADS / LANES;
+  const int lane = threadIdx.x & 31;
+  constexpr unsigned kAll = 0xFFFFFFFFu;
+  float s;
+  if constexpr (N == 4) {
+    const bool hi = lane & (LANES / 2), hj = lane & (LANES / 4);
+    float a = hi ? v[2] : v[0], b = hi ? v[3] : v[1];
+    a += __shfl_xor_sync(kAll, hi ? v[0] : v[2], LANES / 2);
+    b += __shfl_xor_sync(kAll, hi ? v[1] : v[3], LANES / 2);
+    s = hj ? b : a;
+    s += __shfl_xor_sync(kAll, hj ? a : b, LANES / 4);
+  } else if constexpr (N == 2) {
+    const bool hi = lane & (LANES / 2);
+    s = hi ? v[1] : v[0];
+    s += __shfl_xor_sync(kAll, hi ? v[0] : v[1], LANES / 2);
+  } else {
+    s = v[0] + __shfl_xor_sync(kAll, v[0], LANES / 2);
+  }
+  constexpr int EACH = N == 1 ? LANES / 2 : LANES / N;  // lanes that now add up one value
 #pragma unroll
-  for (int k = 0; k < N; ++k)
+  for (int m = (N == 1 ? LANES / 4 : EACH / 2); m > 0; m >>= 1) s += __shfl_xor_sync(kAll, s, m);
+  if constexpr (WARPS == 1) {
 #pragma unroll
-    for (int m = LANES / 2; m > 0; m >>= 1) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], m);
-  if constexpr (WARPS > 1) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0)
-#pragma unroll
-      for (int k = 0; k < N; ++k) red[turn][k][warp] = v[k];
+    for (int k = 0; k < N; ++k)  // value k sits in the k-th part of the group's lanes
+      v[k] = N == 1 ? s : __shfl_sync(kAll, s, (lane & ~(LANES - 1)) + k * (LANES / N));
+  } else {
+    const int warp = threadIdx.x >> 5;
+    float* r = red[turn];
+    if (lane % (32 / N) == 0) r[lane / (32 / N) * WARPS + warp] = s;
     __syncthreads();
+    constexpr int LOADS = N * WARPS > 32 ? N * WARPS / 32 : 1, PER = 32 / WARPS;  // values a load
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      v[k] = red[turn][k][lane & (WARPS - 1)];
+    for (int l = 0; l < LOADS; ++l) {
+      s = r[(l * 32 + lane) & (N * WARPS - 1)];
 #pragma unroll
-      for (int m = WARPS / 2; m > 0; m >>= 1) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], m);
+      for (int m = WARPS / 2; m > 0; m >>= 1) s += __shfl_xor_sync(kAll, s, m);
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (LOADS == 1 || k / PER == l)
+          v[k] = N * WARPS <= 32 && N == 1 ? s : __shfl_sync(kAll, s, k % PER * WARPS);
     }
     turn ^= 1;
   }
+}
+
+// 1 / sqrt(v) for v > 0: the approximate root with one Newton step.
+__device__ __forceinline__ float inverse_root(float v) {
+  const float r = rsqrt_fast(max_nan(v, 0x1p-126f));
+  return r == 0.f ? r : fmaf(r * 0.5f, fmaf(-v * r, r, 1.f), r);  // 0 where v overflowed
 }
 
 template <int THREADS>
@@ -60,41 +92,33 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
   using G = Group<THREADS>;
   constexpr int H = kVecElements<T> / 2;  // pairs of a vector
   constexpr int kRow = kStagedRow<THREADS, K, ALIGNED>;
-  __shared__ float red[2][ROWS][32];
+  __shared__ float red[2][ROWS * 32];
   extern __shared__ __align__(16) char shared[];
   const int t = threadIdx.x % THREADS, group = threadIdx.x / THREADS;
   char* mine = shared + group * (kTurns * ROWS * 3 * kRow);
   const float inv = 1.f / p.width;
   const int bytes = p.width * static_cast<int>(sizeof(T));
-  const int64_t turn_rows = static_cast<int64_t>(gridDim.x) * G::kGroups * ROWS;
-  int64_t row0 = (static_cast<int64_t>(blockIdx.x) * G::kGroups + group) * ROWS;
+  const unsigned rows = static_cast<unsigned>(p.rows);  // at most 2^30
+  const unsigned turn_rows = gridDim.x * (G::kGroups * ROWS);
+  unsigned row0 = (blockIdx.x * G::kGroups + group) * ROWS;
   int turn = 0;
 
-  auto stage = [&](int64_t from, int slot) {
+  auto stage = [&](unsigned from, int slot) {
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const int64_t row = from + i;
+      const unsigned row = from + i;
       char* to = mine + (slot * ROWS + i) * 3 * kRow;
-      const bool in = row < p.rows;
-      stage_row<T, THREADS, K, ALIGNED>(
-          to, in ? reinterpret_cast<const char*>(p.f + row * p.ldf) : nullptr,
-          reinterpret_cast<const char*>(p.f), bytes, t);
-      if (p.z)
-        stage_row<T, THREADS, K, ALIGNED>(
-            to + kRow, in ? reinterpret_cast<const char*>(p.z + row * p.ldz) : nullptr,
-            reinterpret_cast<const char*>(p.z), bytes, t);
-      if (p.x)
-        stage_row<T, THREADS, K, ALIGNED>(
-            to + 2 * kRow, in ? reinterpret_cast<const char*>(p.x + row * p.ldx) : nullptr,
-            reinterpret_cast<const char*>(p.x), bytes, t);
+      const int n = row < rows ? bytes : 0;
+      stage_row<T, THREADS, K, ALIGNED>(to, p.f, row, p.ldf, n, t);
+      if (p.z) stage_row<T, THREADS, K, ALIGNED>(to + kRow, p.z, row, p.ldz, n, t);
+      if (p.x) stage_row<T, THREADS, K, ALIGNED>(to + 2 * kRow, p.x, row, p.ldx, n, t);
     }
     cp_async_commit();
   };
   stage(row0, 0);
   int slot = 0;
   // the same number of turns for all groups of a block: the shuffles take whole warps
-  const int64_t block0 = static_cast<int64_t>(blockIdx.x) * G::kGroups * ROWS;
-  for (int64_t at = block0; at < p.rows; at += turn_rows, row0 += turn_rows) {
+  for (unsigned at = blockIdx.x * (G::kGroups * ROWS); at < rows; at += turn_rows, row0 += turn_rows) {
     stage(row0 + turn_rows, slot ^ 1);
     cp_async_wait_group<1>();
     if (!ALIGNED) {
@@ -112,7 +136,7 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           float2 f[H];
-          staged_vector<T, THREADS, ALIGNED>(in + i * 3 * kRow, low_bits(p.f + (row0 + i) * p.ldf),
+          staged_vector<T, THREADS, ALIGNED>(in + i * 3 * kRow, low_bits(row_of(p.f, row0 + i, p.ldf)),
                                              t, k, f);
 #pragma unroll
           for (int e = 0; e < H; ++e) sum = fma2(f[e], f[e], sum);
@@ -121,7 +145,7 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
       }
       group_sums<ROWS, THREADS>(r1, red, turn);
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) r1[i] = 1.f / sqrtf(fmaf(r1[i], inv, p.eps));
+      for (int i = 0; i < ROWS; ++i) r1[i] = inverse_root(fmaf(r1[i], inv, p.eps));
     }
     float2 v[ROWS][K][H];
     float r2[ROWS];
@@ -134,17 +158,17 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
       for (int i = 0; i < ROWS; ++i) {
         const char* at_row = in + i * 3 * kRow;
         float2 q[H];
-        staged_vector<T, THREADS, ALIGNED>(at_row, low_bits(p.f + (row0 + i) * p.ldf), t, k, q);
+        staged_vector<T, THREADS, ALIGNED>(at_row, low_bits(row_of(p.f, row0 + i, p.ldf)), t, k, q);
 #pragma unroll
         for (int e = 0; e < H; ++e) v[i][k][e] = q[e] * both(r1[i]) * w[e];
         if (p.z) {
-          staged_vector<T, THREADS, ALIGNED>(at_row + kRow, low_bits(p.z + (row0 + i) * p.ldz), t,
+          staged_vector<T, THREADS, ALIGNED>(at_row + kRow, low_bits(row_of(p.z, row0 + i, p.ldz)), t,
                                              k, q);
 #pragma unroll
           for (int e = 0; e < H; ++e) v[i][k][e] = v[i][k][e] * gate_of<false>(q[e], p.gate).act;
         }
         if (p.x) {
-          staged_vector<T, THREADS, ALIGNED>(at_row + 2 * kRow, low_bits(p.x + (row0 + i) * p.ldx),
+          staged_vector<T, THREADS, ALIGNED>(at_row + 2 * kRow, low_bits(row_of(p.x, row0 + i, p.ldx)),
                                              t, k, q);
 #pragma unroll
           for (int e = 0; e < H; ++e) v[i][k][e] = fma2(v[i][k][e], c[e], q[e]);
@@ -161,8 +185,8 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
       for (int k = 0; k < K; ++k) {
 #pragma unroll
         for (int e = 0; e < H; ++e) sum = fma2(v[i][k][e], v[i][k][e], sum);
-        if (y && row0 + i < p.rows)
-          store_vector<T, THREADS, ALIGNED>(y + (row0 + i) * ldy, t, k, p.width, v[i][k]);
+        if (y && row0 + i < rows)
+          store_vector<T, THREADS, ALIGNED>(row_of(y, row0 + i, ldy), t, k, p.width, v[i][k]);
       }
       r2[i] = sum.x + sum.y;
     }
@@ -179,12 +203,12 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
       load_params<T, THREADS, ALIGNED>(p.w_pre, 1.f, t, k, p.width, w);
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
-        const float r = 1.f / sqrtf(fmaf(r2[i], inv, p.eps));
+        const float r = inverse_root(fmaf(r2[i], inv, p.eps));
         float2 q[H];
 #pragma unroll
         for (int e = 0; e < H; ++e) q[e] = v[i][k][e] * (both(r) * w[e]);
-        if (row0 + i < p.rows)
-          store_vector<T, THREADS, ALIGNED>(u + (row0 + i) * ldu, t, k, p.width, q);
+        if (row0 + i < rows)
+          store_vector<T, THREADS, ALIGNED>(row_of(u, row0 + i, ldu), t, k, p.width, q);
       }
     }
   }
@@ -204,15 +228,16 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
   using G = Group<THREADS>;
   constexpr int H = kVecElements<T> / 2;
   constexpr int kRow = kStagedRow<THREADS, K, ALIGNED>;
-  __shared__ float red[2][ROWS][32];
-  __shared__ float red2[2][2 * ROWS][32];
+  __shared__ float red[2][ROWS * 32];
+  __shared__ float red2[2][2 * ROWS * 32];
   extern __shared__ __align__(16) char shared[];
   const int t = threadIdx.x % THREADS, group = threadIdx.x / THREADS;
   char* mine = shared + group * (kTurns * ROWS * 5 * kRow);
   const float inv = 1.f / p.width;
   const int bytes = p.width * static_cast<int>(sizeof(T));
-  const int64_t turn_rows = static_cast<int64_t>(gridDim.x) * G::kGroups * ROWS;
-  int64_t row0 = (static_cast<int64_t>(blockIdx.x) * G::kGroups + group) * ROWS;
+  const unsigned rows = static_cast<unsigned>(p.rows);  // at most 2^30
+  const unsigned turn_rows = gridDim.x * (G::kGroups * ROWS);
+  unsigned row0 = (blockIdx.x * G::kGroups + group) * ROWS;
   int turn = 0, turn2 = 0;
   float2 sw[K][H], sc[K][H], sp[K][H];  // the sums dw_post, dscale, dw_pre
 #pragma unroll
@@ -220,28 +245,23 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
 #pragma unroll
     for (int e = 0; e < H; ++e) sw[k][e] = sc[k][e] = sp[k][e] = both(0.f);
 
-  auto one = [&](char* to, const T* base, int64_t ld, int64_t row) {
-    if (base)
-      stage_row<T, THREADS, K, ALIGNED>(
-          to, row < p.rows ? reinterpret_cast<const char*>(base + row * ld) : nullptr,
-          reinterpret_cast<const char*>(base), bytes, t);
-  };
-  auto stage = [&](int64_t from, int slot) {
+  auto stage = [&](unsigned from, int slot) {
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
+      const unsigned row = from + i;
       char* to = mine + (slot * ROWS + i) * 5 * kRow;
-      one(to, p.f, p.ldf, from + i);
-      one(to + kRow, p.z, p.ldz, from + i);
-      one(to + 2 * kRow, p.x, p.ldx, from + i);
-      one(to + 3 * kRow, g.dy, g.lddy, from + i);
-      one(to + 4 * kRow, g.du, g.lddu, from + i);
+      const int n = row < rows ? bytes : 0;
+      stage_row<T, THREADS, K, ALIGNED>(to, p.f, row, p.ldf, n, t);
+      if (p.z) stage_row<T, THREADS, K, ALIGNED>(to + kRow, p.z, row, p.ldz, n, t);
+      if (p.x) stage_row<T, THREADS, K, ALIGNED>(to + 2 * kRow, p.x, row, p.ldx, n, t);
+      if (g.dy) stage_row<T, THREADS, K, ALIGNED>(to + 3 * kRow, g.dy, row, g.lddy, n, t);
+      if (g.du) stage_row<T, THREADS, K, ALIGNED>(to + 4 * kRow, g.du, row, g.lddu, n, t);
     }
     cp_async_commit();
   };
   stage(row0, 0);
   int slot = 0;
-  const int64_t block0 = static_cast<int64_t>(blockIdx.x) * G::kGroups * ROWS;
-  for (int64_t at = block0; at < p.rows; at += turn_rows, row0 += turn_rows) {
+  for (unsigned at = blockIdx.x * (G::kGroups * ROWS); at < rows; at += turn_rows, row0 += turn_rows) {
     stage(row0 + turn_rows, slot ^ 1);
     cp_async_wait_group<1>();
     if (!ALIGNED) {
@@ -251,7 +271,7 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
     slot ^= 1;
     auto read = [&](int operand, const T* base, int64_t ld, int i, int k, float2* v) {
       staged_vector<T, THREADS, ALIGNED>(in + (i * 5 + operand) * kRow,
-                                         low_bits(base + (row0 + i) * ld), t, k, v);
+                                         low_bits(row_of(base, row0 + i, ld)), t, k, v);
     };
     float r1[ROWS];
 #pragma unroll
@@ -271,7 +291,7 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
       }
       group_sums<ROWS, THREADS>(r1, red, turn);
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) r1[i] = 1.f / sqrtf(fmaf(r1[i], inv, p.eps));
+      for (int i = 0; i < ROWS; ++i) r1[i] = inverse_root(fmaf(r1[i], inv, p.eps));
     }
     float2 y[ROWS][K][H];
     float r2[ROWS], back[ROWS];
@@ -331,7 +351,7 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
       group_sums<2 * ROWS, THREADS>(sums, red2, turn2);
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
-        r2[i] = 1.f / sqrtf(fmaf(sums[2 * i], inv, p.eps));
+        r2[i] = inverse_root(fmaf(sums[2 * i], inv, p.eps));
         back[i] = sums[2 * i + 1] * inv * r2[i] * r2[i] * r2[i];
       }
     }
@@ -362,8 +382,8 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
             sp[k][e] = fma2(ur, y[i][k][e], sp[k][e]);
           }
         }
-        if (g.dx && row0 + i < p.rows)
-          store_vector<T, THREADS, ALIGNED>(g.dx + (row0 + i) * g.lddx, t, k, p.width, dn[i][k]);
+        if (g.dx && row0 + i < rows)
+          store_vector<T, THREADS, ALIGNED>(row_of(g.dx, row0 + i, g.lddx), t, k, p.width, dn[i][k]);
       }
       float2 c[H];
       load_params<T, THREADS, ALIGNED>(p.w_post, 1.f, t, k, p.width, w);
@@ -385,8 +405,8 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
           dn[i][k][e] = da * w[e];
           dot[i] = fma2(dn[i][k][e], n, dot[i]);
         }
-        if (g.dz && row0 + i < p.rows)
-          store_vector<T, THREADS, ALIGNED>(g.dz + (row0 + i) * g.lddz, t, k, p.width, dz);
+        if (g.dz && row0 + i < rows)
+          store_vector<T, THREADS, ALIGNED>(row_of(g.dz, row0 + i, g.lddz), t, k, p.width, dz);
       }
     }
     if (p.w_post) {
@@ -406,8 +426,8 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
           for (int e = 0; e < H; ++e)
             dn[i][k][e] = both(r1[i]) * fma2(f[e], both(m), dn[i][k][e]);
         }
-        if (row0 + i < p.rows)
-          store_vector<T, THREADS, ALIGNED>(g.df + (row0 + i) * g.lddf, t, k, p.width, dn[i][k]);
+        if (row0 + i < rows)
+          store_vector<T, THREADS, ALIGNED>(row_of(g.df, row0 + i, g.lddf), t, k, p.width, dn[i][k]);
       }
     if (!ALIGNED) {  // every thread has read its rows before they are overwritten
       if (THREADS > 32) __syncthreads(); else __syncwarp();
@@ -468,7 +488,7 @@ gnorm_sums_kernel(int width, int parts, const float* __restrict__ partial, float
 // ------------------------------------------------------------------ long rows
 constexpr int kLong = 1024;
 
-__device__ __forceinline__ float block_sum(float v, float (*red)[1][32], int& turn) {
+__device__ __forceinline__ float block_sum(float v, float (*red)[32], int& turn) {
   float s[1] = {v};
   group_sums<1, kLong>(s, red, turn);
   return s[0];
@@ -483,7 +503,7 @@ __device__ __forceinline__ float new_residual(const GnormRows<T>& p, int64_t row
 }
 
 template <typename T>
-__device__ __forceinline__ float post_norm(const GnormRows<T>& p, int64_t row, float (*red)[1][32],
+__device__ __forceinline__ float post_norm(const GnormRows<T>& p, int64_t row, float (*red)[32],
                                            int& turn) {
   if (!p.w_post) return 1.f;
   float sum = 0.f;
@@ -491,13 +511,13 @@ __device__ __forceinline__ float post_norm(const GnormRows<T>& p, int64_t row, f
     const float v = to_f32(p.f[row * p.ldf + c]);
     sum = fmaf(v, v, sum);
   }
-  return 1.f / sqrtf(fmaf(block_sum(sum, red, turn), 1.f / p.width, p.eps));
+  return inverse_root(fmaf(block_sum(sum, red, turn), 1.f / p.width, p.eps));
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kLong)
 gnorm_long_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, int64_t ldu) {
-  __shared__ float red[2][1][32];
+  __shared__ float red[2][32];
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const float r1 = post_norm(p, row, red, turn);
@@ -508,7 +528,7 @@ gnorm_long_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict_
         const float v = new_residual(p, row, c, r1);
         sum = fmaf(v, v, sum);
       }
-      r2 = 1.f / sqrtf(fmaf(block_sum(sum, red, turn), 1.f / p.width, p.eps));
+      r2 = inverse_root(fmaf(block_sum(sum, red, turn), 1.f / p.width, p.eps));
     }
     for (int c = threadIdx.x; c < p.width; c += kLong) {
       const float v = new_residual(p, row, c, r1);
@@ -521,7 +541,7 @@ gnorm_long_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict_
 template <typename T>
 __global__ void __launch_bounds__(kLong)
 gnorm_long_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ partial) {
-  __shared__ float red[2][1][32];
+  __shared__ float red[2][32];
   int turn = 0;
   const float inv = 1.f / p.width;
   float* part = partial + static_cast<int64_t>(blockIdx.x) * 3 * p.width;
@@ -538,7 +558,7 @@ gnorm_long_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ 
         sum = fmaf(v, v, sum);
         dot = fmaf(to_f32(g.du[row * g.lddu + c]) * p.w_pre[c], v, dot);
       }
-      r2 = 1.f / sqrtf(fmaf(block_sum(sum, red, turn), inv, p.eps));
+      r2 = inverse_root(fmaf(block_sum(sum, red, turn), inv, p.eps));
       back = block_sum(dot, red, turn) * inv * r2 * r2 * r2;
     }
     float dot = 0.f;

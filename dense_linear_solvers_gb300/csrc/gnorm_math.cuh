@@ -2,6 +2,8 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 #include "grec_math.cuh"
@@ -48,32 +50,40 @@ __device__ __forceinline__ int row_element(int t, int k, int e) {
 template <int THREADS, int K, bool ALIGNED>
 constexpr int kStagedRow = (THREADS * K + (ALIGNED ? 0 : 1)) * 16;
 
-// Copies a row into smem, zeros behind its `bytes`. ALIGNED: every thread what it will itself read.
-// row == nullptr: a row of zeros. `base` the operand's first byte: nothing in front is read.
+// Row `row` of an operand (rows and row distances in bytes fit 32 bits, their product need not).
+template <typename T>
+__device__ __forceinline__ T* row_of(T* base, unsigned row, int64_t ld) {
+  using C = typename std::conditional<std::is_const<T>::value, const char, char>::type;
+  return reinterpret_cast<T*>(reinterpret_cast<C*>(base) +
+                              static_cast<uint64_t>(row) *
+                                  (static_cast<unsigned>(ld) * static_cast<unsigned>(sizeof(T))));
+}
+
+// Copies `bytes` of row `row` into smem, zeros behind them (bytes == 0: a row of zeros, nothing is
+// read). ALIGNED: every thread what it will itself read. Nothing in front of the operand is read.
 template <typename T, int THREADS, int K, bool ALIGNED>
-__device__ __forceinline__ void stage_row(char* smem, const char* row, const char* base, int bytes,
-                                          int t) {
+__device__ __forceinline__ void stage_row(char* smem, const T* base, unsigned row, int64_t ld,
+                                          int bytes, int t) {
+  const char* src = reinterpret_cast<const char*>(row_of(base, row, ld));
   if constexpr (ALIGNED) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int at = (k * THREADS + t) * 16;
-      int left = row == nullptr ? 0 : bytes - at;
+      int left = bytes - at;
       left = left < 0 ? 0 : (left > 16 ? 16 : left);
-      cp_async_16(smem + at, left ? row + at : base, left);
+      cp_async_16(smem + at, src + at, left);
     }
   } else {
-    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
-    const char* zero = reinterpret_cast<const char*>(
-        (reinterpret_cast<uintptr_t>(base) + 15) & ~static_cast<uintptr_t>(15));
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
 #pragma unroll
     for (int k = 0; k <= K; ++k) {
       if (k == K && t != 0) break;
       const int piece = k == K ? K * THREADS : k * THREADS + t;
-      const char* from = row - shift + piece * 16;
-      int left = row == nullptr ? 0 : bytes + shift - piece * 16;
+      const char* from = src - shift + piece * 16;
+      int left = bytes == 0 ? 0 : bytes + shift - piece * 16;
       left = left < 0 ? 0 : (left > 16 ? 16 : left);
-      if (left == 0 || from >= base) {
-        cp_async_16(smem + piece * 16, left ? from : zero, left);
+      if (left == 0 || from >= reinterpret_cast<const char*>(base)) {
+        cp_async_16(smem + piece * 16, from, left);
       } else {  // the boundary lies in front of the operand: its first elements one by one
         for (int b = shift; b < 16; b += static_cast<int>(sizeof(T)))
           *reinterpret_cast<T*>(smem + b) =
