@@ -74,6 +74,8 @@ class BsolveError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded libbsolve.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -569,11 +571,14 @@ def bs_getrf_getrs_batched_host_static(A, B, ipiv, info, layout: int = ROW_MAJOR
 
 # --------------------------------------------------------------- row operators
 _ROW_CODES = {}
+_F32 = None
 
 
 def _row_code(dtype) -> int:
+    global _F32
     if not _ROW_CODES:
         import torch
+        _F32 = torch.float32
         _ROW_CODES.update({torch.float32: BS_FP32, torch.bfloat16: BS_BF16,
                            torch.float16: BS_FP16})
     code = _ROW_CODES.get(dtype)
@@ -582,74 +587,95 @@ def _row_code(dtype) -> int:
     return code
 
 
-def _row(t, name: str, like):
-    """(pointer, ld) of a row operand: of like's shape and dtype, on its device, the last stride 1
-    and the rows at one distance (ld elements). None: (0, 0)."""
-    if t is None:
-        return 0, 0
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {like.dtype}")
-    shape, st = t.shape, t.stride()
-    if shape != like.shape:
-        raise ValueError(f"{name}: shape {tuple(shape)}, expected {tuple(like.shape)}")
-    if t.device != like.device or not t.is_cuda:
-        raise ValueError(f"{name}: bsolve operands are device tensors of one device")
+def _rows(dtype, shape, device, named) -> list:
+    """pointer, ld of each row operand (name, tensor) in turn: of this dtype and shape, on this
+    device, the last stride 1 and the rows at one distance (ld elements). None: 0, 0."""
+    out = []
     width = shape[-1]
-    if width > 1 and st[-1] != 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if len(shape) == 2:
-        ld = st[0] if shape[0] > 1 else width
-    else:
-        b, n = shape[0], shape[1]
-        ld = st[1] if n > 1 else (st[0] if b > 1 else width)
-        if b > 1 and n > 1 and st[0] != n * ld:
-            raise ValueError(f"{name}: the rows of all sequences must lie at one distance")
-    if ld < width and t.numel():
-        raise ValueError(f"{name}: rows overlap")
-    return t.data_ptr(), max(ld, width)
+    three = len(shape) == 3
+    for name, t in named:
+        if t is None:
+            out += (0, 0)
+            continue
+        if t.dtype is not dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.get_device() != device or device < 0:
+            raise ValueError(f"{name}: bsolve operands are device tensors of one device")
+        st = t.stride()
+        if width > 1 and st[-1] != 1:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        if three:
+            b, n = shape[0], shape[1]
+            ld = st[1] if n > 1 else (st[0] if b > 1 else width)
+            if b > 1 and n > 1 and st[0] != n * ld:
+                raise ValueError(f"{name}: the rows of all sequences must lie at one distance")
+        else:
+            ld = st[0] if shape[0] > 1 else width
+        if ld < width:
+            if t.numel():
+                raise ValueError(f"{name}: rows overlap")
+            ld = width
+        out += (t.data_ptr(), ld)
+    return out
 
 
-def _vec(t, name: str, like, numel: int, dtype=None) -> int:
+def _vec(t, name: str, device, numel: int, dtype=None) -> int:
     """The pointer of a contiguous operand of numel elements (FP32 unless dtype says otherwise)
-    on like's device. None: 0."""
+    on this device. None: 0."""
     if t is None:
         return 0
-    if dtype is None:
-        import torch
-        dtype = torch.float32
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    want = dtype or _F32
+    if t.dtype is not want:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {want}")
     if t.numel() != numel:
         raise ValueError(f"{name}: {t.numel()} elements, expected {numel}")
-    if t.device != like.device or not t.is_cuda:
+    if t.get_device() != device or device < 0:
         raise ValueError(f"{name}: bsolve operands are device tensors of one device")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
 
 
-def _work(work, like):
+_raw_stream = None
+
+
+def _row_stream(stream, device) -> int:
+    """_stream() without a Stream object where torch offers its handle alone: a third of the small
+    calls' time."""
+    global _raw_stream
+    if stream is not None:
+        return _stream(stream)
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(device)
+
+
+def _work(work, device):
     import torch
     if work is None:
         return 0, 0
-    return _vec(work, "work", like, work.numel(), torch.uint8), work.numel()
+    return _vec(work, "work", device, work.numel(), torch.uint8), work.numel()
 
 
-def _sequences(x, offsets):
+def _sequences(x, offsets, device):
     """(batch, rows, channels, pointer of offsets) of a recurrence call."""
+    shape = x.shape
     if offsets is None:
-        if x.dim() != 3:
-            raise ValueError(f"x: shape {tuple(x.shape)}, expected (batch, length, channels), or "
+        if len(shape) != 3:
+            raise ValueError(f"x: shape {tuple(shape)}, expected (batch, length, channels), or "
                              "(rows, channels) with offsets")
-        batch, length, channels = x.shape
-        return batch, batch * length, channels, 0
+        return shape[0], shape[0] * shape[1], shape[2], 0
     import torch
-    if x.dim() != 2:
-        raise ValueError(f"x: shape {tuple(x.shape)}, expected (rows, channels) with offsets")
+    if len(shape) != 2:
+        raise ValueError(f"x: shape {tuple(shape)}, expected (rows, channels) with offsets")
     if offsets.numel() < 1:
         raise ValueError("offsets: batch + 1 row numbers expected")
-    at = _vec(offsets, "offsets", x, offsets.numel(), torch.int64)
-    return offsets.numel() - 1, x.shape[0], x.shape[1], at
+    at = _vec(offsets, "offsets", device, offsets.numel(), torch.int64)
+    return offsets.numel() - 1, shape[0], shape[1], at
 
 
 def bs_grec_tape_rows(batch: int, rows: int) -> int:
@@ -668,20 +694,20 @@ def bs_grec_batched(x, r, i, lam, h, h0=None, hT=None, offsets=None, tape=None,
     (batch, length, channels), or (rows, channels) with offsets, batch + 1 int64 row numbers;
     h0, hT: (batch, channels) float32; tape: (bs_grec_tape_rows(...), channels) float32, for
     the backward call."""
-    batch, rows, channels, at = _sequences(x, offsets)
-    code = _row_code(x.dtype)
-    px, ldx = _row(x, "x", x)
-    pr, ldr = _row(r, "r", x)
-    pi, ldi = _row(i, "i", x)
-    ph, ldh = _row(h, "h", x)
+    code, dev = _row_code(x.dtype), x.get_device()
+    batch, rows, channels, at = _sequences(x, offsets, dev)
+    px, ldx, pr, ldr, pi, ldi, ph, ldh = _rows(
+        x.dtype, x.shape, dev, (("x", x), ("r", r), ("i", i), ("h", h)))
     L = lib()
     st = L.bs_grec_batched(
         code, channels, batch, rows, at, px, ldx, pr, ldr, pi, ldi,
-        _vec(lam, "lam", x, channels), kappa, _vec(h0, "h0", x, batch * channels), ph, ldh,
-        _vec(hT, "hT", x, batch * channels),
-        0 if tape is None else _vec(tape, "tape", x, L.bs_grec_tape_rows(batch, rows) * channels),
-        _stream(stream))
-    _check(st, "bs_grec_batched")
+        _vec(lam, "lam", dev, channels), kappa, _vec(h0, "h0", dev, batch * channels), ph, ldh,
+        _vec(hT, "hT", dev, batch * channels),
+        0 if tape is None else _vec(tape, "tape", dev,
+                                    L.bs_grec_tape_rows(batch, rows) * channels),
+        _row_stream(stream, dev))
+    if st:
+        _check(st, "bs_grec_batched")
 
 
 def bs_grec_backward_batched(x, r, i, lam, tape, dh, dx, dr, di, dlam, work, dhT=None, dh0=None,
@@ -689,25 +715,22 @@ def bs_grec_backward_batched(x, r, i, lam, tape, dh, dx, dr, di, dlam, work, dhT
     """Gradients of bs_grec_batched from its inputs, its tape and the gradients of h (and hT):
     dx, dr, di, dlam (and dh0) are written (see bsolve.h). work: uint8, at least
     bs_grec_backward_workspace(...) elements."""
-    batch, rows, channels, at = _sequences(x, offsets)
-    code = _row_code(x.dtype)
-    px, ldx = _row(x, "x", x)
-    pr, ldr = _row(r, "r", x)
-    pi, ldi = _row(i, "i", x)
-    pdh, lddh = _row(dh, "dh", x)
-    pdx, lddx = _row(dx, "dx", x)
-    pdr, lddr = _row(dr, "dr", x)
-    pdi, lddi = _row(di, "di", x)
-    pw, nw = _work(work, x)
+    code, dev = _row_code(x.dtype), x.get_device()
+    batch, rows, channels, at = _sequences(x, offsets, dev)
+    px, ldx, pr, ldr, pi, ldi, pdh, lddh, pdx, lddx, pdr, lddr, pdi, lddi = _rows(
+        x.dtype, x.shape, dev, (("x", x), ("r", r), ("i", i), ("dh", dh), ("dx", dx), ("dr", dr),
+                                ("di", di)))
+    pw, nw = _work(work, dev)
     L = lib()
     st = L.bs_grec_backward_batched(
         code, channels, batch, rows, at, px, ldx, pr, ldr, pi, ldi,
-        _vec(lam, "lam", x, channels), kappa,
-        _vec(tape, "tape", x, L.bs_grec_tape_rows(batch, rows) * channels), pdh, lddh,
-        _vec(dhT, "dhT", x, batch * channels), pdx, lddx, pdr, lddr, pdi, lddi,
-        _vec(dlam, "dlam", x, channels), _vec(dh0, "dh0", x, batch * channels), pw, nw,
-        _stream(stream))
-    _check(st, "bs_grec_backward_batched")
+        _vec(lam, "lam", dev, channels), kappa,
+        _vec(tape, "tape", dev, L.bs_grec_tape_rows(batch, rows) * channels), pdh, lddh,
+        _vec(dhT, "dhT", dev, batch * channels), pdx, lddx, pdr, lddr, pdi, lddi,
+        _vec(dlam, "dlam", dev, channels), _vec(dh0, "dh0", dev, batch * channels), pw, nw,
+        _row_stream(stream, dev))
+    if st:
+        _check(st, "bs_grec_backward_batched")
 
 
 def bs_grec_step_batched(x, r, i, lam, state, y, slots=None, kappa: float = 8.0,
@@ -716,21 +739,21 @@ def bs_grec_step_batched(x, r, i, lam, state, y, slots=None, kappa: float = 8.0,
     float32, advances in place and y <- the new states (see bsolve.h). x, r, i, y: (batch,
     channels); slots: batch int32 rows of state, None: row j for sequence j."""
     import torch
-    if x.dim() != 2:
-        raise ValueError(f"x: shape {tuple(x.shape)}, expected (batch, channels)")
-    batch, channels = x.shape
-    if state.dim() != 2 or state.shape[1] != channels:
-        raise ValueError(f"state: shape {tuple(state.shape)}, expected (num_slots, {channels})")
-    code = _row_code(x.dtype)
-    px, ldx = _row(x, "x", x)
-    pr, ldr = _row(r, "r", x)
-    pi, ldi = _row(i, "i", x)
-    py, ldy = _row(y, "y", x)
+    shape, held = x.shape, state.shape
+    if len(shape) != 2:
+        raise ValueError(f"x: shape {tuple(shape)}, expected (batch, channels)")
+    batch, channels = shape
+    if len(held) != 2 or held[1] != channels:
+        raise ValueError(f"state: shape {tuple(held)}, expected (num_slots, {channels})")
+    code, dev = _row_code(x.dtype), x.get_device()
+    px, ldx, pr, ldr, pi, ldi, py, ldy = _rows(
+        x.dtype, shape, dev, (("x", x), ("r", r), ("i", i), ("y", y)))
     st = lib().bs_grec_step_batched(
-        code, channels, batch, px, ldx, pr, ldr, pi, ldi, _vec(lam, "lam", x, channels), kappa,
-        _vec(state, "state", x, state.numel()), state.shape[0],
-        _vec(slots, "slots", x, batch, torch.int32), py, ldy, _stream(stream))
-    _check(st, "bs_grec_step_batched")
+        code, channels, batch, px, ldx, pr, ldr, pi, ldi, _vec(lam, "lam", dev, channels), kappa,
+        _vec(state, "state", dev, held[0] * channels), held[0],
+        _vec(slots, "slots", dev, batch, torch.int32), py, ldy, _row_stream(stream, dev))
+    if st:
+        _check(st, "bs_grec_step_batched")
 
 
 def bs_gnorm_backward_workspace(width: int, rows: int) -> int:
@@ -743,18 +766,16 @@ def bs_gnorm_batched(f, y=None, z=None, x=None, w_post=None, scale=None, w_pre=N
     """y <- x + scale * (f / rms(f) * w_post * act(z)), u <- y / rms(y) * w_pre; every part but f
     and one output optional (see bsolve.h). f, z, x, y, u: (rows, width) or (batch, length,
     width); w_post, scale, w_pre: width float32 elements."""
-    width = f.shape[-1]
-    code = _row_code(f.dtype)
-    pf, ldf = _row(f, "f", f)
-    pz, ldz = _row(z, "z", f)
-    px, ldx = _row(x, "x", f)
-    py, ldy = _row(y, "y", f)
-    pu, ldu = _row(u, "u", f)
+    code, dev, shape = _row_code(f.dtype), f.get_device(), f.shape
+    width = shape[-1]
+    pf, ldf, pz, ldz, px, ldx, py, ldy, pu, ldu = _rows(
+        f.dtype, shape, dev, (("f", f), ("z", z), ("x", x), ("y", y), ("u", u)))
     st = lib().bs_gnorm_batched(
         code, f.numel() // width if width else 0, width, pf, ldf, pz, ldz, px, ldx,
-        _vec(w_post, "w_post", f, width), _vec(scale, "scale", f, width),
-        _vec(w_pre, "w_pre", f, width), eps, gate, py, ldy, pu, ldu, _stream(stream))
-    _check(st, "bs_gnorm_batched")
+        _vec(w_post, "w_post", dev, width), _vec(scale, "scale", dev, width),
+        _vec(w_pre, "w_pre", dev, width), eps, gate, py, ldy, pu, ldu, _row_stream(stream, dev))
+    if st:
+        _check(st, "bs_gnorm_batched")
 
 
 def bs_gnorm_backward_batched(f, dy, df, work=None, z=None, x=None, w_post=None, scale=None,
@@ -764,21 +785,17 @@ def bs_gnorm_backward_batched(f, dy, df, work=None, z=None, x=None, w_post=None,
     """Gradients of bs_gnorm_batched from its inputs and the gradients of y and u (either may be
     None): df and, where given, dz, dx, dw_post, dscale, dw_pre are written (see bsolve.h).
     work: uint8, at least bs_gnorm_backward_workspace(...) elements, for the last three."""
-    width = f.shape[-1]
-    code = _row_code(f.dtype)
-    pf, ldf = _row(f, "f", f)
-    pz, ldz = _row(z, "z", f)
-    px, ldx = _row(x, "x", f)
-    pdy, lddy = _row(dy, "dy", f)
-    pdu, lddu = _row(du, "du", f)
-    pdf, lddf = _row(df, "df", f)
-    pdz, lddz = _row(dz, "dz", f)
-    pdx, lddx = _row(dx, "dx", f)
-    pw, nw = _work(work, f)
+    code, dev, shape = _row_code(f.dtype), f.get_device(), f.shape
+    width = shape[-1]
+    pf, ldf, pz, ldz, px, ldx, pdy, lddy, pdu, lddu, pdf, lddf, pdz, lddz, pdx, lddx = _rows(
+        f.dtype, shape, dev, (("f", f), ("z", z), ("x", x), ("dy", dy), ("du", du), ("df", df),
+                              ("dz", dz), ("dx", dx)))
+    pw, nw = _work(work, dev)
     st = lib().bs_gnorm_backward_batched(
         code, f.numel() // width if width else 0, width, pf, ldf, pz, ldz, px, ldx,
-        _vec(w_post, "w_post", f, width), _vec(scale, "scale", f, width),
-        _vec(w_pre, "w_pre", f, width), eps, gate, pdy, lddy, pdu, lddu, pdf, lddf, pdz, lddz,
-        pdx, lddx, _vec(dw_post, "dw_post", f, width), _vec(dscale, "dscale", f, width),
-        _vec(dw_pre, "dw_pre", f, width), pw, nw, _stream(stream))
-    _check(st, "bs_gnorm_backward_batched")
+        _vec(w_post, "w_post", dev, width), _vec(scale, "scale", dev, width),
+        _vec(w_pre, "w_pre", dev, width), eps, gate, pdy, lddy, pdu, lddu, pdf, lddf, pdz, lddz,
+        pdx, lddx, _vec(dw_post, "dw_post", dev, width), _vec(dscale, "dscale", dev, width),
+        _vec(dw_pre, "dw_pre", dev, width), pw, nw, _row_stream(stream, dev))
+    if st:
+        _check(st, "bs_gnorm_backward_batched")

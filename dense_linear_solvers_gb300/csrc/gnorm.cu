@@ -22,54 +22,73 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kTurns = 2;  // turns of rows in shared memory: this one and the next
 
-// Sums of N (1, 2 or 4) values over a group's threads, the same bits in all of them. While lanes hold
-// several values, a step hands half of them to the lanes across and keeps the other half, so that N
-// values take little more than one value's shuffles. Consecutive calls take the two halves of
-// `red` in turn, so that one barrier a call is enough.
+// Sums of N values (a power of two) over a group's threads, the same bits in all of them. While
+// lanes hold several values, a step hands half of them to the lanes across and keeps the other
+// half, so that N values take few more shuffles than one; then lane part k of a warp holds value k's
+// sum. The warps' sums meet in `red`, [2][WARPS][N] and, behind that, [WARPS][N]; consecutive calls
+// take its two halves in turn, so that one barrier a call is enough.
 template <int N, int THREADS>
-__device__ __forceinline__ void group_sums(float (&v)[N], float (*red)[N * 32], int& turn) {
+constexpr int kRedFloats = THREADS > 32 ? 3 * N * (THREADS / 32) : 1;
+
+template <int N, int THREADS>
+__device__ __forceinline__ void group_sums(float (&v)[N], float* red, int& turn) {
   constexpr int LANES = THREADS < 32 ? THREADS : 32, WARPS = THREADS / LANES;
-  const int lane = threadIdx.x & 31;
   constexpr unsigned kAll = 0xFFFFFFFFu;
-  float s;
-  if constexpr (N == 4) {
-    const bool hi = lane & (LANES / 2), hj = lane & (LANES / 4);
-    float a = hi ? v[2] : v[0], b = hi ? v[3] : v[1];
-    a += __shfl_xor_sync(kAll, hi ? v[0] : v[2], LANES / 2);
-    b += __shfl_xor_sync(kAll, hi ? v[1] : v[3], LANES / 2);
-    s = hj ? b : a;
-    s += __shfl_xor_sync(kAll, hj ? a : b, LANES / 4);
-  } else if constexpr (N == 2) {
-    const bool hi = lane & (LANES / 2);
-    s = hi ? v[1] : v[0];
-    s += __shfl_xor_sync(kAll, hi ? v[0] : v[1], LANES / 2);
+  if constexpr (N > LANES) {  // two halves
+    float a[N / 2], b[N / 2];
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) a[k] = v[k], b[k] = v[k + N / 2];
+    group_sums<N / 2, THREADS>(a, red, turn);
+    group_sums<N / 2, THREADS>(b, red, turn);
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) v[k] = a[k], v[k + N / 2] = b[k];
   } else {
-    s = v[0] + __shfl_xor_sync(kAll, v[0], LANES / 2);
-  }
-  constexpr int EACH = N == 1 ? LANES / 2 : LANES / N;  // lanes that now add up one value
+    const int lane = threadIdx.x & 31;
+    int m = LANES / 2;
 #pragma unroll
-  for (int m = (N == 1 ? LANES / 4 : EACH / 2); m > 0; m >>= 1) s += __shfl_xor_sync(kAll, s, m);
-  if constexpr (WARPS == 1) {
+    for (int n = N / 2; n > 0; n >>= 1, m >>= 1) {
+      const bool high = lane & m;
 #pragma unroll
-    for (int k = 0; k < N; ++k)  // value k sits in the k-th part of the group's lanes
-      v[k] = N == 1 ? s : __shfl_sync(kAll, s, (lane & ~(LANES - 1)) + k * (LANES / N));
-  } else {
-    const int warp = threadIdx.x >> 5;
-    float* r = red[turn];
-    if (lane % (32 / N) == 0) r[lane / (32 / N) * WARPS + warp] = s;
-    __syncthreads();
-    constexpr int LOADS = N * WARPS > 32 ? N * WARPS / 32 : 1, PER = 32 / WARPS;  // values a load
+      for (int k = 0; k < n; ++k) {
+        const float keep = high ? v[k + n] : v[k], give = high ? v[k] : v[k + n];
+        v[k] = keep + __shfl_xor_sync(kAll, give, m);
+      }
+    }
+    float s = v[0];
 #pragma unroll
-    for (int l = 0; l < LOADS; ++l) {
-      s = r[(l * 32 + lane) & (N * WARPS - 1)];
-#pragma unroll
-      for (int m = WARPS / 2; m > 0; m >>= 1) s += __shfl_xor_sync(kAll, s, m);
+    for (; m > 0; m >>= 1) s += __shfl_xor_sync(kAll, s, m);
+    if constexpr (WARPS == 1) {
 #pragma unroll
       for (int k = 0; k < N; ++k)
-        if (LOADS == 1 || k / PER == l)
-          v[k] = N * WARPS <= 32 && N == 1 ? s : __shfl_sync(kAll, s, k % PER * WARPS);
+        v[k] = N == 1 ? s : __shfl_sync(kAll, s, (lane & ~(LANES - 1)) + k * (LANES / N));
+    } else {
+      const int warp = threadIdx.x >> 5;
+      float* r = red + turn * (WARPS * N);
+      turn ^= 1;
+      if (lane % (32 / N) == 0) r[warp * N + lane / (32 / N)] = s;
+      __syncthreads();
+      constexpr int PARTS = 32 / N;  // lanes that add up one value
+      const int value = lane % N, part = lane / N;
+      s = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; w += PARTS)
+        if (WARPS % PARTS == 0 || w + part < WARPS) s += r[(w + part) * N + value];
+#pragma unroll
+      for (int q = N; q < 32; q <<= 1) s += __shfl_xor_sync(kAll, s, q);
+      if constexpr (N <= 2) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = N == 1 ? s : __shfl_sync(kAll, s, k);
+      } else {
+        float* own = red + (2 * WARPS + warp) * N;
+        if (lane < N) own[lane] = s;
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < N; k += 4) {
+          const float4 q = *reinterpret_cast<const float4*>(own + k);
+          v[k] = q.x, v[k + 1] = q.y, v[k + 2] = q.z, v[k + 3] = q.w;
+        }
+      }
     }
-    turn ^= 1;
   }
 }
 
@@ -92,7 +111,7 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
   using G = Group<THREADS>;
   constexpr int H = kVecElements<T> / 2;  // pairs of a vector
   constexpr int kRow = kStagedRow<THREADS, K, ALIGNED>;
-  __shared__ float red[2][ROWS * 32];
+  __shared__ __align__(16) float red[kRedFloats<ROWS, THREADS>];
   extern __shared__ __align__(16) char shared[];
   const int t = threadIdx.x % THREADS, group = threadIdx.x / THREADS;
   char* mine = shared + group * (kTurns * ROWS * 3 * kRow);
@@ -164,8 +183,10 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
         if (p.z) {
           staged_vector<T, THREADS, ALIGNED>(at_row + kRow, low_bits(row_of(p.z, row0 + i, p.ldz)), t,
                                              k, q);
+          float2 act[H], none[H];
+          gate_of<false>(q, p.gate, act, none);
 #pragma unroll
-          for (int e = 0; e < H; ++e) v[i][k][e] = v[i][k][e] * gate_of<false>(q[e], p.gate).act;
+          for (int e = 0; e < H; ++e) v[i][k][e] = v[i][k][e] * act[e];
         }
         if (p.x) {
           staged_vector<T, THREADS, ALIGNED>(at_row + 2 * kRow, low_bits(row_of(p.x, row0 + i, p.ldx)),
@@ -228,8 +249,8 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
   using G = Group<THREADS>;
   constexpr int H = kVecElements<T> / 2;
   constexpr int kRow = kStagedRow<THREADS, K, ALIGNED>;
-  __shared__ float red[2][ROWS * 32];
-  __shared__ float red2[2][2 * ROWS * 32];
+  __shared__ __align__(16) float red[kRedFloats<ROWS, THREADS>];
+  __shared__ __align__(16) float red2[kRedFloats<2 * ROWS, THREADS>];
   extern __shared__ __align__(16) char shared[];
   const int t = threadIdx.x % THREADS, group = threadIdx.x / THREADS;
   char* mine = shared + group * (kTurns * ROWS * 5 * kRow);
@@ -311,8 +332,10 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
           for (int e = 0; e < H; ++e) y[i][k][e] = q[e] * both(r1[i]) * w[e];
           if (p.z) {
             read(1, p.z, p.ldz, i, k, q);
+            float2 act[H], none[H];
+            gate_of<false>(q, p.gate, act, none);
 #pragma unroll
-            for (int e = 0; e < H; ++e) y[i][k][e] = y[i][k][e] * gate_of<false>(q[e], p.gate).act;
+            for (int e = 0; e < H; ++e) y[i][k][e] = y[i][k][e] * act[e];
           }
           if (p.x) {
             read(2, p.x, p.ldx, i, k, q);
@@ -390,17 +413,22 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
       load_params<T, THREADS, ALIGNED>(p.scale, 1.f, t, k, p.width, c);
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
-        float2 f[H], z[H], dz[H];
+        float2 f[H], act[H], slope[H], dz[H];
+        if (p.z) {
+          read(1, p.z, p.ldz, i, k, f);
+          gate_of<true>(f, p.gate, act, slope);
+        } else {
+#pragma unroll
+          for (int e = 0; e < H; ++e) act[e] = both(1.f), slope[e] = both(0.f);
+        }
         read(0, p.f, p.ldf, i, k, f);
-        if (p.z) read(1, p.z, p.ldz, i, k, z);
 #pragma unroll
         for (int e = 0; e < H; ++e) {
-          const Gate q = p.z ? gate_of<true>(z[e], p.gate) : Gate{both(1.f), both(0.f)};
           const float2 n = f[e] * both(r1[i]), nw = n * w[e];
           const float2 d = dn[i][k][e];
-          sc[k][e] = fma2(d * nw, q.act, sc[k][e]);
-          const float2 dt = d * c[e], da = dt * q.act;
-          dz[e] = dt * nw * q.slope;
+          sc[k][e] = fma2(d * nw, act[e], sc[k][e]);
+          const float2 dt = d * c[e], da = dt * act[e];
+          dz[e] = dt * nw * slope[e];
           sw[k][e] = fma2(da, n, sw[k][e]);
           dn[i][k][e] = da * w[e];
           dot[i] = fma2(dn[i][k][e], n, dot[i]);
@@ -488,7 +516,7 @@ gnorm_sums_kernel(int width, int parts, const float* __restrict__ partial, float
 // ------------------------------------------------------------------ long rows
 constexpr int kLong = 1024;
 
-__device__ __forceinline__ float block_sum(float v, float (*red)[32], int& turn) {
+__device__ __forceinline__ float block_sum(float v, float* red, int& turn) {
   float s[1] = {v};
   group_sums<1, kLong>(s, red, turn);
   return s[0];
@@ -498,12 +526,12 @@ template <typename T>
 __device__ __forceinline__ float new_residual(const GnormRows<T>& p, int64_t row, int c, float r1) {
   float t = to_f32(p.f[row * p.ldf + c]);
   if (p.w_post) t = t * r1 * p.w_post[c];
-  if (p.z) t *= gate_of<false>(both(to_f32(p.z[row * p.ldz + c])), p.gate).act.x;
+  if (p.z) t *= gate_of(to_f32(p.z[row * p.ldz + c]), p.gate).act;
   return fmaf(t, p.scale ? p.scale[c] : 1.f, p.x ? to_f32(p.x[row * p.ldx + c]) : 0.f);
 }
 
 template <typename T>
-__device__ __forceinline__ float post_norm(const GnormRows<T>& p, int64_t row, float (*red)[32],
+__device__ __forceinline__ float post_norm(const GnormRows<T>& p, int64_t row, float* red,
                                            int& turn) {
   if (!p.w_post) return 1.f;
   float sum = 0.f;
@@ -517,7 +545,7 @@ __device__ __forceinline__ float post_norm(const GnormRows<T>& p, int64_t row, f
 template <typename T>
 __global__ void __launch_bounds__(kLong)
 gnorm_long_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, int64_t ldu) {
-  __shared__ float red[2][32];
+  __shared__ float red[kRedFloats<1, kLong>];
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const float r1 = post_norm(p, row, red, turn);
@@ -541,7 +569,7 @@ gnorm_long_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict_
 template <typename T>
 __global__ void __launch_bounds__(kLong)
 gnorm_long_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ partial) {
-  __shared__ float red[2][32];
+  __shared__ float red[kRedFloats<1, kLong>];
   int turn = 0;
   const float inv = 1.f / p.width;
   float* part = partial + static_cast<int64_t>(blockIdx.x) * 3 * p.width;
@@ -573,12 +601,11 @@ gnorm_long_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ 
       if (g.dx) g.dx[row * g.lddx + c] = from_f32<T>(d);
       const float n = to_f32(p.f[row * p.ldf + c]) * r1;
       const float w = p.w_post ? p.w_post[c] : 1.f;
-      const Gate q = p.z ? gate_of<true>(both(to_f32(p.z[row * p.ldz + c])), p.gate)
-                         : Gate{both(1.f), both(0.f)};
-      if (g.dscale) part[p.width + c] += d * (n * w) * q.act.x;
+      const Gate q = p.z ? gate_of(to_f32(p.z[row * p.ldz + c]), p.gate) : Gate{1.f, 0.f};
+      if (g.dscale) part[p.width + c] += d * (n * w) * q.act;
       const float dt = p.scale ? d * p.scale[c] : d;
-      if (g.dz) g.dz[row * g.lddz + c] = from_f32<T>(dt * (n * w) * q.slope.x);
-      const float da = dt * q.act.x;
+      if (g.dz) g.dz[row * g.lddz + c] = from_f32<T>(dt * (n * w) * q.slope);
+      const float da = dt * q.act;
       if (g.dw_post) part[c] += da * n;
       dot = fmaf(da * w, n, dot);
     }
@@ -589,7 +616,7 @@ gnorm_long_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ 
         d = fmaf(-new_residual(p, row, c, r1), back,
                  fmaf(to_f32(g.du[row * g.lddu + c]) * p.w_pre[c], r2, d));
       if (p.scale) d *= p.scale[c];
-      if (p.z) d *= gate_of<false>(both(to_f32(p.z[row * p.ldz + c])), p.gate).act.x;
+      if (p.z) d *= gate_of(to_f32(p.z[row * p.ldz + c]), p.gate).act;
       if (p.w_post)
         d = r1 * fmaf(-(to_f32(p.f[row * p.ldf + c]) * r1), mean, d * p.w_post[c]);
       g.df[row * g.lddf + c] = from_f32<T>(d);

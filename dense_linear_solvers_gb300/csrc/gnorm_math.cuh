@@ -12,25 +12,50 @@
 
 namespace bsolve {
 
-// act(z) and its derivative, for two elements; kind: a bs_gate. sigma(z) = 1 / (1 + e^-z),
+// act(z) and its derivative, for H pairs of elements; KIND: a bs_gate. sigma(z) = 1 / (1 + e^-z),
 // 1 - sigma(z) = e^-z sigma(z) with e^-z kept finite there. The approximate exponential and
 // reciprocal are within 2 ulp.
+template <int KIND, bool SLOPE, int H>
+__device__ __forceinline__ void gate_kind(const float2 (&z)[H], float2 (&act)[H], float2 (&slope)[H]) {
+#pragma unroll
+  for (int k = 0; k < H; ++k) {
+    if constexpr (KIND == 2) {
+      act[k] = z[k];
+      slope[k] = both(1.f);
+    } else {
+      float2 e = z[k] * both(-kLog2e);
+      e = make_float2(ex2(e.x), ex2(e.y));
+      float2 s = e + both(1.f);
+      s = make_float2(rcp(s.x), rcp(s.y));
+      act[k] = KIND == 1 ? s : z[k] * s;
+      if constexpr (SLOPE) {
+        const float2 c = make_float2(fminf(e.x, 0x1p126f), fminf(e.y, 0x1p126f)) * s;
+        slope[k] = KIND == 1 ? s * c : fma2(act[k], c, s);
+      }
+    }
+  }
+}
+// The kind's branch once for all of them, so that their instructions interleave.
+template <bool SLOPE, int H>
+__device__ __forceinline__ void gate_of(const float2 (&z)[H], int kind, float2 (&act)[H],
+                                        float2 (&slope)[H]) {
+  if (kind == 0) {
+    gate_kind<0, SLOPE>(z, act, slope);
+  } else if (kind == 1) {
+    gate_kind<1, SLOPE>(z, act, slope);
+  } else {
+    gate_kind<2, SLOPE>(z, act, slope);
+  }
+}
+// One element.
 struct Gate {
-  float2 act, slope;
+  float act, slope;
 };
-
-template <bool SLOPE>
-__device__ __forceinline__ Gate gate_of(float2 z, int kind) {
-  if (kind == 2) return {z, both(1.f)};
-  float2 e = z * both(-kLog2e);
-  e = make_float2(ex2(e.x), ex2(e.y));
-  float2 s = e + both(1.f);
-  s = make_float2(rcp(s.x), rcp(s.y));
-  const float2 zs = z * s;
-  if (!SLOPE) return {kind == 1 ? s : zs, s};
-  const float2 c = make_float2(fminf(e.x, 0x1p126f), fminf(e.y, 0x1p126f)) * s;
-  if (kind == 1) return {s, s * c};
-  return {zs, fma2(zs, c, s)};
+__device__ __forceinline__ Gate gate_of(float z, int kind) {
+  const float2 v[1] = {both(z)};
+  float2 act[1], slope[1];
+  gate_of<true>(v, kind, act, slope);
+  return {act[0].x, slope[0].x};
 }
 
 // A thread's elements of a row, VE of them a vector. ALIGNED: 16-byte vectors, thread t the vectors t,

@@ -41,7 +41,11 @@ struct Pair<__half> {
 };
 
 __device__ __forceinline__ float2 to_f32(float2 v) { return v; }
-__device__ __forceinline__ float2 to_f32(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+// A BF16 number is the upper half of the FP32 number of its value: one shift, one mask.
+__device__ __forceinline__ float2 to_f32(__nv_bfloat162 v) {
+  const unsigned u = *reinterpret_cast<const unsigned*>(&v);
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
 __device__ __forceinline__ float2 to_f32(__half2 v) { return __half22float2(v); }
 
 template <typename T>

@@ -174,9 +174,9 @@ def test_binding_raises():
     with pytest.raises(ValueError, match="state"):
         bs.bs_grec_step_batched(x[0], x[0], x[0], lam, torch.zeros(3, 9), x[0])
     with pytest.raises(TypeError, match="dtype"):
-        bs._row(x.half(), "r", x)
+        bs._rows(x.dtype, x.shape, 0, [("r", x.half())])
     with pytest.raises(ValueError, match="shape"):
-        bs._row(x[:, :9], "r", x)
+        bs._rows(x.dtype, x.shape, 0, [("r", x[:, :9])])
     with pytest.raises(TypeError, match="unsupported"):
         bs.bs_gnorm_batched(x.double(), x)
     with pytest.raises(ValueError, match="device"):
