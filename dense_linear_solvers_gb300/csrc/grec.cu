@@ -249,17 +249,19 @@ cudaError_t launch_forward(const GrecRows<T>& p, const float* lam, float kappa, 
   if (held.status != cudaSuccess) return held.status;
   const int64_t tiles = (p.channels + kTileC - 1) / kTileC;
   const int64_t length = p.offsets ? p.rows / p.batch + 1 : p.length;
-  const int cluster = grec_cluster(held, tiles * p.batch, length, W * kR);
+  const int cluster =
+      W == 4 ? 1 : grec_cluster(held, tiles, p.batch, length, p.offsets != nullptr, W * kR);
   return launch_clusters(kernel, dim3(static_cast<unsigned>(tiles * cluster),
                                       static_cast<unsigned>(p.batch < 65535 ? p.batch : 65535)),
                          32 * W, S::kBytes, cluster, stream, p, lam, kappa, h0, h, ldh,
                          pair_stores(h, ldh), hT, tape);
 }
 
-// Blocks of four warps while the pairs of a sequence and a tile fill the GPU by themselves (152 SMs
-// with three blocks): 64 x 512 rows x 2,048 channels BF16 take 96 us, with eight warps 106.
-// Otherwise eight, which meet less often: one sequence of 65,536 x 4,096 takes 457 us, with
-// four warps 501.
+// Blocks of four warps, without clusters, while the pairs of a sequence and a tile fill the GPU by
+// themselves (152 SMs with three blocks): 64 x 512 rows x 2,048 channels BF16 take 94 us, with eight
+// warps 106; 24 packed prompts of 500 rows on average 60 us, with clusters of two 66. Otherwise
+// eight, which meet less often: one sequence of 65,536 x 4,096 takes 450 us, with four
+// warps 501.
 constexpr int64_t kFourWarpUnits = 3 * 152;
 
 }  // namespace

@@ -312,7 +312,8 @@ cudaError_t launch_backward(const GrecRows<T>& p, const GrecGradRows<T>& g, cons
   static const Held held = held_clusters(kernel, 32 * kWarps, S::kBytes);
   if (held.status != cudaSuccess) return held.status;
   const int64_t length = p.offsets ? p.rows / p.batch + 1 : p.length;
-  const int cluster = grec_cluster(held, tiles_of(p.channels) * p.batch, length, kTapeRows);
+  const int cluster = grec_cluster(held, tiles_of(p.channels), p.batch, length,
+                                   p.offsets != nullptr, kTapeRows);
   *parts = grid_y(p.batch) * cluster;
   return launch_clusters(kernel,
                          dim3(static_cast<unsigned>(tiles_of(p.channels) * cluster),
