@@ -105,12 +105,91 @@ struct Group {
 };
 
 // ------------------------------------------------------------------ forward
-template <typename T, int K, int THREADS, int ROWS, bool ALIGNED>
+// How a call's operands lie. kFull: every operand there, 16-byte bases, row distances and widths; kAligned:
+// 16-byte bases and row distances; kAny.
+enum Mode : int { kFull = 0, kAligned = 1, kAny = 2 };
+
+// One group's thread and its part of a row: VE = 2 H elements a vector, K vectors.
+template <typename T, int H, int K, int THREADS, int ROWS, int MODE>
+struct Part {
+  static constexpr bool kAl = MODE != kAny;
+  static constexpr int VE = 2 * H;
+  // a thread reads its own copies; otherwise its warp's, or (kAny) its block's
+  static constexpr bool kPrivate = kAl && VE * sizeof(T) == 16;
+  static constexpr int kRow = kStagedRow<T, VE * THREADS * K, kAl>;
+
+  // Stages ROWS rows of one operand from row `from`, `distance` apart.
+  static __device__ __forceinline__ void stage(char* to, int distance, const T* base, unsigned from,
+                                               unsigned rows, int64_t ld, int bytes, int t) {
+    if constexpr (MODE == kFull && kPrivate) {
+      const unsigned pitch = static_cast<unsigned>(ld) * static_cast<unsigned>(sizeof(T));
+      if (from + ROWS <= rows) {
+        const char* src = reinterpret_cast<const char*>(base) + t * 16 +
+                          static_cast<uint64_t>(from) * pitch;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            const int at = (k * THREADS + t) * 16;
+            cp_async_16(to + i * distance + at, src + i * static_cast<uint64_t>(pitch) + k * THREADS * 16,
+                        at < bytes ? 16 : 0);
+          }
+        return;
+      }
+    }
+    if (MODE == kFull || base)
+      stage_rows<T, VE, THREADS, K, ROWS, kAl>(to, distance, base, from, rows, ld, bytes, t);
+  }
+
+  // Parameters of vector k; `fill` where the vector is absent, 0 behind the row's end.
+  static __device__ __forceinline__ void params(const float* w, float fill, int t, int k, int width,
+                                                float2 (&v)[H]) {
+    if constexpr (MODE == kFull) {
+      const int at = (k * THREADS + t) * VE;
+      if (at < width) {
+#pragma unroll
+        for (int e = 0; e < H; e += 2) {
+          const float4 q = __ldg(reinterpret_cast<const float4*>(w + at + 2 * e));
+          v[e] = make_float2(q.x, q.y);
+          v[e + 1] = make_float2(q.z, q.w);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < H; ++e) v[e] = both(0.f);
+      }
+    } else {
+      load_params<THREADS, kAl>(w, fill, t, k, width, v);
+    }
+  }
+
+  static __device__ __forceinline__ void store(T* base, unsigned row, int64_t ld, int t, int k,
+                                               int width, const float2 (&v)[H]) {
+    if constexpr (MODE == kFull) {
+      const int at = (k * THREADS + t) * VE;
+      PairVec<T, H> q;
+#pragma unroll
+      for (int e = 0; e < H; ++e) q.p[e] = pair_from_f32<T>(v[e]);
+      if (at < width) *reinterpret_cast<PairVec<T, H>*>(row_of(base + at, row, ld)) = q;
+    } else {
+      store_vector<T, THREADS, kAl>(row_of(base, row, ld), t, k, width, v);
+    }
+  }
+
+  // Waits between copies and reads, and between reads and the copies that overwrite them.
+  static __device__ __forceinline__ void meet() {
+    if constexpr (!kPrivate) {
+      if (!kAl && THREADS > 32) __syncthreads(); else __syncwarp();
+    }
+  }
+};
+
+template <typename T, int H, int K, int THREADS, int ROWS, int MODE>
 __global__ void __launch_bounds__(Group<THREADS>::kBlock, 1024 / Group<THREADS>::kBlock)
 gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, int64_t ldu) {
   using G = Group<THREADS>;
-  constexpr int H = kVecElements<T> / 2;  // pairs of a vector
-  constexpr int kRow = kStagedRow<THREADS, K, ALIGNED>;
+  using P = Part<T, H, K, THREADS, ROWS, MODE>;
+  constexpr int kRow = P::kRow;
+  constexpr bool kAll = MODE == kFull;
   __shared__ __align__(16) float red[kRedFloats<ROWS, THREADS>];
   extern __shared__ __align__(16) char shared[];
   const int t = threadIdx.x % THREADS, group = threadIdx.x / THREADS;
@@ -122,16 +201,14 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
   unsigned row0 = (blockIdx.x * G::kGroups + group) * ROWS;
   int turn = 0;
 
+  auto one = [&](char* to, const T* base, int64_t ld, unsigned from) {
+    P::stage(to, 3 * kRow, base, from, rows, ld, bytes, t);
+  };
   auto stage = [&](unsigned from, int slot) {
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const unsigned row = from + i;
-      char* to = mine + (slot * ROWS + i) * 3 * kRow;
-      const int n = row < rows ? bytes : 0;
-      stage_row<T, THREADS, K, ALIGNED>(to, p.f, row, p.ldf, n, t);
-      if (p.z) stage_row<T, THREADS, K, ALIGNED>(to + kRow, p.z, row, p.ldz, n, t);
-      if (p.x) stage_row<T, THREADS, K, ALIGNED>(to + 2 * kRow, p.x, row, p.ldx, n, t);
-    }
+    char* to = mine + slot * ROWS * 3 * kRow;
+    one(to, p.f, p.ldf, from);
+    one(to + kRow, p.z, p.ldz, from);
+    one(to + 2 * kRow, p.x, p.ldx, from);
     cp_async_commit();
   };
   stage(row0, 0);
@@ -140,22 +217,20 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
   for (unsigned at = blockIdx.x * (G::kGroups * ROWS); at < rows; at += turn_rows, row0 += turn_rows) {
     stage(row0 + turn_rows, slot ^ 1);
     cp_async_wait_group<1>();
-    if (!ALIGNED) {
-      if (THREADS > 32) __syncthreads(); else __syncwarp();
-    }
+    P::meet();
     const char* in = mine + slot * ROWS * 3 * kRow;
     slot ^= 1;
     float r1[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) r1[i] = 1.f;
-    if (p.w_post) {
+    if (kAll || p.w_post) {
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
         float2 sum = both(0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           float2 f[H];
-          staged_vector<T, THREADS, ALIGNED>(in + i * 3 * kRow, low_bits(row_of(p.f, row0 + i, p.ldf)),
+          staged_vector<T, THREADS, P::kAl>(in + i * 3 * kRow, low_bits(row_of(p.f, row0 + i, p.ldf)),
                                              t, k, f);
 #pragma unroll
           for (int e = 0; e < H; ++e) sum = fma2(f[e], f[e], sum);
@@ -171,25 +246,25 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float2 w[H], c[H];
-      load_params<T, THREADS, ALIGNED>(p.w_post, 1.f, t, k, p.width, w);
-      load_params<T, THREADS, ALIGNED>(p.scale, 1.f, t, k, p.width, c);
+      P::params(p.w_post, 1.f, t, k, p.width, w);
+      P::params(p.scale, 1.f, t, k, p.width, c);
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
         const char* at_row = in + i * 3 * kRow;
         float2 q[H];
-        staged_vector<T, THREADS, ALIGNED>(at_row, low_bits(row_of(p.f, row0 + i, p.ldf)), t, k, q);
+        staged_vector<T, THREADS, P::kAl>(at_row, low_bits(row_of(p.f, row0 + i, p.ldf)), t, k, q);
 #pragma unroll
         for (int e = 0; e < H; ++e) v[i][k][e] = q[e] * both(r1[i]) * w[e];
-        if (p.z) {
-          staged_vector<T, THREADS, ALIGNED>(at_row + kRow, low_bits(row_of(p.z, row0 + i, p.ldz)), t,
+        if (kAll || p.z) {
+          staged_vector<T, THREADS, P::kAl>(at_row + kRow, low_bits(row_of(p.z, row0 + i, p.ldz)), t,
                                              k, q);
           float2 act[H], none[H];
           gate_of<false>(q, p.gate, act, none);
 #pragma unroll
           for (int e = 0; e < H; ++e) v[i][k][e] = v[i][k][e] * act[e];
         }
-        if (p.x) {
-          staged_vector<T, THREADS, ALIGNED>(at_row + 2 * kRow, low_bits(row_of(p.x, row0 + i, p.ldx)),
+        if (kAll || p.x) {
+          staged_vector<T, THREADS, P::kAl>(at_row + 2 * kRow, low_bits(row_of(p.x, row0 + i, p.ldx)),
                                              t, k, q);
 #pragma unroll
           for (int e = 0; e < H; ++e) v[i][k][e] = fma2(v[i][k][e], c[e], q[e]);
@@ -206,22 +281,20 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
       for (int k = 0; k < K; ++k) {
 #pragma unroll
         for (int e = 0; e < H; ++e) sum = fma2(v[i][k][e], v[i][k][e], sum);
-        if (y && row0 + i < rows)
-          store_vector<T, THREADS, ALIGNED>(row_of(y, row0 + i, ldy), t, k, p.width, v[i][k]);
+        if ((kAll || y) && row0 + i < rows)
+          P::store(y, row0 + i, ldy, t, k, p.width, v[i][k]);
       }
       r2[i] = sum.x + sum.y;
     }
-    if (!u) {
-      // every thread has read its rows before they are overwritten (a barrier of the sums else)
-      if (!ALIGNED && THREADS > 32) __syncthreads();
-      if (!ALIGNED && THREADS <= 32) __syncwarp();
+    if (!kAll && !u) {
+      P::meet();  // every thread has read its rows before they are overwritten
       continue;
     }
     group_sums<ROWS, THREADS>(r2, red, turn);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float2 w[H];
-      load_params<T, THREADS, ALIGNED>(p.w_pre, 1.f, t, k, p.width, w);
+      P::params(p.w_pre, 1.f, t, k, p.width, w);
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
         const float r = inverse_root(fmaf(r2[i], inv, p.eps));
@@ -229,7 +302,7 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
 #pragma unroll
         for (int e = 0; e < H; ++e) q[e] = v[i][k][e] * (both(r) * w[e]);
         if (row0 + i < rows)
-          store_vector<T, THREADS, ALIGNED>(row_of(u, row0 + i, ldu), t, k, p.width, q);
+          P::store(u, row0 + i, ldu, t, k, p.width, q);
       }
     }
   }
@@ -242,13 +315,14 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
 //   dx = dy + q du w_pre - y q^3 mean(du w_pre y),     dt = dx scale,
 //   dz = dt n w_post act'(z),  dn = dt act(z) w_post,  df = r1 (dn - n mean(dn n)),
 //   dw_pre = sum du y q,  dscale = sum dx t,  dw_post = sum dt act(z) n.
-template <typename T, int K, int THREADS, int ROWS, bool ALIGNED>
+template <typename T, int H, int K, int THREADS, int ROWS, int MODE>
 __global__ void __launch_bounds__(Group<THREADS>::kBlock,
-                                  THREADS >= 512 ? 1 : 512 / Group<THREADS>::kBlock)
+                                  (K * ROWS * H == 8 ? 512 : 1024) / Group<THREADS>::kBlock)
 gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ partial) {
   using G = Group<THREADS>;
-  constexpr int H = kVecElements<T> / 2;
-  constexpr int kRow = kStagedRow<THREADS, K, ALIGNED>;
+  using P = Part<T, H, K, THREADS, ROWS, MODE>;
+  constexpr int kRow = P::kRow;
+  constexpr bool kAll = MODE == kFull;
   __shared__ __align__(16) float red[kRedFloats<ROWS, THREADS>];
   __shared__ __align__(16) float red2[kRedFloats<2 * ROWS, THREADS>];
   extern __shared__ __align__(16) char shared[];
@@ -266,18 +340,16 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
 #pragma unroll
     for (int e = 0; e < H; ++e) sw[k][e] = sc[k][e] = sp[k][e] = both(0.f);
 
+  auto one = [&](char* to, const T* base, int64_t ld, unsigned from) {
+    P::stage(to, 5 * kRow, base, from, rows, ld, bytes, t);
+  };
   auto stage = [&](unsigned from, int slot) {
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const unsigned row = from + i;
-      char* to = mine + (slot * ROWS + i) * 5 * kRow;
-      const int n = row < rows ? bytes : 0;
-      stage_row<T, THREADS, K, ALIGNED>(to, p.f, row, p.ldf, n, t);
-      if (p.z) stage_row<T, THREADS, K, ALIGNED>(to + kRow, p.z, row, p.ldz, n, t);
-      if (p.x) stage_row<T, THREADS, K, ALIGNED>(to + 2 * kRow, p.x, row, p.ldx, n, t);
-      if (g.dy) stage_row<T, THREADS, K, ALIGNED>(to + 3 * kRow, g.dy, row, g.lddy, n, t);
-      if (g.du) stage_row<T, THREADS, K, ALIGNED>(to + 4 * kRow, g.du, row, g.lddu, n, t);
-    }
+    char* to = mine + slot * ROWS * 5 * kRow;
+    one(to, p.f, p.ldf, from);
+    one(to + kRow, p.z, p.ldz, from);
+    one(to + 2 * kRow, p.x, p.ldx, from);
+    one(to + 3 * kRow, g.dy, g.lddy, from);
+    one(to + 4 * kRow, g.du, g.lddu, from);
     cp_async_commit();
   };
   stage(row0, 0);
@@ -285,19 +357,17 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
   for (unsigned at = blockIdx.x * (G::kGroups * ROWS); at < rows; at += turn_rows, row0 += turn_rows) {
     stage(row0 + turn_rows, slot ^ 1);
     cp_async_wait_group<1>();
-    if (!ALIGNED) {
-      if (THREADS > 32) __syncthreads(); else __syncwarp();
-    }
+    P::meet();
     const char* in = mine + slot * ROWS * 5 * kRow;
     slot ^= 1;
-    auto read = [&](int operand, const T* base, int64_t ld, int i, int k, float2* v) {
-      staged_vector<T, THREADS, ALIGNED>(in + (i * 5 + operand) * kRow,
+    auto read = [&](int operand, const T* base, int64_t ld, int i, int k, float2 (&v)[H]) {
+      staged_vector<T, THREADS, P::kAl>(in + (i * 5 + operand) * kRow,
                                          low_bits(row_of(base, row0 + i, ld)), t, k, v);
     };
     float r1[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) r1[i] = 1.f;
-    if (p.w_post) {
+    if (kAll || p.w_post) {
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
         float2 sum = both(0.f);
@@ -318,26 +388,26 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
     float r2[ROWS], back[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) r2[i] = back[i] = 0.f;
-    if (g.du) {
+    if (kAll || g.du) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         float2 w[H], c[H];
-        load_params<T, THREADS, ALIGNED>(p.w_post, 1.f, t, k, p.width, w);
-        load_params<T, THREADS, ALIGNED>(p.scale, 1.f, t, k, p.width, c);
+        P::params(p.w_post, 1.f, t, k, p.width, w);
+        P::params(p.scale, 1.f, t, k, p.width, c);
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
           float2 q[H];
           read(0, p.f, p.ldf, i, k, q);
 #pragma unroll
           for (int e = 0; e < H; ++e) y[i][k][e] = q[e] * both(r1[i]) * w[e];
-          if (p.z) {
+          if (kAll || p.z) {
             read(1, p.z, p.ldz, i, k, q);
             float2 act[H], none[H];
             gate_of<false>(q, p.gate, act, none);
 #pragma unroll
             for (int e = 0; e < H; ++e) y[i][k][e] = y[i][k][e] * act[e];
           }
-          if (p.x) {
+          if (kAll || p.x) {
             read(2, p.x, p.ldx, i, k, q);
 #pragma unroll
             for (int e = 0; e < H; ++e) y[i][k][e] = fma2(y[i][k][e], c[e], q[e]);
@@ -354,7 +424,7 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         float2 w[H];
-        load_params<T, THREADS, ALIGNED>(p.w_pre, 0.f, t, k, p.width, w);
+        P::params(p.w_pre, 0.f, t, k, p.width, w);
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
           float2 q[H];
@@ -386,16 +456,16 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float2 w[H];
-      load_params<T, THREADS, ALIGNED>(p.w_pre, 0.f, t, k, p.width, w);
+      P::params(p.w_pre, 0.f, t, k, p.width, w);
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {  // dn holds dx for now
-        if (g.dy) {
+        if (kAll || g.dy) {
           read(3, g.dy, g.lddy, i, k, dn[i][k]);
         } else {
 #pragma unroll
           for (int e = 0; e < H; ++e) dn[i][k][e] = both(0.f);
         }
-        if (g.du) {
+        if (kAll || g.du) {
           float2 q[H];
           read(4, g.du, g.lddu, i, k, q);
 #pragma unroll
@@ -405,16 +475,16 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
             sp[k][e] = fma2(ur, y[i][k][e], sp[k][e]);
           }
         }
-        if (g.dx && row0 + i < rows)
-          store_vector<T, THREADS, ALIGNED>(row_of(g.dx, row0 + i, g.lddx), t, k, p.width, dn[i][k]);
+        if ((kAll || g.dx) && row0 + i < rows)
+          P::store(g.dx, row0 + i, g.lddx, t, k, p.width, dn[i][k]);
       }
       float2 c[H];
-      load_params<T, THREADS, ALIGNED>(p.w_post, 1.f, t, k, p.width, w);
-      load_params<T, THREADS, ALIGNED>(p.scale, 1.f, t, k, p.width, c);
+      P::params(p.w_post, 1.f, t, k, p.width, w);
+      P::params(p.scale, 1.f, t, k, p.width, c);
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
         float2 f[H], act[H], slope[H], dz[H];
-        if (p.z) {
+        if (kAll || p.z) {
           read(1, p.z, p.ldz, i, k, f);
           gate_of<true>(f, p.gate, act, slope);
         } else {
@@ -433,11 +503,11 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
           dn[i][k][e] = da * w[e];
           dot[i] = fma2(dn[i][k][e], n, dot[i]);
         }
-        if (g.dz && row0 + i < rows)
-          store_vector<T, THREADS, ALIGNED>(row_of(g.dz, row0 + i, g.lddz), t, k, p.width, dz);
+        if ((kAll || g.dz) && row0 + i < rows)
+          P::store(g.dz, row0 + i, g.lddz, t, k, p.width, dz);
       }
     }
-    if (p.w_post) {
+    if (kAll || p.w_post) {
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) mean[i] = dot[i].x + dot[i].y;
       group_sums<ROWS, THREADS>(mean, red, turn);
@@ -446,7 +516,7 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
-        if (p.w_post) {  // r1 (dn - f r1 mean)
+        if (kAll || p.w_post) {  // r1 (dn - f r1 mean)
           float2 f[H];
           read(0, p.f, p.ldf, i, k, f);
           const float m = -r1[i] * (mean[i] * inv);
@@ -455,11 +525,9 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
             dn[i][k][e] = both(r1[i]) * fma2(f[e], both(m), dn[i][k][e]);
         }
         if (row0 + i < rows)
-          store_vector<T, THREADS, ALIGNED>(row_of(g.df, row0 + i, g.lddf), t, k, p.width, dn[i][k]);
+          P::store(g.df, row0 + i, g.lddf, t, k, p.width, dn[i][k]);
       }
-    if (!ALIGNED) {  // every thread has read its rows before they are overwritten
-      if (THREADS > 32) __syncthreads(); else __syncwarp();
-    }
+    P::meet();  // every thread has read its rows before they are overwritten
   }
   cp_async_wait_all();
   if (!partial) return;
@@ -471,7 +539,7 @@ gnorm_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ parti
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int e = 0; e < 2 * H; ++e) {
-        const int c = row_element<T, THREADS, ALIGNED>(t, k, e);
+        const int c = row_element<2 * H, THREADS, P::kAl>(t, k, e);
         float sum = e % 2 ? v[k][e / 2].y : v[k][e / 2].x;
         if constexpr (G::kGroups > 1) {
           __syncthreads();
@@ -626,123 +694,147 @@ gnorm_long_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ 
 
 // ------------------------------------------------------------------ launches
 
-// Threads of a row, from the 16-byte vectors it has: the fewest with one vector each, 8 at least; two
-// vectors each for the longest; 0: the looped kernels.
+// Threads of a row, vectors a thread and rows a turn; threads == 0: the looped kernels.
 struct Shape {
-  int threads, vectors;
+  int threads, vectors, rows;
 };
 
-Shape shape_of(int width, int vec) {
-  const int n = (width + vec - 1) / vec;
-  for (int threads = 8; threads <= 1024; threads *= 2)
-    if (n <= threads) return {threads, 1};
-  return n <= 2048 ? Shape{1024, 2} : Shape{0, 0};
+// Forward, with 16-byte vectors: the fewest threads with one each, 8 at least, two rows a turn; one row
+// for blocks of 1024 threads, two vectors each for the longest rows.
+Shape forward_shape(int width, int es) {
+  const int n = (width * es + 15) / 16;
+  for (int threads = 8; threads <= 512; threads *= 2)
+    if (n <= threads) return {threads, 1, 2};
+  if (n <= 1024) return {1024, 1, 1};
+  return n <= 2048 ? Shape{1024, 2, 1} : Shape{0, 0, 1};
+}
+
+// Backward. 16 bits: 16-byte vectors, two rows a turn, which 128 registers a thread hold, 16 warps an
+// SM: what a turn costs beside its elements is then spread over 16 of them. FP32: one row a turn
+// with 64 registers and 32 warps, for which shared memory has room. Rows of more than 4096
+// elements: 1024 threads, in 16 bits with two vectors of four elements each.
+Shape backward_shape(int width, int es) {
+  const int n = (width * es + 15) / 16, rows = es == 2 ? 2 : 1;
+  for (int threads = 8; threads <= 512; threads *= 2)
+    if (n <= threads) return {threads, 1, rows};
+  return n <= 1024 ? Shape{1024, es == 2 ? 2 : 1, 1} : Shape{0, 0, 1};
 }
 
 int block_of(const Shape& s) { return s.threads == 0 ? kLong : (s.threads <= 32 ? 128 : s.threads); }
 
-// Rows a block takes in a turn: two a group, one where a block has 1024 threads and 64 registers
-// each (or, looping, none to spare).
-int turn_rows(const Shape& s) {
-  return s.threads == 0 || s.threads == 1024 ? 1 : 2 * block_of(s) / s.threads;
-}
-
-// Persistent blocks: what the GPU holds of `threads` threads an SM, or what the rows need.
-int blocks_for(const Shape& s, int64_t rows, int threads) {
-  const int64_t need = (rows + turn_rows(s) - 1) / turn_rows(s);
-  const int64_t held = kSms * (threads > block_of(s) ? threads / block_of(s) : 1);
+// Persistent blocks: what the GPU holds with 1024 threads an SM, or what the rows need.
+int blocks_for(const Shape& s, int64_t rows, int threads = 1024) {
+  const int64_t turn = s.threads == 0 ? 1 : s.rows * (block_of(s) / s.threads);
+  const int64_t need = (rows + turn - 1) / turn;
+  const int64_t held = static_cast<int64_t>(kSms) * (threads / block_of(s));
   return static_cast<int>(need < held ? need : held);
 }
 
-constexpr int kForwardThreads = 1024, kBackwardThreads = 512;  // of an SM
-
-int backward_blocks(int width, int vec, int64_t rows) {
-  return blocks_for(shape_of(width, vec), rows, kBackwardThreads);
+int backward_blocks(int width, int es, int64_t rows) {
+  const Shape s = backward_shape(width, es);
+  return blocks_for(s, rows, s.rows == 2 ? 512 : 1024);
 }
 
 bool vec16(const void* p, int64_t bytes) {
   return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(bytes)) & 15) == 0;
 }
 
-// Calls f with (vectors, threads, rows of a group) as compile-time values.
-template <int K, int THREADS, int ROWS>
+// Calls f with a shape as compile-time values.
+template <int PAIRS, int K, int THREADS, int ROWS>
 struct Config {
-  static constexpr int vectors = K, threads = THREADS, rows = ROWS;
+  static constexpr int pairs = PAIRS, vectors = K, threads = THREADS, rows = ROWS;
 };
-template <typename F>
-cudaError_t with_shape(const Shape& s, F&& f) {
-  switch (s.threads) {
-    case 8: return f(Config<1, 8, 2>());
-    case 16: return f(Config<1, 16, 2>());
-    case 32: return f(Config<1, 32, 2>());
-    case 64: return f(Config<1, 64, 2>());
-    case 128: return f(Config<1, 128, 2>());
-    case 256: return f(Config<1, 256, 2>());
-    case 512: return f(Config<1, 512, 2>());
-    default: return s.vectors == 1 ? f(Config<1, 1024, 1>()) : f(Config<2, 1024, 1>());
+template <int PAIRS, int ROWS, typename F>
+cudaError_t with_threads(int threads, F&& f) {
+  switch (threads) {
+    case 8: return f(Config<PAIRS, 1, 8, ROWS>());
+    case 16: return f(Config<PAIRS, 1, 16, ROWS>());
+    case 32: return f(Config<PAIRS, 1, 32, ROWS>());
+    case 64: return f(Config<PAIRS, 1, 64, ROWS>());
+    case 128: return f(Config<PAIRS, 1, 128, ROWS>());
+    case 256: return f(Config<PAIRS, 1, 256, ROWS>());
+    default: return f(Config<PAIRS, 1, 512, ROWS>());
   }
 }
 
-template <typename T, bool ALIGNED>
+template <typename T, int MODE>
 cudaError_t launch_forward(const Shape& s, const GnormRows<T>& p, T* y, int64_t ldy, T* u,
                            int64_t ldu, cudaStream_t stream) {
-  return with_shape(s, [&](auto c) {
+  constexpr int H = kVecElements<T> / 2;
+  auto run = [&](auto c) {
     using C = decltype(c);
-    constexpr int kShared = Group<C::threads>::kGroups * kTurns * C::rows * 3 *
-                            kStagedRow<C::threads, C::vectors, ALIGNED>;
-    auto* kernel = gnorm_kernel<T, C::vectors, C::threads, C::rows, ALIGNED>;
+    using P = Part<T, H, C::vectors, C::threads, C::rows, MODE>;
+    constexpr int kShared = Group<C::threads>::kGroups * kTurns * C::rows * 3 * P::kRow;
+    auto* kernel = gnorm_kernel<T, H, C::vectors, C::threads, C::rows, MODE>;
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
     if (e != cudaSuccess) return e;
-    kernel<<<blocks_for(s, p.rows, kForwardThreads), Group<C::threads>::kBlock, kShared, stream>>>(
-        p, y, ldy, u, ldu);
+    kernel<<<blocks_for(s, p.rows), Group<C::threads>::kBlock, kShared, stream>>>(p, y, ldy, u, ldu);
     return cudaGetLastError();
-  });
+  };
+  if (s.threads < 1024) return with_threads<H, 2>(s.threads, run);
+  return s.vectors == 1 ? run(Config<H, 1, 1024, 1>()) : run(Config<H, 2, 1024, 1>());
 }
 
-template <typename T, bool ALIGNED>
+template <typename T, int MODE>
 cudaError_t launch_backward(const Shape& s, const GnormRows<T>& p, const GnormGrads<T>& g,
                             float* partial, int parts, cudaStream_t stream) {
-  return with_shape(s, [&](auto c) {
+  auto run = [&](auto c) {
     using C = decltype(c);
-    constexpr int kShared = Group<C::threads>::kGroups * kTurns * C::rows * 5 *
-                            kStagedRow<C::threads, C::vectors, ALIGNED>;
-    if constexpr (kShared > 227 * 1024 - 4096) {
-      // two vectors a thread and five operands do not fit: the looped kernel takes those rows
-      gnorm_long_backward_kernel<T><<<parts, kLong, 0, stream>>>(p, g, partial);
-    } else {
-      auto* kernel = gnorm_backward_kernel<T, C::vectors, C::threads, C::rows, ALIGNED>;
-      const cudaError_t e =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
-      if (e != cudaSuccess) return e;
-      kernel<<<parts, Group<C::threads>::kBlock, kShared, stream>>>(p, g, partial);
-    }
+    using P = Part<T, C::pairs, C::vectors, C::threads, C::rows, MODE>;
+    constexpr int kShared = Group<C::threads>::kGroups * kTurns * C::rows * 5 * P::kRow;
+    auto* kernel = gnorm_backward_kernel<T, C::pairs, C::vectors, C::threads, C::rows, MODE>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+    if (e != cudaSuccess) return e;
+    kernel<<<parts, Group<C::threads>::kBlock, kShared, stream>>>(p, g, partial);
     return cudaGetLastError();
-  });
+  };
+  constexpr int H = kVecElements<T> / 2;
+  if (s.threads < 1024) return with_threads<H, sizeof(T) == 2 ? 2 : 1>(s.threads, run);
+  return run(Config<2, sizeof(T) == 2 ? 2 : 1, 1024, 1>());
 }
+
+// Whether an operand is there (or need not be) and lies on 16-byte boundaries.
+template <typename T>
+struct Lies {
+  bool all = true, aligned = true;
+  template <typename V>
+  Lies& with(const V* p, int64_t ld) {
+    all = all && p != nullptr;
+    aligned = aligned && vec16(p, ld * static_cast<int64_t>(sizeof(V)));
+    return *this;
+  }
+  Mode mode(int width) const {
+    if (!aligned) return kAny;
+    return all && width * sizeof(T) % 16 == 0 ? kFull : kAligned;
+  }
+};
 
 }  // namespace
 
 size_t gnorm_backward_workspace(int width, int64_t rows) {
-  // 16-bit rows have the fewest vectors; the larger of the two types' needs
-  const int a = backward_blocks(width, 8, rows), b = backward_blocks(width, 4, rows);
+  // the larger of the two element sizes' needs
+  const int a = backward_blocks(width, 2, rows), b = backward_blocks(width, 4, rows);
   return static_cast<size_t>(a > b ? a : b) * 3 * width * sizeof(float);
 }
 
 template <typename T>
 cudaError_t launch_gnorm(const GnormRows<T>& p, T* y, int64_t ldy, T* u, int64_t ldu,
                          cudaStream_t stream) {
-  const Shape s = shape_of(p.width, kVecElements<T>);
-  const int64_t es = sizeof(T);
+  const Shape s = forward_shape(p.width, sizeof(T));
   if (s.threads == 0) {
     gnorm_long_kernel<T><<<blocks_for(s, p.rows, 2 * kLong), kLong, 0, stream>>>(p, y, ldy, u, ldu);
     return cudaGetLastError();
   }
-  const bool aligned = vec16(p.f, p.ldf * es) && vec16(p.z, p.ldz * es) && vec16(p.x, p.ldx * es) &&
-                       vec16(y, ldy * es) && vec16(u, ldu * es) && vec16(p.w_post, 0) &&
-                       vec16(p.scale, 0) && vec16(p.w_pre, 0);
-  return aligned ? launch_forward<T, true>(s, p, y, ldy, u, ldu, stream)
-                 : launch_forward<T, false>(s, p, y, ldy, u, ldu, stream);
+  const Mode mode = Lies<T>()
+                        .with(p.f, p.ldf).with(p.z, p.ldz).with(p.x, p.ldx).with(y, ldy)
+                        .with(u, ldu).with(p.w_post, 0).with(p.scale, 0).with(p.w_pre, 0)
+                        .mode(p.width);
+  auto* launch = mode == kFull      ? launch_forward<T, kFull>
+                 : mode == kAligned ? launch_forward<T, kAligned>
+                                    : launch_forward<T, kAny>;
+  return launch(s, p, y, ldy, u, ldu, stream);
 }
 
 template <typename T>
@@ -750,22 +842,24 @@ cudaError_t launch_gnorm_backward(const GnormRows<T>& p, const GnormGrads<T>& g,
                                   cudaStream_t stream) {
   const bool sums = g.dw_post || g.dscale || g.dw_pre;
   float* partial = sums ? static_cast<float*>(work) : nullptr;
-  const Shape s = shape_of(p.width, kVecElements<T>);
-  const int parts = backward_blocks(p.width, kVecElements<T>, p.rows);
-  const int64_t es = sizeof(T);
+  const Shape s = backward_shape(p.width, sizeof(T));
+  const int parts = backward_blocks(p.width, sizeof(T), p.rows);
   if (parts > 0) {
     cudaError_t e;
     if (s.threads == 0) {
       gnorm_long_backward_kernel<T><<<parts, kLong, 0, stream>>>(p, g, partial);
       e = cudaGetLastError();
     } else {
-      const bool aligned =
-          vec16(p.f, p.ldf * es) && vec16(p.z, p.ldz * es) && vec16(p.x, p.ldx * es) &&
-          vec16(g.dy, g.lddy * es) && vec16(g.du, g.lddu * es) && vec16(g.df, g.lddf * es) &&
-          vec16(g.dz, g.lddz * es) && vec16(g.dx, g.lddx * es) && vec16(p.w_post, 0) &&
-          vec16(p.scale, 0) && vec16(p.w_pre, 0);
-      e = aligned ? launch_backward<T, true>(s, p, g, partial, parts, stream)
-                  : launch_backward<T, false>(s, p, g, partial, parts, stream);
+      const Mode mode = Lies<T>()
+                            .with(p.f, p.ldf).with(p.z, p.ldz).with(p.x, p.ldx)
+                            .with(g.dy, g.lddy).with(g.du, g.lddu).with(g.df, g.lddf)
+                            .with(g.dz, g.lddz).with(g.dx, g.lddx).with(p.w_post, 0)
+                            .with(p.scale, 0).with(p.w_pre, 0)
+                            .mode(p.width);
+      auto* launch = mode == kFull      ? launch_backward<T, kFull>
+                     : mode == kAligned ? launch_backward<T, kAligned>
+                                        : launch_backward<T, kAny>;
+      e = launch(s, p, g, partial, parts, stream);
     }
     if (e != cudaSuccess) return e;
   }

@@ -58,22 +58,21 @@ __device__ __forceinline__ Gate gate_of(float z, int kind) {
   return {act[0].x, slope[0].x};
 }
 
-// A thread's elements of a row, VE of them a vector. ALIGNED: 16-byte vectors, thread t the vectors t,
+// A thread's elements of a row, VE of them a vector. ALIGNED: whole vectors, thread t the vectors t,
 // t + threads, ...; otherwise single elements, t, t + threads, ..., so that a warp's stores are
 // still one stretch.
 template <typename T>
 constexpr int kVecElements = 16 / static_cast<int>(sizeof(T));
 
-template <typename T, int THREADS, bool ALIGNED>
+template <int VE, int THREADS, bool ALIGNED>
 __device__ __forceinline__ int row_element(int t, int k, int e) {
-  constexpr int VE = kVecElements<T>;
   return ALIGNED ? (k * THREADS + t) * VE + e : (k * VE + e) * THREADS + t;
 }
 
-// Bytes that a row takes in shared memory. Where it is not aligned it is staged from the 16-byte
-// boundary at or below its first element, one piece more.
-template <int THREADS, int K, bool ALIGNED>
-constexpr int kStagedRow = (THREADS * K + (ALIGNED ? 0 : 1)) * 16;
+// Bytes that a row of `elements` takes in shared memory. Where it is not aligned it is staged from the
+// 16-byte boundary at or below its first element, one piece more.
+template <typename T, int ELEMENTS, bool ALIGNED>
+constexpr int kStagedRow = ELEMENTS * static_cast<int>(sizeof(T)) + (ALIGNED ? 0 : 16);
 
 // Row `row` of an operand (rows and row distances in bytes fit 32 bits, their product need not).
 template <typename T>
@@ -84,80 +83,97 @@ __device__ __forceinline__ T* row_of(T* base, unsigned row, int64_t ld) {
                                   (static_cast<unsigned>(ld) * static_cast<unsigned>(sizeof(T))));
 }
 
-// Copies `bytes` of row `row` into smem, zeros behind them (bytes == 0: a row of zeros, nothing is
-// read). ALIGNED: every thread what it will itself read. Nothing in front of the operand is read.
-template <typename T, int THREADS, int K, bool ALIGNED>
-__device__ __forceinline__ void stage_row(char* smem, const T* base, unsigned row, int64_t ld,
-                                          int bytes, int t) {
+// Copies piece `piece` (16 bytes) of the first `bytes` of a row into smem, zeros behind them (bytes ==
+// 0: a row of zeros, nothing is read). Nothing in front of the operand is read.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void stage_piece(char* smem, const T* base, unsigned row, int64_t ld,
+                                            int bytes, int piece) {
   const char* src = reinterpret_cast<const char*>(row_of(base, row, ld));
-  if constexpr (ALIGNED) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int at = (k * THREADS + t) * 16;
-      int left = bytes - at;
-      left = left < 0 ? 0 : (left > 16 ? 16 : left);
-      cp_async_16(smem + at, src + at, left);
-    }
-  } else {
-    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
-#pragma unroll
-    for (int k = 0; k <= K; ++k) {
-      if (k == K && t != 0) break;
-      const int piece = k == K ? K * THREADS : k * THREADS + t;
-      const char* from = src - shift + piece * 16;
-      int left = bytes == 0 ? 0 : bytes + shift - piece * 16;
-      left = left < 0 ? 0 : (left > 16 ? 16 : left);
-      if (left == 0 || from >= reinterpret_cast<const char*>(base)) {
-        cp_async_16(smem + piece * 16, from, left);
-      } else {  // the boundary lies in front of the operand: its first elements one by one
-        for (int b = shift; b < 16; b += static_cast<int>(sizeof(T)))
-          *reinterpret_cast<T*>(smem + b) =
-              b < shift + bytes ? *reinterpret_cast<const T*>(from + b) : from_f32<T>(0.f);
-      }
-    }
+  const int shift = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
+  const char* from = src - shift + piece * 16;
+  int left = bytes == 0 ? 0 : bytes + shift - piece * 16;
+  left = left < 0 ? 0 : (left > 16 ? 16 : left);
+  if (ALIGNED || left == 0 || from >= reinterpret_cast<const char*>(base)) {
+    cp_async_16(smem + piece * 16, from, left);
+  } else {  // the boundary lies in front of the operand: its first elements one by one
+    for (int b = shift; b < 16; b += static_cast<int>(sizeof(T)))
+      *reinterpret_cast<T*>(smem + b) =
+          b < shift + bytes ? *reinterpret_cast<const T*>(from + b) : from_f32<T>(0.f);
   }
 }
 
-// The thread's vector k of a staged row in FP32; `row` the row's address (its low bits are used).
-template <typename T, int THREADS, bool ALIGNED>
-__device__ __forceinline__ void staged_vector(const char* smem, unsigned row, int t, int k,
-                                              float2* v) {
-  constexpr int VE = kVecElements<T>;
-  using P = typename Pair<T>::type;
-  if constexpr (ALIGNED) {
-    struct alignas(16) Vec {
-      P p[VE / 2];
-    };
-    const Vec q = *reinterpret_cast<const Vec*>(smem + (k * THREADS + t) * 16);
+// Stages one operand's ROWS rows for a group of threads, VE elements a thread and vector, row i at
+// smem + i * distance. The threads that share a 16-byte piece of a row (two where a vector has 8
+// bytes) take one row's each, so that with ALIGNED data a thread reads what its own warp copied.
+template <typename T, int VE, int THREADS, int K, int ROWS, bool ALIGNED>
+__device__ __forceinline__ void stage_rows(char* smem, int distance, const T* base, unsigned row0,
+                                           unsigned rows, int64_t ld, int bytes, int t) {
+  constexpr int kShare = 16 / (VE * static_cast<int>(sizeof(T)));  // threads of a piece: 1 or 2
+  constexpr int kPieces = THREADS * K / kShare;                    // of a row
+  static_assert(kShare == 1 || ROWS == 2 || K == 2, "a thread for every piece");
+  if constexpr (kShare == 1) {
 #pragma unroll
-    for (int e = 0; e < VE / 2; ++e) v[e] = to_f32(q.p[e]);
+    for (int i = 0; i < ROWS; ++i) {
+      const int n = row0 + i < rows ? bytes : 0;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        stage_piece<T, ALIGNED>(smem + i * distance, base, row0 + i, ld, n, k * THREADS + t);
+      if (!ALIGNED && t == 0)
+        stage_piece<T, ALIGNED>(smem + i * distance, base, row0 + i, ld, n, kPieces);
+    }
+  } else {
+    // ROWS == 2: the even thread row 0, the odd one row 1; one row: each the half of its vectors
+    const int i = ROWS == 2 ? t & 1 : 0;
+    const int n = row0 + i < rows ? bytes : 0;
+#pragma unroll
+    for (int k = 0; k < (ROWS == 2 ? K : K / 2); ++k) {
+      const int v = ROWS == 2 ? k : 2 * k + (t & 1);
+      stage_piece<T, ALIGNED>(smem + i * distance, base, row0 + i, ld, n, (v * THREADS + t) / 2);
+    }
+    if (!ALIGNED && t < ROWS)
+      stage_piece<T, ALIGNED>(smem + i * distance, base, row0 + i, ld, n, kPieces);
+  }
+}
+
+// H pairs of elements as stored.
+template <typename T, int H>
+struct alignas(sizeof(T) * 2 * H) PairVec {
+  typename Pair<T>::type p[H];
+};
+
+// The thread's vector k of a staged row in FP32; `row` the row's address (its low bits are used).
+template <typename T, int THREADS, bool ALIGNED, int H>
+__device__ __forceinline__ void staged_vector(const char* smem, unsigned row, int t, int k,
+                                              float2 (&v)[H]) {
+  if constexpr (ALIGNED) {
+    const auto q = *reinterpret_cast<const PairVec<T, H>*>(
+        smem + (k * THREADS + t) * static_cast<int>(sizeof(PairVec<T, H>)));
+#pragma unroll
+    for (int e = 0; e < H; ++e) v[e] = to_f32(q.p[e]);
   } else {
     const T* at = reinterpret_cast<const T*>(smem + (row & 15u));
 #pragma unroll
-    for (int e = 0; e < VE / 2; ++e)
-      v[e] = make_float2(to_f32(at[row_element<T, THREADS, false>(t, k, 2 * e)]),
-                         to_f32(at[row_element<T, THREADS, false>(t, k, 2 * e + 1)]));
+    for (int e = 0; e < H; ++e)
+      v[e] = make_float2(to_f32(at[row_element<2 * H, THREADS, false>(t, k, 2 * e)]),
+                         to_f32(at[row_element<2 * H, THREADS, false>(t, k, 2 * e + 1)]));
   }
 }
 
-template <typename T, int THREADS, bool ALIGNED>
-__device__ __forceinline__ void store_vector(T* row, int t, int k, int width, const float2* v) {
-  constexpr int VE = kVecElements<T>;
-  using P = typename Pair<T>::type;
-  const int at = row_element<T, THREADS, ALIGNED>(t, k, 0);
-  struct alignas(16) Vec {
-    P p[VE / 2];
-  } q;
+template <typename T, int THREADS, bool ALIGNED, int H>
+__device__ __forceinline__ void store_vector(T* row, int t, int k, int width,
+                                             const float2 (&v)[H]) {
+  const int at = row_element<2 * H, THREADS, ALIGNED>(t, k, 0);
+  PairVec<T, H> q;
 #pragma unroll
-  for (int e = 0; e < VE / 2; ++e) q.p[e] = pair_from_f32<T>(v[e]);
-  if (ALIGNED && at + VE <= width) {
-    *reinterpret_cast<Vec*>(row + at) = q;
+  for (int e = 0; e < H; ++e) q.p[e] = pair_from_f32<T>(v[e]);
+  if (ALIGNED && at + 2 * H <= width) {
+    *reinterpret_cast<PairVec<T, H>*>(row + at) = q;
     return;
   }
 #pragma unroll
-  for (int e = 0; e < VE / 2; ++e) {
-    const int c = row_element<T, THREADS, ALIGNED>(t, k, 2 * e),
-              d = row_element<T, THREADS, ALIGNED>(t, k, 2 * e + 1);
+  for (int e = 0; e < H; ++e) {
+    const int c = row_element<2 * H, THREADS, ALIGNED>(t, k, 2 * e),
+              d = row_element<2 * H, THREADS, ALIGNED>(t, k, 2 * e + 1);
     if (c < width) row[c] = q.p[e].x;
     if (d < width) row[d] = q.p[e].y;
   }
@@ -165,14 +181,13 @@ __device__ __forceinline__ void store_vector(T* row, int t, int k, int width, co
 
 // The vector's parameters (`fill` where they are absent, 0 behind the row's end); they stay in the
 // first cache level over the rows that a block walks.
-template <typename T, int THREADS, bool ALIGNED>
+template <int THREADS, bool ALIGNED, int H>
 __device__ __forceinline__ void load_params(const float* w, float fill, int t, int k, int width,
-                                            float2* v) {
-  constexpr int VE = kVecElements<T>;
-  const int at = row_element<T, THREADS, ALIGNED>(t, k, 0);
-  if (ALIGNED && w != nullptr && at + VE <= width) {
+                                            float2 (&v)[H]) {
+  const int at = row_element<2 * H, THREADS, ALIGNED>(t, k, 0);
+  if (ALIGNED && w != nullptr && at + 2 * H <= width) {
 #pragma unroll
-    for (int e = 0; e < VE / 2; e += 2) {
+    for (int e = 0; e < H; e += 2) {
       const float4 q = __ldg(reinterpret_cast<const float4*>(w + at + 2 * e));
       v[e] = make_float2(q.x, q.y);
       v[e + 1] = make_float2(q.z, q.w);
@@ -180,9 +195,9 @@ __device__ __forceinline__ void load_params(const float* w, float fill, int t, i
     return;
   }
 #pragma unroll
-  for (int e = 0; e < VE / 2; ++e) {
-    const int c = row_element<T, THREADS, ALIGNED>(t, k, 2 * e),
-              d = row_element<T, THREADS, ALIGNED>(t, k, 2 * e + 1);
+  for (int e = 0; e < H; ++e) {
+    const int c = row_element<2 * H, THREADS, ALIGNED>(t, k, 2 * e),
+              d = row_element<2 * H, THREADS, ALIGNED>(t, k, 2 * e + 1);
     v[e].x = w == nullptr ? fill : (c < width ? __ldg(w + c) : 0.f);
     v[e].y = w == nullptr ? fill : (d < width ? __ldg(w + d) : 0.f);
   }
