@@ -25,7 +25,8 @@ LIB_SOURCES = ["api.cu", "lu_reg.cu", "lu_reg_f32_row.cu", "lu_reg_f32_col.cu", 
                "lu_reg_f64_col.cu", "lu_reg_il_f32_row.cu", "lu_reg_il_f32_col.cu", "lu_reg_il_f64_row.cu",
                "lu_reg_il_f64_col.cu", "lu_rows2.cu", "lu_cta.cu",
                "smem_solvers.cu", "chol_sys.cu", "chol_cluster.cu", "bdsv.cu", "bdmv.cu", "solve.cu",
-               "solve_lane.cu", "api_rows.cu", "grec.cu", "grec_bwd.cu", "gnorm.cu"]
+               "solve_lane.cu", "api_rows.cu", "grec.cu", "grec_bwd.cu", "gnorm.cu",
+               "gnorm_f32.cu", "gnorm_bf16.cu", "gnorm_f16.cu"]
 PROBE_SOURCES = ["fma_peak.cu"]
 
 

@@ -1,5 +1,6 @@
 // Gated linear recurrence (bs_grec calls of bsolve.h): forward over sequences, and one row from kept
 // states.
+#include <algorithm>
 #include <type_traits>
 
 #include "cluster.cuh"
@@ -209,36 +210,49 @@ grec_forward_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa, c
   if (peers > 1) cluster_sync();  // no block leaves while another may still write to it
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128)
-grec_step_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa,
-                 float* __restrict__ state, int64_t num_slots, const int32_t* __restrict__ slots,
-                 T* __restrict__ y, int64_t ldy) {
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= p.channels) return;
-  const float rate = grec_rate(lam[c], kappa);
-  for (int64_t j = blockIdx.y; j < p.batch; j += gridDim.y) {
-    const int64_t slot = slots ? slots[j] : j;
-    float h = 0.f;
-    if (slot >= 0 && slot < num_slots) {
-      const Gates g = grec_gates<false>(grec_exp_neg<false>(both(to_f32(p.r[j * p.ldr + c]))),
-                                        grec_exp_neg<false>(both(to_f32(p.i[j * p.ldi + c]))),
-                                        both(rate));
-      float* at = state + slot * p.channels + c;
-      h = fmaf(g.a.x, *at, g.s.x * g.si.x * to_f32(p.x[j * p.ldx + c]));
-      *at = h;
-    }
-    y[j * ldy + c] = from_f32<T>(h);
+// ------------------------------------------------------------------ one row
+//
+// A thread takes two neighbouring channels of the rows that its block walks (every gridDim.y-th), so that
+// their rate is worked out once. PAIRS: every row of every operand starts on a pair of elements.
+constexpr int kStepThreads = 64;
+
+template <typename T, bool PAIRS>
+__device__ __forceinline__ float2 load_pair(const T* at, bool second) {
+  if constexpr (PAIRS) {
+    return to_f32(*reinterpret_cast<const typename Pair<T>::type*>(at));
+  } else {
+    return make_float2(to_f32(at[0]), second ? to_f32(at[1]) : 0.f);
   }
 }
 
-dim3 grid_of(int channels, int64_t batch) {
-  return dim3((channels + 127) / 128, static_cast<unsigned>(batch < 65535 ? batch : 65535));
+template <typename T, bool PAIRS>
+__global__ void __launch_bounds__(kStepThreads)
+grec_step_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa,
+                 float* __restrict__ state, int64_t num_slots, const int32_t* __restrict__ slots,
+                 T* __restrict__ y, int64_t ldy) {
+  const int c = 2 * (blockIdx.x * kStepThreads + threadIdx.x);
+  if (c >= p.channels) return;
+  const bool second = c + 1 < p.channels;
+  const float2 rate = make_float2(grec_rate(lam[c], kappa),
+                                  second ? grec_rate(lam[c + 1], kappa) : 0.f);
+#pragma unroll 2
+  for (int64_t j = blockIdx.y; j < p.batch; j += gridDim.y) {
+    const int64_t slot = slots ? slots[j] : j;
+    const bool live = slot >= 0 && slot < num_slots;
+    const float2 r = load_pair<T, PAIRS>(p.r + j * p.ldr + c, second),
+                 i = load_pair<T, PAIRS>(p.i + j * p.ldi + c, second),
+                 x = load_pair<T, PAIRS>(p.x + j * p.ldx + c, second);
+    float2 h = make_float2(0.f, 0.f);
+    if (live) {
+      float* at = state + slot * p.channels + c;
+      h = load_pair<float, PAIRS>(at, second);
+      const Gates g = grec_gates<false>(grec_exp_neg<false>(r), grec_exp_neg<false>(i), rate);
+      h = fma2(g.a, h, g.s * g.si * x);
+      store_pair<float, PAIRS>(at, h, false, true, second);
+    }
+    store_pair<T, PAIRS>(y + j * ldy + c, h, false, true, second);
+  }
 }
-
-}  // namespace
-
-namespace {
 
 template <typename T, int W, bool ALIGNED>
 cudaError_t launch_forward(const GrecRows<T>& p, const float* lam, float kappa, const float* h0,
@@ -281,8 +295,15 @@ template <typename T>
 cudaError_t launch_grec_step(const GrecRows<T>& p, const float* lam, float kappa, float* state,
                              int64_t num_slots, const int32_t* slots, T* y, int64_t ldy,
                              cudaStream_t stream) {
-  grec_step_kernel<T><<<grid_of(p.channels, p.batch), 128, 0, stream>>>(p, lam, kappa, state,
-                                                                       num_slots, slots, y, ldy);
+  const unsigned across = (p.channels + 2 * kStepThreads - 1) / (2 * kStepThreads);
+  // 16 blocks an SM; more rows a block beyond that
+  const int64_t down = std::max<int64_t>(1, 16 * 152 / across);
+  const dim3 grid(across, static_cast<unsigned>(p.batch < down ? p.batch : down));
+  const bool pairs = p.channels % 2 == 0 && pair_stores(p.x, p.ldx) && pair_stores(p.r, p.ldr) &&
+                     pair_stores(p.i, p.ldi) && pair_stores(y, ldy) &&
+                     pair_stores(state, p.channels);
+  auto* kernel = pairs ? grec_step_kernel<T, true> : grec_step_kernel<T, false>;
+  kernel<<<grid, kStepThreads, 0, stream>>>(p, lam, kappa, state, num_slots, slots, y, ldy);
   return cudaGetLastError();
 }
 

@@ -290,8 +290,10 @@ grec_dlam_kernel(int channels, int64_t parts, const float* __restrict__ lam,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + lane;
   float sum = 0.f;
-  if (c < channels)
+  if (c < channels) {
+#pragma unroll 8
     for (int64_t k = warp; k < parts; k += kSumWarps) sum += partial[k * channels + c];
+  }
   sums[warp][lane] = sum;
   __syncthreads();
   if (warp != 0 || c >= channels) return;
