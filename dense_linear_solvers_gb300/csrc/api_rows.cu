@@ -223,7 +223,7 @@ bs_status bs_grec_step_batched(bs_dtype dtype, int channels, int64_t batch, cons
 }
 
 int64_t bs_grec_tape_rows(int64_t batch, int64_t rows) {
-  return batch < 0 || rows < 0 ? 0 : rows / 64 + batch;
+  return batch < 0 || rows < 0 ? 0 : rows / 32 + batch;
 }
 
 size_t bs_grec_backward_workspace(int channels, int64_t batch, int64_t rows) {

@@ -86,7 +86,7 @@ grec_forward_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa, c
     const int length = static_cast<int>(end - start);
     unsigned row = static_cast<unsigned>(start) + ahead;  // the warp's first row of this step
     int left = length - ahead;                            // from there to the sequence's end
-    // a warp whose rows start at a multiple of 64 puts its state on the tape
+    // a warp whose rows start at a multiple of 32 puts its state on the tape
     float* tape_at = tape == nullptr || ahead % kTapeRows != 0
                          ? nullptr
                          : tape + (tape_base(start, s) + ahead / kTapeRows) * p.channels + c;
@@ -271,11 +271,11 @@ cudaError_t launch_forward(const GrecRows<T>& p, const float* lam, float kappa, 
                          pair_stores(h, ldh), hT, tape);
 }
 
-// Blocks of four warps, without clusters, while the pairs of a sequence and a tile fill the GPU by
+// Blocks of four warps, without clusters, on 16-bit rows while the pairs of a sequence and a tile fill the GPU by
 // themselves (152 SMs with three blocks): 64 x 512 rows x 2,048 channels BF16 take 94 us, with eight
 // warps 106; 24 packed prompts of 500 rows on average 60 us, with clusters of two 66. Otherwise
 // eight, which meet less often: one sequence of 65,536 x 4,096 takes 450 us, with four
-// warps 501.
+// warps 501; 4 x 4,096 x 2,048 FP32 86 us and 90.
 constexpr int64_t kFourWarpUnits = 3 * 152;
 
 }  // namespace
@@ -285,7 +285,8 @@ cudaError_t launch_grec(const GrecRows<T>& p, const float* lam, float kappa, con
                         T* h, int64_t ldh, float* hT, float* tape, cudaStream_t stream) {
   const bool aligned = rows_aligned(p.x, p.ldx) && rows_aligned(p.r, p.ldr) &&
                        rows_aligned(p.i, p.ldi);
-  const bool four = (p.channels + kTileC - 1) / kTileC * p.batch >= kFourWarpUnits;
+  const int64_t units = (p.channels + kTileC - 1) / kTileC * p.batch;
+  const bool four = sizeof(T) == 2 && units >= kFourWarpUnits;
   auto* launch = four ? (aligned ? launch_forward<T, 4, true> : launch_forward<T, 4, false>)
                       : (aligned ? launch_forward<T, 8, true> : launch_forward<T, 8, false>);
   return launch(p, lam, kappa, h0, h, ldh, hT, tape, stream);

@@ -8,7 +8,7 @@
 // the gradients need: four reads and three writes an element.
 //
 // The mapping is the forward pass's: 64 channels a block, two a lane, R rows a warp, pieces of
-// kWarps * R = 64 rows, one tape state each, so that the states need no exchange between blocks;
+// W * R rows, which start at a state on the tape, so that the states need no exchange between blocks;
 // consecutive pieces lie on the blocks of a cluster, which walk the sequence from its end.
 // One step:
 //   each warp turns its rows into a_t, the gates and the three compositions' parts: A the product
@@ -30,9 +30,8 @@
 namespace bsolve {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kR = 8;
-static_assert(kWarps * kR == kTapeRows, "a block's piece starts at a state on the tape");
+constexpr int kStages = 2;  // steps staged ahead
 
 struct Exchange {  // of two channels
   float2 A, P;
@@ -43,15 +42,15 @@ __device__ __forceinline__ Exchange compose(const Exchange& second, const Exchan
   return {second.A * first.A, apply(second, first.P)};
 }
 
-template <typename T, bool ALIGNED, int STAGES>
+template <typename T, int W, bool ALIGNED>
 struct GrecBackwardShared {
   static constexpr int kOperand = kR * Tile<T, ALIGNED>::kRowBytes;  // one warp's rows
   static constexpr int kStage = 4 * kOperand;
-  static constexpr int kWarp = STAGES * kStage;
-  static constexpr int kSegments = 2 * kWarps * 32 * sizeof(Exchange);
-  static constexpr int kStates = 2 * kWarps * 32 * sizeof(float2);
+  static constexpr int kWarp = kStages * kStage;
+  static constexpr int kSegments = 2 * W * 32 * sizeof(Exchange);
+  static constexpr int kStates = 2 * W * 32 * sizeof(float2);
   static constexpr int kBlocks = 2 * kMaxCluster * 32 * sizeof(Exchange);
-  static constexpr int kBytes = kSegments + kStates + kBlocks + kWarps * kWarp;
+  static constexpr int kBytes = kSegments + kStates + kBlocks + W * kWarp;
 };
 
 template <typename T>
@@ -62,12 +61,14 @@ struct GrecGradRows {
   bool px, pr, pi;  // pairs of elements stored as one value
 };
 
-template <typename T, bool ALIGNED, int STAGES>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1)
+template <typename T, int W, bool ALIGNED>
+__global__ void __launch_bounds__(32 * W, (sizeof(T) == 2 ? 16 : 8) / W)
 grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__ lam, float kappa,
                      const float* __restrict__ tape, const float* dhT, float* dh0,
                      float* __restrict__ partial) {
-  using S = GrecBackwardShared<T, ALIGNED, STAGES>;
+  using S = GrecBackwardShared<T, W, ALIGNED>;
+  constexpr int kPiece = W * kR;  // rows of a block in a step
+  static_assert(kPiece % kTapeRows == 0, "a block's piece starts at a state on the tape");
   extern __shared__ __align__(16) char shared[];
   Exchange* segments = reinterpret_cast<Exchange*>(shared);
   Exchange* blocks = reinterpret_cast<Exchange*>(shared + S::kSegments);
@@ -85,7 +86,7 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
   const unsigned es = sizeof(T);
   const unsigned pdx = g.lddx * es, pdr = g.lddr * es, pdi = g.lddi * es;
   const bool wide = valid == kTileC, whole = g.px && g.pr && g.pi && wide;
-  const int step_rows = peers * kTapeRows;
+  const int step_rows = peers * kPiece;
   float2 dlam = make_float2(0.f, 0.f);
   int parity = 0;
   if (peers > 1) cluster_sync();  // every block runs before one writes to another
@@ -101,7 +102,7 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
     const int length = static_cast<int>(end - start);
     const int steps = (length + step_rows - 1) / step_rows;
     // the block's first row of this step, counted from the sequence's; the last step first
-    int piece = (steps - 1) * step_rows + rank * kTapeRows;
+    int piece = (steps - 1) * step_rows + rank * kPiece;
     unsigned row = static_cast<unsigned>(start) + piece + warp * kR;  // the warp's first
     const float* tape_at = tape + (tape_base(start, s) + piece / kTapeRows) * p.channels + c;
 
@@ -120,7 +121,7 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
       cp_async_commit();
     };
 #pragma unroll
-    for (int k = 0; k < STAGES; ++k) stage(k, k);
+    for (int k = 0; k < kStages; ++k) stage(k, k);
 
     int slot = 0;
     for (; piece >= 0; piece -= step_rows, row -= step_rows) {
@@ -131,8 +132,8 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
         if (first) before.x = tape_at[0];
         if (second) before.y = tape_at[1];
       }
-      tape_at -= peers * static_cast<int64_t>(p.channels);
-      cp_async_wait_group<STAGES - 1>();
+      tape_at -= step_rows / kTapeRows * static_cast<int64_t>(p.channels);
+      cp_async_wait_group<kStages - 1>();
       __syncwarp();
       const char* in = mine + slot * S::kStage;
       const Shift lx = shift_of<T, ALIGNED>(p.x, row, p.ldx),
@@ -175,14 +176,14 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
           if (j < n) back(j);
       }
 
-      Exchange* seg = segments + parity * kWarps * 32 + lane;
-      float2* st = states + parity * kWarps * 32 + lane;
+      Exchange* seg = segments + parity * W * 32 + lane;
+      float2* st = states + parity * W * 32 + lane;
       seg[warp * 32] = m;
       st[warp * 32] = H;
       __syncthreads();
       Exchange behind{both(1.f), both(0.f)};  // the block's rows behind the warp's
 #pragma unroll
-      for (int w = kWarps - 1; w > 0; --w)
+      for (int w = W - 1; w > 0; --w)
         if (w > warp) behind = compose(seg[w * 32], behind);
       float2 after = carry;  // what comes from behind the block's, then the warp's rows
       if (peers > 1) {
@@ -201,11 +202,11 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
         }
       } else {
 #pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) carry = apply(seg[w * 32], carry);
+        for (int w = W - 1; w >= 0; --w) carry = apply(seg[w * 32], carry);
       }
       after = apply(behind, after);
 #pragma unroll
-      for (int w = 0; w < kWarps - 1; ++w)
+      for (int w = 0; w < W - 1; ++w)
         if (w < warp) before = fma2(seg[w * 32].A, before, st[w * 32]);
       parity ^= 1;
 
@@ -253,8 +254,8 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
           if (j < n) emit(j, std::false_type(), std::false_type());
       }
       __syncwarp();
-      stage(slot, STAGES);
-      slot = slot + 1 == STAGES ? 0 : slot + 1;
+      stage(slot, kStages);
+      slot = slot + 1 == kStages ? 0 : slot + 1;
     }
     cp_async_wait_all();
     if (dh0 && rank == 0 && warp == 0) {
@@ -271,7 +272,7 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
   if (warp == 0) {
     float2 sum = sums[lane];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) sum = sum + sums[w * 32 + lane];
+    for (int w = 1; w < W; ++w) sum = sum + sums[w * 32 + lane];
     float* at = partial + (static_cast<int64_t>(blockIdx.y) * peers + rank) * p.channels + c;
     if (first) at[0] = sum.x;
     if (second) at[1] = sum.y;
@@ -302,25 +303,31 @@ grec_dlam_kernel(int channels, int64_t parts, const float* __restrict__ lam,
   dlam[c] = sum * grec_rate_slope(lam[c]);
 }
 
+// Blocks of four warps on 16-bit rows where there is a pair of a sequence and a tile for every SM: 24
+// packed sequences of 1,000 rows on average, 2,048 channels BF16, take 201 us, with eight warps
+// 222; 64 x 512 rows 227 and 239. Otherwise eight, which meet less often: one sequence of
+// 32,768 rows takes 310 us, with four warps 380; 4 x 4,096 rows FP32 183 and 193.
+constexpr int64_t kFourWarpUnits = 152;
+
 int64_t tiles_of(int channels) { return (channels + kTileC - 1) / kTileC; }
 int64_t grid_y(int64_t batch) { return batch < 65535 ? batch : 65535; }
 
-template <typename T, bool ALIGNED, int STAGES>
+template <typename T, int W, bool ALIGNED>
 cudaError_t launch_backward(const GrecRows<T>& p, const GrecGradRows<T>& g, const float* lam,
                             float kappa, const float* tape, const float* dhT, float* dh0,
                             float* partial, int64_t* parts, cudaStream_t stream) {
-  using S = GrecBackwardShared<T, ALIGNED, STAGES>;
-  auto* kernel = grec_backward_kernel<T, ALIGNED, STAGES>;
-  static const Held held = held_clusters(kernel, 32 * kWarps, S::kBytes);
+  using S = GrecBackwardShared<T, W, ALIGNED>;
+  auto* kernel = grec_backward_kernel<T, W, ALIGNED>;
+  static const Held held = held_clusters(kernel, 32 * W, S::kBytes);
   if (held.status != cudaSuccess) return held.status;
   const int64_t length = p.offsets ? p.rows / p.batch + 1 : p.length;
   const int cluster = grec_cluster(held, tiles_of(p.channels), p.batch, length,
-                                   p.offsets != nullptr, kTapeRows);
+                                   p.offsets != nullptr, W * kR);
   *parts = grid_y(p.batch) * cluster;
   return launch_clusters(kernel,
                          dim3(static_cast<unsigned>(tiles_of(p.channels) * cluster),
                               static_cast<unsigned>(grid_y(p.batch))),
-                         32 * kWarps, S::kBytes, cluster, stream, p, g, lam, kappa, tape, dhT, dh0,
+                         32 * W, S::kBytes, cluster, stream, p, g, lam, kappa, tape, dhT, dh0,
                          partial);
 }
 
@@ -345,11 +352,10 @@ cudaError_t launch_grec_backward(const GrecRows<T>& p, const float* lam, float k
                             pair_stores(dx, lddx), pair_stores(dr, lddr), pair_stores(di, lddi)};
     const bool aligned = rows_aligned(p.x, p.ldx) && rows_aligned(p.r, p.ldr) &&
                          rows_aligned(p.i, p.ldi) && rows_aligned(dh, lddh);
-    const cudaError_t e =
-        aligned ? launch_backward<T, true, 2>(p, g, lam, kappa, tape, dhT, dh0, partial, &parts,
-                                              stream)
-                : launch_backward<T, false, 2>(p, g, lam, kappa, tape, dhT, dh0, partial, &parts,
-                                               stream);
+    const bool four = sizeof(T) == 2 && tiles_of(p.channels) * p.batch >= kFourWarpUnits;
+    auto* launch = four ? (aligned ? launch_backward<T, 4, true> : launch_backward<T, 4, false>)
+                        : (aligned ? launch_backward<T, 8, true> : launch_backward<T, 8, false>);
+    const cudaError_t e = launch(p, g, lam, kappa, tape, dhT, dh0, partial, &parts, stream);
     if (e != cudaSuccess) return e;
   }
   grec_dlam_kernel<<<(p.channels + 31) / 32, 32 * kSumWarps, 0, stream>>>(p.channels, parts, lam,

@@ -6,10 +6,10 @@
 
 namespace bsolve {
 
-constexpr int kTapeRows = 64;  // rows of a sequence between two states on the tape
+constexpr int kTapeRows = 32;  // rows of a sequence between two states on the tape
 
 // First tape row of the sequence that starts at row `start` and is number s: the sequences'
-// parts do not overlap, since floor(b / 64) - floor(a / 64) + 1 >= ceil((b - a) / 64).
+// parts do not overlap, since floor(b / 32) - floor(a / 32) + 1 >= ceil((b - a) / 32).
 __host__ __device__ __forceinline__ int64_t tape_base(int64_t start, int64_t s) {
   return start / kTapeRows + s;
 }

@@ -380,7 +380,7 @@ BS_API bs_status bs_bdmv2_batched(bs_dtype dtype, int num_block_rows, int block_
  *   h     the states of every row.
  *   hT    batch x channels final states, or NULL.
  *   tape  bs_grec_tape_rows(batch, rows) x channels, or NULL: the states that
- *         bs_grec_backward_batched restarts from (the state before rows 0, 64, 128, ... of
+ *         bs_grec_backward_batched restarts from (the state before rows 0, 32, 64, ... of
  *         each sequence).
  * bs_grec_backward_batched: x, r, i, lam, kappa, offsets and tape as in the forward call;
  *   dh    the gradient of h;  dhT  batch x channels, the gradient of hT, or NULL for zeros.

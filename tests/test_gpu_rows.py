@@ -83,8 +83,8 @@ def run_recurrence(rng, kind, c, spans, rows, *, kappa=8.0, packed=True, h0=True
     assert untouched(th, whole)
     assert bool((th[torch.from_numpy(~live).cuda()] == MARK).all())
     for b, (p, q) in enumerate(spans):
-        for k, t in enumerate(range(p, q, 64)):
-            near(tape[p // 64 + b + k], ref.before[t], ref.err_before[t], "f32", "tape")
+        for k, t in enumerate(range(p, q, 32)):
+            near(tape[p // 32 + b + k], ref.before[t], ref.err_before[t], "f32", "tape")
     if not train:
         return
     dh = values(rng, (rows, c), kind)
@@ -111,7 +111,7 @@ def uniform(batch, length):
     return [(b * length, (b + 1) * length) for b in range(batch)]
 
 
-# one row, around the tape's 64 rows, several tiles, more than one pass of the largest split
+# one row, around the tape's 32 rows, several tiles, more than one pass of the largest split
 LENGTHS = [1, 2, 15, 16, 17, 63, 64, 65, 127, 130, 257, 700]
 
 

@@ -133,7 +133,7 @@ def test_norm_backward_refusals(lib):
 
 
 def test_queries(lib):
-    assert bs.bs_grec_tape_rows(3, 130) == 130 // 64 + 3
+    assert bs.bs_grec_tape_rows(3, 130) == 130 // 32 + 3
     assert bs.bs_grec_tape_rows(-1, 5) == 0
     assert lib.bs_grec_backward_workspace(0, 1, 1) == 0
     assert lib.bs_gnorm_backward_workspace(0, 1) == 0
@@ -148,7 +148,7 @@ def test_queries(lib):
 
 
 def test_tape_parts_do_not_overlap():
-    """Sequence s that starts at row a has its tape at a // 64 + s: ceil(length / 64) rows fit in front
+    """Sequence s that starts at row a has its tape at a // 32 + s: ceil(length / 32) rows fit in front
     of the next one's, and the last inside bs_grec_tape_rows."""
     import random
     rng = random.Random(0)
@@ -156,9 +156,9 @@ def test_tape_parts_do_not_overlap():
         cuts = sorted(rng.randrange(2000) for _ in range(rng.randrange(2, 12)))
         end = 0
         for s, (a, b) in enumerate(zip(cuts[:-1], cuts[1:])):
-            base = a // 64 + s
+            base = a // 32 + s
             assert base >= end
-            end = base + -(-(b - a) // 64)
+            end = base + -(-(b - a) // 32)
         assert end <= bs.bs_grec_tape_rows(len(cuts) - 1, cuts[-1])
 
 
