@@ -995,6 +995,6 @@ int bs_bdsv_supported(bs_dtype dtype, int num_block_rows, int block_size) {
   return bdsv_supported(dtype, num_block_rows, block_size) ? 1 : 0;
 }
 
-int bs_version(void) { return 100; }
+int bs_version(void) { return 200; }
 
 }  // extern "C"
