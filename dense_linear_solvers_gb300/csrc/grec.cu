@@ -45,7 +45,8 @@ struct GrecForwardShared {
   static constexpr int kStage = 3 * kOperand;
   static constexpr int kWarp = kStages * kStage;
   static constexpr int kSegments = 2 * W * 32 * sizeof(Composition);
-  static constexpr int kBlocks = 2 * kMaxCluster * 32 * sizeof(Composition);
+  // four-warp blocks run without clusters; an SM then holds four of them
+  static constexpr int kBlocks = W == 4 ? 0 : 2 * kMaxCluster * 32 * sizeof(Composition);
   static constexpr int kBytes = kSegments + kBlocks + W * kWarp;
 };
 
@@ -60,7 +61,7 @@ grec_forward_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa, c
   Composition* blocks = reinterpret_cast<Composition*>(shared + S::kSegments);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   char* mine = shared + S::kSegments + S::kBlocks + warp * S::kWarp;
-  const int peers = cluster_size(), rank = cluster_rank();
+  const int peers = W == 4 ? 1 : cluster_size(), rank = W == 4 ? 0 : cluster_rank();
   const int c0 = static_cast<int>(blockIdx.x) / peers * kTileC;
   const int valid = p.channels - c0 < kTileC ? p.channels - c0 : kTileC;
   const int c = c0 + 2 * lane;
