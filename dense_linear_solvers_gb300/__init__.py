@@ -570,112 +570,32 @@ def bs_getrf_getrs_batched_host_static(A, B, ipiv, info, layout: int = ROW_MAJOR
 
 
 # --------------------------------------------------------------- row operators
-_ROW_CODES = {}
-_F32 = None
-
-
-def _row_code(dtype) -> int:
-    global _F32
-    if not _ROW_CODES:
-        import torch
-        _F32 = torch.float32
-        _ROW_CODES.update({torch.float32: BS_FP32, torch.bfloat16: BS_BF16,
-                           torch.float16: BS_FP16})
-    code = _ROW_CODES.get(dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dtype}: float32, bfloat16 or float16")
-    return code
-
-
-def _rows(dtype, shape, device, named) -> list:
-    """pointer, ld of each row operand (name, tensor) in turn: of this dtype and shape, on this
-    device, the last stride 1 and the rows at one distance (ld elements). None: 0, 0."""
-    out = []
-    width = shape[-1]
-    three = len(shape) == 3
-    for name, t in named:
-        if t is None:
-            out += (0, 0)
-            continue
-        if t.dtype is not dtype:
-            raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.get_device() != device or device < 0:
-            raise ValueError(f"{name}: bsolve operands are device tensors of one device")
-        st = t.stride()
-        if width > 1 and st[-1] != 1:
-            raise ValueError(f"{name}: the elements of a row must be contiguous")
-        if three:
-            b, n = shape[0], shape[1]
-            ld = st[1] if n > 1 else (st[0] if b > 1 else width)
-            if b > 1 and n > 1 and st[0] != n * ld:
-                raise ValueError(f"{name}: the rows of all sequences must lie at one distance")
-        else:
-            ld = st[0] if shape[0] > 1 else width
-        if ld < width:
-            if t.numel():
-                raise ValueError(f"{name}: rows overlap")
-            ld = width
-        out += (t.data_ptr(), ld)
-    return out
-
-
-def _vec(t, name: str, device, numel: int, dtype=None) -> int:
-    """The pointer of a contiguous operand of numel elements (FP32 unless dtype says otherwise)
-    on this device. None: 0."""
-    if t is None:
-        return 0
-    want = dtype or _F32
-    if t.dtype is not want:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {want}")
-    if t.numel() != numel:
-        raise ValueError(f"{name}: {t.numel()} elements, expected {numel}")
-    if t.get_device() != device or device < 0:
-        raise ValueError(f"{name}: bsolve operands are device tensors of one device")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
-
-
+_marshal = None
 _raw_stream = None
 
 
-def _row_stream(stream, device) -> int:
-    """_stream() without a Stream object where torch offers its handle alone: a third of the small
-    calls' time."""
-    global _raw_stream
-    if stream is not None:
-        return _stream(stream)
-    if _raw_stream is None:
+def _rows():
+    """The native module that marshals these calls (csrc/rowcall.cpp): types, shapes, row distances
+    and devices are checked there, against the first operand's."""
+    global _marshal, _raw_stream
+    if _marshal is None:
+        lib()
+        import importlib
+
         import torch
+        module = importlib.import_module(__name__ + "._rowcall")
+        # the current stream's handle without a Stream object, where torch offers it
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
-    return _raw_stream(device)
+        _marshal = module
+    return _marshal
 
 
-def _work(work, device):
-    import torch
-    if work is None:
-        return 0, 0
-    return _vec(work, "work", device, work.numel(), torch.uint8), work.numel()
-
-
-def _sequences(x, offsets, device):
-    """(batch, rows, channels, pointer of offsets) of a recurrence call."""
-    shape = x.shape
-    if offsets is None:
-        if len(shape) != 3:
-            raise ValueError(f"x: shape {tuple(shape)}, expected (batch, length, channels), or "
-                             "(rows, channels) with offsets")
-        return shape[0], shape[0] * shape[1], shape[2], 0
-    import torch
-    if len(shape) != 2:
-        raise ValueError(f"x: shape {tuple(shape)}, expected (rows, channels) with offsets")
-    if offsets.numel() < 1:
-        raise ValueError("offsets: batch + 1 row numbers expected")
-    at = _vec(offsets, "offsets", device, offsets.numel(), torch.int64)
-    return offsets.numel() - 1, shape[0], shape[1], at
+def _row_stream(stream, like) -> int:
+    if stream is not None:
+        return _stream(stream)
+    device = like.get_device()
+    return _raw_stream(device) if device >= 0 else 0  # a host tensor: refused by the call
 
 
 def bs_grec_tape_rows(batch: int, rows: int) -> int:
@@ -694,18 +614,7 @@ def bs_grec_batched(x, r, i, lam, h, h0=None, hT=None, offsets=None, tape=None,
     (batch, length, channels), or (rows, channels) with offsets, batch + 1 int64 row numbers;
     h0, hT: (batch, channels) float32; tape: (bs_grec_tape_rows(...), channels) float32, for
     the backward call."""
-    code, dev = _row_code(x.dtype), x.get_device()
-    batch, rows, channels, at = _sequences(x, offsets, dev)
-    px, ldx, pr, ldr, pi, ldi, ph, ldh = _rows(
-        x.dtype, x.shape, dev, (("x", x), ("r", r), ("i", i), ("h", h)))
-    L = lib()
-    st = L.bs_grec_batched(
-        code, channels, batch, rows, at, px, ldx, pr, ldr, pi, ldi,
-        _vec(lam, "lam", dev, channels), kappa, _vec(h0, "h0", dev, batch * channels), ph, ldh,
-        _vec(hT, "hT", dev, batch * channels),
-        0 if tape is None else _vec(tape, "tape", dev,
-                                    L.bs_grec_tape_rows(batch, rows) * channels),
-        _row_stream(stream, dev))
+    st = _rows().grec(x, r, i, lam, h, h0, hT, offsets, tape, kappa, _row_stream(stream, x))
     if st:
         _check(st, "bs_grec_batched")
 
@@ -715,20 +624,8 @@ def bs_grec_backward_batched(x, r, i, lam, tape, dh, dx, dr, di, dlam, work, dhT
     """Gradients of bs_grec_batched from its inputs, its tape and the gradients of h (and hT):
     dx, dr, di, dlam (and dh0) are written (see bsolve.h). work: uint8, at least
     bs_grec_backward_workspace(...) elements."""
-    code, dev = _row_code(x.dtype), x.get_device()
-    batch, rows, channels, at = _sequences(x, offsets, dev)
-    px, ldx, pr, ldr, pi, ldi, pdh, lddh, pdx, lddx, pdr, lddr, pdi, lddi = _rows(
-        x.dtype, x.shape, dev, (("x", x), ("r", r), ("i", i), ("dh", dh), ("dx", dx), ("dr", dr),
-                                ("di", di)))
-    pw, nw = _work(work, dev)
-    L = lib()
-    st = L.bs_grec_backward_batched(
-        code, channels, batch, rows, at, px, ldx, pr, ldr, pi, ldi,
-        _vec(lam, "lam", dev, channels), kappa,
-        _vec(tape, "tape", dev, L.bs_grec_tape_rows(batch, rows) * channels), pdh, lddh,
-        _vec(dhT, "dhT", dev, batch * channels), pdx, lddx, pdr, lddr, pdi, lddi,
-        _vec(dlam, "dlam", dev, channels), _vec(dh0, "dh0", dev, batch * channels), pw, nw,
-        _row_stream(stream, dev))
+    st = _rows().grec_backward(x, r, i, lam, tape, dh, dx, dr, di, dlam, work, dhT, dh0, offsets,
+                               kappa, _row_stream(stream, x))
     if st:
         _check(st, "bs_grec_backward_batched")
 
@@ -738,20 +635,7 @@ def bs_grec_step_batched(x, r, i, lam, state, y, slots=None, kappa: float = 8.0,
     """One row of the recurrence for each of a batch of sequences: state, (num_slots, channels)
     float32, advances in place and y <- the new states (see bsolve.h). x, r, i, y: (batch,
     channels); slots: batch int32 rows of state, None: row j for sequence j."""
-    import torch
-    shape, held = x.shape, state.shape
-    if len(shape) != 2:
-        raise ValueError(f"x: shape {tuple(shape)}, expected (batch, channels)")
-    batch, channels = shape
-    if len(held) != 2 or held[1] != channels:
-        raise ValueError(f"state: shape {tuple(held)}, expected (num_slots, {channels})")
-    code, dev = _row_code(x.dtype), x.get_device()
-    px, ldx, pr, ldr, pi, ldi, py, ldy = _rows(
-        x.dtype, shape, dev, (("x", x), ("r", r), ("i", i), ("y", y)))
-    st = lib().bs_grec_step_batched(
-        code, channels, batch, px, ldx, pr, ldr, pi, ldi, _vec(lam, "lam", dev, channels), kappa,
-        _vec(state, "state", dev, held[0] * channels), held[0],
-        _vec(slots, "slots", dev, batch, torch.int32), py, ldy, _row_stream(stream, dev))
+    st = _rows().grec_step(x, r, i, lam, state, y, slots, kappa, _row_stream(stream, x))
     if st:
         _check(st, "bs_grec_step_batched")
 
@@ -766,14 +650,7 @@ def bs_gnorm_batched(f, y=None, z=None, x=None, w_post=None, scale=None, w_pre=N
     """y <- x + scale * (f / rms(f) * w_post * act(z)), u <- y / rms(y) * w_pre; every part but f
     and one output optional (see bsolve.h). f, z, x, y, u: (rows, width) or (batch, length,
     width); w_post, scale, w_pre: width float32 elements."""
-    code, dev, shape = _row_code(f.dtype), f.get_device(), f.shape
-    width = shape[-1]
-    pf, ldf, pz, ldz, px, ldx, py, ldy, pu, ldu = _rows(
-        f.dtype, shape, dev, (("f", f), ("z", z), ("x", x), ("y", y), ("u", u)))
-    st = lib().bs_gnorm_batched(
-        code, f.numel() // width if width else 0, width, pf, ldf, pz, ldz, px, ldx,
-        _vec(w_post, "w_post", dev, width), _vec(scale, "scale", dev, width),
-        _vec(w_pre, "w_pre", dev, width), eps, gate, py, ldy, pu, ldu, _row_stream(stream, dev))
+    st = _rows().gnorm(f, y, z, x, w_post, scale, w_pre, u, eps, gate, _row_stream(stream, f))
     if st:
         _check(st, "bs_gnorm_batched")
 
@@ -785,17 +662,7 @@ def bs_gnorm_backward_batched(f, dy, df, work=None, z=None, x=None, w_post=None,
     """Gradients of bs_gnorm_batched from its inputs and the gradients of y and u (either may be
     None): df and, where given, dz, dx, dw_post, dscale, dw_pre are written (see bsolve.h).
     work: uint8, at least bs_gnorm_backward_workspace(...) elements, for the last three."""
-    code, dev, shape = _row_code(f.dtype), f.get_device(), f.shape
-    width = shape[-1]
-    pf, ldf, pz, ldz, px, ldx, pdy, lddy, pdu, lddu, pdf, lddf, pdz, lddz, pdx, lddx = _rows(
-        f.dtype, shape, dev, (("f", f), ("z", z), ("x", x), ("dy", dy), ("du", du), ("df", df),
-                              ("dz", dz), ("dx", dx)))
-    pw, nw = _work(work, dev)
-    st = lib().bs_gnorm_backward_batched(
-        code, f.numel() // width if width else 0, width, pf, ldf, pz, ldz, px, ldx,
-        _vec(w_post, "w_post", dev, width), _vec(scale, "scale", dev, width),
-        _vec(w_pre, "w_pre", dev, width), eps, gate, pdy, lddy, pdu, lddu, pdf, lddf, pdz, lddz,
-        pdx, lddx, _vec(dw_post, "dw_post", dev, width), _vec(dscale, "dscale", dev, width),
-        _vec(dw_pre, "dw_pre", dev, width), pw, nw, _row_stream(stream, dev))
+    st = _rows().gnorm_backward(f, dy, df, work, z, x, w_post, scale, w_pre, du, dz, dx, dw_post,
+                                dscale, dw_pre, eps, gate, _row_stream(stream, f))
     if st:
         _check(st, "bs_gnorm_backward_batched")

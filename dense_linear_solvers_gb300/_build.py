@@ -1,4 +1,5 @@
-"""In-tree build of libbsolve.so (and the arithmetic-throughput probe) with nvcc.
+"""In-tree build of libbsolve.so (and the arithmetic-throughput probe) with nvcc, and of the
+row operators' Python module with g++.
 
 Every translation unit is compiled for sm_103a only, in parallel, then linked into a
 shared library next to this file. Nothing is installed into site-packages.
@@ -9,6 +10,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbsolve.so")
 PROBE_LIB = os.path.join(PKG, "libbsolve_probe.so")
+ROWCALL = os.path.join(PKG, "_rowcall.so")  # the Python module, against torch's and Python's headers
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--fmad=false", "-Xcompiler", "-fPIC",
@@ -51,6 +54,30 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _compile_rowcall() -> str:
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "rowcall.o")
+    subprocess.check_call([
+        "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+        "-I", sysconfig.get_paths()["include"], "-isystem", base,
+        "-isystem", os.path.join(base, "torch", "csrc", "api", "include"),
+        "-c", os.path.join(CSRC, "rowcall.cpp"), "-o", obj])
+    return obj
+
+
+def _link_rowcall(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = ROWCALL + f".tmp{os.getpid()}"
+    subprocess.check_call([
+        "g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB),
+        "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+        "-Wl,-rpath," + libs])
+    os.replace(tmp, ROWCALL)
+
+
 def _link(objs: list[str], out: str) -> None:
     tmp = out + f".tmp{os.getpid()}"
     subprocess.check_call([nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs])
@@ -58,17 +85,20 @@ def _link(objs: list[str], out: str) -> None:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile and link libbsolve.so (and libbsolve_probe.so) if stale; returns the path."""
+    """Compile and link libbsolve.so, libbsolve_probe.so and _rowcall.so if stale; returns the
+    library's path."""
     os.makedirs(BUILD, exist_ok=True)
     newest = _newest_input_mtime()
     stale = force or any(
-        (not os.path.exists(p)) or os.path.getmtime(p) < newest for p in (LIB, PROBE_LIB))
+        (not os.path.exists(p)) or os.path.getmtime(p) < newest for p in (LIB, PROBE_LIB, ROWCALL))
     if not stale:
         return LIB
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    with cf.ThreadPoolExecutor(max_workers=len(LIB_SOURCES) + len(PROBE_SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(LIB_SOURCES) + len(PROBE_SOURCES) + 1) as ex:
+        rowcall = ex.submit(_compile_rowcall)
         lib_objs = list(ex.map(lambda s: _compile(s, extra), LIB_SOURCES))
         probe_objs = list(ex.map(lambda s: _compile(s, extra), PROBE_SOURCES))
     _link(lib_objs, LIB)
     _link(probe_objs, PROBE_LIB)
+    _link_rowcall(rowcall.result())
     return LIB

@@ -491,3 +491,40 @@ def test_empty_calls():
                                  dscale=s[1], dw_pre=s[2])
     assert all(bool((t == 0).all()) for t in s)
     bs.bs_grec_step_batched(e, e, e, la, h0, e)
+
+
+def test_binding_refuses():
+    """Operands of another type, shape, device or layout than the first one's."""
+    x = torch.zeros(2, 10, 8, device="cuda")
+    lam = torch.zeros(8, device="cuda")
+    h = torch.empty_like(x)
+    bad = [
+        (TypeError, "dtype", dict(r=x.half())), (ValueError, "shape", dict(r=x[:, :9])),
+        (ValueError, "device", dict(i=x.cpu())), (ValueError, "contiguous", dict(h=x.mT.contiguous().mT)),
+        (ValueError, "one distance", dict(x=x[:, :9], r=x[:, :9], i=x[:, :9], h=x[:, :9])),
+        (ValueError, "one distance", dict(i=x[:, :1].expand(2, 10, 8))),
+        (TypeError, "dtype", dict(lam=lam.double())), (ValueError, "elements", dict(lam=lam[:7])),
+        (ValueError, "elements", dict(h0=torch.zeros(3, 8, device="cuda"))),
+        (ValueError, "device", dict(hT=torch.zeros(2, 8))),
+        (ValueError, "contiguous", dict(hT=torch.zeros(8, 2, device="cuda").T)),
+        (ValueError, "elements", dict(tape=torch.zeros(1, 8, device="cuda"))),
+        (ValueError, "expected", dict(offsets=torch.zeros(3, dtype=torch.int64, device="cuda"))),
+        (TypeError, "tensor", dict(lam=3.0)),
+    ]
+    for error, text, change in bad:
+        with pytest.raises(error, match=text):
+            bs.bs_grec_batched(**{**dict(x=x, r=x, i=x, lam=lam, h=h), **change})
+    with pytest.raises(ValueError, match="rows overlap"):
+        bs.bs_gnorm_batched(x[0, :1].expand(10, 8), h[0])
+    with pytest.raises(TypeError, match="dtype"):
+        bs.bs_grec_batched(x[0], x[0], x[0], lam, h[0],
+                           offsets=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="state"):
+        bs.bs_grec_step_batched(x[0], x[0], x[0], lam, torch.zeros(3, 9, device="cuda"), h[0])
+    with pytest.raises(TypeError, match="dtype"):
+        bs.bs_grec_step_batched(x[0], x[0], x[0], lam, torch.zeros(10, 8, device="cuda"), h[0],
+                                slots=torch.zeros(10, device="cuda"))
+    with pytest.raises(bs.BsolveError, match="INVALID_ARG"):
+        bs.bs_grec_batched(x, x, x, lam, x)  # the output over its inputs
+    with pytest.raises(TypeError, match="dtype"):
+        bs.bs_gnorm_backward_batched(x, x, h, work=lam)
