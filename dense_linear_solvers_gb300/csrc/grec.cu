@@ -14,8 +14,8 @@ namespace {
 
 // ------------------------------------------------------------------ forward
 //
-// A block takes a tile of 64 channels, a lane two of them, and W * 16 consecutive rows at a time,
-// a warp 16 of them; a cluster of blocks takes consecutive such pieces of one sequence. One step:
+// A block takes a tile of 64 channels, a lane two of them, and W * kR consecutive rows at a time,
+// a warp kR of them; a cluster of blocks takes consecutive such pieces of one sequence. One step:
 //   every warp turns its rows into compositions h_j = A_j h_in + H_j from its first row on (A the
 //     product of the a_t, H the state from zero), kept in registers;
 //   the warps' last compositions meet in shared memory, the blocks' in every block's shared
@@ -25,7 +25,6 @@ namespace {
 //   every warp applies its compositions to its own true state, one product-sum an element, and
 //     stores the states.
 // Each element is read and written once. The order of every sum follows from the sizes alone.
-constexpr int kR = 16;      // rows a warp keeps in registers
 constexpr int kStages = 2;  // steps staged ahead
 
 struct Composition {  // of two channels
@@ -39,7 +38,7 @@ __device__ __forceinline__ Composition compose(const Composition& second, const 
   return {second.A * first.A, apply(second, first.H)};
 }
 
-template <typename T, int W, bool ALIGNED>
+template <typename T, int W, int kR, bool ALIGNED>
 struct GrecForwardShared {
   static constexpr int kOperand = kR * Tile<T, ALIGNED>::kRowBytes;  // one warp's rows
   static constexpr int kStage = 3 * kOperand;
@@ -50,12 +49,12 @@ struct GrecForwardShared {
   static constexpr int kBytes = kSegments + kBlocks + W * kWarp;
 };
 
-template <typename T, int W, bool ALIGNED>
-__global__ void __launch_bounds__(32 * W, (sizeof(T) == 2 ? 16 : 8) / W)
+template <typename T, int W, int kR, bool ALIGNED>
+__global__ void __launch_bounds__(32 * W, (sizeof(T) == 2 || kR == 8 ? 16 : 8) / W)
 grec_forward_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa, const float* h0,
                     T* __restrict__ h, int64_t ldh, bool pairs, float* hT,
                     float* __restrict__ tape) {
-  using S = GrecForwardShared<T, W, ALIGNED>;
+  using S = GrecForwardShared<T, W, kR, ALIGNED>;
   extern __shared__ __align__(16) char shared[];
   Composition* segments = reinterpret_cast<Composition*>(shared);
   Composition* blocks = reinterpret_cast<Composition*>(shared + S::kSegments);
@@ -255,11 +254,11 @@ grec_step_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa,
   }
 }
 
-template <typename T, int W, bool ALIGNED>
+template <typename T, int W, int kR, bool ALIGNED>
 cudaError_t launch_forward(const GrecRows<T>& p, const float* lam, float kappa, const float* h0,
                            T* h, int64_t ldh, float* hT, float* tape, cudaStream_t stream) {
-  using S = GrecForwardShared<T, W, ALIGNED>;
-  auto* kernel = grec_forward_kernel<T, W, ALIGNED>;
+  using S = GrecForwardShared<T, W, kR, ALIGNED>;
+  auto* kernel = grec_forward_kernel<T, W, kR, ALIGNED>;
   static const Held held = held_clusters(kernel, 32 * W, S::kBytes);
   if (held.status != cudaSuccess) return held.status;
   const int64_t tiles = (p.channels + kTileC - 1) / kTileC;
@@ -288,8 +287,11 @@ cudaError_t launch_grec(const GrecRows<T>& p, const float* lam, float kappa, con
                        rows_aligned(p.i, p.ldi);
   const int64_t units = (p.channels + kTileC - 1) / kTileC * p.batch;
   const bool four = sizeof(T) == 2 && units >= kFourWarpUnits;
-  auto* launch = four ? (aligned ? launch_forward<T, 4, true> : launch_forward<T, 4, false>)
-                      : (aligned ? launch_forward<T, 8, true> : launch_forward<T, 8, false>);
+  // Rows that are not aligned take more shared memory and instructions to stage: eight rows a warp, so that
+  // an SM holds two blocks (5 x 777 x 523 FP16 27 to 17 us; aligned rows lose 5 to 25%).
+  auto* launch = four      ? (aligned ? launch_forward<T, 4, 16, true> : launch_forward<T, 4, 16, false>)
+                 : aligned ? launch_forward<T, 8, 16, true>
+                           : launch_forward<T, 8, 8, false>;
   return launch(p, lam, kappa, h0, h, ldh, hT, tape, stream);
 }
 

@@ -238,6 +238,9 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
         if (small && whole) {
 #pragma unroll
           for (int j = kR - 1; j >= 0; --j) emit(j, std::true_type(), std::true_type());
+        } else if (!ALIGNED && small) {
+#pragma unroll
+          for (int j = kR - 1; j >= 0; --j) emit(j, std::true_type(), std::false_type());
         } else if (whole) {
 #pragma unroll
           for (int j = kR - 1; j >= 0; --j) emit(j, std::false_type(), std::true_type());
