@@ -75,7 +75,10 @@ grec_forward_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa, c
   int parity = 0;
   if (peers > 1) cluster_sync();  // every block runs before one writes to another
 
-  for (int64_t s = blockIdx.y; s < p.batch; s += gridDim.y) {
+  for (int64_t y = blockIdx.y; y < p.batch; y += gridDim.y) {
+    const int64_t s = p.offsets != nullptr && p.batch <= kSortedBatch
+                          ? nth_longest(p.offsets, static_cast<int>(p.batch), static_cast<int>(y))
+                          : y;
     int64_t start, end;
     sequence_rows(p.offsets, s, p.length, p.rows, &start, &end);
     float2 state = make_float2(0.f, 0.f);

@@ -91,7 +91,10 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
   int parity = 0;
   if (peers > 1) cluster_sync();  // every block runs before one writes to another
 
-  for (int64_t s = blockIdx.y; s < p.batch; s += gridDim.y) {
+  for (int64_t y = blockIdx.y; y < p.batch; y += gridDim.y) {
+    const int64_t s = p.offsets != nullptr && p.batch <= kSortedBatch
+                          ? nth_longest(p.offsets, static_cast<int>(p.batch), static_cast<int>(y))
+                          : y;
     int64_t start, end;
     sequence_rows(p.offsets, s, p.length, p.rows, &start, &end);
     float2 carry = make_float2(0.f, 0.f);  // a_{t+1} g_{t+1} at the end of the step's rows

@@ -97,6 +97,26 @@ __device__ __forceinline__ void stage_tile(char* smem, const T* base, unsigned r
   }
 }
 
+// Packed sequences of few batches are taken longest first, since the last to start is the last to
+// end: the number of the n-th longest, the same for a whole block. All threads take part.
+constexpr int kSortedBatch = 128;
+
+__device__ __forceinline__ int64_t nth_longest(const int64_t* offsets, int batch, int n) {
+  __shared__ int64_t lengths[kSortedBatch];
+  __shared__ int chosen;
+  const int t = threadIdx.x;
+  if (t < batch) lengths[t] = offsets[t + 1] - offsets[t];
+  __syncthreads();
+  if (t < batch) {
+    const int64_t mine = lengths[t];
+    int rank = 0;
+    for (int j = 0; j < batch; ++j) rank += lengths[j] > mine || (lengths[j] == mine && j < t);
+    if (rank == n) chosen = t;
+  }
+  __syncthreads();
+  return chosen;
+}
+
 // What staged_pair() needs to know of an operand's rows from row `row` where they are not aligned.
 struct Shift {
   unsigned low, pitch;

@@ -1,6 +1,7 @@
 /*
  * bsolve.h -- C ABI of libbsolve.so: batched solution of many independent small dense
- * linear systems A x = b on one GPU (sm_103a).
+ * linear systems A x = b on one GPU (sm_103a), and the row operators of recurrent layers
+ * (bs_grec, bs_gnorm: their own sections below).
  *
  * Every entry point solves `batch` independent systems in one asynchronous launch (two
  * when a factor and a solve run apart: a fused call with more than 8 right-hand sides,
@@ -19,8 +20,9 @@
  * take the interleaved AoSoA/SoA layouts: bs_options.interleave.)
  *
  * Errors are reported synchronously, before anything is launched:
- *   BS_ERR_INVALID_ARG  null pointer, negative size, a base address not 16-byte aligned,
- *                       or two operands of the call whose byte ranges overlap;
+ *   BS_ERR_INVALID_ARG  null pointer, negative size, a base address not 16-byte aligned
+ *                       (bs_grec and bs_gnorm calls: not aligned to its elements), or two
+ *                       operands of the call whose byte ranges overlap;
  *   BS_ERR_UNSUPPORTED  a shape, dtype, layout or fill with no kernel instance (there is
  *                       no CPU fallback: the caller chooses another path);
  *   BS_ERR_CUDA         the launch itself failed (bs_last_cuda_error() gives the code).
@@ -395,6 +397,7 @@ BS_API bs_status bs_bdmv2_batched(bs_dtype dtype, int num_block_rows, int block_
  *            slot outside 0 .. num_slots - 1 changes no state and gets y = 0. Two rows with
  *            one slot: unspecified states.
  *   y        the new states, in dtype.
+ * batch == 0: nothing is launched but the backward call's zeros in dlam.
  * Results do not depend on the stream or the run: no atomics, a fixed order of every sum.
  * Supported: 1 <= channels <= 2^20, batch <= 2^31 - 1, rows <= 2^30, ld <= 2^21, kappa finite
  * and > 0.

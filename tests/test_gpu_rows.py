@@ -158,6 +158,19 @@ def test_recurrence_many_sequences():
     run_recurrence(rng, "bf16", 10, uniform(1500, 5), 7500, packed=False)
 
 
+@pytest.mark.parametrize("kind,channels", [("bf16", 104), ("bf16", 99), ("f16", 128), ("f32", 100)])
+def test_recurrence_many_sequences_of_several_steps(kind, channels):
+    """Enough pairs of a sequence and a tile that blocks of four warps take each alone."""
+    rng = np.random.default_rng(18)
+    run_recurrence(rng, kind, channels, uniform(230, 133), 230 * 133, packed=False)
+
+
+def test_recurrence_more_sequences_than_a_grid_has_rows():
+    rng = np.random.default_rng(19)
+    cuts = np.concatenate([[0, 1], np.arange(2, 70001), [70300]])
+    run_recurrence(rng, "bf16", 5, list(zip(cuts[:-1].tolist(), cuts[1:].tolist())), 70300)
+
+
 def test_recurrence_without_states():
     rng = np.random.default_rng(9)
     run_recurrence(rng, "bf16", 64, uniform(2, 100), 200, packed=False, h0=False)
@@ -247,7 +260,8 @@ def test_recurrence_offsets_past_32_bits():
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("batch,c,pad", [(1, 1, 0), (1, 2048, 0), (3, 65, 0), (17, 200, 3),
-                                         (300, 128, 8), (5, 1000, 1)])
+                                         (300, 128, 8), (5, 1000, 1),
+                                         (6000, 66, 0)])
 @pytest.mark.parametrize("slots", [False, True])
 def test_step(kind, batch, c, pad, slots):
     rng = np.random.default_rng(batch + c)
@@ -368,6 +382,15 @@ def test_norms_widths(kind, width):
 @pytest.mark.parametrize("rows,width", [(1, 64), (1, 4096), (1237, 96), (700, 1024), (3000, 40)])
 def test_norms_rows(kind, rows, width):
     run_norms(np.random.default_rng(rows), kind, rows, width)
+
+
+@pytest.mark.parametrize("kind,rows,width,pads", [
+    ("bf16", 5000, 1024, (0, 0)), ("f16", 1500, 4096, (0, 8)), ("f32", 1300, 4096, (0, 0)),
+    ("bf16", 700, 8192, (0, 0)), ("bf16", 1400, 4000, (1, 0)), ("f32", 2600, 1001, (0, 0)),
+    ("f16", 40001, 64, (0, 0)), ("bf16", 30011, 100, (0, 4)), ("bf16", 400, 17000, (0, 0))])
+def test_norms_more_rows_than_blocks_hold(kind, rows, width, pads):
+    """Blocks walk several turns of rows, the last of them short."""
+    run_norms(np.random.default_rng(rows), kind, rows, width, pads=pads)
 
 
 @pytest.mark.parametrize("parts", ["".join(p) for n in range(7)
