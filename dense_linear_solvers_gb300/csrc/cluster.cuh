@@ -52,10 +52,6 @@ __device__ __forceinline__ void store_remote(V* at, int rank, const V& v) {
                : "memory");
 }
 
-__device__ __forceinline__ unsigned low_bits(const void* p) {
-  return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p));
-}
-
 // Stores two neighbouring elements, as one value where `pairs` says that they are aligned.
 // WHOLE: both are there and aligned.
 template <typename T, bool WHOLE>

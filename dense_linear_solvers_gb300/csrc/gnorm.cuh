@@ -14,7 +14,6 @@
 
 #include <type_traits>
 
-#include "cluster.cuh"
 #include "gnorm_math.cuh"
 #include "gnorm_shapes.cuh"
 #include "kernels.h"

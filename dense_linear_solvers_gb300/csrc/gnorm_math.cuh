@@ -6,8 +6,8 @@
 
 #include <cuda_runtime.h>
 
+#include "common.cuh"
 #include "grec_math.cuh"
-#include "grec_tile.cuh"
 #include "row_types.cuh"
 
 namespace bsolve {

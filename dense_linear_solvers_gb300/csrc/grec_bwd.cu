@@ -23,6 +23,7 @@
 
 #include "cluster.cuh"
 #include "grec_math.cuh"
+#include "grec_order.cuh"
 #include "grec_tile.cuh"
 #include "kernels.h"
 #include "row_types.cuh"
@@ -93,7 +94,8 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
 
   for (int64_t y = blockIdx.y; y < p.batch; y += gridDim.y) {
     const int64_t s = p.offsets != nullptr && p.batch <= kSortedBatch
-                          ? nth_longest(p.offsets, static_cast<int>(p.batch), static_cast<int>(y))
+                          ? nth_longest(p.offsets, static_cast<int>(p.batch), static_cast<int>(y),
+                                        reinterpret_cast<int64_t*>(shared))
                           : y;
     int64_t start, end;
     sequence_rows(p.offsets, s, p.length, p.rows, &start, &end);

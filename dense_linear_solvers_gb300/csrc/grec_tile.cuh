@@ -24,12 +24,6 @@ struct Tile {
   static constexpr int kRowBytes = kTileC * sizeof(T) + (kShifted ? 16 : 0);
 };
 
-__device__ __forceinline__ void cp_async_16(void* smem, const void* gmem, int bytes) {
-  const unsigned d = static_cast<unsigned>(__cvta_generic_to_shared(smem));
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(d), "l"(gmem), "r"(bytes)
-               : "memory");
-}
-
 // Copies `rows` rows from row `row` of an operand, columns from c0 (`valid` of them are there), into
 // smem (whole: R rows of 64 elements). All lanes of the warp take part. Nothing outside the
 // operand is read; what lies behind a row's valid elements in shared memory is unspecified.
@@ -95,26 +89,6 @@ __device__ __forceinline__ void stage_tile(char* smem, const T* base, unsigned r
         cp_async_16(to + 16 * kPieces, from + 16 * kPieces, bytes + shift - 16 * kPieces);
     }
   }
-}
-
-// Packed sequences of few batches are taken longest first, since the last to start is the last to
-// end: the number of the n-th longest, the same for a whole block. All threads take part.
-constexpr int kSortedBatch = 128;
-
-__device__ __forceinline__ int64_t nth_longest(const int64_t* offsets, int batch, int n) {
-  __shared__ int64_t lengths[kSortedBatch];
-  __shared__ int chosen;
-  const int t = threadIdx.x;
-  if (t < batch) lengths[t] = offsets[t + 1] - offsets[t];
-  __syncthreads();
-  if (t < batch) {
-    const int64_t mine = lengths[t];
-    int rank = 0;
-    for (int j = 0; j < batch; ++j) rank += lengths[j] > mine || (lengths[j] == mine && j < t);
-    if (rank == n) chosen = t;
-  }
-  __syncthreads();
-  return chosen;
 }
 
 // What staged_pair() needs to know of an operand's rows from row `row` where they are not aligned.

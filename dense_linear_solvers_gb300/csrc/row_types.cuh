@@ -24,6 +24,11 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
+// The low bits of an address.
+__device__ __forceinline__ unsigned low_bits(const void* p) {
+  return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p));
+}
+
 // Two neighbouring elements: as one value of twice the size, and in FP32.
 template <typename T>
 struct Pair;
