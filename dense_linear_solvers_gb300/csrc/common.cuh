@@ -90,13 +90,6 @@ __device__ __forceinline__ void cp_async_elem(T* smem_dst, const T* gmem_src) {
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(d), "l"(gmem_src) : "memory");
 }
-// 16 bytes of which the first `bytes` are read, the others zero (both addresses 16-byte aligned);
-// past the first cache level.
-__device__ __forceinline__ void cp_async_16(void* smem, const void* gmem, int bytes) {
-  const unsigned d = static_cast<unsigned>(__cvta_generic_to_shared(smem));
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(d), "l"(gmem), "r"(bytes)
-               : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;\n" ::: "memory");
 }

@@ -29,6 +29,14 @@ __device__ __forceinline__ unsigned low_bits(const void* p) {
   return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p));
 }
 
+// Asynchronous copy to shared memory: 16 bytes of which the first `bytes` are read, the others zero (both addresses 16-byte aligned);
+// past the first cache level.
+__device__ __forceinline__ void cp_async_16(void* smem, const void* gmem, int bytes) {
+  const unsigned d = static_cast<unsigned>(__cvta_generic_to_shared(smem));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(d), "l"(gmem), "r"(bytes)
+               : "memory");
+}
+
 // Two neighbouring elements: as one value of twice the size, and in FP32.
 template <typename T>
 struct Pair;
