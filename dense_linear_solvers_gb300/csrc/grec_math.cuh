@@ -80,7 +80,8 @@ __device__ __forceinline__ float grec_rate_slope(float lam) {
 //     a >= 0.6): m = t - t^2 q(t), q the polynomial of degree 3 with the least relative error
 //     of m on [0, 0.5], 2^-24. Otherwise t = n ln 2 + f with |f| <= ln 2 / 2,
 //     m = (1 - 2^-n) + 2^-n (f - f^2 q(f)), q of degree 4 (2^-27), t bounded at 80, where a is 2e-35.
-//     On 16,384 x 4,096 BF16 rows the two take 26 and 32 instructions an element.
+//     On 16,384 x 4,096 BF16 rows the two forward passes take 28 and 34 instructions an element,
+//     117 and 126 us.
 //   2^-124 more in t, which no other value notices, keeps the root below away from 0 / 0:
 //   s = sqrt(1 - a^2) = w rsqrt(w), t / s = t rsqrt(w).
 // The approximate exponential, reciprocal and root are within 2 ulp of FP32 (2^-22), two
