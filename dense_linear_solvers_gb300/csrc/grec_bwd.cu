@@ -11,12 +11,11 @@
 // W * R rows, which start at a state on the tape, so that the states need no exchange between blocks;
 // consecutive pieces lie on the blocks of a cluster, which walk the sequence from its end.
 // One step:
-//   each warp turns its rows into a_t, the gates and the three compositions' parts: A the product
-//     of the a_t, H the state from zero (forward), P the gradient a_t g_t handed on from
-//     zero (backward);
+//   each warp turns its rows into running compositions, A the product of the a_t and H the state from
+//     zero, kept in registers, and P = sum of A_t dh_t, the gradient a_t g_t handed on from zero;
 //   the warps meet in shared memory, the blocks' (A, P) in every block's over the cluster;
-//   each warp runs its rows forward from its true state, then backward from its true gradient,
-//     writing the three gradients.
+//   each warp walks its rows backward from its true gradient, each with the state that its
+//     composition gives from the warp's true one, writing the three gradients.
 // The gradient of lam: every lane sums D = dL/dl * l over its rows, the block's warps are added at
 // the end and each block writes one partial sum a channel; a second kernel adds those in order.
 #include <type_traits>
@@ -149,19 +148,18 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
         return staged_pair<T, ALIGNED>(in + operand * S::kOperand, j, at);
       };
 
-      float2 a[kR], er[kR], ei[kR], hb[kR];
+      // of row j: e^-r, e^-i; from the warp's first row to it the product of a and the state from zero
+      float2 er[kR], ei[kR], A[kR] = {}, H[kR] = {};
       Exchange m{both(1.f), both(0.f)};
-      float2 H = both(0.f);
       auto element = [&](int j, auto kind) {
         er[j] = grec_exp_neg<true>(read(1, j, lr));
         ei[j] = grec_exp_neg<true>(read(2, j, li));
         const Gates q = grec_gates<decltype(kind)::value>(er[j], ei[j], rate);
-        a[j] = q.a;
-        hb[j] = q.s * q.si * read(0, j, lx);  // u, until the states are known
-        H = fma2(a[j], H, hb[j]);
-        m.A = m.A * a[j];
+        const float2 u = q.s * q.si * read(0, j, lx);
+        A[j] = j == 0 ? q.a : q.a * A[j > 0 ? j - 1 : 0];
+        H[j] = j == 0 ? u : fma2(q.a, H[j > 0 ? j - 1 : 0], u);
+        m.P = fma2(A[j], read(3, j, lh), m.P);
       };
-      auto back = [&](int j) { m.P = a[j] * (m.P + read(3, j, lh)); };
       if (n == kR) {
         if (small) {
 #pragma unroll
@@ -170,35 +168,43 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
 #pragma unroll
           for (int j = 0; j < kR; ++j) element(j, std::false_type());
         }
-#pragma unroll
-        for (int j = kR - 1; j >= 0; --j) back(j);
       } else {
 #pragma unroll
-        for (int j = 0; j < kR; ++j)
-          if (j < n) element(j, std::false_type());
-#pragma unroll
-        for (int j = kR - 1; j >= 0; --j)
-          if (j < n) back(j);
+        for (int j = 0; j < kR; ++j) {
+          if (j < n) {
+            element(j, std::false_type());
+          } else {  // past the sequence's end a row hands on what it gets
+            A[j] = j == 0 ? both(1.f) : A[j > 0 ? j - 1 : 0];
+            H[j] = j == 0 ? both(0.f) : H[j > 0 ? j - 1 : 0];
+          }
+        }
       }
+      m.A = A[kR - 1];
 
       Exchange* seg = segments + parity * W * 32 + lane;
       float2* st = states + parity * W * 32 + lane;
       seg[warp * 32] = m;
-      st[warp * 32] = H;
+      st[warp * 32] = H[kR - 1];
       __syncthreads();
       Exchange behind{both(1.f), both(0.f)};  // the block's rows behind the warp's
 #pragma unroll
       for (int w = W - 1; w > 0; --w)
         if (w > warp) behind = compose(seg[w * 32], behind);
-      float2 after = carry;  // what comes from behind the block's, then the warp's rows
+      Exchange* blk = blocks + parity * kMaxCluster * 32 + lane;
       if (peers > 1) {
-        Exchange* blk = blocks + parity * kMaxCluster * 32 + lane;
         if (warp == 0) {
           const Exchange all = compose(m, behind);
           for (int q = 0; q < peers; ++q) store_remote(blk + rank * 32, q, all);
           cluster_publish();
         }
-        cluster_sync();
+        cluster_arrive();
+      }
+#pragma unroll
+      for (int w = 0; w < W - 1; ++w)
+        if (w < warp) before = fma2(seg[w * 32].A, before, st[w * 32]);
+      float2 after = carry;  // what comes from behind the block's, then the warp's rows
+      if (peers > 1) {
+        cluster_wait();
 #pragma unroll
         for (int q = kMaxCluster - 1; q >= 0; --q) {
           if (q >= peers) continue;
@@ -210,36 +216,28 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
         for (int w = W - 1; w >= 0; --w) carry = apply(seg[w * 32], carry);
       }
       after = apply(behind, after);
-#pragma unroll
-      for (int w = 0; w < W - 1; ++w)
-        if (w < warp) before = fma2(seg[w * 32].A, before, st[w * 32]);
       parity ^= 1;
 
       T* dx = g.dx + c + row * g.lddx;
       T* dr = g.dr + c + row * g.lddr;
       T* di = g.di + c + row * g.lddi;
-      auto forth = [&](int j) {
-        const float2 u = hb[j];
-        hb[j] = before;
-        before = fma2(a[j], before, u);
-      };
       auto emit = [&](int j, auto kind, auto all) {
         constexpr bool kWhole = decltype(all)::value;
         const float2 x = read(0, j, lx);
         const float2 gt = read(3, j, lh) + after;
-        after = a[j] * gt;
         // the gates again from their exponentials: fewer registers than keeping them all
         const Gates q = grec_gates<decltype(kind)::value>(er[j], ei[j], rate);
+        after = q.a * gt;
         const float2 y = q.si * x, gs = gt * q.s;
-        const float2 d = after * (y * a[j] * (q.t * q.rs) + both(-1.f) * (q.t * hb[j]));
+        // the state before the row, and D = g a t (sigma(i) x a / s - h)
+        const float2 h = j == 0 ? before : fma2(A[j > 0 ? j - 1 : 0], before, H[j > 0 ? j - 1 : 0]);
+        const float2 d = after * q.t * fma2(y * q.a, q.rs, h * both(-1.f));
         dlam = dlam + d;
         store_pair<T, kWhole>(row_at(dx, j, pdx), gs * q.si, g.px, first, second);
         store_pair<T, kWhole>(row_at(di, j, pdi), gs * y * (ei[j] * q.si), g.pi, first, second);
         store_pair<T, kWhole>(row_at(dr, j, pdr), d * (er[j] * q.sr), g.pr, first, second);
       };
       if (n == kR) {
-#pragma unroll
-        for (int j = 0; j < kR; ++j) forth(j);
         if (small && whole) {
 #pragma unroll
           for (int j = kR - 1; j >= 0; --j) emit(j, std::true_type(), std::true_type());
@@ -254,9 +252,6 @@ grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__
           for (int j = kR - 1; j >= 0; --j) emit(j, std::false_type(), std::false_type());
         }
       } else {
-#pragma unroll
-        for (int j = 0; j < kR; ++j)
-          if (j < n) forth(j);
 #pragma unroll
         for (int j = kR - 1; j >= 0; --j)
           if (j < n) emit(j, std::false_type(), std::false_type());
