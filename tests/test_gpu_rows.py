@@ -309,6 +309,57 @@ def test_steps_equal_the_sequence():
     near(hT, ref.hT, ref.err["hT"], "f32", "hT")
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_recurrence_norm_of_the_error(kind):
+    """The worst-case bounds above grow with the memory; the errors themselves are independent roundings.
+    A 32-bit result sums up to 1000 rows' errors of 2^-22, which add like their root to 2^-17 of the
+    result's norm at most; a stored 16-bit row has its own rounding, uniform in half a unit, of
+    at most 2^-8 (2^-11) / sqrt(3), besides."""
+    rng = np.random.default_rng(20)
+    rows, c = 2000, 256
+    x, r, i, dh = (values(rng, (rows, c), kind) for _ in range(4))
+    la = rng.uniform(-7, 0, c).astype(np.float32).astype(np.float64)
+    start, dT = (rng.standard_normal((2, c)).astype(np.float32).astype(np.float64) for _ in range(2))
+    ref = Recurrence(x, r, i, la, 8.0, uniform(2, 1000), start).backward(dh, dT)
+    t = [torch.from_numpy(v).to(DT[kind]).cuda().view(2, 1000, c) for v in (x, r, i, dh)]
+    out = {k: torch.empty_like(t[0]) for k in ("h", "dx", "dr", "di")}
+    out.update({k: torch.empty(2, c, device="cuda") for k in ("hT", "dh0")}, dlam=torch.empty(c, device="cuda"))
+    tape = torch.empty(bs.bs_grec_tape_rows(2, rows), c, device="cuda")
+    work = torch.empty(bs.bs_grec_backward_workspace(c, 2, rows), dtype=torch.uint8, device="cuda")
+    bs.bs_grec_batched(*t[:3], f32(la), out["h"], h0=f32(start), hT=out["hT"], tape=tape)
+    bs.bs_grec_backward_batched(*t[:3], f32(la), tape, t[3], out["dx"], out["dr"], out["di"],
+                                out["dlam"], work, dhT=f32(dT), dh0=out["dh0"])
+    for k, v in out.items():
+        want = getattr(ref, k)
+        own = {"f32": 0.0, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[kind] / np.sqrt(3) if v.dim() == 3 else 0.0
+        off = np.linalg.norm(v.double().cpu().numpy().reshape(want.shape) - want)
+        assert off <= (2.0 ** -17 + own) * np.linalg.norm(want), (k, off / np.linalg.norm(want))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_norms_norm_of_the_error(kind):
+    """As above: 32-bit results sum the rows' or the elements' errors of 2^-22 like their root."""
+    rng = np.random.default_rng(21)
+    rows, w = 500, 1024
+    f, z, x, dy, du = (values(rng, (rows, w), kind) for _ in range(5))
+    ws = [(1 + 0.3 * rng.standard_normal(w)).astype(np.float32).astype(np.float64) for _ in range(3)]
+    ref = Norms(f, z, x, *ws).backward(dy, du)
+    tf, tz, tx, tdy, tdu = (torch.from_numpy(v).to(DT[kind]).cuda() for v in (f, z, x, dy, du))
+    vec = [f32(v) for v in ws]
+    out = {k: torch.empty_like(tf) for k in ("y", "u", "df", "dz", "dx")}
+    out.update({k: torch.empty(w, device="cuda") for k in ("dw_post", "dscale", "dw_pre")})
+    bs.bs_gnorm_batched(tf, out["y"], z=tz, x=tx, w_post=vec[0], scale=vec[1], w_pre=vec[2], u=out["u"])
+    work = torch.empty(bs.bs_gnorm_backward_workspace(w, rows), dtype=torch.uint8, device="cuda")
+    bs.bs_gnorm_backward_batched(
+        tf, tdy, out["df"], work, z=tz, x=tx, w_post=vec[0], scale=vec[1], w_pre=vec[2], du=tdu,
+        **{k: out[k] for k in ("dz", "dx", "dw_post", "dscale", "dw_pre")})
+    for k, v in out.items():
+        want = getattr(ref, k)
+        own = {"f32": 0.0, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[kind] / np.sqrt(3) if v.dim() == 2 else 0.0
+        off = np.linalg.norm(v.double().cpu().numpy() - want)
+        assert off <= (2.0 ** -17 + own) * np.linalg.norm(want), (k, off / np.linalg.norm(want))
+
+
 def test_recurrence_is_the_same_every_time():
     rng = np.random.default_rng(16)
     c, rows = 520, 5000
