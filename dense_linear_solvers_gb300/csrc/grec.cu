@@ -276,12 +276,13 @@ cudaError_t launch_forward(const GrecRows<T>& p, const float* lam, float kappa, 
                          pair_stores(h, ldh), hT, tape);
 }
 
-// Blocks of four warps, without clusters, on 16-bit rows while the pairs of a sequence and a tile fill the GPU by
-// themselves (152 SMs with three blocks): 64 x 512 rows x 2,048 channels BF16 take 94 us, with eight
-// warps 106; 24 packed prompts of 500 rows on average 60 us, with clusters of two 66. Otherwise
-// eight, which meet less often: one sequence of 65,536 x 4,096 takes 450 us, with four
-// warps 501; 4 x 4,096 x 2,048 FP32 86 us and 90.
-constexpr int64_t kFourWarpUnits = 3 * 152;
+// Blocks of four warps, without clusters, on 16-bit rows while there is a pair of a sequence and a tile
+// for every SM: 64 x 512 rows x 2,048 channels BF16 take 89 us, with eight warps 102; 8 x 4,096 rows
+// 108 and 112. Otherwise eight, which meet less often: one sequence of 65,536 x 4,096 takes 445
+// us, with four warps 501; 4 x 4,096 x 2,048 FP32 86 and 90. Packed sequences end with their longest,
+// which more warps and clusters shorten (60 of 670 rows on average x 1,024: 70 us with eight, 75
+// with four), until there are so many that it does not show (128 of 470: 93 with four, 115).
+constexpr int64_t kFourWarpUnits = 152, kFourWarpUnitsPacked = 10 * 152;
 
 }  // namespace
 
@@ -291,7 +292,8 @@ cudaError_t launch_grec(const GrecRows<T>& p, const float* lam, float kappa, con
   const bool aligned = rows_aligned(p.x, p.ldx) && rows_aligned(p.r, p.ldr) &&
                        rows_aligned(p.i, p.ldi);
   const int64_t units = (p.channels + kTileC - 1) / kTileC * p.batch;
-  const bool four = sizeof(T) == 2 && units >= kFourWarpUnits;
+  const bool four =
+      sizeof(T) == 2 && units >= (p.offsets ? kFourWarpUnitsPacked : kFourWarpUnits);
   // Rows that are not aligned take more shared memory and instructions to stage: eight rows a warp, so that
   // an SM holds two blocks (5 x 777 x 523 FP16 27 to 17 us; aligned rows lose 5 to 25%).
   auto* launch = four      ? (aligned ? launch_forward<T, 4, 16, true> : launch_forward<T, 4, 16, false>)

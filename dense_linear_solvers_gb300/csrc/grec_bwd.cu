@@ -306,10 +306,10 @@ grec_dlam_kernel(int channels, int64_t parts, const float* __restrict__ lam,
   dlam[c] = sum * grec_rate_slope(lam[c]);
 }
 
-// Blocks of four warps on 16-bit rows where there is a pair of a sequence and a tile for every SM: 24
-// packed sequences of 1,000 rows on average, 2,048 channels BF16, take 201 us, with eight warps
-// 222; 64 x 512 rows 227 and 239. Otherwise eight, which meet less often: one sequence of
-// 32,768 rows takes 310 us, with four warps 380; 4 x 4,096 rows FP32 183 and 193.
+// Blocks of four warps on 16-bit rows where there is a pair of a sequence and a tile for every SM: 64 x
+// 512 rows x 2,048 channels BF16 take 221 us, with eight warps 230 and more; 24 packed sequences of
+// 1,000 rows on average 181 and 184. Otherwise eight, which meet less often: one sequence of
+// 32,768 rows takes 288 us, with four warps 70 more; 4 x 4,096 rows FP32 178 and 10 more.
 constexpr int64_t kFourWarpUnits = 152;
 
 int64_t tiles_of(int channels) { return (channels + kTileC - 1) / kTileC; }
