@@ -1,15 +1,21 @@
 // The norms around a block with its gate and residual scale (bs_gnorm calls of bsolve.h): kernels and
 // launchers, one instance a row type (gnorm_f32.cu, gnorm_bf16.cu, gnorm_f16.cu).
 //
-// A row belongs to a group of 8 to 1024 threads, each with K 16-byte vectors of it; a group takes
-// ROWS rows at a time, and persistent blocks walk all of them. Each thread copies its own vectors of
-// the rows of the next turn into shared memory with cp.async while it works on these, so that
-// the loads need no registers and no barrier, and reads them as often as it needs them; the rows'
-// sums go through shuffles and, for groups of several warps, one barrier for all rows of the
-// turn. The parameters stay in the first cache level. The backward pass keeps its three sums over rows in
-// registers, every thread those of its own columns, and each block writes one part of them at
-// its end; a second kernel adds the parts in order. Rows too long for that run the looped kernels at
-// the end, which read a row once for each mean and once for the outputs.
+// A row belongs to a group of 8 to 1024 threads, each with K vectors of it; a group takes ROWS rows
+// at a time, and persistent blocks walk all of them. Each thread copies its own vectors of the rows of the
+// next turn into shared memory with cp.async while it works on these, so that the loads need no
+// registers and no barrier, and reads them as often as it needs them; the rows' sums go through shuffles
+// and, for groups of several warps, one barrier for all rows of the turn, the last sums of a turn
+// together with the first of the next. The parameters stay in the first cache level. The backward pass
+// keeps its three sums over rows in registers, every thread those of its own columns, and each
+// block writes one part of them at its end; a second kernel adds the parts in order. Rows too long for
+// that run the looped kernels at the end, which read a row once for each mean and once for the
+// outputs.
+//
+// 16,384 x 4,096 BF16: forward 112 us (6.0 TB/s of its five operands, 88% of a copy's rate), backward 234
+// us (4.6 TB/s of its eight; one block of 512 threads an SM, which waits at its two reductions a turn).
+// Measured without gain there: every sum in one reduction by expanding sum y^2 (296 against 279 at the
+// time), four elements a thread and twice the warps (279), two vectors a thread and one row (340).
 #pragma once
 
 #include <type_traits>

