@@ -600,12 +600,12 @@ def _row_stream(stream, like) -> int:
 
 def bs_grec_tape_rows(batch: int, rows: int) -> int:
     """Rows of the tape of a recurrence call over batch sequences of rows rows in all."""
-    return lib().bs_grec_tape_rows(batch, rows)
+    return _rows().grec_tape_rows(batch, rows)
 
 
 def bs_grec_backward_workspace(channels: int, batch: int, rows: int) -> int:
     """Bytes of bs_grec_backward_batched's workspace."""
-    return lib().bs_grec_backward_workspace(channels, batch, rows)
+    return _rows().grec_backward_workspace(channels, batch, rows)
 
 
 def bs_grec_batched(x, r, i, lam, h, h0=None, hT=None, offsets=None, tape=None,
@@ -642,7 +642,7 @@ def bs_grec_step_batched(x, r, i, lam, state, y, slots=None, kappa: float = 8.0,
 
 def bs_gnorm_backward_workspace(width: int, rows: int) -> int:
     """Bytes of bs_gnorm_backward_batched's workspace."""
-    return lib().bs_gnorm_backward_workspace(width, rows)
+    return _rows().gnorm_backward_workspace(width, rows)
 
 
 def bs_gnorm_batched(f, y=None, z=None, x=None, w_post=None, scale=None, w_pre=None, u=None,

@@ -268,6 +268,36 @@ PyObject* gnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The size queries: n integers in, one out.
+template <typename F>
+PyObject* query(Py_ssize_t given, Py_ssize_t wanted, F&& f) {
+  if (given != wanted) {
+    PyErr_Format(PyExc_TypeError, "%zd arguments, %zd expected", given, wanted);
+    return nullptr;
+  }
+  try {
+    return PyLong_FromLongLong(static_cast<long long>(f()));
+  } catch (const Refused&) {
+    return nullptr;
+  }
+}
+int small(PyObject* o) {
+  const long long v = integer(o);
+  return v < INT32_MIN || v > INT32_MAX ? -1 : static_cast<int>(v);
+}
+
+PyObject* grec_tape_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return query(n, 2, [&] { return bs_grec_tape_rows(integer(a[0]), integer(a[1])); });
+}
+PyObject* grec_backward_workspace(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return query(n, 3, [&] {
+    return bs_grec_backward_workspace(small(a[0]), integer(a[1]), integer(a[2]));
+  });
+}
+PyObject* gnorm_backward_workspace(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return query(n, 2, [&] { return bs_gnorm_backward_workspace(small(a[0]), integer(a[1])); });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL,
@@ -276,7 +306,11 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<grec>("grec"), method<grec_backward>("grec_backward"),
                          method<grec_step>("grec_step"), method<gnorm>("gnorm"),
-                         method<gnorm_backward>("gnorm_backward"), {nullptr, nullptr, 0, nullptr}};
+                         method<gnorm_backward>("gnorm_backward"),
+                         method<grec_tape_rows>("grec_tape_rows"),
+                         method<grec_backward_workspace>("grec_backward_workspace"),
+                         method<gnorm_backward_workspace>("gnorm_backward_workspace"),
+                         {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rowcall", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
