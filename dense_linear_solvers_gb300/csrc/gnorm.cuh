@@ -655,7 +655,7 @@ gnorm_long_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict_
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLong)
+__global__ void __launch_bounds__(kLong, 2)
 gnorm_long_backward_kernel(GnormRows<T> p, GnormGrads<T> g, float* __restrict__ partial) {
   __shared__ float red[kRedFloats<1, kLong>];
   int turn = 0;

@@ -47,7 +47,9 @@ inline int blocks_for(const Shape& s, int64_t rows, int threads = 1024) {
 
 inline int backward_blocks(int width, int es, int64_t rows) {
   const Shape s = backward_shape(width, es);
-  return blocks_for(s, rows, s.rows == 2 ? 512 : 1024);
+  // looped: two blocks of 1024 threads with 32 registers each (4,096 x 8,192 FP32 training pass: 851 us,
+  // with one block 1,093)
+  return blocks_for(s, rows, s.threads == 0 ? 2 * kLong : (s.rows == 2 ? 512 : 1024));
 }
 
 // dw_post, dscale, dw_pre (null: not wanted) from `parts` partial sums, [parts][3][width].
