@@ -75,13 +75,15 @@ __device__ __forceinline__ float grec_rate_slope(float lam) {
 // What one element's gates give, with l = -t:
 //   sigma(r) = 1 / (1 + e^-r); 1 - sigma(r) = e^-r sigma(r), without cancellation where e^-r is
 //     kept finite (grec_exp_neg<true>, at most 2^100: the sigma below is then 2^-100, not 0).
-//   a = e^-t and 1 - a^2 both come from m = 1 - e^-t, since near a = 1 (long memory) 1 - a^2 =
-//     m (1 + a) keeps its digits while 1 - a*a loses them. SMALL (rate at most kSmallRate, so that
-//     a >= 0.6): m = t - t^2 q(t), q the polynomial of degree 3 with the least relative error
-//     of m on [0, 0.5], 2^-24. Otherwise t = n ln 2 + f with |f| <= ln 2 / 2,
-//     m = (1 - 2^-n) + 2^-n (f - f^2 q(f)), q of degree 4 (2^-27), t bounded at 80, where a is 2e-35.
-//     On 16,384 x 4,096 BF16 rows the two forward passes take 28 and 34 instructions an element,
-//     117 and 126 us.
+//   1 - a^2 comes from m = 1 - e^-t, since near a = 1 (long memory) 1 - a^2 = m (1 + a) keeps its
+//     digits while 1 - a*a loses them. SMALL (rate at most kSmallRate, so that a >= 0.6): m =
+//     t - t^2 q(t), q the polynomial of degree 3 with the least relative error of m on [0, 0.5],
+//     2^-24, and a = 1 - m. Otherwise t = n ln 2 + f with |f| <= ln 2 / 2 (Cody and Waite: n rounded
+//     by adding 1.5 * 2^23, ln 2 in two parts), e = 1 - e^-f = f - f^2 q(f), q of degree 4 (2^-27),
+//     m = (1 - 2^-n) + 2^-n e and a = 2^-n - 2^-n e: taken from m, a small a would keep the
+//     digits of 1 only (6% off at t = 16, 0 from t = 17 on). t is bounded at 80, where a is 2e-35.
+//     On 16,384 x 4,096 BF16 rows the two forward passes take 119 and 130 us (with the sign of e in a
+//     paired product of its own 134).
 //   2^-124 more in t, which no other value notices, keeps the root below away from 0 / 0:
 //   s = sqrt(1 - a^2) = w rsqrt(w), t / s = t rsqrt(w).
 // The approximate exponential, reciprocal and root are within 2 ulp of FP32 (2^-22), two
@@ -123,6 +125,7 @@ __device__ __forceinline__ Gates grec_gates(float2 er, float2 ei, float2 rate) {
     c = fma2(t, c, both(1.6654362e-1f));
     c = fma2(t, c, both(-4.9999245e-1f));
     m = fma2(t * t, c, t);
+    g.a = fma2(m, both(-1.f), both(1.f));
   } else {
     g.t = make_float2(min_nan(g.t.x, 80.f), min_nan(g.t.y, 80.f));
     const float2 k = fma2(g.t, both(-kLog2e), both(12582912.f));  // 1.5 * 2^23: -n in the low bits
@@ -137,8 +140,8 @@ __device__ __forceinline__ Gates grec_gates(float2 er, float2 ei, float2 rate) {
     const float2 two_n = make_float2(__int_as_float((__float_as_int(k.x) << 23) + 0x3f800000),
                                      __int_as_float((__float_as_int(k.y) << 23) + 0x3f800000));
     m = fma2(two_n, e, fma2(two_n, both(-1.f), both(1.f)));
+    g.a = make_float2(fmaf(-two_n.x, e.x, two_n.x), fmaf(-two_n.y, e.y, two_n.y));
   }
-  g.a = fma2(m, both(-1.f), both(1.f));
   const float2 w = fma2(m, g.a, m);
   g.rs = make_float2(rsqrt_fast(w.x), rsqrt_fast(w.y));
   g.s = w * g.rs;
