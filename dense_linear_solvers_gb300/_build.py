@@ -40,6 +40,11 @@ def nvcc() -> str:
     return path
 
 
+def _cuda() -> str:
+    # the toolkit that nvcc belongs to
+    return os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+
+
 def _newest_input_mtime() -> float:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     files.append(os.path.join(INCLUDE, "bsolve.h"))
@@ -61,7 +66,8 @@ def _compile_rowcall() -> str:
     subprocess.check_call([
         "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
-        "-I", sysconfig.get_paths()["include"], "-isystem", base,
+        "-I", sysconfig.get_paths()["include"], "-I", os.path.join(_cuda(), "include"),
+        "-isystem", base,
         "-isystem", os.path.join(base, "torch", "csrc", "api", "include"),
         "-c", os.path.join(CSRC, "rowcall.cpp"), "-o", obj])
     return obj
@@ -74,7 +80,7 @@ def _link_rowcall(obj: str) -> None:
     subprocess.check_call([
         "g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB),
         "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
-        "-Wl,-rpath," + libs])
+        "-Wl,-rpath," + libs, "-L", os.path.join(_cuda(), "lib64"), "-lcudart"])
     os.replace(tmp, ROWCALL)
 
 

@@ -5,9 +5,11 @@
 #include <Python.h>
 
 #include <cstdint>
+#include <stdexcept>
 #include <string>
 
 #include <ATen/core/Tensor.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "bsolve.h"
@@ -167,6 +169,37 @@ struct Sequences {
   }
 };
 
+// Makes a device current while it lives.
+class OnDevice {
+ public:
+  explicit OnDevice(int64_t device) {
+    check(cudaGetDevice(&before_));
+    if (device == before_) return;
+    check(cudaSetDevice(static_cast<int>(device)));
+    changed_ = true;
+  }
+  ~OnDevice() {
+    if (changed_) cudaSetDevice(before_);
+  }
+  OnDevice(const OnDevice&) = delete;
+  OnDevice& operator=(const OnDevice&) = delete;
+
+ private:
+  static void check(cudaError_t e) {
+    if (e != cudaSuccess) throw std::runtime_error(cudaGetErrorString(e));
+  }
+  int before_ = 0;
+  bool changed_ = false;
+};
+
+// An entry of the C ABI, its arguments all worked out, on the operands' device: the entries launch
+// on the current one, and the null stream that they are often given is every device's.
+template <typename... P, typename... A>
+bs_status enter(const Like& like, bs_status (*entry)(P...), A... args) {
+  const OnDevice device(like.device);
+  return entry(args...);
+}
+
 template <typename F>
 PyObject* guarded(const char* name, Py_ssize_t given, Py_ssize_t wanted, F&& f) {
   if (given != wanted) {
@@ -190,8 +223,8 @@ PyObject* grec(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Row x = row(a[0], "x", l), r = row(a[1], "r", l), i = row(a[2], "i", l),
               h = row(a[4], "h", l);
     const int c = static_cast<int>(l.width);
-    return bs_grec_batched(
-        l.code, c, s.batch, s.rows, s.offsets, x.p, x.ld, r.p, r.ld, i.p, i.ld,
+    return enter(
+        l, bs_grec_batched, l.code, c, s.batch, s.rows, s.offsets, x.p, x.ld, r.p, r.ld, i.p, i.ld,
         f32(a[3], "lam", l, c), number(a[9]), f32(a[5], "h0", l, s.batch * c), h.p, h.ld,
         f32(a[6], "hT", l, s.batch * c),
         f32(a[8], "tape", l, bs_grec_tape_rows(s.batch, s.rows) * c), handle(a[10]));
@@ -208,9 +241,9 @@ PyObject* grec_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int c = static_cast<int>(l.width);
     void* work = vec<void>(a[10], "work", l, -1, at::kByte);
     const size_t bytes = work ? static_cast<size_t>(tensor(a[10], "work")->numel()) : 0;
-    return bs_grec_backward_batched(
-        l.code, c, s.batch, s.rows, s.offsets, x.p, x.ld, r.p, r.ld, i.p, i.ld,
-        f32(a[3], "lam", l, c), number(a[14]),
+    return enter(
+        l, bs_grec_backward_batched, l.code, c, s.batch, s.rows, s.offsets, x.p, x.ld, r.p, r.ld,
+        i.p, i.ld, f32(a[3], "lam", l, c), number(a[14]),
         f32(a[4], "tape", l, bs_grec_tape_rows(s.batch, s.rows) * c), dh.p, dh.ld,
         f32(a[11], "dhT", l, s.batch * c), dx.p, dx.ld, dr.p, dr.ld, di.p, di.ld,
         f32(a[9], "dlam", l, c), f32(a[12], "dh0", l, s.batch * c), work, bytes, handle(a[15]));
@@ -229,9 +262,9 @@ PyObject* grec_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!state || state->dim() != 2 || state->size(1) != c)
       value_error("state: shape " + (state ? text(state->sizes()) : std::string("None")) +
                   ", expected (num_slots, " + std::to_string(c) + ")");
-    return bs_grec_step_batched(
-        l.code, static_cast<int>(c), batch, x.p, x.ld, r.p, r.ld, i.p, i.ld,
-        f32(a[3], "lam", l, c), number(a[7]), f32(a[4], "state", l, state->size(0) * c),
+    return enter(
+        l, bs_grec_step_batched, l.code, static_cast<int>(c), batch, x.p, x.ld, r.p, r.ld, i.p,
+        i.ld, f32(a[3], "lam", l, c), number(a[7]), f32(a[4], "state", l, state->size(0) * c),
         state->size(0), vec<int32_t>(a[6], "slots", l, batch, at::kInt), y.p, y.ld, handle(a[8]));
   });
 }
@@ -242,11 +275,10 @@ PyObject* gnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Row f = row(a[0], "f", l), y = row(a[1], "y", l), z = row(a[2], "z", l),
               x = row(a[3], "x", l), u = row(a[7], "u", l);
     const int w = static_cast<int>(l.width);
-    return bs_gnorm_batched(l.code, l.rows(), w, f.p, f.ld, z.p, z.ld, x.p, x.ld,
-                            f32(a[4], "w_post", l, w), f32(a[5], "scale", l, w),
-                            f32(a[6], "w_pre", l, w), number(a[8]),
-                            static_cast<bs_gate>(integer(a[9])), y.p, y.ld, u.p, u.ld,
-                            handle(a[10]));
+    return enter(
+        l, bs_gnorm_batched, l.code, l.rows(), w, f.p, f.ld, z.p, z.ld, x.p, x.ld,
+        f32(a[4], "w_post", l, w), f32(a[5], "scale", l, w), f32(a[6], "w_pre", l, w),
+        number(a[8]), static_cast<bs_gate>(integer(a[9])), y.p, y.ld, u.p, u.ld, handle(a[10]));
   });
 }
 
@@ -259,9 +291,9 @@ PyObject* gnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int w = static_cast<int>(l.width);
     void* work = vec<void>(a[3], "work", l, -1, at::kByte);
     const size_t bytes = work ? static_cast<size_t>(tensor(a[3], "work")->numel()) : 0;
-    return bs_gnorm_backward_batched(
-        l.code, l.rows(), w, f.p, f.ld, z.p, z.ld, x.p, x.ld, f32(a[6], "w_post", l, w),
-        f32(a[7], "scale", l, w), f32(a[8], "w_pre", l, w), number(a[15]),
+    return enter(
+        l, bs_gnorm_backward_batched, l.code, l.rows(), w, f.p, f.ld, z.p, z.ld, x.p, x.ld,
+        f32(a[6], "w_post", l, w), f32(a[7], "scale", l, w), f32(a[8], "w_pre", l, w), number(a[15]),
         static_cast<bs_gate>(integer(a[16])), dy.p, dy.ld, du.p, du.ld, df.p, df.ld, dz.p, dz.ld,
         dx.p, dx.ld, f32(a[12], "dw_post", l, w), f32(a[13], "dscale", l, w),
         f32(a[14], "dw_pre", l, w), work, bytes, handle(a[17]));
