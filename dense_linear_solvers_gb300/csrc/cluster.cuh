@@ -2,8 +2,9 @@
 // shared memory, and the launch.
 #pragma once
 
-#include <cstdint>
 #include <cmath>
+#include <cstdint>
+#include <mutex>
 #include <cuda_runtime.h>
 
 #include "row_types.cuh"
@@ -96,25 +97,50 @@ inline cudaLaunchConfig_t cluster_config(cudaLaunchAttribute* attr, dim3 grid, i
   return config;
 }
 
-// How many clusters of 1, 2, 4, 8 blocks of a kernel the GPU holds at once; asked of the
-// driver at the kernel's first launch.
+// How many clusters of 1, 2, 4, 8 blocks of a kernel the current device holds at once.
 struct Held {
   int clusters[kMaxCluster + 1];
-  cudaError_t status;
 };
 
-template <typename... P>
-Held held_clusters(void (*kernel)(P...), int threads, int shared) {
-  Held h{};
-  h.status = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
-  for (int n = 1; n <= kMaxCluster && h.status == cudaSuccess; n *= 2) {
-    cudaLaunchAttribute attr{};
-    const cudaLaunchConfig_t config =
-        cluster_config(&attr, dim3(n), threads, shared, n, nullptr);
-    h.status = cudaOccupancyMaxActiveClusters(&h.clusters[n], kernel, &config);
+// The answers for one kernel, asked of the driver at its first launch on a device (a few us each); an
+// error is handed on and asked again by the next launch.
+class HeldClusters {
+ public:
+  template <typename... P>
+  cudaError_t of(void (*kernel)(P...), int threads, int shared, Held* held) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    // a device's own limit: raised before every launch, as by the other launchers
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+    if (e != cudaSuccess) return e;
+    const std::lock_guard<std::mutex> lock(mutex_);
+    const bool kept = device < kDevices;
+    if (kept && known_[device]) {
+      *held = held_[device];
+      return cudaSuccess;
+    }
+    Held h{};
+    for (int n = 1; n <= kMaxCluster; n *= 2) {
+      cudaLaunchAttribute attr{};
+      const cudaLaunchConfig_t config = cluster_config(&attr, dim3(n), threads, shared, n, nullptr);
+      e = cudaOccupancyMaxActiveClusters(&h.clusters[n], kernel, &config);
+      if (e != cudaSuccess) return e;
+    }
+    if (kept) {
+      held_[device] = h;
+      known_[device] = true;
+    }
+    *held = h;
+    return cudaSuccess;
   }
-  return h;
-}
+
+ private:
+  static constexpr int kDevices = 64;  // beyond: asked every time
+  std::mutex mutex_;
+  bool known_[kDevices] = {};
+  Held held_[kDevices] = {};
+};
 
 // Above so many pairs of a sequence and a channel tile, a block takes each alone.
 constexpr int64_t kManyUnits = 8192;

@@ -267,8 +267,10 @@ cudaError_t launch_forward(const GrecRows<T>& p, const float* lam, float kappa, 
                            T* h, int64_t ldh, float* hT, float* tape, cudaStream_t stream) {
   using S = GrecForwardShared<T, W, kR, ALIGNED>;
   auto* kernel = grec_forward_kernel<T, W, kR, ALIGNED>;
-  static const Held held = held_clusters(kernel, 32 * W, S::kBytes);
-  if (held.status != cudaSuccess) return held.status;
+  static HeldClusters known;
+  Held held;
+  const cudaError_t e = known.of(kernel, 32 * W, S::kBytes, &held);
+  if (e != cudaSuccess) return e;
   const int64_t tiles = (p.channels + kTileC - 1) / kTileC;
   const int64_t length = p.offsets ? p.rows / p.batch + 1 : p.length;
   const int cluster =

@@ -321,8 +321,10 @@ cudaError_t launch_backward(const GrecRows<T>& p, const GrecGradRows<T>& g, cons
                             float* partial, int64_t* parts, cudaStream_t stream) {
   using S = GrecBackwardShared<T, ALIGNED>;
   auto* kernel = grec_backward_kernel<T, ALIGNED>;
-  static const Held held = held_clusters(kernel, 32 * W, S::kBytes);
-  if (held.status != cudaSuccess) return held.status;
+  static HeldClusters known;
+  Held held;
+  const cudaError_t e = known.of(kernel, 32 * W, S::kBytes, &held);
+  if (e != cudaSuccess) return e;
   const int64_t length = p.offsets ? p.rows / p.batch + 1 : p.length;
   const int cluster = grec_cluster(held, tiles_of(p.channels), p.batch, length,
                                    p.offsets != nullptr, W * kR);
