@@ -100,10 +100,15 @@ __device__ __forceinline__ void group_sums(float (&v)[N], float* red, int& turn)
   }
 }
 
-// 1 / sqrt(v) for v > 0: the approximate root with one Newton step.
+// 1 / sqrt(v) for v > 0: the approximate root with one Newton step. Below 2^-100 (rows of zeros under a
+// small eps, subnormal numbers included) that of v 2^100, so that neither the root, which takes a
+// subnormal number for 0, nor the step loses digits.
 __device__ __forceinline__ float inverse_root(float v) {
-  const float r = rsqrt_fast(max_nan(v, 0x1p-126f));
-  return r == 0.f ? r : fmaf(r * 0.5f, fmaf(-v * r, r, 1.f), r);  // 0 where v overflowed
+  const bool low = v < 0x1p-100f;
+  if (low) v *= 0x1p100f;
+  const float r = rsqrt_fast(v);
+  const float s = r == 0.f ? r : fmaf(r * 0.5f, fmaf(-v * r, r, 1.f), r);  // 0 where v overflowed
+  return low ? s * 0x1p50f : s;
 }
 
 template <int THREADS>
