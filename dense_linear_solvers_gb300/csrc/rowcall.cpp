@@ -139,6 +139,11 @@ long long integer(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw Refused();
   return v;
 }
+// An int argument: what does not fit is -1, which the calls refuse.
+int small(PyObject* o) {
+  const long long v = integer(o);
+  return v < INT32_MIN || v > INT32_MAX ? -1 : static_cast<int>(v);
+}
 void* handle(PyObject* o) {
   void* v = PyLong_AsVoidPtr(o);
   if (!v && PyErr_Occurred()) throw Refused();
@@ -278,7 +283,7 @@ PyObject* gnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return enter(
         l, bs_gnorm_batched, l.code, l.rows(), w, f.p, f.ld, z.p, z.ld, x.p, x.ld,
         f32(a[4], "w_post", l, w), f32(a[5], "scale", l, w), f32(a[6], "w_pre", l, w),
-        number(a[8]), static_cast<bs_gate>(integer(a[9])), y.p, y.ld, u.p, u.ld, handle(a[10]));
+        number(a[8]), static_cast<bs_gate>(small(a[9])), y.p, y.ld, u.p, u.ld, handle(a[10]));
   });
 }
 
@@ -294,7 +299,7 @@ PyObject* gnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return enter(
         l, bs_gnorm_backward_batched, l.code, l.rows(), w, f.p, f.ld, z.p, z.ld, x.p, x.ld,
         f32(a[6], "w_post", l, w), f32(a[7], "scale", l, w), f32(a[8], "w_pre", l, w), number(a[15]),
-        static_cast<bs_gate>(integer(a[16])), dy.p, dy.ld, du.p, du.ld, df.p, df.ld, dz.p, dz.ld,
+        static_cast<bs_gate>(small(a[16])), dy.p, dy.ld, du.p, du.ld, df.p, df.ld, dz.p, dz.ld,
         dx.p, dx.ld, f32(a[12], "dw_post", l, w), f32(a[13], "dscale", l, w),
         f32(a[14], "dw_pre", l, w), work, bytes, handle(a[17]));
   });
@@ -312,10 +317,6 @@ PyObject* query(Py_ssize_t given, Py_ssize_t wanted, F&& f) {
   } catch (const Refused&) {
     return nullptr;
   }
-}
-int small(PyObject* o) {
-  const long long v = integer(o);
-  return v < INT32_MIN || v > INT32_MAX ? -1 : static_cast<int>(v);
 }
 
 PyObject* grec_tape_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {

@@ -33,3 +33,12 @@ def test_norms_of_small_rows_under_a_small_eps(eps, width):
     want -= n * (dy.double() * 0.5 * n).mean(1, keepdim=True) / eps ** 0.5
     size = dy.double().abs().amax(1, keepdim=True) / eps ** 0.5
     assert bool(((df.double() - want).abs() <= 16 * EPS * size).all())
+
+
+def test_a_gate_past_32_bits_is_refused():
+    f = torch.ones(2, 8, device="cuda")
+    for gate in (1 << 32, (1 << 32) + 1, -(1 << 32), 3, -1):
+        with pytest.raises(bs.BsolveError, match="INVALID_ARG"):
+            bs.bs_gnorm_batched(f, torch.empty_like(f), gate=gate)
+        with pytest.raises(bs.BsolveError, match="INVALID_ARG"):
+            bs.bs_gnorm_backward_batched(f, f, torch.empty_like(f), gate=gate)
