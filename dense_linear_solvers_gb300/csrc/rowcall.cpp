@@ -72,6 +72,14 @@ struct Like {
   int64_t rows() const { return shape.size() == 3 ? shape[0] * shape[1] : shape[0]; }
 };
 
+// The address of a tensor's first element, as stored: a view that torch reads with the other sign
+// (the imaginary part of a conjugate) would be taken for its negative.
+void* address(const at::Tensor& t, const char* name) {
+  if (t.is_neg())
+    value_error(std::string(name) + ": a view with a pending sign; resolve_neg() it first");
+  return t.data_ptr();
+}
+
 struct Row {
   void* p = nullptr;
   int64_t ld = 0;
@@ -105,7 +113,7 @@ Row row(PyObject* o, const char* name, const Like& like) {
     if (t->numel()) value_error(std::string(name) + ": rows overlap");
     r.ld = like.width;
   }
-  r.p = t->data_ptr();
+  r.p = address(*t, name);
   return r;
 }
 
@@ -123,7 +131,7 @@ V* vec(PyObject* o, const char* name, const Like& like, int64_t numel, at::Scala
   if (!t->is_cuda() || t->get_device() != like.device)
     value_error(std::string(name) + ": bsolve operands are device tensors of one device");
   if (!t->is_contiguous()) value_error(std::string(name) + ": must be contiguous");
-  return static_cast<V*>(t->data_ptr());
+  return static_cast<V*>(address(*t, name));
 }
 float* f32(PyObject* o, const char* name, const Like& like, int64_t numel) {
   return vec<float>(o, name, like, numel, at::kFloat);

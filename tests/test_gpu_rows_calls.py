@@ -42,3 +42,15 @@ def test_a_gate_past_32_bits_is_refused():
             bs.bs_gnorm_batched(f, torch.empty_like(f), gate=gate)
         with pytest.raises(bs.BsolveError, match="INVALID_ARG"):
             bs.bs_gnorm_backward_batched(f, f, torch.empty_like(f), gate=gate)
+
+
+def test_views_with_a_pending_sign_are_refused():
+    """Memory that torch reads with the other sign: its values are not the tensor's."""
+    x, lam = torch.ones(2, 10, 8, device="cuda"), torch.zeros(8, device="cuda")
+    neg = torch._neg_view
+    with pytest.raises(ValueError, match="sign"):
+        bs.bs_grec_batched(neg(x), x, x, lam, torch.empty_like(x))
+    with pytest.raises(ValueError, match="sign"):
+        bs.bs_grec_batched(x, x, x, neg(lam), torch.empty_like(x))
+    with pytest.raises(ValueError, match="sign"):
+        bs.bs_gnorm_batched(x, neg(torch.empty_like(x)))
