@@ -205,10 +205,23 @@ class OnDevice {
   bool changed_ = false;
 };
 
+// Lets the program's other threads run: a launch behind a full queue waits for the GPU.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 // An entry of the C ABI, its arguments all worked out, on the operands' device: the entries launch
 // on the current one, and the null stream that they are often given is every device's.
 template <typename... P, typename... A>
 bs_status enter(const Like& like, bs_status (*entry)(P...), A... args) {
+  const Unlocked unlocked;
   const OnDevice device(like.device);
   return entry(args...);
 }

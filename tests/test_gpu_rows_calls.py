@@ -1,4 +1,7 @@
 """Calls of the row operators on the GPU that are rare in use."""
+import threading
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -54,3 +57,71 @@ def test_views_with_a_pending_sign_are_refused():
         bs.bs_grec_batched(x, x, x, neg(lam), torch.empty_like(x))
     with pytest.raises(ValueError, match="sign"):
         bs.bs_gnorm_batched(x, neg(torch.empty_like(x)))
+
+
+def test_other_threads_run_while_a_launch_waits():
+    """A launch behind a full queue waits for the GPU; the other threads of the program do not."""
+    f = torch.ones(2, 8, device="cuda")
+    y = torch.empty_like(f)
+    bs.bs_gnorm_batched(f, y)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    with torch.cuda.stream(stream):
+        start.record()
+        torch.cuda._sleep(1_500_000_000)  # about 0.8 seconds
+        end.record()
+
+    def launch():
+        for _ in range(4000):  # more than a queue holds
+            bs.bs_gnorm_batched(f, y, stream=stream)
+
+    other = threading.Thread(target=launch)
+    longest, last = 0.0, time.perf_counter()
+    other.start()
+    while other.is_alive():
+        time.sleep(0.001)
+        now = time.perf_counter()
+        longest, last = max(longest, now - last), now
+    other.join()
+    torch.cuda.synchronize()
+    assert longest < 0.4e-3 * start.elapsed_time(end), longest
+
+
+def test_threads_on_their_own_streams():
+    """First calls of an instance from several threads at once, then many more."""
+    torch.manual_seed(0)
+    data = [torch.randn(2, 300, 4 * 72, device="cuda").half() for _ in range(4)]
+    lam = torch.rand(72, device="cuda") * 4 - 5
+
+    def calls(p, stream):
+        x, r, i, z = p.split(72, -1)
+        with torch.cuda.stream(stream):
+            h, y = (torch.empty(2, 300, 72, dtype=p.dtype, device="cuda") for _ in range(2))
+            tape = torch.empty(bs.bs_grec_tape_rows(2, 600), 72, device="cuda")
+            g, dlam = [torch.empty_like(h) for _ in range(3)], torch.empty_like(lam)
+            work = torch.empty(bs.bs_grec_backward_workspace(72, 2, 600), dtype=torch.uint8,
+                               device="cuda")
+            bs.bs_grec_batched(x, r, i, lam, h, tape=tape)
+            bs.bs_gnorm_batched(h, y, z=z)
+            bs.bs_grec_backward_batched(x, r, i, lam, tape, y, *g, dlam, work)
+            stream.synchronize()
+        return [h, y, *g, dlam]
+
+    torch.cuda.synchronize()
+    streams, seen = [torch.cuda.Stream() for _ in data], [[] for _ in data]
+
+    def thread(k):
+        for _ in range(20):
+            seen[k].append(calls(data[k], streams[k]))
+
+    threads = [threading.Thread(target=thread, args=(k,)) for k in range(len(data))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for k, p in enumerate(data):
+        want = calls(p, torch.cuda.current_stream())
+        assert len(seen[k]) == 20
+        for got in seen[k]:
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
