@@ -583,7 +583,19 @@ def _rows():
         import importlib
 
         import torch
+
+        from . import _build
+        if not os.path.exists(_build.ROWCALL):
+            raise RuntimeError(
+                f"{_build.ROWCALL} is missing: build it with "
+                "dense_linear_solvers_gb300._build.build(), which needs torch's and Python's headers")
         module = importlib.import_module(__name__ + "._rowcall")
+        if module.target != _build.rowcall_target(torch.__version__):
+            # it reads tensors by the object layout that it was compiled for
+            raise RuntimeError(
+                f"{_build.ROWCALL} was compiled for {module.target}, not "
+                f"{_build.rowcall_target(torch.__version__)}: build it again with "
+                "dense_linear_solvers_gb300._build.build()")
         # the current stream's handle without a Stream object, where torch offers it
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)

@@ -371,4 +371,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rowcall", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__rowcall() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__rowcall() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "target", BSOLVE_ROWCALL_TARGET) != 0) Py_CLEAR(m);
+  return m;
+}
