@@ -42,59 +42,50 @@ template <int N, int THREADS>
 __device__ __forceinline__ void group_sums(float (&v)[N], float* red, int& turn) {
   constexpr int LANES = THREADS < 32 ? THREADS : 32, WARPS = THREADS / LANES;
   constexpr unsigned kAll = 0xFFFFFFFFu;
-  if constexpr (N > LANES) {  // two halves
-    float a[N / 2], b[N / 2];
+  static_assert(N <= LANES, "a lane part for every value");
+  const int lane = threadIdx.x & 31;
+  int m = LANES / 2;
 #pragma unroll
-    for (int k = 0; k < N / 2; ++k) a[k] = v[k], b[k] = v[k + N / 2];
-    group_sums<N / 2, THREADS>(a, red, turn);
-    group_sums<N / 2, THREADS>(b, red, turn);
+  for (int n = N / 2; n > 0; n >>= 1, m >>= 1) {
+    const bool high = lane & m;
 #pragma unroll
-    for (int k = 0; k < N / 2; ++k) v[k] = a[k], v[k + N / 2] = b[k];
-  } else {
-    const int lane = threadIdx.x & 31;
-    int m = LANES / 2;
-#pragma unroll
-    for (int n = N / 2; n > 0; n >>= 1, m >>= 1) {
-      const bool high = lane & m;
-#pragma unroll
-      for (int k = 0; k < n; ++k) {
-        const float keep = high ? v[k + n] : v[k], give = high ? v[k] : v[k + n];
-        v[k] = keep + __shfl_xor_sync(kAll, give, m);
-      }
+    for (int k = 0; k < n; ++k) {
+      const float keep = high ? v[k + n] : v[k], give = high ? v[k] : v[k + n];
+      v[k] = keep + __shfl_xor_sync(kAll, give, m);
     }
-    float s = v[0];
+  }
+  float s = v[0];
 #pragma unroll
-    for (; m > 0; m >>= 1) s += __shfl_xor_sync(kAll, s, m);
-    if constexpr (WARPS == 1) {
+  for (; m > 0; m >>= 1) s += __shfl_xor_sync(kAll, s, m);
+  if constexpr (WARPS == 1) {
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        v[k] = N == 1 ? s : __shfl_sync(kAll, s, (lane & ~(LANES - 1)) + k * (LANES / N));
+    for (int k = 0; k < N; ++k)
+      v[k] = N == 1 ? s : __shfl_sync(kAll, s, (lane & ~(LANES - 1)) + k * (LANES / N));
+  } else {
+    const int warp = threadIdx.x >> 5;
+    float* r = red + turn * (WARPS * N);
+    turn ^= 1;
+    if (lane % (32 / N) == 0) r[warp * N + lane / (32 / N)] = s;
+    __syncthreads();
+    constexpr int PARTS = 32 / N;  // lanes that add up one value
+    const int value = lane % N, part = lane / N;
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; w += PARTS)
+      if (WARPS % PARTS == 0 || w + part < WARPS) s += r[(w + part) * N + value];
+#pragma unroll
+    for (int q = N; q < 32; q <<= 1) s += __shfl_xor_sync(kAll, s, q);
+    if constexpr (N <= 2) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = N == 1 ? s : __shfl_sync(kAll, s, k);
     } else {
-      const int warp = threadIdx.x >> 5;
-      float* r = red + turn * (WARPS * N);
-      turn ^= 1;
-      if (lane % (32 / N) == 0) r[warp * N + lane / (32 / N)] = s;
-      __syncthreads();
-      constexpr int PARTS = 32 / N;  // lanes that add up one value
-      const int value = lane % N, part = lane / N;
-      s = 0.f;
+      float* own = red + (2 * WARPS + warp) * N;
+      if (lane < N) own[lane] = s;
+      __syncwarp();
 #pragma unroll
-      for (int w = 0; w < WARPS; w += PARTS)
-        if (WARPS % PARTS == 0 || w + part < WARPS) s += r[(w + part) * N + value];
-#pragma unroll
-      for (int q = N; q < 32; q <<= 1) s += __shfl_xor_sync(kAll, s, q);
-      if constexpr (N <= 2) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = N == 1 ? s : __shfl_sync(kAll, s, k);
-      } else {
-        float* own = red + (2 * WARPS + warp) * N;
-        if (lane < N) own[lane] = s;
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < N; k += 4) {
-          const float4 q = *reinterpret_cast<const float4*>(own + k);
-          v[k] = q.x, v[k + 1] = q.y, v[k + 2] = q.z, v[k + 3] = q.w;
-        }
+      for (int k = 0; k < N; k += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(own + k);
+        v[k] = q.x, v[k + 1] = q.y, v[k + 2] = q.z, v[k + 3] = q.w;
       }
     }
   }
@@ -113,7 +104,7 @@ __device__ __forceinline__ float inverse_root(float v) {
 
 template <int THREADS>
 struct Group {
-  static constexpr int kBlock = THREADS < 128 && THREADS <= 32 ? 128 : THREADS;
+  static constexpr int kBlock = THREADS <= 32 ? 128 : THREADS;
   static constexpr int kGroups = kBlock / THREADS;
 };
 

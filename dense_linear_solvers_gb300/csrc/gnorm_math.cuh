@@ -103,14 +103,14 @@ __device__ __forceinline__ void stage_piece(char* smem, const T* base, unsigned 
 }
 
 // Stages one operand's ROWS rows for a group of threads, VE elements a thread and vector, row i at
-// smem + i * distance. The threads that share a 16-byte piece of a row (two where a vector has 8
-// bytes) take one row's each, so that with ALIGNED data a thread reads what its own warp copied.
+// smem + i * distance. Where a vector has 8 bytes, two threads share a 16-byte piece and each copies
+// one of their two vectors' pieces, so that with ALIGNED data a thread reads what its own warp copied.
 template <typename T, int VE, int THREADS, int K, int ROWS, bool ALIGNED>
 __device__ __forceinline__ void stage_rows(char* smem, int distance, const T* base, unsigned row0,
                                            unsigned rows, int64_t ld, int bytes, int t) {
   constexpr int kShare = 16 / (VE * static_cast<int>(sizeof(T)));  // threads of a piece: 1 or 2
   constexpr int kPieces = THREADS * K / kShare;                    // of a row
-  static_assert(kShare == 1 || ROWS == 2 || K == 2, "a thread for every piece");
+  static_assert(kShare == 1 || (ROWS == 1 && K == 2), "a thread for every piece");
   if constexpr (kShare == 1) {
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -122,16 +122,10 @@ __device__ __forceinline__ void stage_rows(char* smem, int distance, const T* ba
         stage_piece<T, ALIGNED>(smem + i * distance, base, row0 + i, ld, n, kPieces);
     }
   } else {
-    // ROWS == 2: the even thread row 0, the odd one row 1; one row: each the half of its vectors
-    const int i = ROWS == 2 ? t & 1 : 0;
-    const int n = row0 + i < rows ? bytes : 0;
-#pragma unroll
-    for (int k = 0; k < (ROWS == 2 ? K : K / 2); ++k) {
-      const int v = ROWS == 2 ? k : 2 * k + (t & 1);
-      stage_piece<T, ALIGNED>(smem + i * distance, base, row0 + i, ld, n, (v * THREADS + t) / 2);
-    }
-    if (!ALIGNED && t < ROWS)
-      stage_piece<T, ALIGNED>(smem + i * distance, base, row0 + i, ld, n, kPieces);
+    // one row, each of the two threads the half of its vectors
+    const int n = row0 < rows ? bytes : 0;
+    stage_piece<T, ALIGNED>(smem, base, row0, ld, n, ((t & 1) * THREADS + t) / 2);
+    if (!ALIGNED && t == 0) stage_piece<T, ALIGNED>(smem, base, row0, ld, n, kPieces);
   }
 }
 

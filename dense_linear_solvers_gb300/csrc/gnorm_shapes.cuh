@@ -4,9 +4,10 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "kernels.h"
+
 namespace bsolve {
 
-constexpr int kSms = 152;
 constexpr int kLong = 1024;  // threads of the looped kernels
 
 // Threads of a row, vectors a thread and rows a turn; threads == 0: the looped kernels.

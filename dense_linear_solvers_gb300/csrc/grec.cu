@@ -287,7 +287,7 @@ cudaError_t launch_forward(const GrecRows<T>& p, const float* lam, float kappa, 
 // us, with four warps 501; 4 x 4,096 x 2,048 FP32 86 and 90. Packed sequences end with their longest,
 // which more warps and clusters shorten (60 of 670 rows on average x 1,024: 70 us with eight, 75
 // with four), until there are so many that it does not show (128 of 470: 93 with four, 115).
-constexpr int64_t kFourWarpUnits = 152, kFourWarpUnitsPacked = 10 * 152;
+constexpr int64_t kFourWarpUnits = kSms, kFourWarpUnitsPacked = 10 * kSms;
 
 }  // namespace
 
@@ -296,14 +296,16 @@ cudaError_t launch_grec(const GrecRows<T>& p, const float* lam, float kappa, con
                         T* h, int64_t ldh, float* hT, float* tape, cudaStream_t stream) {
   const bool aligned = rows_aligned(p.x, p.ldx) && rows_aligned(p.r, p.ldr) &&
                        rows_aligned(p.i, p.ldi);
-  const int64_t units = (p.channels + kTileC - 1) / kTileC * p.batch;
-  const bool four =
-      sizeof(T) == 2 && units >= (p.offsets ? kFourWarpUnitsPacked : kFourWarpUnits);
+  if constexpr (sizeof(T) == 2) {
+    const int64_t units = (p.channels + kTileC - 1) / kTileC * p.batch;
+    if (units >= (p.offsets ? kFourWarpUnitsPacked : kFourWarpUnits)) {
+      auto* launch = aligned ? launch_forward<T, 4, 16, true> : launch_forward<T, 4, 16, false>;
+      return launch(p, lam, kappa, h0, h, ldh, hT, tape, stream);
+    }
+  }
   // Rows that are not aligned take more shared memory and instructions to stage: eight rows a warp, so that
   // an SM holds two blocks (5 x 777 x 523 FP16 27 to 17 us; aligned rows lose 5 to 25%).
-  auto* launch = four      ? (aligned ? launch_forward<T, 4, 16, true> : launch_forward<T, 4, 16, false>)
-                 : aligned ? launch_forward<T, 8, 16, true>
-                           : launch_forward<T, 8, 8, false>;
+  auto* launch = aligned ? launch_forward<T, 8, 16, true> : launch_forward<T, 8, 8, false>;
   return launch(p, lam, kappa, h0, h, ldh, hT, tape, stream);
 }
 
@@ -313,7 +315,7 @@ cudaError_t launch_grec_step(const GrecRows<T>& p, const float* lam, float kappa
                              cudaStream_t stream) {
   const unsigned across = (p.channels + 2 * kStepThreads - 1) / (2 * kStepThreads);
   // 16 blocks an SM; more rows a block beyond that
-  const int64_t down = std::max<int64_t>(1, 16 * 152 / across);
+  const int64_t down = std::max<int64_t>(1, 16 * kSms / across);
   const dim3 grid(across, static_cast<unsigned>(p.batch < down ? p.batch : down));
   const bool pairs = p.channels % 2 == 0 && pair_stores(p.x, p.ldx) && pair_stores(p.r, p.ldr) &&
                      pair_stores(p.i, p.ldi) && pair_stores(y, ldy) &&

@@ -112,6 +112,9 @@ size_t lu_cta_bytes(int n, int nrhs, int elem_size);
 size_t chol_smem_bytes(int n, int nrhs, int elem_size);
 size_t chol_sys_bytes(int n, int nrhs, int elem_size);
 
+// SMs of the GPU that the row operators' grids and thresholds are made for.
+constexpr int kSms = 152;
+
 // The row operators (bs_grec and bs_gnorm calls): operands of T (float, __nv_bfloat16 or
 // __half) as rows of contiguous elements, row j at j * ld of its base.
 

@@ -1,4 +1,5 @@
 """Calls of the row operators on the GPU that are rare in use."""
+import itertools
 import threading
 import time
 
@@ -13,6 +14,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 from tests.rows_ref import EPS  # noqa: E402
+from tests.test_gpu_rows import run_norms  # noqa: E402
 
 
 @pytest.mark.parametrize("eps", [1e-44, 1e-40, 1e-38, 1e-36])
@@ -125,3 +127,14 @@ def test_threads_on_their_own_streams():
         assert len(seen[k]) == 20
         for got in seen[k]:
             assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("width", [136, 100, 4096, 12000])
+@pytest.mark.parametrize("parts", ["".join(p) for n in range(7)
+                                   for p in itertools.combinations("zxwcpy", n)
+                                   if ("y" in p or "p" in p) and n < 6])
+def test_norms_parts_in_16_bits(kind, width, parts):
+    """Aligned and unaligned rows, of one warp's part, a block and the looped kernels of the backward
+    pass."""
+    run_norms(np.random.default_rng(width), kind, 5, width, parts=parts)

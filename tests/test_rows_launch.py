@@ -126,3 +126,28 @@ for name, entry, args in (("forward", lib.bs_grec_batched, FORWARD),
     out[name] = [first, second, third, fake.stand_in_queries() - asked]
 """)
     assert got == {"forward": [3, 0, 0, 0], "backward": [3, 0, 0, 0]}
+
+
+def test_disjoint_windows_of_one_matrix_are_taken(stand_in):
+    """Operands of one row distance may interleave as column windows; windows that share an element,
+    in one row or around a row's end, or of another row distance may not."""
+    got = child(stand_in, """
+f, b = lib.bs_grec_batched, lib.bs_grec_backward_batched
+one = dict(x=P[0], r=P[0] + 128, i=P[0] + 256, h=P[0] + 384, ldx=256, ldr=256, ldi=256, ldh=256)
+first = dict(x=P[0] + 128, r=P[0] + 256, i=P[0] + 384, h=P[0], ldx=256, ldr=256, ldi=256, ldh=256)
+grads = dict(dx=P[7], dr=P[7] + 128, di=P[7] + 256, lddx=192, lddr=192, lddi=192)
+rest = dict(grads, lddx=256, lddr=256, lddi=256, dh=P[7] + 384, lddh=256)
+before = fake.stand_in_launches()
+out["taken"] = [call(f, FORWARD, **one), call(f, FORWARD, **first), call(b, BACKWARD, **grads),
+                call(b, BACKWARD, **rest),
+                # rows behind another operand's last one, whatever the distances
+                call(f, FORWARD, h=P[0] + 200 * 128), call(f, FORWARD, h=P[0] + 200 * 128, ldh=96)]
+out["launches"] = fake.stand_in_launches() - before
+out["refused"] = [call(f, FORWARD, **dict(one, h=P[0] + 382)), call(f, FORWARD, **dict(one, h=P[0] + 386)),
+                  call(f, FORWARD, **dict(first, h=P[0] + 2)), call(f, FORWARD, **dict(one, ldh=260)),
+                  call(b, BACKWARD, **dict(rest, dh=P[7] + 256)),
+                  call(f, FORWARD, h=P[0] + 200 * 128 - 2)]
+out["launches after"] = fake.stand_in_launches() - before
+""")
+    assert got["taken"] == [0] * 6 and got["launches"] == 4 + 2 * 2
+    assert got["refused"] == [1] * 6 and got["launches after"] == got["launches"]
