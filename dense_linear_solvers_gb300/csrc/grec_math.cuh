@@ -134,7 +134,7 @@ __device__ __forceinline__ Gates grec_gates(float2 er, float2 ei, float2 rate) {
     const float2 e = fma2(f * f, c, f);
     const float2 two_n = make_float2(__int_as_float((__float_as_int(k.x) << 23) + 0x3f800000),
                                      __int_as_float((__float_as_int(k.y) << 23) + 0x3f800000));
-    m = fma2(two_n, e, fma2(two_n, both(-1.f), both(1.f)));
+    m = make_float2(fmaf(two_n.x, e.x, 1.f - two_n.x), fmaf(two_n.y, e.y, 1.f - two_n.y));
     g.a = make_float2(fmaf(-two_n.x, e.x, two_n.x), fmaf(-two_n.y, e.y, two_n.y));
   }
   const float2 w = fma2(m, g.a, m);
