@@ -151,7 +151,7 @@ constexpr int64_t kManyUnits = 8192;
 // Equal sequences run in waves of what the GPU holds, and a wave costs its steps and about two more
 // to fill and drain. Uneven ones fill each other's gaps, but the longest, about 1 + ln(batch)
 // times the average where they were cut at random, cannot take less than its own steps (8 x 1,500
-// rows on average, 2,048 channels BF16: 64 us with the 4 blocks that this gives, 104 with one).
+// rows on average, 2,048 channels BF16: 56 us with the 4 blocks that this gives, 77 with one).
 // The least such cost, the smaller cluster where two are alike.
 inline int grec_cluster(const Held& held, int64_t tiles, int64_t batch, int64_t length,
                         bool packed, int rows) {

@@ -12,7 +12,7 @@
 // that run the looped kernels at the end, which read a row once for each mean and once for the
 // outputs.
 //
-// 16,384 x 4,096 BF16: forward 112 us (6.0 TB/s of its five operands, 88% of a copy's rate), backward 234
+// 16,384 x 4,096 BF16: forward 112 us (6.0 TB/s of its five operands, 89% of a copy's rate), backward 233
 // us (4.6 TB/s of its eight; one block of 512 threads an SM, which waits at its two reductions a turn).
 // Measured without gain there: every sum in one reduction by expanding sum y^2 (296 against 279 at the
 // time), four elements a thread and twice the warps (279), two vectors a thread and one row (340).

@@ -26,8 +26,9 @@ namespace {
 //   every warp applies its compositions to its own true state, one product-sum an element, and
 //     stores the states.
 // Each element is read and written once. The order of every sum follows from the sizes alone.
-// 65,536 x 4,096 BF16 take 445 us (4.8 TB/s; 28 instructions an element on 128 of the 152 SMs, half of
-// the cycles issue), 64 x 512 x 2,048 89 us (6.0 TB/s), 4 x 4,096 x 2,048 FP32 86 us (6.2).
+// 65,536 x 4,096 BF16 take 445 us (4.8 TB/s; 256 blocks on 128 of the 152 SMs, whose schedulers issue
+// on half of their cycles, 28 instructions an element: between them the 16 warps wait for each
+// other and for their own results), 64 x 512 x 2,048 85 us (6.3 TB/s), 4 x 4,096 x 2,048 FP32 83 us (6.5).
 constexpr int kStages = 2;  // steps staged ahead
 
 struct Composition {  // of two channels
@@ -282,11 +283,12 @@ cudaError_t launch_forward(const GrecRows<T>& p, const float* lam, float kappa, 
 }
 
 // Blocks of four warps, without clusters, on 16-bit rows while there is a pair of a sequence and a tile
-// for every SM: 64 x 512 rows x 2,048 channels BF16 take 89 us, with eight warps 102; 8 x 4,096 rows
-// 108 and 112. Otherwise eight, which meet less often: one sequence of 65,536 x 4,096 takes 445
-// us, with four warps 501; 4 x 4,096 x 2,048 FP32 86 and 90. Packed sequences end with their longest,
-// which more warps and clusters shorten (60 of 670 rows on average x 1,024: 70 us with eight, 75
-// with four), until there are so many that it does not show (128 of 470: 93 with four, 115).
+// for every SM: 64 x 512 rows x 2,048 channels BF16 take 85 us, with eight warps 100; 8 x 4,096 rows
+// 103 and 111. Otherwise eight, which meet less often and share a sequence in clusters: one of
+// 65,536 x 4,096 takes 445 us, with four warps 1,053; 4 x 4,096 x 2,048 FP32 86 and 90. Packed
+// sequences end with their longest, which more warps and clusters shorten (60 of 670 rows on average
+// x 1,024: 74 us with eight, 83 with four), until there are so many that it does not show (128 of
+// 470: 100 with four, 115).
 constexpr int64_t kFourWarpUnits = kSms, kFourWarpUnitsPacked = 10 * kSms;
 
 }  // namespace

@@ -19,10 +19,11 @@
 // The gradient of lam: every lane sums D = dL/dl * l over its rows, the block's warps are added at
 // the end and each block writes one partial sum a channel; a second kernel adds those in order.
 //
-// 8 x 4,096 x 2,048 BF16 take 247 us, 3.8 TB/s of the seven operands; FP32 rows reach 5.3. What bounds it is
-// the instruction stream (78 an element, about half of the cycles issue with the 16 warps that 128
-// registers leave). Measured without gain: blocks of four warps (257 us), the exponentials of the
-// gates worked out twice instead of kept (284).
+// 8 x 4,096 x 2,048 BF16 take 244 us, 3.9 TB/s of the seven operands; FP32 rows reach 5.5. What bounds
+// it is how little the 16 warps that 128 registers leave can overlap: the schedulers issue on half of their
+// cycles, 74 instructions an element, of which the gates' second evaluation is a good part; the
+// bytes alone would take 140 us. Measured without gain: blocks of four warps (257 us), the
+// exponentials of the gates worked out twice instead of kept (284).
 #include <type_traits>
 
 #include "cluster.cuh"

@@ -7,7 +7,7 @@
 namespace bsolve {
 
 // A few packed sequences are taken longest first, since what starts last ends last (60 prompts of 670
-// rows on average, 1,024 channels BF16: 100 to 80 us): the number of the n-th longest, the same for
+// rows on average, 1,024 channels BF16: 99 to 74 us): the number of the n-th longest, the same for
 // a whole block. All threads take part; `scratch` holds kSortedBatch + 1 numbers.
 constexpr int kSortedBatch = 128;
 

@@ -362,6 +362,11 @@ BS_API bs_status bs_bdmv2_batched(bs_dtype dtype, int num_block_rows, int block_
  * gradients; lam, every state (h0, hT, tape, the step's states), dhT, dh0 and dlam are
  * FP32. All arithmetic and every state is FP32; each row output is rounded once.
  *
+ * Every row takes the factor sqrt(1 - a_t^2), the first of a sequence too. A model whose
+ * sequences start without it (h_0 = sigma(i_0) x_0) works its first rows out itself, gives
+ * them as h0 and the rest as the sequence. a and u come from the gates alone: these calls
+ * do not solve a system that is given by its coefficients.
+ *
  * Rows: an operand holds `rows` rows of `channels` contiguous elements, row j at element
  * j * ld of its base (ld >= channels; 64-bit offsets), so that operands may be column windows
  * of a wider matrix. offsets == NULL: `batch` sequences of rows / batch rows each, one after
