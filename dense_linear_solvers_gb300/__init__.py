@@ -13,7 +13,8 @@ Storage convention (raw storage tensors, as the C ABI sees memory):
 
 The row operators (gated linear recurrence, norms around a block) take rows of contiguous
 elements, (rows, width) or (batch, length, width), that may be column windows of a wider
-tensor: the last stride is 1, the rows lie at one distance.
+tensor: the last stride is 1, the rows lie at one distance. The gated delta rule's rows are
+(rows, heads, size) or (batch, length, heads, size), the heads of a row one after another.
 """
 from __future__ import annotations
 
@@ -55,6 +56,8 @@ EXPORTED = (
     "bs_grec_tape_rows", "bs_grec_backward_workspace", "bs_grec_supported",
     "bs_gnorm_batched", "bs_gnorm_backward_batched", "bs_gnorm_backward_workspace",
     "bs_gnorm_supported",
+    "bs_gdelta_batched", "bs_gdelta_step_batched", "bs_gdelta_workspace", "bs_gdelta_tape",
+    "bs_gdelta_supported",
     "bs_status_string", "bs_last_cuda_error", "bs_getrf_getrs_supported",
     "bs_potrf_potrs_supported", "bs_bdsv_supported", "bs_version",
 )
@@ -161,6 +164,18 @@ def lib() -> ctypes.CDLL:
             L.bs_grec_supported.restype = i32
             L.bs_gnorm_supported.argtypes = [i32, i32]
             L.bs_gnorm_supported.restype = i32
+            heads = [i32, i32, i32, i32, i32]  # dtype, heads_k, heads_v, dk, dv
+            given = [vp, i64] * 5 + [f64]      # q, k, v, g, beta with their row distances, scale
+            L.bs_gdelta_batched.argtypes = [*heads, i64, i64, vp, *given, vp, vp, i64, vp, vp, vp, sz,
+                                            vp]
+            L.bs_gdelta_step_batched.argtypes = [*heads, i64, *given, vp, i64, vp, vp, i64, vp]
+            for name in ("bs_gdelta_batched", "bs_gdelta_step_batched", "bs_gdelta_supported"):
+                getattr(L, name).restype = i32
+            L.bs_gdelta_supported.argtypes = heads
+            L.bs_gdelta_workspace.argtypes = [i32, i64, i64]
+            L.bs_gdelta_tape.argtypes = [i32, i32, i32, i64, i64]
+            for name in ("bs_gdelta_workspace", "bs_gdelta_tape"):
+                getattr(L, name).restype = sz
             L.bs_status_string.argtypes = [i32]
             L.bs_status_string.restype = ctypes.c_char_p
             L.bs_last_cuda_error.argtypes = []
@@ -678,3 +693,38 @@ def bs_gnorm_backward_batched(f, dy, df, work=None, z=None, x=None, w_post=None,
                                 dscale, dw_pre, eps, gate, _row_stream(stream, f))
     if st:
         _check(st, "bs_gnorm_backward_batched")
+
+
+def bs_gdelta_workspace(heads_v: int, batch: int, rows: int) -> int:
+    """Bytes of bs_gdelta_batched's workspace."""
+    return _rows().gdelta_workspace(heads_v, batch, rows)
+
+
+def bs_gdelta_tape(heads_v: int, dk: int, dv: int, batch: int, rows: int) -> int:
+    """Bytes of the tape of a gated delta rule call over batch sequences of rows rows in all."""
+    return _rows().gdelta_tape(heads_v, dk, dv, batch, rows)
+
+
+def bs_gdelta_batched(q, k, v, g, beta, o, work, h0=None, hT=None, offsets=None, tape=None,
+                      scale: float | None = None, stream=None) -> None:
+    """Gated delta rule over whole sequences: o <- the reads of the states (see bsolve.h). q, k: (batch,
+    length, heads_k, dk); v, o: (batch, length, heads_v, dv); g, beta: (batch, length, heads_v)
+    float32; or rows instead of batch, length, with offsets, batch + 1 int64 row numbers. h0, hT:
+    (batch, heads_v, dk, dv) float32. work: uint8, at least bs_gdelta_workspace(...) elements; tape:
+    uint8, at least bs_gdelta_tape(...) elements, for the backward call. scale: None for
+    dk ** -0.5."""
+    st = _rows().gdelta(q, k, v, g, beta, o, work, h0, hT, offsets, tape, scale,
+                        _row_stream(stream, q))
+    if st:
+        _check(st, "bs_gdelta_batched")
+
+
+def bs_gdelta_step_batched(q, k, v, g, beta, state, o, slots=None, scale: float | None = None,
+                           stream=None) -> None:
+    """One row of the gated delta rule for each of a batch of sequences: state, (num_slots, heads_v,
+    dk, dv) float32, advances in place and o <- its reads (see bsolve.h). q, k: (batch, heads_k,
+    dk); v, o: (batch, heads_v, dv); g, beta: (batch, heads_v) float32; slots: batch int32 entries
+    of state, None: entry j for sequence j."""
+    st = _rows().gdelta_step(q, k, v, g, beta, state, o, slots, scale, _row_stream(stream, q))
+    if st:
+        _check(st, "bs_gdelta_step_batched")

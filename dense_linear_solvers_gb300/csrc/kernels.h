@@ -171,6 +171,76 @@ cudaError_t launch_gnorm_backward(const GnormRows<T>& p, const GnormGrads<T>& g,
                                   cudaStream_t stream);
 size_t gnorm_backward_workspace(int width, int64_t rows);
 
+// Rows in e4m3 with one FP32 scale for each 128 elements.
+struct Bytes8 {
+  uint8_t* q;
+  int64_t ldq;
+  float* s;
+  int64_t lds;
+};
+
+template <typename T>
+cudaError_t launch_gnorm_q8(const GnormRows<T>& p, T* y, int64_t ldy, const Bytes8& out,
+                            cudaStream_t stream);
+
+// y (m x n) from a (m x k) and w (n x k) in e4m3, a scale for each 128 of a row of a and for each
+// 128 x 128 of w.
+template <typename T>
+struct GemmQ8 {
+  int64_t m, n, k;
+  const uint8_t* a;
+  int64_t lda;
+  const float* sa;
+  int64_t ldsa;
+  const uint8_t* w;
+  int64_t ldw;
+  const float* sw;
+  int64_t ldsw;
+  T* y;
+  int64_t ldy;
+};
+
+template <typename T>
+cudaError_t launch_gemm_q8(const GemmQ8<T>& g, cudaStream_t stream);
+
+// The inputs of a gated delta rule: rows of heads_k heads of dk elements (q, k), heads_v of dv (v), and
+// FP32 rows of heads_v (g, beta). offsets == nullptr: sequences of `length` rows.
+template <typename T>
+struct GdeltaRows {
+  int heads_k, heads_v, dk, dv;
+  int64_t batch, rows, length;
+  const int64_t* offsets;
+  const T *q, *k, *v;
+  int64_t ldq, ldk, ldv;
+  const float *g, *beta;
+  int64_t ldg, ldbeta;
+  float scale;
+};
+
+// Whether every head of every row starts on a 16-byte boundary and ends on one.
+template <typename T>
+bool gdelta_aligned(const T* p, int64_t ld, int width) {
+  return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * sizeof(T)) |
+           static_cast<uintptr_t>(width * sizeof(T))) & 15) == 0;
+}
+
+template <typename T>
+cudaError_t launch_gdelta(const GdeltaRows<T>& p, const float* h0, T* o, int64_t ldo, float* hT,
+                          void* tape, void* work, cudaStream_t stream);
+template <typename T>
+cudaError_t launch_gdelta_backward(const GdeltaRows<T>& p, const void* tape, const T* dout,
+                                   int64_t lddo, const float* dhT, T* dq, int64_t lddq, T* dk,
+                                   int64_t lddk, T* dv, int64_t lddv, float* dg, int64_t lddg,
+                                   float* dbeta, int64_t lddbeta, float* dh0, void* work,
+                                   cudaStream_t stream);
+// One row of it for each of p.batch sequences.
+template <typename T>
+cudaError_t launch_gdelta_step(const GdeltaRows<T>& p, float* state, int64_t num_slots,
+                               const int32_t* slots, T* o, int64_t ldo, cudaStream_t stream);
+size_t gdelta_workspace(int heads_v, int64_t batch, int64_t rows);
+size_t gdelta_tape(int heads_v, int dk, int dv, int64_t batch, int64_t rows);
+size_t gdelta_backward_workspace(int heads_v, int dk, int dv, int64_t batch, int64_t rows);
+
 // Records a launch error as the one bs_last_cuda_error() returns.
 void record_cuda_error(cudaError_t e);
 

@@ -1,12 +1,14 @@
-// The row operators' calls (bs_grec and bs_gnorm calls of bsolve.h) from Python: reads devices, types,
+// The row operators' calls (bs_grec, bs_gnorm and bs_gdelta calls of bsolve.h) from Python: reads devices, types,
 // shapes, row distances and pointers from torch tensors, checks them against each other and calls the
 // C ABI. A call costs about 3 us with its launch; reading as much tensor by tensor in Python
 // takes 5 us warm and twice that between a program's other work, more than a small call's kernel.
 #include <Python.h>
 
+#include <cmath>
 #include <cstdint>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include <ATen/core/Tensor.h>
 #include <cuda_runtime_api.h>
@@ -47,7 +49,8 @@ struct Like {
   int64_t width;
   bs_dtype code;
 
-  Like(PyObject* o, const char* name) {
+  // dims 0: rows of elements, (rows, width) or (batch, length, width).
+  Like(PyObject* o, const char* name, size_t dims = 0) {
     const at::Tensor* t = tensor(o, name);
     if (!t) type_error(std::string(name) + ": a torch tensor expected");
     type = t->scalar_type();
@@ -60,7 +63,11 @@ struct Like {
                    ": float32, bfloat16 or float16");
     }
     shape = t->sizes();
-    if (shape.size() != 2 && shape.size() != 3)
+    if (dims && shape.size() != dims)
+      value_error(std::string(name) + ": shape " + text(shape) + ", expected " +
+                  (dims == 4 ? "(batch, length, heads, size), or (rows, heads, size) with offsets"
+                             : "(rows, heads, size)"));
+    if (!dims && shape.size() != 2 && shape.size() != 3)
       value_error(std::string(name) + ": shape " + text(shape) +
                   ", expected (rows, width) or (batch, length, width)");
     if (!t->is_cuda())
@@ -326,6 +333,126 @@ PyObject* gnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Row operands of the gated delta rule: heads of contiguous elements, one after another in a row.
+struct Heads {
+  Like q;               // its shape: the rows' and (heads, elements)
+  c10::IntArrayRef lead;  // the rows' part
+  int64_t heads_k, dk, heads_v, dv, batch, rows;
+  const int64_t* offsets = nullptr;
+
+  // Of q and v; `packed`: with offsets, else (batch, length) or, for a step, (batch).
+  Heads(PyObject* q_, PyObject* v_, PyObject* offsets_, bool step)
+      : q(q_, "q", step || offsets_ != Py_None ? 3 : 4) {
+    lead = q.shape.slice(0, q.shape.size() - 2);
+    heads_k = q.shape[lead.size()], dk = q.width;
+    const at::Tensor* v = tensor(v_, "v");
+    if (!v) type_error("v: a torch tensor expected");
+    if (v->dim() != static_cast<int64_t>(lead.size()) + 2)
+      value_error("v: shape " + text(v->sizes()) + ", expected " + std::to_string(lead.size() + 2) +
+                  " dimensions");
+    heads_v = v->size(lead.size()), dv = v->size(lead.size() + 1);
+    for (int64_t n : {heads_k, heads_v, dv})
+      if (n > INT32_MAX) value_error("heads too many or too long");
+    rows = lead[0] * (lead.size() == 2 ? lead[1] : 1);
+    batch = lead[0];
+    if (const at::Tensor* t = tensor(offsets_, "offsets")) {
+      if (t->numel() < 1) value_error("offsets: batch + 1 row numbers expected");
+      offsets = vec<int64_t>(offsets_, "offsets", q, t->numel(), at::kLong);
+      batch = t->numel() - 1;
+    }
+  }
+
+  // A row operand of `heads` x `size` elements a row (size 0: of `heads` numbers).
+  Row row(PyObject* o, const char* name, int64_t heads, int64_t size, at::ScalarType type) const {
+    const at::Tensor* t = tensor(o, name);
+    if (!t) type_error(std::string(name) + ": a torch tensor expected");
+    if (t->scalar_type() != type)
+      type_error(std::string(name) + ": dtype " + c10::toString(t->scalar_type()) + ", expected " +
+                 c10::toString(type));
+    std::vector<int64_t> want(lead.begin(), lead.end());
+    want.push_back(heads);
+    if (size) want.push_back(size);
+    const auto s = t->sizes(), st = t->strides();
+    if (s != c10::IntArrayRef(want))
+      value_error(std::string(name) + ": shape " + text(s) + ", expected " + text(want));
+    if (!t->is_cuda() || t->get_device() != q.device)
+      value_error(std::string(name) + ": bsolve operands are device tensors of one device");
+    const size_t n = lead.size();
+    const int64_t inner = size ? size : 1, width = heads * inner;
+    if ((size > 1 && st[n + 1] != 1) || (heads > 1 && st[n] != inner))
+      value_error(std::string(name) + ": the heads of a row must be contiguous");
+    Row r;
+    if (n == 2) {
+      r.ld = s[1] > 1 ? st[1] : (s[0] > 1 ? st[0] : width);
+      if (s[0] > 1 && s[1] > 1 && st[0] != s[1] * r.ld)
+        value_error(std::string(name) + ": the rows of all sequences must lie at one distance");
+    } else {
+      r.ld = s[0] > 1 ? st[0] : width;
+    }
+    if (r.ld < width) {
+      if (t->numel()) value_error(std::string(name) + ": rows overlap");
+      r.ld = width;
+    }
+    r.p = address(*t, name);
+    return r;
+  }
+  Row keys(PyObject* o, const char* name) const { return row(o, name, heads_k, dk, q.type); }
+  Row values(PyObject* o, const char* name) const { return row(o, name, heads_v, dv, q.type); }
+  Row gates(PyObject* o, const char* name) const { return row(o, name, heads_v, 0, at::kFloat); }
+  int64_t states() const { return batch * heads_v * dk * dv; }
+  double scale(PyObject* o) const {
+    return o == Py_None ? 1.0 / std::sqrt(static_cast<double>(dk)) : number(o);
+  }
+};
+
+// A buffer of at least `need` bytes. None: null.
+void* bytes_of(PyObject* o, const char* name, const Like& like, size_t need, size_t* have = nullptr) {
+  void* p = vec<void>(o, name, like, -1, at::kByte);
+  const size_t n = p ? static_cast<size_t>(tensor(o, name)->numel()) : 0;
+  if (p && n < need)
+    value_error(std::string(name) + ": " + std::to_string(n) + " bytes, " + std::to_string(need) +
+                " needed");
+  if (have) *have = n;
+  return p;
+}
+
+PyObject* gdelta(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("gdelta", n, 13, [&] {
+    const Heads s(a[0], a[2], a[9], false);
+    const Row q = s.keys(a[0], "q"), k = s.keys(a[1], "k"), v = s.values(a[2], "v"),
+              g = s.gates(a[3], "g"), beta = s.gates(a[4], "beta"), o = s.values(a[5], "o");
+    size_t bytes = 0;
+    void* work = bytes_of(a[6], "work", s.q, bs_gdelta_workspace(s.heads_v, s.batch, s.rows), &bytes);
+    return enter(
+        s.q, bs_gdelta_batched, s.q.code, static_cast<int>(s.heads_k), static_cast<int>(s.heads_v),
+        static_cast<int>(s.dk), static_cast<int>(s.dv), s.batch, s.rows, s.offsets, q.p, q.ld, k.p,
+        k.ld, v.p, v.ld, static_cast<float*>(g.p), g.ld, static_cast<float*>(beta.p), beta.ld,
+        s.scale(a[11]), f32(a[7], "h0", s.q, s.states()), o.p, o.ld,
+        f32(a[8], "hT", s.q, s.states()),
+        bytes_of(a[10], "tape", s.q, bs_gdelta_tape(s.heads_v, s.dk, s.dv, s.batch, s.rows)), work,
+        bytes, handle(a[12]));
+  });
+}
+
+PyObject* gdelta_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("gdelta_step", n, 10, [&] {
+    const Heads s(a[0], a[2], Py_None, true);
+    const Row q = s.keys(a[0], "q"), k = s.keys(a[1], "k"), v = s.values(a[2], "v"),
+              g = s.gates(a[3], "g"), beta = s.gates(a[4], "beta"), o = s.values(a[6], "o");
+    const at::Tensor* state = tensor(a[5], "state");
+    const int64_t want[] = {state && state->dim() ? state->size(0) : 0, s.heads_v, s.dk, s.dv};
+    if (!state || state->sizes() != c10::IntArrayRef(want))
+      value_error("state: shape " + (state ? text(state->sizes()) : std::string("None")) +
+                  ", expected (num_slots, heads_v, dk, dv)");
+    return enter(
+        s.q, bs_gdelta_step_batched, s.q.code, static_cast<int>(s.heads_k),
+        static_cast<int>(s.heads_v), static_cast<int>(s.dk), static_cast<int>(s.dv), s.batch, q.p,
+        q.ld, k.p, k.ld, v.p, v.ld, static_cast<float*>(g.p), g.ld, static_cast<float*>(beta.p),
+        beta.ld, s.scale(a[8]), f32(a[5], "state", s.q, state->numel()), want[0],
+        vec<int32_t>(a[7], "slots", s.q, s.batch, at::kInt), o.p, o.ld, handle(a[9]));
+  });
+}
+
 // The size queries: n integers in, one out.
 template <typename F>
 PyObject* query(Py_ssize_t given, Py_ssize_t wanted, F&& f) {
@@ -352,6 +479,17 @@ PyObject* gnorm_backward_workspace(PyObject*, PyObject* const* a, Py_ssize_t n) 
   return query(n, 2, [&] { return bs_gnorm_backward_workspace(small(a[0]), integer(a[1])); });
 }
 
+PyObject* gdelta_workspace(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return query(n, 3, [&] {
+    return bs_gdelta_workspace(small(a[0]), integer(a[1]), integer(a[2]));
+  });
+}
+PyObject* gdelta_tape(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return query(n, 5, [&] {
+    return bs_gdelta_tape(small(a[0]), small(a[1]), small(a[2]), integer(a[3]), integer(a[4]));
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL,
@@ -364,6 +502,9 @@ PyMethodDef methods[] = {method<grec>("grec"), method<grec_backward>("grec_backw
                          method<grec_tape_rows>("grec_tape_rows"),
                          method<grec_backward_workspace>("grec_backward_workspace"),
                          method<gnorm_backward_workspace>("gnorm_backward_workspace"),
+                         method<gdelta>("gdelta"), method<gdelta_step>("gdelta_step"),
+                         method<gdelta_workspace>("gdelta_workspace"),
+                         method<gdelta_tape>("gdelta_tape"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rowcall", nullptr, -1, methods,

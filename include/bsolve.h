@@ -478,9 +478,73 @@ BS_API bs_status bs_gnorm_backward_batched(bs_dtype dtype, int64_t rows, int wid
                                            size_t work_bytes, void* stream);
 BS_API size_t bs_gnorm_backward_workspace(int width, int64_t rows);
 
+/*
+ * Gated delta rule over long sequences: a matrix state per sequence and value head that forgets,
+ * is corrected by what it holds under each row's key, and is read by each row's query. With
+ * a_t = exp(g_t), S a dk x dv state, q_t and k_t of the value head's key head,
+ *   S_t = a_t S_(t-1) + k_t d_t^T,   d_t = beta_t (v_t - a_t S_(t-1)^T k_t),
+ *   o_t = scale S_t^T q_t.
+ * Over 64 rows at a time this is one unit lower triangular 64 x 64 system a value head, solved
+ * for all of a chunk's d at once from the state in front of it (bs_gdelta_batched); its backward
+ * pass (bs_gdelta_backward_batched); and one row of it from a kept state (bs_gdelta_step_batched).
+ *
+ * dtype (BS_FP32, BS_BF16, BS_FP16) is the type of q, k, v, o and their gradients; g, beta, every
+ * state and its gradient, dg and dbeta are FP32. Sums and states are FP32; operands of matrix products are
+ * taken to 2^-18 of themselves (two BF16 terms), and each row output is rounded once. Nothing
+ * is normalised here: keys are meant to have length one (bs_gnorm_batched over rows of dk elements
+ * with w_post = 1 / sqrt(dk) gives that), g <= 0 and 0 <= beta <= 1 (2 at most) to keep the state bounded.
+ * g = -infinity forgets the state; a g below -1000 counts as -1000.
+ *
+ * Rows: q and k hold heads_k heads of dk contiguous elements a row, v and o heads_v of dv, g and beta
+ * heads_v numbers, row j at element j * ld of its base (ld at least a row's elements), so that
+ * operands may be column windows of one matrix. heads_v is a multiple of heads_k; value head h
+ * uses key head h / (heads_v / heads_k). offsets == NULL: `batch` sequences of rows / batch rows
+ * each (rows a multiple of batch); else batch + 1 increasing int64 row numbers as in the bs_grec
+ * calls (an empty sequence's final state is its initial one; rows of no sequence are
+ * neither read nor written; offsets are clamped to 0 .. rows).
+ *
+ * Base addresses are aligned to their elements (16 bytes for tape and work). 16-byte aligned bases, ld
+ * and head sizes of multiples of 16 bytes serve best. Inputs may overlap each other; an output
+ * may not overlap any other operand, except that row operands of equal ld may interleave as disjoint
+ * column windows and that hT may be h0 itself. Infinities and NaN stay in their sequence and value head (in
+ * gradients of q and k: key head), where they may reach other rows, up to 63 of them in front.
+ *
+ * bs_gdelta_batched:
+ *   h0    batch x heads_v x dk x dv initial states, or NULL for zeros.
+ *   hT    the final states, or NULL.
+ *   tape  device buffer of bs_gdelta_tape(...) bytes, or NULL: what bs_gdelta_backward_batched needs
+ *         of the states.
+ *   work  device workspace of bs_gdelta_workspace(...) bytes. Holds nothing between calls.
+ * bs_gdelta_step_batched: one row for each of `batch` sequences:
+ *   state  num_slots x heads_v x dk x dv, in and out.
+ *   slots  batch int32: the entry of `state` that row j advances; NULL: entry j (num_slots at least
+ *          batch then). Row j with a slot outside 0 .. num_slots - 1 changes no state and gets
+ *          o = 0. Two rows with one slot: unspecified states.
+ * batch == 0: nothing is launched.
+ * Results do not depend on the stream or the run: no atomics, a fixed order of every sum.
+ * Supported: 1 <= dk <= 128, 1 <= dv <= 1024, heads_v <= 65535, batch * heads_v <= 2^24,
+ * rows <= 2^30, ld <= 2^21, scale finite. The queries return 0 for invalid sizes.
+ */
+BS_API bs_status bs_gdelta_batched(bs_dtype dtype, int heads_k, int heads_v, int dk, int dv,
+                                   int64_t batch, int64_t rows, const int64_t* offsets,
+                                   const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                   const void* v, int64_t ldv, const float* g, int64_t ldg,
+                                   const float* beta, int64_t ldbeta, double scale,
+                                   const float* h0, void* o, int64_t ldo, float* hT, void* tape,
+                                   void* work, size_t work_bytes, void* stream);
+BS_API bs_status bs_gdelta_step_batched(bs_dtype dtype, int heads_k, int heads_v, int dk, int dv,
+                                        int64_t batch, const void* q, int64_t ldq, const void* k,
+                                        int64_t ldk, const void* v, int64_t ldv, const float* g,
+                                        int64_t ldg, const float* beta, int64_t ldbeta,
+                                        double scale, float* state, int64_t num_slots,
+                                        const int32_t* slots, void* o, int64_t ldo, void* stream);
+BS_API size_t bs_gdelta_workspace(int heads_v, int64_t batch, int64_t rows);
+BS_API size_t bs_gdelta_tape(int heads_v, int dk, int dv, int64_t batch, int64_t rows);
+
 /* 1 if the calls with this type and row length have a kernel instance, else 0 (no launch). */
 BS_API int bs_grec_supported(bs_dtype dtype, int channels);
 BS_API int bs_gnorm_supported(bs_dtype dtype, int width);
+BS_API int bs_gdelta_supported(bs_dtype dtype, int heads_k, int heads_v, int dk, int dv);
 
 /* Human-readable name of a status code (a static string). */
 BS_API const char* bs_status_string(bs_status status);
