@@ -56,6 +56,7 @@ EXPORTED = (
     "bs_grec_tape_rows", "bs_grec_backward_workspace", "bs_grec_supported",
     "bs_gnorm_batched", "bs_gnorm_backward_batched", "bs_gnorm_backward_workspace",
     "bs_gnorm_supported",
+    "bs_gnorm_q8_batched", "bs_gemm_q8",
     "bs_gdelta_batched", "bs_gdelta_step_batched", "bs_gdelta_workspace", "bs_gdelta_tape",
     "bs_gdelta_supported",
     "bs_status_string", "bs_last_cuda_error", "bs_getrf_getrs_supported",
@@ -164,6 +165,10 @@ def lib() -> ctypes.CDLL:
             L.bs_grec_supported.restype = i32
             L.bs_gnorm_supported.argtypes = [i32, i32]
             L.bs_gnorm_supported.restype = i32
+            L.bs_gnorm_q8_batched.argtypes = [i32, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp,
+                                              f64, i32, vp, i64, vp, i64, vp, i64, vp]
+            L.bs_gemm_q8.argtypes = [i32, i64, i64, i64, *[vp, i64] * 5, vp]
+            L.bs_gnorm_q8_batched.restype = L.bs_gemm_q8.restype = i32
             heads = [i32, i32, i32, i32, i32]  # dtype, heads_k, heads_v, dk, dv
             given = [vp, i64] * 5 + [f64]      # q, k, v, g, beta with their row distances, scale
             L.bs_gdelta_batched.argtypes = [*heads, i64, i64, vp, *given, vp, vp, i64, vp, vp, vp, sz,
@@ -693,6 +698,25 @@ def bs_gnorm_backward_batched(f, dy, df, work=None, z=None, x=None, w_post=None,
                                 dscale, dw_pre, eps, gate, _row_stream(stream, f))
     if st:
         _check(st, "bs_gnorm_backward_batched")
+
+
+def bs_gnorm_q8_batched(f, q, scales, y=None, z=None, x=None, w_post=None, scale=None, w_pre=None,
+                        eps: float = 1e-6, gate: int = BS_GATE_SILU, stream=None) -> None:
+    """bs_gnorm_batched with its last value, u where w_pre is given, else y, in 8 bits (see bsolve.h):
+    q, float8_e4m3fn of f's shape, and scales, float32, one for each 128 elements of a row."""
+    st = _rows().gnorm_q8(f, q, scales, y, z, x, w_post, scale, w_pre, eps, gate,
+                          _row_stream(stream, f))
+    if st:
+        _check(st, "bs_gnorm_q8_batched")
+
+
+def bs_gemm_q8(a, sa, w, sw, y, stream=None) -> None:
+    """y <- a w^T of 8-bit operands under block scales (see bsolve.h). a: (rows, k) or (batch, length, k)
+    float8_e4m3fn, sa: its scales as bs_gnorm_q8_batched leaves them; w: (n, k) float8_e4m3fn, sw:
+    (ceil(n / 128), ceil(k / 128)) float32; y: (..., n) float32, bfloat16 or float16."""
+    st = _rows().gemm_q8(a, sa, w, sw, y, _row_stream(stream, y))
+    if st:
+        _check(st, "bs_gemm_q8")
 
 
 def bs_gdelta_workspace(heads_v: int, batch: int, rows: int) -> int:

@@ -1,4 +1,4 @@
-// C ABI of the row operators (bs_grec and bs_gnorm calls of bsolve.h): argument checks and
+// C ABI of the row operators (bs_grec, bs_gnorm and bs_gemm_q8 calls of bsolve.h): argument checks and
 // dispatch to the kernel launchers.
 #include <cmath>
 #include <cstdint>
@@ -261,6 +261,69 @@ bs_status bs_gnorm_backward_batched(bs_dtype dtype, int64_t rows, int width, con
 size_t bs_gnorm_backward_workspace(int width, int64_t rows) {
   if (width < 1 || width > kMaxWidth || rows < 0) return 0;
   return bsolve::gnorm_backward_workspace(width, rows);
+}
+
+bs_status bs_gnorm_q8_batched(bs_dtype dtype, int64_t rows, int width, const void* f, int64_t ldf,
+                              const void* z, int64_t ldz, const void* x, int64_t ldx,
+                              const float* w_post, const float* scale, const float* w_pre,
+                              double eps, bs_gate gate, void* y, int64_t ldy, uint8_t* q,
+                              int64_t ldq, float* scales, int64_t lds, void* stream) {
+  if (rows < 0 || width < 0) return BS_ERR_INVALID_ARG;
+  if (!(static_cast<float>(eps) > 0.f) || !std::isfinite(static_cast<float>(eps)) ||
+      gate < BS_GATE_SILU || gate > BS_GATE_LINEAR)
+    return BS_ERR_INVALID_ARG;
+  if (!gnorm_ok(dtype, width) || rows > kMaxRows) return BS_ERR_UNSUPPORTED;
+  const int blocks = (width + 127) / 128;
+  if (bad_ld(ldf, width) || (z && bad_ld(ldz, width)) || (x && bad_ld(ldx, width)) ||
+      (y && bad_ld(ldy, width)) || bad_ld(ldq, width) || bad_ld(lds, blocks))
+    return BS_ERR_INVALID_ARG;
+  if (ldf > kMaxLd || (z && ldz > kMaxLd) || (x && ldx > kMaxLd) || (y && ldy > kMaxLd) ||
+      ldq > kMaxLd || lds > kMaxLd)
+    return BS_ERR_UNSUPPORTED;
+  if (rows == 0) return BS_OK;
+  if (!f || !q || !scales) return BS_ERR_INVALID_ARG;
+  const uintptr_t es = element_size(dtype);
+  if (!aligned(f, es) || !aligned(z, es) || !aligned(x, es) || !aligned(y, es) ||
+      !aligned(scales, 4) || !aligned(w_post, 4) || !aligned(scale, 4) || !aligned(w_pre, 4))
+    return BS_ERR_INVALID_ARG;
+  const int64_t e = es, w = width * e, sw = width * int64_t(4);
+  if (!apart({{y, rows, w, ldy * e}, {q, rows, width, ldq}, {scales, rows, blocks * 4, lds * 4}},
+             {{f, rows, w, ldf * e}, {z, rows, w, ldz * e}, {x, rows, w, ldx * e},
+              {w_post, 1, sw, sw}, {scale, 1, sw, sw}, {w_pre, 1, sw, sw}}))
+    return BS_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return done(with_type(dtype, [&](auto zero) {
+    using T = decltype(zero);
+    const bsolve::GnormRows<T> p{rows, width, static_cast<const T*>(f), static_cast<const T*>(z),
+                                 static_cast<const T*>(x), ldf, ldz, ldx, w_post, scale, w_pre,
+                                 static_cast<float>(eps), static_cast<int>(gate)};
+    return bsolve::launch_gnorm_q8<T>(p, static_cast<T*>(y), ldy, {q, ldq, scales, lds}, s);
+  }));
+}
+
+bs_status bs_gemm_q8(bs_dtype dtype, int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t lda,
+                     const float* sa, int64_t ldsa, const uint8_t* w, int64_t ldw, const float* sw,
+                     int64_t ldsw, void* y, int64_t ldy, void* stream) {
+  if (m < 0 || n < 0 || k < 0) return BS_ERR_INVALID_ARG;
+  if (element_size(dtype) == 0 || m > kMaxRows || n > kMaxLd || k > kMaxLd) return BS_ERR_UNSUPPORTED;
+  const int64_t blocks = (k + 127) / 128, groups = (n + 127) / 128;
+  if (lda < k || ldw < k || ldsa < blocks || ldsw < blocks || ldy < n) return BS_ERR_INVALID_ARG;
+  if (lda > kMaxLd || ldw > kMaxLd || ldsa > kMaxLd || ldsw > kMaxLd || ldy > kMaxLd)
+    return BS_ERR_UNSUPPORTED;
+  if (m == 0 || n == 0) return BS_OK;
+  const int64_t es = element_size(dtype);
+  if (!y || (k > 0 && (!a || !sa || !w || !sw))) return BS_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(w, 16) || (m > 1 && lda % 16) || (n > 1 && ldw % 16) ||
+      !aligned(sa, 4) || !aligned(sw, 4) || !aligned(y, es))
+    return BS_ERR_INVALID_ARG;
+  if (!apart({{y, m, n * es, ldy * es}}, {{a, m, k, lda}, {sa, m, blocks * 4, ldsa * 4}, {w, n, k, ldw},
+                                          {sw, groups, blocks * 4, ldsw * 4}}))
+    return BS_ERR_INVALID_ARG;
+  return done(with_type(dtype, [&](auto zero) {
+    using T = decltype(zero);
+    return bsolve::launch_gemm_q8<T>({m, n, k, a, lda, sa, ldsa, w, ldw, sw, ldsw, static_cast<T*>(y), ldy},
+                                     static_cast<cudaStream_t>(stream));
+  }));
 }
 
 int bs_gnorm_supported(bs_dtype dtype, int width) { return gnorm_ok(dtype, width) ? 1 : 0; }

@@ -1,0 +1,416 @@
+// Matrix product of 8-bit operands under block scales (bs_gemm_q8):
+//   y[t][f] = sum over blocks b of 128 of  sa[t][b] sw[f / 128][b] sum over k in b of a[t][k] w[f][k].
+//
+// tcgen05.mma (e4m3, FP32 sums in tensor memory) takes the features as its 128 rows and TOKENS tokens as its
+// columns: a tile's 128 features share one weight scale a block, one token costs 16 columns at
+// least instead of 128 rows, and a lane of the result is a feature, so that a warp's stores of one token are
+// contiguous. Each block of 128 is a result of its own (four instructions of depth 32), which eight warps
+// read back, multiply by its two scales and add up in FP32 registers while the next ones are computed
+// into other columns of tensor memory. One thread keeps TMA copies of both operands several blocks ahead, one
+// issues the products. Persistent blocks, one an SM; where tiles are fewer than SMs, clusters of 2 to
+// 8 blocks share a tile's blocks of k and add their parts through distributed shared memory in order.
+//
+// Every wait is limited (kPatience); a block whose wait ran out stores NaN.
+#include <algorithm>
+#include <atomic>
+
+#include <cuda.h>
+
+#include "cluster.cuh"
+#include "common.cuh"
+#include "grec_math.cuh"
+#include "kernels.h"
+#include "row_types.cuh"
+
+namespace bsolve {
+namespace {
+
+constexpr int kBlock = 128;       // elements under one scale, features of a tile
+constexpr int kSumWarps = 8;      // warps that scale and add
+constexpr int kThreads = (kSumWarps + 2) * 32;
+constexpr int kMaxSplit = 8;
+
+template <int TOKENS>
+struct Config {
+  static constexpr int kStage = (kBlock + TOKENS) * kBlock;  // bytes of both operands' block
+  static constexpr int kStages = TOKENS == 256 ? 4 : TOKENS == 128 ? 6 : 8;
+  static constexpr int kResults = TOKENS == 256 ? 2 : 4;     // results in tensor memory
+  static constexpr int kColumns = TOKENS * kResults < 32 ? 32 : TOKENS * kResults;
+  static constexpr int kOwn = TOKENS / 2;                    // columns of a summing thread
+  static constexpr int kPiece = kOwn < 32 ? kOwn : TOKENS == 256 ? 16 : 32;       // columns read at once
+  static constexpr int kShared = kStages * kStage + 1024;    // the stages start on 1024 bytes
+};
+
+struct Problem {
+  int64_t m, n, k;
+  const float *sa, *sw;
+  int64_t ldsa, ldsw, ldy;
+};
+
+// ---------------------------------------------------------------------------- barriers, copies
+constexpr long long kPatience = 4000000000ll;  // clocks, about two seconds
+
+__device__ __forceinline__ unsigned addr(const void* p) {
+  return static_cast<unsigned>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void barrier_init(uint64_t* b, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(addr(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr(b)) : "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint64_t* b, int bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(addr(b)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool barrier_passed(uint64_t* b, unsigned parity) {
+  unsigned done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done) : "r"(addr(b)), "r"(parity) : "memory");
+  return done;
+}
+// False where the wait ran out, here or (`failed`) elsewhere in the block.
+__device__ __forceinline__ bool wait_for(uint64_t* b, unsigned parity, volatile int* failed) {
+  if (barrier_passed(b, parity)) return true;
+  const long long start = clock64();
+  while (!barrier_passed(b, parity)) {
+    if (*failed) return false;
+    if (clock64() - start > kPatience) {
+      *failed = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ void copy_tile(void* to, const CUtensorMap* map, int x, int y, uint64_t* b) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3}], [%4];" ::"r"(addr(to)),
+      "l"(map), "r"(x), "r"(y), "r"(addr(b))
+      : "memory");
+}
+
+// ---------------------------------------------------------------------------- tensor memory
+// A tile of rows of 128 bytes in shared memory as TMA's 128-byte swizzle leaves it: eight rows (1024 bytes)
+// a group.
+__device__ __forceinline__ uint64_t operand_at(unsigned at) {
+  return static_cast<uint64_t>((at & 0x3FFFF) >> 4) | uint64_t(1) << 16 | uint64_t(1024 >> 4) << 32 |
+         uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+// e4m3 by e4m3 into FP32, both along k, 128 rows, so many columns.
+__host__ __device__ constexpr unsigned instruction(int columns) {
+  return 1u << 4 | static_cast<unsigned>(columns >> 3) << 17 | static_cast<unsigned>(kBlock >> 4) << 24;
+}
+__device__ __forceinline__ void product(unsigned result, uint64_t a, uint64_t b, unsigned kind,
+                                        bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(result),
+      "l"(a), "l"(b), "r"(kind), "r"(static_cast<unsigned>(add))
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   addr(b)) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void read_columns(unsigned at, float (&v)[N]);
+template <>
+__device__ __forceinline__ void read_columns<8>(unsigned at, float (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+                 "=f"(v[7]) : "r"(at));
+}
+template <>
+__device__ __forceinline__ void read_columns<16>(unsigned at, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
+      "[%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]),
+        "=f"(v[15]) : "r"(at));
+}
+template <>
+__device__ __forceinline__ void read_columns<32>(unsigned at, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]),
+        "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]),
+        "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]),
+        "=f"(v[29]), "=f"(v[30]), "=f"(v[31]) : "r"(at));
+}
+
+// ---------------------------------------------------------------------------- kernel
+template <typename T, int TOKENS>
+__global__ void __launch_bounds__(kThreads, 1)
+gemm_q8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+               Problem p, T* __restrict__ y) {
+  using C = Config<TOKENS>;
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(16) float factors[2][TOKENS];
+  __shared__ uint64_t full[C::kStages], empty[C::kStages], ready[C::kResults], taken[C::kResults];
+  __shared__ unsigned columns;
+  __shared__ volatile int failed;
+  unsigned char* stages = raw + (1024 - (addr(raw) & 1023)) % 1024;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int split = cluster_size(), rank = cluster_rank();
+  const int features = static_cast<int>((p.n + kBlock - 1) / kBlock);
+  const int64_t tiles = features * ((p.m + TOKENS - 1) / TOKENS);
+  const int blocks = static_cast<int>((p.k + kBlock - 1) / kBlock);
+  const int first = static_cast<int>(int64_t(blocks) * rank / split),
+            last = static_cast<int>(int64_t(blocks) * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    failed = 0;
+    for (int s = 0; s < C::kStages; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], 1);
+    for (int r = 0; r < C::kResults; ++r) barrier_init(&ready[r], 1), barrier_init(&taken[r], kSumWarps);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kSumWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(addr(&columns)),
+                 "n"(C::kColumns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const unsigned memory = columns;
+  const int64_t turn = gridDim.x / split;
+
+  if (warp == kSumWarps) {
+    if (lane == 0) {  // copies
+      unsigned it = 0;
+      bool ok = true;
+      for (int64_t tile = blockIdx.x / split; ok && tile < tiles; tile += turn) {
+        const int f0 = static_cast<int>(tile % features) * kBlock;
+        const int t0 = static_cast<int>(tile / features) * TOKENS;
+        for (int b = first; b < last; ++b, ++it) {
+          const unsigned s = it % C::kStages;
+          if (!(ok = wait_for(&empty[s], ((it / C::kStages) & 1) ^ 1, &failed))) break;
+          barrier_expect(&full[s], C::kStage);
+          unsigned char* at = stages + s * C::kStage;
+          copy_tile(at, &map_w, b * kBlock, f0, &full[s]);
+          copy_tile(at + kBlock * kBlock, &map_a, b * kBlock, t0, &full[s]);
+        }
+      }
+      // nothing may be in flight when the block ends
+      for (unsigned back = it > C::kStages ? it - C::kStages : 0; back < it; ++back)
+        for (int n = 0; n < 1000000 && !barrier_passed(&full[back % C::kStages], (back / C::kStages) & 1);
+             ++n) {
+        }
+    }
+  } else if (warp == kSumWarps + 1) {
+    if (lane == 0) {  // products
+      unsigned it = 0;
+      bool ok = true;
+      for (int64_t tile = blockIdx.x / split; ok && tile < tiles; tile += turn)
+        for (int b = first; b < last; ++b, ++it) {
+          const unsigned s = it % C::kStages, r = it % C::kResults;
+          if (!(ok = wait_for(&taken[r], ((it / C::kResults) & 1) ^ 1, &failed) &&
+                     wait_for(&full[s], (it / C::kStages) & 1, &failed)))
+            break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const unsigned at = addr(stages + s * C::kStage);
+#pragma unroll
+          for (int k = 0; k < kBlock; k += 32)
+            product(memory + r * TOKENS, operand_at(at + k), operand_at(at + kBlock * kBlock + k),
+                    instruction(TOKENS), k > 0);
+          commit(&empty[s]);
+          commit(&ready[r]);
+        }
+      for (int n = 0; it > 0 && n < 1000000; ++n)  // none may be in flight when the block ends
+        if (barrier_passed(&ready[(it - 1) % C::kResults], ((it - 1) / C::kResults) & 1)) break;
+    }
+  } else {
+    // warp w: lanes (features) 32 (w % 4) .., columns (tokens) of half w / 4
+    const int half = warp / 4 * C::kOwn;
+    const unsigned lanes = static_cast<unsigned>(warp % 4 * 32) << 16;
+    unsigned it = 0;
+    bool ok = true;
+    for (int64_t tile = blockIdx.x / split; tile < tiles; tile += turn) {
+      const int64_t f0 = tile % features, t0 = tile / features * TOKENS;
+      const int64_t token = t0 + threadIdx.x;
+      const bool scales = threadIdx.x < TOKENS && token < p.m;
+      const float* sa = p.sa + token * p.ldsa;
+      const float* sw = p.sw + f0 * p.ldsw;
+      float sum[C::kOwn];
+#pragma unroll
+      for (int j = 0; j < C::kOwn; ++j) sum[j] = 0.f;
+      float next_a = scales && first < last ? sa[first] : 0.f, next_w = first < last ? sw[first] : 0.f;
+      for (int b = first; b < last; ++b, ++it) {  // with `ok` gone too: all warps meet
+        float* f = factors[it & 1];
+        if (threadIdx.x < TOKENS) f[threadIdx.x] = __fmul_rn(next_a, next_w);
+        if (b + 1 < last) {
+          next_a = scales ? sa[b + 1] : 0.f;
+          next_w = sw[b + 1];
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kSumWarps * 32) : "memory");
+        const unsigned r = it % C::kResults;
+        ok = __all_sync(0xFFFFFFFFu, ok && wait_for(&ready[r], (it / C::kResults) & 1, &failed));
+        if (ok) {
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+          for (int c = 0; c < C::kOwn; c += C::kPiece) {
+            float v[C::kPiece];
+            read_columns<C::kPiece>(memory + lanes + r * TOKENS + half + c, v);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+            for (int j = 0; j < C::kPiece; j += 4) {
+              const float4 q = *reinterpret_cast<const float4*>(&f[half + c + j]);
+              const float2 x = fma2(make_float2(v[j], v[j + 1]), make_float2(q.x, q.y),
+                                    make_float2(sum[c + j], sum[c + j + 1]));
+              const float2 z = fma2(make_float2(v[j + 2], v[j + 3]), make_float2(q.z, q.w),
+                                    make_float2(sum[c + j + 2], sum[c + j + 3]));
+              sum[c + j] = x.x, sum[c + j + 1] = x.y, sum[c + j + 2] = z.x, sum[c + j + 3] = z.y;
+            }
+          }
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) barrier_arrive(&taken[r]);
+        }
+      }
+      const int64_t feature = f0 * kBlock + warp % 4 * 32 + lane;
+      if (split == 1) {
+        if (feature < p.n) {
+          T* to = y + t0 * p.ldy + feature;
+          const int64_t left = p.m - t0 - half;
+#pragma unroll
+          for (int j = 0; j < C::kOwn; ++j)
+            if (j < left) to[(half + j) * p.ldy] = from_f32<T>(ok ? sum[j] : __int_as_float(0x7FC00000));
+        }
+      } else {
+        // the parts of a tile (one a cluster): [token][feature] in the stages, whose copies are all used
+        float* part = reinterpret_cast<float*>(stages);
+#pragma unroll
+        for (int j = 0; j < C::kOwn; ++j)
+          part[(half + j) * kBlock + warp % 4 * 32 + lane] = ok ? sum[j] : __int_as_float(0x7FC00000);
+      }
+    }
+  }
+  __syncwarp();
+  if (split > 1) {
+    cluster_publish();
+    cluster_sync();
+    const int64_t tile = blockIdx.x / split;
+    const int64_t f0 = tile % features * kBlock, t0 = tile / features * TOKENS;
+    const unsigned part = addr(stages);
+    for (int j = rank * kThreads + threadIdx.x; j < TOKENS * kBlock; j += split * kThreads) {
+      const int64_t t = t0 + j / kBlock, f = f0 + j % kBlock;
+      if (t >= p.m || f >= p.n) continue;
+      float sum = 0.f;
+      for (int r = 0; r < split; ++r) {
+        unsigned at;
+        float v;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(part + 4 * j), "r"(r));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+        sum = __fadd_rn(sum, v);
+      }
+      y[t * p.ldy + f] = from_f32<T>(sum);
+    }
+    cluster_sync();
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (warp == kSumWarps)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(memory), "n"(C::kColumns));
+}
+
+// ---------------------------------------------------------------------------- launch
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                            const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                            CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                            CUtensorMapFloatOOBfill);
+
+cudaError_t encoder(Encode* out) {
+  static std::atomic<Encode> kept{nullptr};  // the driver's function, the same for the whole process
+  Encode known = kept.load();
+  if (!known) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+    kept.store(known = reinterpret_cast<Encode>(f));
+  }
+  *out = known;
+  return cudaSuccess;
+}
+
+cudaError_t tile_map(Encode encode, CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t width,
+                     int64_t ld, int box) {
+  const cuuint64_t dims[] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[] = {static_cast<cuuint64_t>(ld)};
+  const cuuint32_t tile[] = {kBlock, static_cast<cuuint32_t>(box)}, steps[] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides,
+                            tile, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <typename T, int TOKENS>
+cudaError_t run(Encode encode, const GemmQ8<T>& g, cudaStream_t stream) {
+  using C = Config<TOKENS>;
+  CUtensorMap w, a;
+  cudaError_t e = tile_map(encode, &w, g.w, g.n, g.k, g.ldw, kBlock);
+  if (e == cudaSuccess) e = tile_map(encode, &a, g.a, g.m, g.k, g.lda, TOKENS);
+  auto* kernel = gemm_q8_kernel<T, TOKENS>;
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kShared);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (g.n + kBlock - 1) / kBlock * ((g.m + TOKENS - 1) / TOKENS);
+  const int64_t blocks = (g.k + kBlock - 1) / kBlock;
+  // a tile's blocks of k over a cluster while that leaves no SM with two parts, nor a part without two blocks
+  int split = 1;
+  while (2 * split <= kMaxSplit && tiles * 2 * split <= kSms && blocks >= 4 * split) split *= 2;
+  const int64_t grid = split > 1 ? tiles * split : std::min<int64_t>(tiles, kSms);
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t config = cluster_config(&attr, dim3(static_cast<unsigned>(grid)), kThreads,
+                                                   C::kShared, split, stream);
+  return cudaLaunchKernelEx(&config, kernel, w, a,
+                            Problem{g.m, g.n, g.k, g.sa, g.sw, g.ldsa, g.ldsw, g.ldy}, g.y);
+}
+
+// y = 0: no block of k.
+template <typename T>
+__global__ void zero_kernel(int64_t m, int64_t n, int64_t ldy, T* y) {
+  for (int64_t j = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; j < m * n;
+       j += int64_t(gridDim.x) * blockDim.x)
+    y[j / n * ldy + j % n] = from_f32<T>(0.f);
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t launch_gemm_q8(const GemmQ8<T>& g, cudaStream_t stream) {
+  if (g.k == 0) {
+    zero_kernel<<<kSms, 256, 0, stream>>>(g.m, g.n, g.ldy, g.y);
+    return cudaGetLastError();
+  }
+  Encode encode;
+  const cudaError_t e = encoder(&encode);
+  if (e != cudaSuccess) return e;
+  if (g.m <= 16) return run<T, 16>(encode, g, stream);
+  if (g.m <= 32) return run<T, 32>(encode, g, stream);
+  if (g.m <= 64) return run<T, 64>(encode, g, stream);
+  // The least (turns of all SMs) x (a tile's time): its products take 2 cycles a token and block, its copies
+  // not less than 250 cycles a block, its start and end about 3000.
+  const int64_t features = (g.n + kBlock - 1) / kBlock, blocks = (g.k + kBlock - 1) / kBlock;
+  auto cost = [&](int tokens) {
+    const int64_t tiles = features * ((g.m + tokens - 1) / tokens);
+    return (tiles + kSms - 1) / kSms * (blocks * std::max(2 * tokens, 250) + 3000);
+  };
+  const int64_t c64 = cost(64), c128 = cost(128), c256 = cost(256);
+  if (c256 <= c128 && c256 <= c64) return run<T, 256>(encode, g, stream);
+  return c128 <= c64 ? run<T, 128>(encode, g, stream) : run<T, 64>(encode, g, stream);
+}
+template cudaError_t launch_gemm_q8(const GemmQ8<float>&, cudaStream_t);
+template cudaError_t launch_gemm_q8(const GemmQ8<__nv_bfloat16>&, cudaStream_t);
+template cudaError_t launch_gemm_q8(const GemmQ8<__half>&, cudaStream_t);
+
+}  // namespace bsolve

@@ -20,6 +20,8 @@
 
 #include <type_traits>
 
+#include <cuda_fp8.h>
+
 #include "gnorm_math.cuh"
 #include "gnorm_shapes.cuh"
 #include "kernels.h"
@@ -108,10 +110,110 @@ struct Group {
   static constexpr int kGroups = kBlock / THREADS;
 };
 
-// ------------------------------------------------------------------ forward
 // How a call's operands lie. kFull: every operand there, 16-byte bases, row distances and widths; kAligned:
 // 16-byte bases and row distances; kAny.
 enum Mode : int { kFull = 0, kAligned = 1, kAny = 2 };
+
+// ------------------------------------------------------------------ output in 8 bits
+// bs_gnorm_q8_batched: the row's last value v (u, or y without a norm behind it) as e4m3 numbers v / s under
+// one scale s = max(max |v|, 2^-100) / 448 for each 128 elements. The largest magnitude goes through integer
+// maxima of the numbers' bits, which order them and keep a NaN.
+constexpr int kScaled = 128;  // elements under one scale
+
+struct Scale {
+  float s, inverse;
+};
+__device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ Scale scale_of(unsigned top) {
+  const float m = __uint_as_float(max(top, __float_as_uint(0x1p-100f)));
+  return {__fdiv_rn(m, 448.f), __fdiv_rn(448.f, m)};
+}
+__device__ __forceinline__ unsigned as_e4m3(float2 v) {
+  return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+}
+
+// The numbers of ROWS rows and where they go. `tops`, [ROWS][blocks], is shared memory of the group, used
+// where a thread's elements lie apart (kAny).
+template <int H, int K, int THREADS, int MODE>
+struct Quantise {
+  static constexpr int VE = 2 * H;
+  static constexpr int kBlocks = THREADS * K * VE < kScaled ? 1 : THREADS * K * VE / kScaled;
+  static constexpr int kLanes = kScaled / VE < THREADS ? kScaled / VE : THREADS;  // of a scale
+
+  // Threads of a group wait for each other.
+  static __device__ __forceinline__ void meet() {
+    if (THREADS > 32) __syncthreads(); else __syncwarp();
+  }
+
+  template <int ROWS>
+  static __device__ __forceinline__ void put(const Bytes8& out, unsigned row0, unsigned rows, int t,
+                                             int width, const float2 (&v)[ROWS][K][H],
+                                             unsigned* tops) {
+    if constexpr (MODE != kAny) {
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          unsigned top = 0;
+#pragma unroll
+          for (int e = 0; e < H; ++e)
+            top = max(top, max(magnitude(v[i][k][e].x), magnitude(v[i][k][e].y)));
+#pragma unroll
+          for (int m = 1; m < kLanes; m *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+          const Scale s = scale_of(top);
+          const int at = (k * THREADS + t) * VE;
+          if (row0 + i >= rows || at >= width) continue;
+          const unsigned row = row0 + i;
+          if (at % kScaled == 0) out.s[row * out.lds + at / kScaled] = s.s;
+          unsigned w[H / 2];
+#pragma unroll
+          for (int e = 0; e < H; e += 2)
+            w[e / 2] = as_e4m3(v[i][k][e] * both(s.inverse)) |
+                       as_e4m3(v[i][k][e + 1] * both(s.inverse)) << 16;
+          uint8_t* to = out.q + row * out.ldq + at;
+          if (MODE == kFull || at + VE <= width) {
+            if constexpr (H == 4) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<unsigned*>(to) = w[0];
+          } else {
+            for (int e = 0; e < width - at; ++e) to[e] = static_cast<uint8_t>(w[e / 4] >> (8 * (e % 4)));
+          }
+        }
+    } else {
+      for (int j = t; j < ROWS * kBlocks; j += THREADS) tops[j] = 0;
+      meet();
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            const float x = e & 1 ? v[i][k][e / 2].y : v[i][k][e / 2].x;
+            const int c = row_element<VE, THREADS, false>(t, k, e);
+            if (c < width) atomicMax(&tops[i * kBlocks + c / kScaled], magnitude(x));
+          }
+      meet();
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        if (row0 + i >= rows) continue;
+        const unsigned row = row0 + i;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            const float x = e & 1 ? v[i][k][e / 2].y : v[i][k][e / 2].x;
+            const int c = row_element<VE, THREADS, false>(t, k, e);
+            if (c >= width) continue;
+            const Scale s = scale_of(tops[i * kBlocks + c / kScaled]);
+            out.q[row * out.ldq + c] = static_cast<uint8_t>(as_e4m3(make_float2(x * s.inverse, 0.f)));
+            if (c % kScaled == 0) out.s[row * out.lds + c / kScaled] = s.s;
+          }
+      }
+      meet();
+    }
+  }
+};
+
+// ------------------------------------------------------------------ forward
 
 // One group's thread and its part of a row: VE = 2 H elements a vector, K vectors.
 template <typename T, int H, int K, int THREADS, int ROWS, int MODE>
@@ -201,9 +303,11 @@ struct Part {
   }
 };
 
-template <typename T, int H, int K, int THREADS, int ROWS, int MODE>
+// Q8: u goes out in 8 bits, to `bytes8`.
+template <typename T, int H, int K, int THREADS, int ROWS, int MODE, bool Q8>
 __global__ void __launch_bounds__(Group<THREADS>::kBlock, 1024 / Group<THREADS>::kBlock)
-gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, int64_t ldu) {
+gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, int64_t ldu,
+             Bytes8 bytes8) {
   using G = Group<THREADS>;
   using P = Part<T, H, K, THREADS, ROWS, MODE>;
   constexpr int kRow = P::kRow;
@@ -315,6 +419,26 @@ gnorm_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, 
     P::meet();  // every thread has read its rows before they are overwritten
     stage(row0 + 2 * turn_rows, slot);
     slot ^= 1;
+    if constexpr (Q8) {
+      if (kAll || p.w_pre) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          float2 w[H];
+          P::params(p.w_pre, 1.f, t, k, p.width, w);
+#pragma unroll
+          for (int i = 0; i < ROWS; ++i) {
+            const float r = inverse_root(fmaf(s[i], inv, p.eps));
+#pragma unroll
+            for (int e = 0; e < H; ++e) v[i][k][e] = v[i][k][e] * (both(r) * w[e]);
+          }
+        }
+      }
+      using Q = Quantise<H, K, THREADS, MODE>;
+      __shared__ unsigned tops[MODE == kAny ? G::kGroups * ROWS * Q::kBlocks : 1];
+      Q::template put<ROWS>(bytes8, row0, rows, t, p.width, v,
+                            tops + (MODE == kAny ? group * ROWS * Q::kBlocks : 0));
+      continue;
+    }
     if (!kAll && !u) continue;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -626,15 +750,16 @@ __device__ __forceinline__ float post_norm(const GnormRows<T>& p, int64_t row, f
   return inverse_root(fmaf(block_sum(sum, red, turn), 1.f / p.width, p.eps));
 }
 
-template <typename T>
+template <typename T, bool Q8>
 __global__ void __launch_bounds__(kLong)
-gnorm_long_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, int64_t ldu) {
+gnorm_long_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict__ u, int64_t ldu,
+                  Bytes8 bytes8) {
   __shared__ float red[kRedFloats<1, kLong>];
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const float r1 = post_norm(p, row, red, turn);
     float r2 = 1.f;
-    if (u) {
+    if (Q8 ? p.w_pre != nullptr : u != nullptr) {
       float sum = 0.f;
       for (int c = threadIdx.x; c < p.width; c += kLong) {
         const float v = new_residual(p, row, c, r1);
@@ -642,10 +767,37 @@ gnorm_long_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict_
       }
       r2 = inverse_root(fmaf(block_sum(sum, red, turn), 1.f / p.width, p.eps));
     }
-    for (int c = threadIdx.x; c < p.width; c += kLong) {
-      const float v = new_residual(p, row, c, r1);
-      if (y) y[row * ldy + c] = from_f32<T>(v);
-      if (u) u[row * ldu + c] = from_f32<T>(v * (r2 * p.w_pre[c]));
+    if constexpr (Q8) {  // the 128 elements under a scale by one warp
+      const int lane = threadIdx.x & 31;
+      for (int block = threadIdx.x / 32; block * kScaled < p.width; block += kLong / 32) {
+        float v[kScaled / 32];
+        unsigned top = 0;
+#pragma unroll
+        for (int j = 0; j < kScaled / 32; ++j) {
+          const int c = block * kScaled + j * 32 + lane;
+          v[j] = 0.f;
+          if (c >= p.width) continue;
+          v[j] = new_residual(p, row, c, r1);
+          if (y) y[row * ldy + c] = from_f32<T>(v[j]);
+          if (p.w_pre) v[j] *= r2 * p.w_pre[c];
+          top = max(top, magnitude(v[j]));
+        }
+        const Scale s = scale_of(__reduce_max_sync(0xFFFFFFFFu, top));
+        if (lane == 0) bytes8.s[row * bytes8.lds + block] = s.s;
+#pragma unroll
+        for (int j = 0; j < kScaled / 32; ++j) {
+          const int c = block * kScaled + j * 32 + lane;
+          if (c < p.width)
+            bytes8.q[row * bytes8.ldq + c] =
+                static_cast<uint8_t>(as_e4m3(make_float2(v[j] * s.inverse, 0.f)));
+        }
+      }
+    } else {
+      for (int c = threadIdx.x; c < p.width; c += kLong) {
+        const float v = new_residual(p, row, c, r1);
+        if (y) y[row * ldy + c] = from_f32<T>(v);
+        if (u) u[row * ldu + c] = from_f32<T>(v * (r2 * p.w_pre[c]));
+      }
     }
   }
 }
@@ -732,19 +884,20 @@ cudaError_t with_threads(int threads, F&& f) {
   }
 }
 
-template <typename T, int MODE>
+template <typename T, int MODE, bool Q8>
 cudaError_t launch_forward(const Shape& s, const GnormRows<T>& p, T* y, int64_t ldy, T* u,
-                           int64_t ldu, cudaStream_t stream) {
+                           int64_t ldu, const Bytes8& bytes8, cudaStream_t stream) {
   constexpr int H = kVecElements<T> / 2;
   auto run = [&](auto c) {
     using C = decltype(c);
     using P = Part<T, H, C::vectors, C::threads, C::rows, MODE>;
     constexpr int kShared = Group<C::threads>::kGroups * kTurns * C::rows * 3 * P::kRow;
-    auto* kernel = gnorm_kernel<T, H, C::vectors, C::threads, C::rows, MODE>;
+    auto* kernel = gnorm_kernel<T, H, C::vectors, C::threads, C::rows, MODE, Q8>;
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
     if (e != cudaSuccess) return e;
-    kernel<<<blocks_for(s, p.rows), Group<C::threads>::kBlock, kShared, stream>>>(p, y, ldy, u, ldu);
+    kernel<<<blocks_for(s, p.rows), Group<C::threads>::kBlock, kShared, stream>>>(p, y, ldy, u, ldu,
+                                                                                 bytes8);
     return cudaGetLastError();
   };
   if (s.threads < 1024) return with_threads<H, 2>(s.threads, run);
@@ -793,17 +946,37 @@ cudaError_t launch_gnorm(const GnormRows<T>& p, T* y, int64_t ldy, T* u, int64_t
                          cudaStream_t stream) {
   const Shape s = forward_shape(p.width, sizeof(T));
   if (s.threads == 0) {
-    gnorm_long_kernel<T><<<blocks_for(s, p.rows, 2 * kLong), kLong, 0, stream>>>(p, y, ldy, u, ldu);
+    gnorm_long_kernel<T, false><<<blocks_for(s, p.rows, 2 * kLong), kLong, 0, stream>>>(p, y, ldy, u,
+                                                                                       ldu, {});
     return cudaGetLastError();
   }
   const Mode mode = Lies<T>()
                         .with(p.f, p.ldf).with(p.z, p.ldz).with(p.x, p.ldx).with(y, ldy)
                         .with(u, ldu).with(p.w_post, 0).with(p.scale, 0).with(p.w_pre, 0)
                         .mode(p.width);
-  auto* launch = mode == kFull      ? launch_forward<T, kFull>
-                 : mode == kAligned ? launch_forward<T, kAligned>
-                                    : launch_forward<T, kAny>;
-  return launch(s, p, y, ldy, u, ldu, stream);
+  auto* launch = mode == kFull      ? launch_forward<T, kFull, false>
+                 : mode == kAligned ? launch_forward<T, kAligned, false>
+                                    : launch_forward<T, kAny, false>;
+  return launch(s, p, y, ldy, u, ldu, {}, stream);
+}
+
+template <typename T>
+cudaError_t launch_gnorm_q8(const GnormRows<T>& p, T* y, int64_t ldy, const Bytes8& out,
+                            cudaStream_t stream) {
+  const Shape s = forward_shape(p.width, sizeof(T));
+  if (s.threads == 0) {
+    gnorm_long_kernel<T, true><<<blocks_for(s, p.rows, 2 * kLong), kLong, 0, stream>>>(p, y, ldy, nullptr,
+                                                                                      0, out);
+    return cudaGetLastError();
+  }
+  const Mode mode = Lies<T>()
+                        .with(p.f, p.ldf).with(p.z, p.ldz).with(p.x, p.ldx).with(y, ldy)
+                        .with(out.q, out.ldq).with(p.w_post, 0).with(p.scale, 0).with(p.w_pre, 0)
+                        .mode(p.width);
+  auto* launch = mode == kFull      ? launch_forward<T, kFull, true>
+                 : mode == kAligned ? launch_forward<T, kAligned, true>
+                                    : launch_forward<T, kAny, true>;
+  return launch(s, p, y, ldy, nullptr, 0, out, stream);
 }
 
 template <typename T>
@@ -841,5 +1014,8 @@ cudaError_t launch_gnorm_backward(const GnormRows<T>& p, const GnormGrads<T>& g,
                                        cudaStream_t);                                           \
   template cudaError_t launch_gnorm_backward<T>(const GnormRows<T>&, const GnormGrads<T>&,      \
                                                 void*, cudaStream_t);
+#define BSOLVE_GNORM_Q8(T)                                                                      \
+  template cudaError_t launch_gnorm_q8<T>(const GnormRows<T>&, T*, int64_t, const Bytes8&,      \
+                                          cudaStream_t);
 
 }  // namespace bsolve

@@ -1,4 +1,4 @@
-// The row operators' calls (bs_grec, bs_gnorm and bs_gdelta calls of bsolve.h) from Python: reads devices, types,
+// The row operators' calls (bs_grec, bs_gnorm, bs_gemm_q8 and bs_gdelta calls of bsolve.h) from Python: reads devices, types,
 // shapes, row distances and pointers from torch tensors, checks them against each other and calls the
 // C ABI. A call costs about 3 us with its launch; reading as much tensor by tensor in Python
 // takes 5 us warm and twice that between a program's other work, more than a small call's kernel.
@@ -92,36 +92,41 @@ struct Row {
   int64_t ld = 0;
 };
 
-// A row operand: of the type and shape, on the device, the last stride 1 and the rows at one
-// distance. None: null.
-Row row(PyObject* o, const char* name, const Like& like) {
+// A row operand of a type and shape, on the device, the last stride 1 and the rows at one distance.
+// None: null.
+Row row_of(PyObject* o, const char* name, const Like& like, at::ScalarType type,
+           c10::IntArrayRef shape) {
   const at::Tensor* t = tensor(o, name);
   Row r;
   if (!t) return r;
-  if (t->scalar_type() != like.type)
+  if (t->scalar_type() != type)
     type_error(std::string(name) + ": dtype " + c10::toString(t->scalar_type()) + ", expected " +
-               c10::toString(like.type));
+               c10::toString(type));
   const auto s = t->sizes();
-  if (s != like.shape)
-    value_error(std::string(name) + ": shape " + text(s) + ", expected " + text(like.shape));
+  const int64_t width = shape.back();
+  if (s != shape)
+    value_error(std::string(name) + ": shape " + text(s) + ", expected " + text(shape));
   if (!t->is_cuda() || t->get_device() != like.device)
     value_error(std::string(name) + ": bsolve operands are device tensors of one device");
   const auto st = t->strides();
-  if (like.width > 1 && st.back() != 1)
+  if (width > 1 && st.back() != 1)
     value_error(std::string(name) + ": the elements of a row must be contiguous");
   if (s.size() == 3) {
-    r.ld = s[1] > 1 ? st[1] : (s[0] > 1 ? st[0] : like.width);
+    r.ld = s[1] > 1 ? st[1] : (s[0] > 1 ? st[0] : width);
     if (s[0] > 1 && s[1] > 1 && st[0] != s[1] * r.ld)
       value_error(std::string(name) + ": the rows of all sequences must lie at one distance");
   } else {
-    r.ld = s[0] > 1 ? st[0] : like.width;
+    r.ld = s[0] > 1 ? st[0] : width;
   }
-  if (r.ld < like.width) {
+  if (r.ld < width) {
     if (t->numel()) value_error(std::string(name) + ": rows overlap");
-    r.ld = like.width;
+    r.ld = width;
   }
   r.p = address(*t, name);
   return r;
+}
+Row row(PyObject* o, const char* name, const Like& like) {
+  return row_of(o, name, like, like.type, like.shape);
 }
 
 // A contiguous operand of numel elements. None: null.
@@ -333,6 +338,46 @@ PyObject* gnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The shape of rows that lie beside others', `width` elements each.
+std::vector<int64_t> beside(c10::IntArrayRef shape, int64_t width) {
+  std::vector<int64_t> v(shape.begin(), shape.end());
+  v.back() = width;
+  return v;
+}
+
+PyObject* gnorm_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("gnorm_q8", n, 12, [&] {
+    const Like l(a[0], "f");
+    const Row f = row(a[0], "f", l), q = row_of(a[1], "q", l, at::kFloat8_e4m3fn, l.shape),
+              s = row_of(a[2], "scales", l, at::kFloat, beside(l.shape, (l.width + 127) / 128)),
+              y = row(a[3], "y", l), z = row(a[4], "z", l), x = row(a[5], "x", l);
+    const int w = static_cast<int>(l.width);
+    return enter(l, bs_gnorm_q8_batched, l.code, l.rows(), w, f.p, f.ld, z.p, z.ld, x.p, x.ld,
+                 f32(a[6], "w_post", l, w), f32(a[7], "scale", l, w), f32(a[8], "w_pre", l, w),
+                 number(a[9]), static_cast<bs_gate>(small(a[10])), y.p, y.ld,
+                 static_cast<uint8_t*>(q.p), q.ld, static_cast<float*>(s.p), s.ld, handle(a[11]));
+  });
+}
+
+PyObject* gemm_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("gemm_q8", n, 6, [&] {
+    const Like l(a[4], "y");
+    const at::Tensor* w = tensor(a[2], "w");
+    if (!w || w->dim() != 2)
+      value_error("w: shape " + (w ? text(w->sizes()) : std::string("None")) + ", expected (n, k)");
+    const int64_t k = w->size(1), blocks = (k + 127) / 128;
+    const int64_t own[] = {l.width, k}, groups[] = {(l.width + 127) / 128, blocks};
+    const Row y = row(a[4], "y", l),
+              ra = row_of(a[0], "a", l, at::kFloat8_e4m3fn, beside(l.shape, k)),
+              sa = row_of(a[1], "sa", l, at::kFloat, beside(l.shape, blocks)),
+              rw = row_of(a[2], "w", l, at::kFloat8_e4m3fn, own),
+              sw = row_of(a[3], "sw", l, at::kFloat, groups);
+    return enter(l, bs_gemm_q8, l.code, l.rows(), l.width, k, static_cast<const uint8_t*>(ra.p), ra.ld,
+                 static_cast<const float*>(sa.p), sa.ld, static_cast<const uint8_t*>(rw.p), rw.ld,
+                 static_cast<const float*>(sw.p), sw.ld, y.p, y.ld, handle(a[5]));
+  });
+}
+
 // Row operands of the gated delta rule: heads of contiguous elements, one after another in a row.
 struct Heads {
   Like q;               // its shape: the rows' and (heads, elements)
@@ -502,6 +547,7 @@ PyMethodDef methods[] = {method<grec>("grec"), method<grec_backward>("grec_backw
                          method<grec_tape_rows>("grec_tape_rows"),
                          method<grec_backward_workspace>("grec_backward_workspace"),
                          method<gnorm_backward_workspace>("gnorm_backward_workspace"),
+                         method<gnorm_q8>("gnorm_q8"), method<gemm_q8>("gemm_q8"),
                          method<gdelta>("gdelta"), method<gdelta_step>("gdelta_step"),
                          method<gdelta_workspace>("gdelta_workspace"),
                          method<gdelta_tape>("gdelta_tape"),

@@ -479,6 +479,44 @@ BS_API bs_status bs_gnorm_backward_batched(bs_dtype dtype, int64_t rows, int wid
 BS_API size_t bs_gnorm_backward_workspace(int width, int64_t rows);
 
 /*
+ * bs_gnorm_batched with its last output in 8 bits, for a product on 8-bit operands: where w_pre
+ * is given q holds u, else y (before its rounding to dtype; all of z, x, w_post, scale, w_pre and y are
+ * optional). With v that value and B the 128-element block of a row that it belongs to (the
+ * last one of a row may be shorter),
+ *   scales[B] = max(max_B |v|, 2^-100) / 448,   q = v / scales[B] rounded to e4m3 (to nearest even).
+ *   q       rows of `width` e4m3 numbers (1 sign, 4 exponent, 3 fraction bits, largest 448), ldq
+ *           bytes apart;
+ *   scales  rows of ceil(width / 128) FP32 numbers, lds apart.
+ * A NaN or an infinity makes its block's scale NaN or infinite. Everything else as bs_gnorm_batched.
+ */
+BS_API bs_status bs_gnorm_q8_batched(bs_dtype dtype, int64_t rows, int width, const void* f,
+                                     int64_t ldf, const void* z, int64_t ldz, const void* x,
+                                     int64_t ldx, const float* w_post, const float* scale,
+                                     const float* w_pre, double eps, bs_gate gate, void* y,
+                                     int64_t ldy, uint8_t* q, int64_t ldq, float* scales,
+                                     int64_t lds, void* stream);
+
+/*
+ * Matrix product on 8-bit operands under block scales: with b = k / 128,
+ *   y[i][j] = sum_k (a[i][k] sa[i][b]) (w[j][k] sw[j / 128][b]).
+ *   a   m rows of k e4m3 numbers, lda apart, sa m rows of ceil(k / 128) FP32 scales, ldsa apart
+ *       (bs_gnorm_q8_batched's outputs);
+ *   w   n rows of k e4m3 numbers, ldw apart, sw ceil(n / 128) rows of ceil(k / 128) scales, ldsw apart:
+ *       one for each 128 x 128 block;
+ *   y   m rows of n elements of dtype (BS_FP32, BS_BF16, BS_FP16), ldy apart.
+ * The products of a block of 128 are summed on the tensor cores in FP32, the blocks in FP32 after their
+ * scales, in an order that the sizes fix; y is rounded once. a and w are 16-byte aligned, lda (of
+ * more than one row) and ldw multiples of 16 bytes; scales and y aligned to their elements. Inputs
+ * may overlap each other, y no operand. k == 0 gives y = 0; m == 0 or n == 0 launches nothing. NaN
+ * and infinite scales stay in their row of a, or in the columns of y that a block of w reaches.
+ * Supported: m <= 2^30, n, k and every ld <= 2^21.
+ */
+BS_API bs_status bs_gemm_q8(bs_dtype dtype, int64_t m, int64_t n, int64_t k, const uint8_t* a,
+                            int64_t lda, const float* sa, int64_t ldsa, const uint8_t* w,
+                            int64_t ldw, const float* sw, int64_t ldsw, void* y, int64_t ldy,
+                            void* stream);
+
+/*
  * Gated delta rule over long sequences: a matrix state per sequence and value head that forgets,
  * is corrected by what it holds under each row's key, and is read by each row's query. With
  * a_t = exp(g_t), S a dk x dv state, q_t and k_t of the value head's key head,
