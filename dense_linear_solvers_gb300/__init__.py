@@ -57,7 +57,8 @@ EXPORTED = (
     "bs_gnorm_batched", "bs_gnorm_backward_batched", "bs_gnorm_backward_workspace",
     "bs_gnorm_supported",
     "bs_gnorm_q8_batched", "bs_gemm_q8",
-    "bs_gdelta_batched", "bs_gdelta_step_batched", "bs_gdelta_workspace", "bs_gdelta_tape",
+    "bs_gdelta_batched", "bs_gdelta_backward_batched", "bs_gdelta_backward_workspace",
+    "bs_gdelta_step_batched", "bs_gdelta_workspace", "bs_gdelta_tape",
     "bs_gdelta_supported",
     "bs_status_string", "bs_last_cuda_error", "bs_getrf_getrs_supported",
     "bs_potrf_potrs_supported", "bs_bdsv_supported", "bs_version",
@@ -173,13 +174,17 @@ def lib() -> ctypes.CDLL:
             given = [vp, i64] * 5 + [f64]      # q, k, v, g, beta with their row distances, scale
             L.bs_gdelta_batched.argtypes = [*heads, i64, i64, vp, *given, vp, vp, i64, vp, vp, vp, sz,
                                             vp]
+            L.bs_gdelta_backward_batched.argtypes = [*heads, i64, i64, vp, *given, vp, vp, i64, vp,
+                                                     *[vp, i64] * 5, vp, vp, sz, vp]
             L.bs_gdelta_step_batched.argtypes = [*heads, i64, *given, vp, i64, vp, vp, i64, vp]
-            for name in ("bs_gdelta_batched", "bs_gdelta_step_batched", "bs_gdelta_supported"):
+            for name in ("bs_gdelta_batched", "bs_gdelta_backward_batched", "bs_gdelta_step_batched",
+                         "bs_gdelta_supported"):
                 getattr(L, name).restype = i32
             L.bs_gdelta_supported.argtypes = heads
             L.bs_gdelta_workspace.argtypes = [i32, i64, i64]
             L.bs_gdelta_tape.argtypes = [i32, i32, i32, i64, i64]
-            for name in ("bs_gdelta_workspace", "bs_gdelta_tape"):
+            L.bs_gdelta_backward_workspace.argtypes = [i32, i32, i32, i64, i64]
+            for name in ("bs_gdelta_workspace", "bs_gdelta_tape", "bs_gdelta_backward_workspace"):
                 getattr(L, name).restype = sz
             L.bs_status_string.argtypes = [i32]
             L.bs_status_string.restype = ctypes.c_char_p
@@ -741,6 +746,23 @@ def bs_gdelta_batched(q, k, v, g, beta, o, work, h0=None, hT=None, offsets=None,
                         _row_stream(stream, q))
     if st:
         _check(st, "bs_gdelta_batched")
+
+
+def bs_gdelta_backward_workspace(heads_v: int, dk: int, dv: int, batch: int, rows: int) -> int:
+    """Bytes of bs_gdelta_backward_batched's workspace."""
+    return _rows().gdelta_backward_workspace(heads_v, dk, dv, batch, rows)
+
+
+def bs_gdelta_backward_batched(q, k, v, g, beta, tape, do, dq, dk, dv, dg, dbeta, work, dhT=None,
+                               dh0=None, offsets=None, scale: float | None = None,
+                               stream=None) -> None:
+    """Gradients of bs_gdelta_batched from its inputs, its tape and the gradients of o (and hT): dq, dk,
+    dv, dg, dbeta (and dh0) are written (see bsolve.h). work: uint8, at least
+    bs_gdelta_backward_workspace(...) elements."""
+    st = _rows().gdelta_backward(q, k, v, g, beta, tape, do, dq, dk, dv, dg, dbeta, work, dhT, dh0,
+                                 offsets, scale, _row_stream(stream, q))
+    if st:
+        _check(st, "bs_gdelta_backward_batched")
 
 
 def bs_gdelta_step_batched(q, k, v, g, beta, state, o, slots=None, scale: float | None = None,

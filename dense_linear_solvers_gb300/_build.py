@@ -33,7 +33,8 @@ LIB_SOURCES = ["api.cu", "lu_reg.cu", "lu_reg_f32_row.cu", "lu_reg_f32_col.cu", 
                "smem_solvers.cu", "chol_sys.cu", "chol_cluster.cu", "bdsv.cu", "bdmv.cu", "solve.cu",
                "solve_lane.cu", "api_rows.cu", "grec.cu", "grec_bwd.cu", "gnorm.cu",
                "gnorm_f32.cu", "gnorm_bf16.cu", "gnorm_f16.cu",
-               "api_delta.cu", "gdelta_prep.cu", "gdelta.cu", "gdelta_step.cu",
+               "api_delta.cu", "gdelta_prep.cu", "gdelta.cu", "gdelta_step.cu", "gdelta_bwd.cu",
+               "gdelta_grad.cu",
                "gnorm_q8_f32.cu", "gnorm_q8_bf16.cu", "gnorm_q8_f16.cu", "gemm_q8.cu"]
 PROBE_SOURCES = ["fma_peak.cu"]
 

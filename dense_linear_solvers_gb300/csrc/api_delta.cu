@@ -102,6 +102,50 @@ bs_status bs_gdelta_batched(bs_dtype dtype, int heads_k, int heads_v, int dk, in
   }));
 }
 
+bs_status bs_gdelta_backward_batched(bs_dtype dtype, int heads_k, int heads_v, int dk, int dv,
+                                     int64_t batch, int64_t rows, const int64_t* offsets,
+                                     const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                     const void* v, int64_t ldv, const float* g, int64_t ldg,
+                                     const float* beta, int64_t ldbeta, double scale,
+                                     const void* tape, const void* d_o, int64_t lddo,
+                                     const float* dhT, void* dq, int64_t lddq, void* d_k,
+                                     int64_t lddk, void* d_v, int64_t lddv, float* dg, int64_t lddg,
+                                     float* dbeta, int64_t lddbeta, float* dh0, void* work,
+                                     size_t work_bytes, void* stream) {
+  const int es = element_size(dtype);
+  const int64_t wk = int64_t(heads_k) * dk, wv = int64_t(heads_v) * dv;
+  const RowArg aq{q, ldq, wk, es}, ak{k, ldk, wk, es}, av{v, ldv, wv, es}, ag{g, ldg, heads_v, 4},
+      ab{beta, ldbeta, heads_v, 4}, ao{d_o, lddo, wv, es}, bq{dq, lddq, wk, es},
+      bk{d_k, lddk, wk, es}, bv{d_v, lddv, wv, es}, bg{dg, lddg, heads_v, 4},
+      bb{dbeta, lddbeta, heads_v, 4};
+  const bs_status st = gdelta_sizes(dtype, heads_k, heads_v, dk, dv, batch, rows, scale,
+                                    {aq, ak, av, ag, ab, ao, bq, bk, bv, bg, bb});
+  if (st != BS_OK) return st;
+  if (batch == 0) return BS_OK;
+  if (!offsets && rows % batch != 0) return BS_ERR_INVALID_ARG;
+  if (!aligned(dhT, 4) || !aligned(dh0, 4) || !aligned(tape, 16) || !aligned(work, 16) ||
+      !aligned(offsets, 8))
+    return BS_ERR_INVALID_ARG;
+  const size_t need = bs_gdelta_backward_workspace(heads_v, dk, dv, batch, rows);
+  if (!tape || !work || work_bytes < need) return BS_ERR_INVALID_ARG;
+  const int64_t state = batch * heads_v * dk * dv * 4;
+  if (!apart({operand(bq, rows), operand(bk, rows), operand(bv, rows), operand(bg, rows),
+              operand(bb, rows), block(dh0, state), block(work, need)},
+             {operand(aq, rows), operand(ak, rows), operand(av, rows), operand(ag, rows),
+              operand(ab, rows), operand(ao, rows), block(dhT == dh0 ? nullptr : dhT, state),
+              block(tape, bs_gdelta_tape(heads_v, dk, dv, batch, rows)),
+              block(offsets, (batch + 1) * 8)}))
+    return BS_ERR_INVALID_ARG;
+  return done(with_type(dtype, [&](auto zero) {
+    using T = decltype(zero);
+    return bsolve::launch_gdelta_backward<T>(
+        gdelta_rows<T>(heads_k, heads_v, dk, dv, batch, rows, offsets, aq, ak, av, ag, ab, scale),
+        tape, static_cast<const T*>(d_o), lddo, dhT, static_cast<T*>(dq), lddq,
+        static_cast<T*>(d_k), lddk, static_cast<T*>(d_v), lddv, dg, lddg, dbeta, lddbeta, dh0, work,
+        static_cast<cudaStream_t>(stream));
+  }));
+}
+
 bs_status bs_gdelta_step_batched(bs_dtype dtype, int heads_k, int heads_v, int dk, int dv,
                                  int64_t batch, const void* q, int64_t ldq, const void* k,
                                  int64_t ldk, const void* v, int64_t ldv, const float* g,
@@ -144,6 +188,13 @@ size_t bs_gdelta_tape(int heads_v, int dk, int dv, int64_t batch, int64_t rows) 
       !gdelta_counts(batch, heads_v, rows))
     return 0;
   return bsolve::gdelta_tape(heads_v, dk, dv, batch, rows);
+}
+
+size_t bs_gdelta_backward_workspace(int heads_v, int dk, int dv, int64_t batch, int64_t rows) {
+  if (!gdelta_ok(BS_FP32, 1, heads_v, dk, dv) || batch < 0 || rows < 0 ||
+      !gdelta_counts(batch, heads_v, rows))
+    return 0;
+  return bsolve::gdelta_backward_workspace(heads_v, dk, dv, batch, rows);
 }
 
 int bs_gdelta_supported(bs_dtype dtype, int heads_k, int heads_v, int dk, int dv) {

@@ -2,34 +2,18 @@
 //
 // With S the state in front of a chunk (dk x dv), and the inverse X, the mixing matrix A, the
 // decays f (from the chunk's start) and e (to its end) that gdelta_prep.cu has made,
-//   R = diag(beta) (V - diag(f) K S),   U = X R,
+//   M = X (V - diag(f) K S),   U = diag(beta) M,
 //   O = scale diag(f) Q S + A U,        S' = f_last S + (diag(e) K)^T U.
 // Columns of S are independent of each other, so that a warp keeps 16 of them, transposed (16 x dk, the sums of
 // its products), in registers from the first chunk to the last, and nothing is exchanged between warps:
-// the layout of a product's result is that of the next one's first operand, so that S^T, R^T and U^T go
+// the layout of a product's result is that of the next one's first operand, so that S^T, M^T and U^T go
 // from one product into the next by way of their split into two BF16 terms. K, Q and V come through
 // shared memory for the block's warps. Bound by the rate of mma.sync and by the chain:
 // one block per (sequence, head) has 1 to 8 warps.
-#include "gdelta_tile.cuh"
-#include "grec_order.cuh"
+#include "gdelta_chain.cuh"
 
 namespace bsolve {
 namespace {
-
-constexpr int kMaxWarps = 8;
-
-// Tiles of one stage for a block of `warps` warps: q, k as terms, v as stored, the prepared chunk.
-template <typename T, int DK>
-struct Stage {
-  static constexpr int kStride = DK + 8;
-  static constexpr int kTerm = kChunk * kStride;                 // BF16 elements
-  static constexpr int kQk = Terms<T>::n * kTerm * 2;            // bytes of q or k
-  __host__ __device__ static constexpr int v_stride(int warps) { return warps * 16 + 16 / static_cast<int>(sizeof(T)); }
-  __host__ __device__ static constexpr int bytes(int warps) {
-    return 2 * kQk + kChunk * v_stride(warps) * static_cast<int>(sizeof(T)) +
-           static_cast<int>(sizeof(Prepared));
-  }
-};
 
 template <typename T>
 struct ChainOut {
@@ -41,34 +25,6 @@ struct ChainOut {
   const Prepared* prepared;
 };
 
-template <typename T, int DK, bool VEC>
-__device__ __forceinline__ void load_stage(unsigned char* stage, const GdeltaRows<T>& p,
-                                           const Prepared* prepared, int64_t row, int n, int kh, int h,
-                                           int col, int v_stride) {
-  using S = Stage<T, DK>;
-  auto* q = reinterpret_cast<__nv_bfloat16*>(stage);
-  auto* k = reinterpret_cast<__nv_bfloat16*>(stage + S::kQk);
-  T* v = reinterpret_cast<T*>(stage + 2 * S::kQk);
-  auto* own = reinterpret_cast<uint4*>(stage + 2 * S::kQk + kChunk * v_stride * sizeof(T));
-  load_terms<T, DK, S::kStride, VEC>(q, p.q + row * p.ldq + kh * p.dk, p.ldq, n, p.dk);
-  load_terms<T, DK, S::kStride, VEC>(k, p.k + row * p.ldk + kh * p.dk, p.ldk, n, p.dk);
-  const int width = min(p.dv - col, static_cast<int>(blockDim.x) / 2);
-  load_rows<T, VEC>(v, v_stride, blockDim.x / 2, p.v + row * p.ldv + h * p.dv + col, p.ldv, n, width);
-  for (int j = threadIdx.x; j < static_cast<int>(sizeof(Prepared) / 16); j += blockDim.x)
-    cp_async_16(own + j, reinterpret_cast<const uint4*>(prepared) + j, 16);
-  cp_async_commit();
-}
-
-// c += a b over one 16-deep piece: a in two terms, b in NB.
-template <int NB>
-__device__ __forceinline__ void mma_terms(float (&c)[4], const unsigned (&hi)[4],
-                                          const unsigned (&lo)[4], unsigned b0, unsigned b1,
-                                          unsigned l0, unsigned l1) {
-  mma(c, hi, b0, b1);
-  mma(c, lo, b0, b1);
-  if constexpr (NB == 2) mma(c, hi, l0, l1);
-}
-
 template <typename T, int DK, bool VEC, int STAGES>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 chain_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
@@ -77,40 +33,23 @@ chain_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ int64_t scratch[kSortedBatch + 1];
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int g = lane / 4, t2 = (lane & 3) * 2;
-  const int v_stride = St::v_stride(warps), stage_bytes = St::bytes(warps);
-
-  const int64_t part = static_cast<int64_t>(p.heads_v) * slices;
-  int64_t s = blockIdx.x / part;
-  const int rest = static_cast<int>(blockIdx.x % part), h = rest / slices, slice = rest % slices;
-  if (p.offsets && p.batch > 1 && p.batch <= min(kSortedBatch, static_cast<int>(blockDim.x)))
-    s = nth_longest(p.offsets, static_cast<int>(p.batch), static_cast<int>(s), scratch);
-  int64_t start, end;
-  sequence_rows(p, s, &start, &end);
-  const int kh = h / (p.heads_v / p.heads_k);
-  const int block_col = slice * warps * 16, col = block_col + warp * 16;
-  const int64_t place = start / kChunk + s, head = s * p.heads_v + h;
+  const int t2 = (lane & 3) * 2, v_stride = St::v_stride(warps), stage_bytes = St::bytes(warps);
+  const Place at = place_of(p, slices, scratch);
+  const int64_t start = at.start, end = at.end;
+  const int col = at.col + warp * 16;
   const bool mine = col < p.dv;  // this warp has columns
-
-  // S^T: rows g and g + 8 of the warp's columns, elements 8 n + t2, + 1 of dk
+  const int64_t state = at.head * p.dk * p.dv;
   float S[NB][4];
-#pragma unroll
-  for (int n = 0; n < NB; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int c = col + g + (e / 2) * 8, d = n * 8 + t2 + (e & 1);
-      S[n][e] = out.h0 && c < p.dv && d < p.dk
-                    ? out.h0[(head * p.dk + d) * p.dv + c] : 0.f;
-    }
+  load_state(S, out.h0 ? out.h0 + state : nullptr, p.dk, p.dv, col);
 
   const int64_t chunks = (end - start + kChunk - 1) / kChunk;
   auto rows_of = [&](int64_t c) {
     return static_cast<int>(min(end - start - c * kChunk, static_cast<int64_t>(kChunk)));
   };
   auto load = [&](int64_t c) {
-    load_stage<T, DK, VEC>(raw + (c % STAGES) * stage_bytes, p,
-                           out.prepared + (place + c) * p.heads_v + h, start + c * kChunk, rows_of(c),
-                           kh, h, block_col, v_stride);
+    load_stage<T, DK, VEC>(raw + (c % STAGES) * stage_bytes, p, p.v, p.ldv,
+                           out.prepared + (at.chunk + c) * p.heads_v + at.h, start + c * kChunk,
+                           rows_of(c), at.kh, at.h, at.col, v_stride);
   };
   if (STAGES == 2 && chunks > 0) load(0);
   for (int64_t c = 0; c < chunks; ++c) {
@@ -127,19 +66,13 @@ chain_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
     if (mine) {
       unsigned char* stage = raw + (c % STAGES) * stage_bytes;
       const unsigned q = smem_addr(stage), k = q + St::kQk;
-      T* v = reinterpret_cast<T*>(stage + 2 * St::kQk);
+      T* v = reinterpret_cast<T*>(stage + 2 * St::kQk) + warp * 16;
       const auto& own = *reinterpret_cast<const Prepared*>(stage + 2 * St::kQk +
                                                            kChunk * v_stride * sizeof(T));
-      if (out.tape) {
-        // the state as second operand of products over dv (rows of S): 8 x 8 blocks transposed
-        uint4* at = out.tape + (((place + c) * p.heads_v + h) * ((p.dv + 15) / 16) + col / 16) *
-                                   (NB * 32) + lane;
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          const Split a = split(S[n][0], S[n][1]), b = split(S[n][2], S[n][3]);
-          at[n * 32] = make_uint4(transposed(a.hi), transposed(b.hi), transposed(a.lo), transposed(b.lo));
-        }
-      }
+      uint4* kept = out.tape ? out.tape + (((at.chunk + c) * p.heads_v + at.h) * gdelta_groups(p.dv) +
+                                           col / 16) * (kept_pieces(DK) * 32)
+                             : nullptr;
+      if (kept) keep_pieces(kept, S);
       // (K S)^T and (Q S)^T
       float R[8][4], O[8][4];
 #pragma unroll
@@ -163,41 +96,23 @@ chain_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
           mma_terms<NT>(O[2 * n + 1], hi, lo, b[2], b[3], l[2], l[3]);
         }
       }
-      // R^T = (V^T - (K S)^T f) beta, O^T = scale f (Q S)^T
+      // R^T = V^T - (K S)^T f, O^T = scale f (Q S)^T
 #pragma unroll
       for (int n = 0; n < 8; n += 2) {
         float x[2][4];
-        if constexpr (sizeof(T) == 2) {
-          unsigned w[4];
-          const int l7 = lane & 7;
-          ldmatrix4_trans(w, smem_addr(v + (n * 8 + l7 + ((lane & 16) >> 1)) * v_stride + warp * 16 +
-                                       (lane & 8)));
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = to_f32(*reinterpret_cast<const typename Pair<T>::type*>(&w[j]));
-            x[j / 2][(j & 1) * 2] = f.x;
-            x[j / 2][(j & 1) * 2 + 1] = f.y;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[j][e] = to_f32(v[((n + j) * 8 + t2 + (e & 1)) * v_stride + warp * 16 + g + (e / 2) * 8]);
-        }
+        read_transposed(x, v, v_stride, n);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float2 f = *reinterpret_cast<const float2*>(&own.front[(n + j) * 8 + t2]);
-          const float2 b = *reinterpret_cast<const float2*>(&own.beta[(n + j) * 8 + t2]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float fe = e & 1 ? f.y : f.x, be = e & 1 ? b.y : b.x;
-            R[n + j][e] = __fmul_rn(be, __fmaf_rn(-fe, R[n + j][e], x[j][e]));
+            const float fe = e & 1 ? f.y : f.x;
+            R[n + j][e] = __fmaf_rn(-fe, R[n + j][e], x[j][e]);
             O[n + j][e] = __fmul_rn(O[n + j][e], __fmul_rn(p.scale, fe));
           }
         }
       }
-      // U^T = R^T X^T
+      // M^T = R^T X^T, U^T = M^T beta
       float U[8][4];
 #pragma unroll
       for (int n = 0; n < 8; ++n)
@@ -209,9 +124,16 @@ chain_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
         split_operand(hi, lo, R[2 * kb], R[2 * kb + 1]);
 #pragma unroll
         for (int n = 2 * kb; n < 8; ++n) {
-          const uint4 b = own.inverse[lower_piece(n, kb)][lane];
+          const uint4 b = own.inverse[lower_piece(n / 2, n & 1, kb)][lane];
           mma_terms<2>(U[n], hi, lo, b.x, b.y, b.z, b.w);
         }
+      }
+      if (kept) keep_pieces(kept + NB * 32, U);
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const float2 b = *reinterpret_cast<const float2*>(&own.beta[n * 8 + t2]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) U[n][e] = __fmul_rn(U[n][e], e & 1 ? b.y : b.x);
       }
       // O^T += U^T A^T; then S^T = f_last S^T + (U^T e) K
       const float whole = own.front[kChunk - 1];
@@ -225,7 +147,7 @@ chain_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
         split_operand(hi, lo, U[2 * kb], U[2 * kb + 1]);
 #pragma unroll
         for (int n = 2 * kb; n < 8; ++n) {
-          const uint4 b = own.mixing[lower_piece(n, kb)][lane];
+          const uint4 b = own.mixing[lower_piece(n / 2, n & 1, kb)][lane];
           mma_terms<2>(O[n], hi, lo, b.x, b.y, b.z, b.w);
         }
 #pragma unroll
@@ -245,69 +167,18 @@ chain_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
           mma_terms<NT>(S[n + 1], hi, lo, b[2], b[3], l[2], l[3]);
         }
       }
-      // O through the warp's columns of v's tile, which no other warp reads
-      __syncwarp();
-      if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int n = 0; n < 8; n += 2) {
-          unsigned w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const auto pair = pair_from_f32<T>(make_float2(O[n + j / 2][(j & 1) * 2],
-                                                           O[n + j / 2][(j & 1) * 2 + 1]));
-            w[j] = *reinterpret_cast<const unsigned*>(&pair);
-          }
-          stmatrix4_trans(smem_addr(v + (n * 8 + (lane & 7) + ((lane & 16) >> 1)) * v_stride + warp * 16 +
-                                    (lane & 8)), w[0], w[1], w[2], w[3]);
-        }
-      } else {
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[(n * 8 + t2 + (e & 1)) * v_stride + warp * 16 + g + (e / 2) * 8] = from_f32<T>(O[n][e]);
-      }
-      __syncwarp();
-      T* to = out.o + row * out.ldo + h * p.dv + col;
-      const T* from = v + warp * 16;
-      if constexpr (VEC) {
-        constexpr int kV = 16 / sizeof(T), kVecs = 16 / kV;
-        for (int j = lane; j < n_rows * kVecs; j += 32) {
-          const int r = j / kVecs, x = (j % kVecs) * kV;
-          if (col + x < p.dv)
-            *reinterpret_cast<uint4*>(to + r * out.ldo + x) =
-                *reinterpret_cast<const uint4*>(from + r * v_stride + x);
-        }
-      } else {
-        for (int j = lane; j < n_rows * 16; j += 32) {
-          const int r = j / 16, x = j % 16;
-          if (col + x < p.dv) to[r * out.ldo + x] = from[r * v_stride + x];
-        }
-      }
+      store_transposed<T, VEC>(O, v, v_stride, out.o + row * out.ldo + at.h * p.dv + col, out.ldo, n_rows,
+                               p.dv - col);
     }
     __syncthreads();  // the stage is free
   }
-  if (out.hT) {
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = col + g + (e / 2) * 8, d = n * 8 + t2 + (e & 1);
-        if (c < p.dv && d < p.dk) out.hT[(head * p.dk + d) * p.dv + c] = S[n][e];
-      }
-  }
+  if (out.hT) store_state(S, out.hT + state, p.dk, p.dv, col);
 }
 
 template <typename T, int DK, bool VEC>
 cudaError_t chain(const GdeltaRows<T>& p, const ChainOut<T>& out, cudaStream_t stream) {
   constexpr int STAGES = Terms<T>::n == 1 ? 2 : 1;
-  // As many warps a block as dv has groups of 16 columns, fewer where that leaves SMs without a block.
-  const int groups = (p.dv + 15) / 16;
-  int warps = 1;
-  while (warps < kMaxWarps && warps < groups &&
-         p.batch * p.heads_v * ((groups + 2 * warps - 1) / (2 * warps)) >= kSms)
-    warps *= 2;
-  const int slices = (groups + warps - 1) / warps;
+  const int warps = chain_warps(p), slices = (gdelta_groups(p.dv) + warps - 1) / warps;
   const int shared = STAGES * Stage<T, DK>::bytes(warps);
   auto* kernel = chain_kernel<T, DK, VEC, STAGES>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
@@ -343,7 +214,7 @@ size_t gdelta_workspace(int heads_v, int64_t batch, int64_t rows) {
 }
 
 size_t gdelta_tape(int heads_v, int dk, int dv, int64_t batch, int64_t rows) {
-  return gdelta_places(batch, rows) * heads_v * ((dv + 15) / 16) * ((dk <= 64 ? 64 : 128) / 8) * 512;
+  return kept_bytes(heads_v, dk, dv, batch, rows);
 }
 
 }  // namespace bsolve

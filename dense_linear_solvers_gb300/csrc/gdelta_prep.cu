@@ -2,7 +2,8 @@
 // of 64 rows and key head, all chunks at once.
 //
 // With b the running sum of the chunk's log decays, D_ri = e^(b_r - b_i) for i <= r and 0 above,
-//   L = diag(beta) strict(K K^T o D),    inverse = (I + L)^-1,    mixing = scale (Q K^T o D).
+//   N = strict(K K^T o D),    mixing = scale (Q K^T o D),
+//   inverse = (I + N diag(beta))^-1 for the forward pass, (I + diag(beta) N)^-1 for the backward one.
 // The inverse of the unit lower triangular 64 x 64 system: four diagonal blocks of 16 by
 // substitution, a column a lane; then two pairs of them, and the pair of these, by
 // [X1 0; -X2 L21 X1, X2], in FP32. K K^T and Q K^T are taken once for all value heads of the
@@ -75,21 +76,22 @@ prepare_kernel(GdeltaRows<T> p, int per, Prepared* out) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
   {
-    const auto& first = mixes && !BACKWARD ? sh.q : sh.k;
-    const auto& second = mixes && BACKWARD ? sh.q : sh.k;
+    constexpr unsigned kTerm = kChunk * STRIDE * 2;
+    const unsigned q_at = smem_addr(&sh.q[0][0][0]), k_at = smem_addr(&sh.k[0][0][0]);
+    const unsigned first = mixes && !BACKWARD ? q_at : k_at, second = mixes && BACKWARD ? q_at : k_at;
     const bool upper = mixes && BACKWARD;
     for (int k = 0; k < DK; k += 16) {
       unsigned a[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        ldmatrix4(a[n], across(smem_addr(&first[n][0][0]), STRIDE, mb * 16, k));
+        ldmatrix4(a[n], across(first + n * kTerm, STRIDE, mb * 16, k));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (upper ? j < mb : j > mb) continue;
         unsigned b[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          ldmatrix4(b[n], along<STRIDE>(smem_addr(&second[n][0][0]), j * 16, k));
+          ldmatrix4(b[n], along<STRIDE>(second + n * kTerm, j * 16, k));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           mma(acc[2 * j + h], a[0], b[0][2 * h], b[0][2 * h + 1]);
@@ -128,21 +130,19 @@ prepare_kernel(GdeltaRows<T> p, int per, Prepared* out) {
       for (int e = 0; e < 2; ++e) {
         const int r = 2 * lane + e;
         const double b = before + s[e];
-        sh.sum_hi[r] = static_cast<float>(b);
-        sh.sum_lo[r] = static_cast<float>(b - static_cast<double>(sh.sum_hi[r]));
+        o.sum_hi[r] = sh.sum_hi[r] = static_cast<float>(b);
+        o.sum_lo[r] = sh.sum_lo[r] = static_cast<float>(b - static_cast<double>(sh.sum_hi[r]));
         sh.beta[r] = beta[e];
         o.front[r] = expf(static_cast<float>(b));
         o.back[r] = expf(static_cast<float>(last - b));
         o.beta[r] = beta[e];
       }
     } else {
-      for (int j = threadIdx.x - 32; j < kChunk * kLs; j += kThreads - 32) (&sh.x[0][0])[j] = 0.f;
+      for (int j = threadIdx.x - 32; j < kChunk * kLs; j += kThreads - 32) sh.x[j / kLs][j % kLs] = 0.f;
     }
     __syncthreads();
     // the decayed products: L into shared memory, the mixing matrix into its place
-    auto decay = [&](int r, int i) {
-      return expf(__fadd_rn(__fsub_rn(sh.sum_hi[r], sh.sum_hi[i]), __fsub_rn(sh.sum_lo[r], sh.sum_lo[i])));
-    };
+    auto decay = [&](int r, int i) { return decay_between(sh.sum_hi, sh.sum_lo, r, i); };
     if (!mixes) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -150,7 +150,8 @@ prepare_kernel(GdeltaRows<T> p, int per, Prepared* out) {
         for (int e = 0; e < 4; ++e) {
           const int r = mb * 16 + g + (e / 2) * 8, i = j * 8 + t2 + (e & 1);
           if (j / 2 <= mb)
-            sh.low[r][i] = i < r ? __fmul_rn(sh.beta[r], __fmul_rn(acc[j][e], decay(r, i))) : 0.f;
+            sh.low[r][i] = i < r ? __fmul_rn(sh.beta[BACKWARD ? r : i],
+                                             __fmul_rn(acc[j][e], decay(r, i))) : 0.f;
         }
     } else {
 #pragma unroll
@@ -169,8 +170,7 @@ prepare_kernel(GdeltaRows<T> p, int per, Prepared* out) {
         for (int half = 0; half < 2; ++half) {
           const Split a = split(v[0][2 * half], v[0][2 * half + 1]),
                       b = split(v[1][2 * half], v[1][2 * half + 1]);
-          const int n = 2 * mb + half;
-          o.mixing[BACKWARD ? upper_piece(n, k) : lower_piece(n, k)][lane] =
+          o.mixing[BACKWARD ? upper_piece(mb, half, k) : lower_piece(mb, half, k)][lane] =
               make_uint4(a.hi, b.hi, a.lo, b.lo);
         }
       }
@@ -206,18 +206,21 @@ prepare_kernel(GdeltaRows<T> p, int per, Prepared* out) {
             row_times(&sh.x[base + size + r][base + size], &sh.m[pair * 16][c], kMs, size, -1.f);
       __syncthreads();
     }
-    for (int piece = warp; piece < kPieces; piece += kThreads / 32) {
-      int n = 0, k = piece;
-      if (BACKWARD) {
-        while (k >= 4 - n / 2) k -= 4 - n / 2, ++n;
-        k += n / 2;
-      } else {
-        while (k > n / 2) k -= n / 2 + 1, ++n;
+    // a warp has the pieces of one group of columns
+    const int pair = warp / 2, half = warp & 1, col = warp * 8 + g;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (BACKWARD ? k < pair : k > pair) continue;
+      const int d = k * 16 + t2;
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int depth = d + (e & 1) + (e / 2) * 8;
+        v[e] = BACKWARD ? sh.x[depth][col] : sh.x[col][depth];
       }
-      const int col = n * 8 + g, d = k * 16 + t2;
-      auto at = [&](int depth) { return BACKWARD ? sh.x[depth][col] : sh.x[col][depth]; };
-      const Split a = split(at(d), at(d + 1)), b = split(at(d + 8), at(d + 9));
-      o.inverse[piece][lane] = make_uint4(a.hi, b.hi, a.lo, b.lo);
+      const Split a = split(v[0], v[1]), b = split(v[2], v[3]);
+      o.inverse[BACKWARD ? upper_piece(pair, half, k) : lower_piece(pair, half, k)][lane] =
+          make_uint4(a.hi, b.hi, a.lo, b.lo);
     }
   }
 }

@@ -217,22 +217,36 @@ __device__ __forceinline__ unsigned across(unsigned tile, int stride, int k, int
 // ---------------------------------------------------------------------------- prepared chunks
 // What a chunk's chain needs of each value head, made from q, k, g, beta alone: the inverse and the mixing matrix, lower triangular, as second operands in
 // registers' order (20 pieces of 8 columns and 16 deep, hi and lo, 16 bytes a lane), and by row
-// the decay from the chunk's start, beta, and the decay to its end.
+// the decay from the chunk's start, beta, the decay to its end, and the log decays' sum.
 constexpr int kPieces = 20;
 struct Prepared {
   uint4 inverse[kPieces][32];
   uint4 mixing[kPieces][32];
   float front[kChunk], beta[kChunk], back[kChunk];
+  float sum_hi[kChunk], sum_lo[kChunk];  // the running sum of the log decays
 };
 static_assert(sizeof(Prepared) % 16 == 0, "copied in pieces of 16 bytes");
-// Piece (n, k) of a lower triangle, columns n * 8 .. + 7 (rows of the matrix), depth k * 16 .. + 15.
-__host__ __device__ constexpr int lower_piece(int n, int k) {
-  // in front of column group n: 1 + 1 + 2 + 2 + ...
-  return (n / 2) * (n / 2 + 1) + (n & 1) * (n / 2 + 1) + k;
+// Where a piece of the lower triangle is: columns (2 pair + half) * 8 .. + 7, which are rows of the matrix, depth
+// k * 16 .. + 15, k <= pair; and of the upper one, k >= pair, for the transposed products.
+__host__ __device__ constexpr int lower_piece(int pair, int half, int k) {
+  return pair * (pair + 1) + half * (pair + 1) + k;
 }
-// Of an upper one (depth k >= n / 2), for the transposed products.
-__host__ __device__ constexpr int upper_piece(int n, int k) {
-  return n * 4 - ((n / 2) * (n / 2 - 1) + (n & 1) * (n / 2)) + k - n / 2;
+__host__ __device__ constexpr int upper_piece(int pair, int half, int k) {
+  return pair * (9 - pair) + half * (4 - pair) + k - pair;
+}
+
+// e^(b_r - b_i) from the sums' two parts.
+__device__ __forceinline__ float decay_between(const float* hi, const float* lo, int r, int i) {
+  return expf(__fadd_rn(__fsub_rn(hi[r], hi[i]), __fsub_rn(lo[r], lo[i])));
+}
+
+// What the chains leave for the gradients of a chunk, by value head and 16 columns of dv: a state (or its gradient) and 64
+// rows, both as second operands of products over dv, in pieces of 8 columns and 16 deep as above.
+__host__ __device__ constexpr int gdelta_groups(int dv) { return (dv + 15) / 16; }
+constexpr int gdelta_deep(int dk) { return dk <= 64 ? 64 : 128; }   // dk as the kernels pad it
+__host__ __device__ constexpr int64_t kept_pieces(int deep) { return deep / 8 + kChunk / 8; }
+inline size_t kept_bytes(int heads_v, int dk, int dv, int64_t batch, int64_t rows) {
+  return gdelta_places(batch, rows) * heads_v * gdelta_groups(dv) * kept_pieces(gdelta_deep(dk)) * 512;
 }
 
 template <typename T>

@@ -479,6 +479,28 @@ PyObject* gdelta(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+PyObject* gdelta_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("gdelta_backward", n, 18, [&] {
+    const Heads s(a[0], a[2], a[15], false);
+    const Row q = s.keys(a[0], "q"), k = s.keys(a[1], "k"), v = s.values(a[2], "v"),
+              g = s.gates(a[3], "g"), beta = s.gates(a[4], "beta"), o = s.values(a[6], "do"),
+              dq = s.keys(a[7], "dq"), dk = s.keys(a[8], "dk"), dv = s.values(a[9], "dv"),
+              dg = s.gates(a[10], "dg"), dbeta = s.gates(a[11], "dbeta");
+    size_t bytes = 0;
+    void* work = bytes_of(
+        a[12], "work", s.q, bs_gdelta_backward_workspace(s.heads_v, s.dk, s.dv, s.batch, s.rows), &bytes);
+    return enter(
+        s.q, bs_gdelta_backward_batched, s.q.code, static_cast<int>(s.heads_k),
+        static_cast<int>(s.heads_v), static_cast<int>(s.dk), static_cast<int>(s.dv), s.batch, s.rows,
+        s.offsets, q.p, q.ld, k.p, k.ld, v.p, v.ld, static_cast<float*>(g.p), g.ld,
+        static_cast<float*>(beta.p), beta.ld, s.scale(a[16]),
+        bytes_of(a[5], "tape", s.q, bs_gdelta_tape(s.heads_v, s.dk, s.dv, s.batch, s.rows)), o.p, o.ld,
+        f32(a[13], "dhT", s.q, s.states()), dq.p, dq.ld, dk.p, dk.ld, dv.p, dv.ld,
+        static_cast<float*>(dg.p), dg.ld, static_cast<float*>(dbeta.p), dbeta.ld,
+        f32(a[14], "dh0", s.q, s.states()), work, bytes, handle(a[17]));
+  });
+}
+
 PyObject* gdelta_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("gdelta_step", n, 10, [&] {
     const Heads s(a[0], a[2], Py_None, true);
@@ -535,6 +557,13 @@ PyObject* gdelta_tape(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+PyObject* gdelta_backward_workspace(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return query(n, 5, [&] {
+    return bs_gdelta_backward_workspace(small(a[0]), small(a[1]), small(a[2]), integer(a[3]),
+                                        integer(a[4]));
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL,
@@ -549,6 +578,8 @@ PyMethodDef methods[] = {method<grec>("grec"), method<grec_backward>("grec_backw
                          method<gnorm_backward_workspace>("gnorm_backward_workspace"),
                          method<gnorm_q8>("gnorm_q8"), method<gemm_q8>("gemm_q8"),
                          method<gdelta>("gdelta"), method<gdelta_step>("gdelta_step"),
+                         method<gdelta_backward>("gdelta_backward"),
+                         method<gdelta_backward_workspace>("gdelta_backward_workspace"),
                          method<gdelta_workspace>("gdelta_workspace"),
                          method<gdelta_tape>("gdelta_tape"),
                          {nullptr, nullptr, 0, nullptr}};

@@ -553,6 +553,13 @@ BS_API bs_status bs_gemm_q8(bs_dtype dtype, int64_t m, int64_t n, int64_t k, con
  *   tape  device buffer of bs_gdelta_tape(...) bytes, or NULL: what bs_gdelta_backward_batched needs
  *         of the states.
  *   work  device workspace of bs_gdelta_workspace(...) bytes. Holds nothing between calls.
+ * bs_gdelta_backward_batched: q, k, v, g, beta, scale, offsets and tape as in the forward call (v is not
+ *   read, but has to be there);
+ *   d_o   the gradient of o;  dhT  the gradient of hT, or NULL for zeros.
+ *   dq, d_k, d_v   the gradients of q, k, v (those of a key head summed over its value heads in
+ *         order);  dg, dbeta   rows of heads_v FP32 numbers.
+ *   dh0   the gradient of h0, or NULL; may be dhT itself.
+ *   work  device workspace of bs_gdelta_backward_workspace(...) bytes. Holds nothing between calls.
  * bs_gdelta_step_batched: one row for each of `batch` sequences:
  *   state  num_slots x heads_v x dk x dv, in and out.
  *   slots  batch int32: the entry of `state` that row j advances; NULL: entry j (num_slots at least
@@ -570,6 +577,13 @@ BS_API bs_status bs_gdelta_batched(bs_dtype dtype, int heads_k, int heads_v, int
                                    const float* beta, int64_t ldbeta, double scale,
                                    const float* h0, void* o, int64_t ldo, float* hT, void* tape,
                                    void* work, size_t work_bytes, void* stream);
+BS_API bs_status bs_gdelta_backward_batched(
+    bs_dtype dtype, int heads_k, int heads_v, int dk, int dv, int64_t batch, int64_t rows,
+    const int64_t* offsets, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+    int64_t ldv, const float* g, int64_t ldg, const float* beta, int64_t ldbeta, double scale,
+    const void* tape, const void* d_o, int64_t lddo, const float* dhT, void* dq, int64_t lddq,
+    void* d_k, int64_t lddk, void* d_v, int64_t lddv, float* dg, int64_t lddg, float* dbeta,
+    int64_t lddbeta, float* dh0, void* work, size_t work_bytes, void* stream);
 BS_API bs_status bs_gdelta_step_batched(bs_dtype dtype, int heads_k, int heads_v, int dk, int dv,
                                         int64_t batch, const void* q, int64_t ldq, const void* k,
                                         int64_t ldk, const void* v, int64_t ldv, const float* g,
@@ -578,6 +592,8 @@ BS_API bs_status bs_gdelta_step_batched(bs_dtype dtype, int heads_k, int heads_v
                                         const int32_t* slots, void* o, int64_t ldo, void* stream);
 BS_API size_t bs_gdelta_workspace(int heads_v, int64_t batch, int64_t rows);
 BS_API size_t bs_gdelta_tape(int heads_v, int dk, int dv, int64_t batch, int64_t rows);
+BS_API size_t bs_gdelta_backward_workspace(int heads_v, int dk, int dv, int64_t batch,
+                                           int64_t rows);
 
 /* 1 if the calls with this type and row length have a kernel instance, else 0 (no launch). */
 BS_API int bs_grec_supported(bs_dtype dtype, int channels);

@@ -39,6 +39,30 @@ def forward(q, k, v, g, beta, batch, offsets=None, **more):
     return o
 
 
+def backward(x, tape, do, batch, offsets=None, dhT=None, dh0=None, into=None, **more):
+    """dq, dk, dv, dg, dbeta; into: given outputs."""
+    q, v = x[0], x[2]
+    out = into or [torch.full(t.shape, 7.0, device="cuda").to(t.dtype) for t in x]
+    work = torch.empty(bs.bs_gdelta_backward_workspace(v.shape[1], q.shape[2], v.shape[2], batch,
+                                                       q.shape[0]), dtype=torch.uint8, device="cuda")
+    as_given = (lambda t: t) if offsets is not None else (lambda t: t.unflatten(0, (batch, -1)))  # noqa: E731
+    bs.bs_gdelta_backward_batched(*(as_given(t) for t in x), tape, as_given(do),
+                                  *(as_given(t) for t in out), work, dhT=dhT, dh0=dh0, offsets=offsets,
+                                  **more)
+    return dict(zip(("dq", "dk", "dv", "dg", "dbeta"), out))
+
+
+def tape_of(x, batch):
+    return torch.empty(bs.bs_gdelta_tape(x[2].shape[1], x[0].shape[2], x[2].shape[2], batch,
+                                         x[0].shape[0]), dtype=torch.uint8, device="cuda")
+
+
+def check_gradients(ref, got, kind):
+    for name, t in got.items():
+        ok, worst = ref.close(name, t, kind if name in ("dq", "dk", "dv") else torch.float32)
+        assert ok, (name, worst)
+
+
 def reference(q, k, v, g, beta, spans, **more):
     return Delta(*(t.double() for t in (q, k, v, g, beta)), spans, **more)
 
@@ -184,3 +208,86 @@ def test_steps_continue_a_sequence():
         got[:, t] = y
     assert ref.close("o", got.flatten(0, 1), torch.float32)[0]
     assert ref.close("hT", state, torch.float32)[0]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("batch, length, hk, hv, dk, dv, pad", [
+    (1, 1, 1, 1, 64, 64, 0), (2, 64, 1, 2, 64, 64, 16), (1, 65, 1, 1, 128, 128, 0),
+    (2, 130, 2, 4, 93, 77, 0), (1, 200, 1, 3, 128, 24, 3), (2, 70, 1, 1, 1, 1, 0),
+    (1, 100, 1, 2, 40, 300, 0), (3, 191, 2, 2, 64, 48, 8)])
+def test_gradients(kind, batch, length, hk, hv, dk, dv, pad):
+    x = inputs(kind, batch * length, hk, hv, dk, dv, seed=8, pad=pad)
+    do = torch.randn(batch * length, hv, dv, device="cuda").to(KINDS[kind])
+    h0, dhT = (torch.randn(batch, hv, dk, dv, device="cuda") for _ in range(2))
+    tape, dh0 = tape_of(x, batch), torch.empty_like(h0)
+    o = forward(*x, batch, h0=h0, tape=tape)
+    assert torch.equal(o, forward(*x, batch, h0=h0))
+    got = backward(x, tape, do, batch, dhT=dhT, dh0=dh0)
+    spans = [(b * length, (b + 1) * length) for b in range(batch)]
+    ref = reference(*x, spans, h0=h0.double()).backward(do.double(), dhT.double())
+    check_gradients(ref, dict(got, dh0=dh0), KINDS[kind])
+    # the same bits again; the final states' gradient overwritten in place; none given
+    state = dhT.clone()
+    again = backward(x, tape, do, batch, dhT=state, dh0=state)
+    assert all(torch.equal(again[n], got[n]) for n in got) and torch.equal(state, dh0)
+    none = backward(x, tape, do, batch)
+    check_gradients(reference(*x, spans, h0=h0.double()).backward(do.double()), none, KINDS[kind])
+
+
+@pytest.mark.parametrize("kind, hk, hv, dk, dv", [("bf16", 2, 4, 128, 128), ("f16", 1, 3, 64, 72),
+                                                  ("f32", 1, 2, 51, 33)])
+def test_packed_gradients(kind, hk, hv, dk, dv):
+    """Into column windows of one matrix; rows of no sequence keep what was there."""
+    cuts = [5, 5, 6, 70, 134, 134, 400, 463]
+    x = inputs(kind, 470, hk, hv, dk, dv, seed=9)
+    for t in x:
+        t[:5], t[463:] = float("nan"), float("nan")
+    batch, offsets = len(cuts) - 1, torch.tensor(cuts, device="cuda")
+    do = torch.randn(470, hv, dv, device="cuda").to(KINDS[kind])
+    do[:5], do[463:] = float("nan"), float("nan")
+    tape = tape_of(x, batch)
+    forward(*x, batch, offsets, tape=tape)
+    wide = torch.full((470, 2 * hk * dk + hv * dv), 7.0, device="cuda").to(KINDS[kind])
+    parts = [p.unflatten(1, t.shape[1:]) for p, t in zip(wide.split([hk * dk, hk * dk, hv * dv], 1), x)]
+    parts += [torch.full((470, hv), 7.0, device="cuda") for _ in range(2)]
+    dhT, dh0 = torch.randn(batch, hv, dk, dv, device="cuda"), torch.empty(batch, hv, dk, dv, device="cuda")
+    got = backward(x, tape, do, batch, offsets, dhT=dhT, dh0=dh0, into=parts)
+    ref = reference(*x, list(zip(cuts[:-1], cuts[1:]))).backward(do.double(), dhT.double())
+    for t in parts:
+        assert bool((t[:5] == 7).all()) and bool((t[463:] == 7).all())
+        t[:5], t[463:] = 0, 0
+    check_gradients(ref, dict(got, dh0=dh0), KINDS[kind])
+    assert torch.equal(dh0[0], dhT[0]) and torch.equal(dh0[4], dhT[4])
+
+
+def test_gradients_of_strong_decays_and_idle_rows():
+    """Resets, rows that write nothing (beta = 0: dbeta is what they would have written) and rates of 2."""
+    x = inputs("f32", 200, 1, 2, 64, 32, seed=10)
+    x[3][50, 0], x[3][90, 1], x[3][::9] = float("-inf"), -500.0, -3.0
+    x[4][30:40], x[4][120:125] = 0.0, 2.0
+    do = torch.randn(200, 2, 32, device="cuda")
+    tape = tape_of(x, 1)
+    forward(*x, 1, tape=tape)
+    got = backward(x, tape, do, 1)
+    check_gradients(reference(*x, [(0, 200)]).backward(do.double()), got, torch.float32)
+
+
+def test_gradients_against_differences():
+    """Central differences of the 64-bit forward pass, to which the 64-bit gradients are held too."""
+    x = inputs("f32", 67, 1, 2, 8, 5, seed=11)
+    do = torch.randn(67, 2, 5, device="cuda")
+    tape = tape_of(x, 1)
+    forward(*x, 1, tape=tape)
+    got = backward(x, tape, do, 1)
+    gen = torch.Generator("cuda").manual_seed(1)
+    wide = [t.double() for t in x]
+    for n, name in enumerate(("dq", "dk", "dv", "dg", "dbeta")):
+        way = torch.randn(x[n].shape, generator=gen, device="cuda", dtype=torch.float64)
+        step, ends = 1e-5, []
+        for sign in (1, -1):
+            moved = [t + sign * step * way if m == n else t for m, t in enumerate(wide)]
+            ends.append((Delta(*moved, [(0, 67)]).o * do.double()).sum())
+        slope = (ends[0] - ends[1]) / (2 * step)
+        ref = (got[name].double() * way).sum()
+        # the quotient is good to step^2; the gradients to 2^-18 of their terms
+        assert abs(float(ref - slope)) <= 1e-4 * float((got[name].double().abs() * way.abs()).sum())
