@@ -2,6 +2,9 @@
 // columns of them, its state in registers.
 #pragma once
 
+#include <type_traits>
+
+#include "barrier.cuh"
 #include "gdelta_tile.cuh"
 #include "grec_order.cuh"
 
@@ -9,6 +12,7 @@ namespace bsolve {
 namespace {
 
 constexpr int kMaxWarps = 8;
+constexpr int kMaxShared = 230000;  // bytes of dynamic shared memory, beside what the kernels declare
 
 // Tiles of one stage for a block of `warps` warps: q, k as terms, v (or a gradient of its shape) as stored, the prepared chunk.
 template <typename T, int DK>
@@ -26,19 +30,66 @@ struct Stage {
 template <typename T, int DK, bool VEC>
 __device__ __forceinline__ void load_stage(unsigned char* stage, const GdeltaRows<T>& p,
                                            const T* v_rows, int64_t ldv, const Prepared* prepared,
-                                           int64_t row, int n, int kh, int h, int col, int v_stride) {
+                                           int64_t row, int n, int kh, int h, int col, int cols,
+                                           int v_stride, int thread, int threads) {
   using S = Stage<T, DK>;
   auto* q = reinterpret_cast<__nv_bfloat16*>(stage);
   auto* k = reinterpret_cast<__nv_bfloat16*>(stage + S::kQk);
   T* v = reinterpret_cast<T*>(stage + 2 * S::kQk);
   auto* own = reinterpret_cast<uint4*>(stage + 2 * S::kQk + kChunk * v_stride * sizeof(T));
-  load_terms<T, DK, S::kStride, VEC>(q, p.q + row * p.ldq + kh * p.dk, p.ldq, n, p.dk);
-  load_terms<T, DK, S::kStride, VEC>(k, p.k + row * p.ldk + kh * p.dk, p.ldk, n, p.dk);
-  const int width = min(p.dv - col, static_cast<int>(blockDim.x) / 2);
-  load_rows<T, VEC>(v, v_stride, blockDim.x / 2, v_rows + row * ldv + h * p.dv + col, ldv, n, width);
-  for (int j = threadIdx.x; j < static_cast<int>(sizeof(Prepared) / 16); j += blockDim.x)
+  load_terms<T, DK, S::kStride, VEC>(q, p.q + row * p.ldq + kh * p.dk, p.ldq, n, p.dk, thread,
+                                         threads);
+  load_terms<T, DK, S::kStride, VEC>(k, p.k + row * p.ldk + kh * p.dk, p.ldk, n, p.dk, thread,
+                                         threads);
+  const int width = min(p.dv - col, cols);
+  load_rows<T, VEC>(v, v_stride, cols, v_rows + row * ldv + h * p.dv + col, ldv, n, width, thread, threads);
+  for (int j = thread; j < static_cast<int>(sizeof(Prepared) / 16); j += threads)
     cp_async_16(own + j, reinterpret_cast<const uint4*>(prepared) + j, 16);
-  cp_async_commit();
+}
+
+// Whether a stage comes by bulk copies (rows that need no other form): a row an instruction instead of 16
+// bytes, which is what a block of few warps otherwise spends a third of its time on.
+template <typename T, bool VEC>
+constexpr bool kBulk = VEC && Terms<T>::n == 1;
+
+// Zeros in a block's stages, once, where copies leave columns behind dk or rows behind a sequence.
+__device__ __forceinline__ void clear_stages(unsigned char* stages, int bytes) {
+  for (int j = threadIdx.x * 16; j < bytes; j += blockDim.x * 16)
+    *reinterpret_cast<uint4*>(stages + j) = make_uint4(0, 0, 0, 0);
+  writes_before_copies();
+}
+
+template <typename T, int DK>
+__device__ __forceinline__ void copy_stage(unsigned char* stage, uint64_t* barrier, const GdeltaRows<T>& p,
+                                           const T* v_rows, int64_t ldv, const Prepared* prepared,
+                                           int64_t row, int n, int kh, int h, int col, int cols,
+                                           int v_stride) {
+  using S = Stage<T, DK>;
+  auto* q = reinterpret_cast<T*>(stage);
+  auto* k = reinterpret_cast<T*>(stage + S::kQk);
+  T* v = reinterpret_cast<T*>(stage + 2 * S::kQk);
+  const int width = min(p.dv - col, cols), dk_bytes = p.dk * static_cast<int>(sizeof(T)),
+            v_bytes = width * static_cast<int>(sizeof(T));
+  if (threadIdx.x == 0)
+    barrier_expect(barrier, n * (2 * dk_bytes + v_bytes) + static_cast<int>(sizeof(Prepared)));
+  for (int j = threadIdx.x; j < 3 * kChunk + 1; j += blockDim.x) {
+    const int r = j % kChunk, which = j / kChunk;
+    if (which == 3) {
+      copy_bytes(stage + 2 * S::kQk + kChunk * v_stride * sizeof(T), prepared, sizeof(Prepared), barrier);
+      continue;
+    }
+    T* to = which == 0 ? q + r * S::kStride : which == 1 ? k + r * S::kStride : v + r * v_stride;
+    const int bytes = which == 2 ? v_bytes : dk_bytes;
+    if (r < n) {
+      const T* from = which == 0 ? p.q + (row + r) * p.ldq + kh * p.dk
+                      : which == 1 ? p.k + (row + r) * p.ldk + kh * p.dk
+                                   : v_rows + (row + r) * ldv + h * p.dv + col;
+      copy_bytes(to, from, bytes, barrier);
+    } else {
+      for (int b = 0; b < bytes; b += 16)
+        *reinterpret_cast<uint4*>(reinterpret_cast<char*>(to) + b) = make_uint4(0, 0, 0, 0);
+    }
+  }
 }
 
 // The warp's 16 columns (from `v`) of rows 8 n .. 8 n + 15 of a tile, transposed: as two neighbouring 16 x 8
@@ -117,30 +168,61 @@ __device__ __forceinline__ void keep_pieces(uint4* at, const float (&x)[N][4]) {
     at[n * 32 + lane] = make_uint4(transposed(a.hi), transposed(b.hi), transposed(a.lo), transposed(b.lo));
   }
 }
+// The 64 rows as first operands over the warp's 16 columns, [16 rows][hi, lo]; all of them, or one group of eight.
+__device__ __forceinline__ void keep_rows(uint4* at, const float (&x)[8][4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const Split a = split(x[2 * m][0], x[2 * m][1]), b = split(x[2 * m][2], x[2 * m][3]),
+                c = split(x[2 * m + 1][0], x[2 * m + 1][1]), d = split(x[2 * m + 1][2], x[2 * m + 1][3]);
+    at[2 * m * 32 + lane] = make_uint4(transposed(a.hi), transposed(c.hi), transposed(b.hi), transposed(d.hi));
+    at[(2 * m + 1) * 32 + lane] =
+        make_uint4(transposed(a.lo), transposed(c.lo), transposed(b.lo), transposed(d.lo));
+  }
+}
+__device__ __forceinline__ void keep_row_group(uint4* at, int n, const float (&x)[4]) {
+  const Split a = split(x[0], x[1]), b = split(x[2], x[3]);
+  unsigned* to = reinterpret_cast<unsigned*>(at + n / 2 * 64 + (threadIdx.x & 31)) + (n & 1);
+  to[0] = transposed(a.hi);
+  to[2] = transposed(b.hi);
+  to[128] = transposed(a.lo);
+  to[130] = transposed(b.lo);
+}
 
 // The warp's 16 columns of a dk x dv state in and out of global memory, transposed in registers: rows g and
-// g + 8 of the columns, elements 8 n + t2, + 1 of dk.
+// g + 8 of the columns, elements from + 8 n + t2, + 1 of dk.
 template <int NB>
-__device__ __forceinline__ void load_state(float (&S)[NB][4], const float* state, int dk, int dv, int col) {
+__device__ __forceinline__ void load_state(float (&S)[NB][4], const float* state, int dk, int dv, int col,
+                                           int from = 0) {
   const int lane = threadIdx.x & 31, g = lane / 4, t2 = (lane & 3) * 2;
 #pragma unroll
   for (int n = 0; n < NB; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int c = col + g + (e / 2) * 8, d = n * 8 + t2 + (e & 1);
+      const int c = col + g + (e / 2) * 8, d = from + n * 8 + t2 + (e & 1);
       S[n][e] = state && c < dv && d < dk ? state[d * dv + c] : 0.f;
     }
 }
 template <int NB>
-__device__ __forceinline__ void store_state(const float (&S)[NB][4], float* state, int dk, int dv, int col) {
+__device__ __forceinline__ void store_state(const float (&S)[NB][4], float* state, int dk, int dv, int col,
+                                            int from = 0) {
   const int lane = threadIdx.x & 31, g = lane / 4, t2 = (lane & 3) * 2;
 #pragma unroll
   for (int n = 0; n < NB; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int c = col + g + (e / 2) * 8, d = n * 8 + t2 + (e & 1);
+      const int c = col + g + (e / 2) * 8, d = from + n * 8 + t2 + (e & 1);
       if (c < dv && d < dk) state[d * dv + c] = S[n][e];
     }
+}
+
+// What follows from a copy that never came: NaN in every later result.
+template <int NB>
+__device__ __forceinline__ void poison(float (&S)[NB][4]) {
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[n][e] = __int_as_float(0x7FC00000);
 }
 
 // The sequence, head and columns of a block.
@@ -150,7 +232,7 @@ struct Place {
   int sequence, h, kh, col;
 };
 template <typename T>
-__device__ __forceinline__ Place place_of(const GdeltaRows<T>& p, int slices, int64_t* scratch) {
+__device__ __forceinline__ Place place_of(const GdeltaRows<T>& p, int slices, int cols, int64_t* scratch) {
   const int64_t part = static_cast<int64_t>(p.heads_v) * slices;
   int64_t s = blockIdx.x / part;
   const int rest = static_cast<int>(blockIdx.x % part);
@@ -160,31 +242,250 @@ __device__ __forceinline__ Place place_of(const GdeltaRows<T>& p, int slices, in
   sequence_rows(p, s, &at.start, &at.end);
   at.h = rest / slices;
   at.kh = at.h / (p.heads_v / p.heads_k);
-  at.col = rest % slices * (blockDim.x / 2);
+  at.col = rest % slices * cols;
   at.chunk = at.start / kChunk + s;
   at.head = s * p.heads_v + at.h;
   return at;
 }
 
-// As many warps a block as dv has groups of 16 columns, fewer where that leaves SMs without a block.
-template <typename T>
-int chain_warps(const GdeltaRows<T>& p) {
-  const int groups = gdelta_groups(p.dv);
-  int warps = 1;
-  while (warps < kMaxWarps && warps < groups &&
-         p.batch * p.heads_v * ((groups + 2 * warps - 1) / (2 * warps)) >= kSms)
-    warps *= 2;
-  return warps;
+// Products one 16-deep piece at a time. A result is asked for again only after those of the others: a product
+// waits some 18 cycles for its sum's last one (4 warps an SM: 4.8 us a chunk with the terms of one
+// result behind each other, see gdelta.cu).
+//
+// c[n] += a (rows n of a tile, along their elements from k), for all eight groups of rows.
+template <int NT, int STRIDE>
+__device__ __forceinline__ void along_rows(float (&c)[8][4], const unsigned (&hi)[4], const unsigned (&lo)[4],
+                                           unsigned tile, unsigned term, int k) {
+  unsigned b[4][4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) ldmatrix4(b[n], along<STRIDE>(tile, n * 16, k));
+#pragma unroll
+  for (int n = 0; n < 8; ++n) mma(c[n], hi, b[n / 2][(n & 1) * 2], b[n / 2][(n & 1) * 2 + 1]);
+#pragma unroll
+  for (int n = 0; n < 8; ++n) mma(c[n], lo, b[n / 2][(n & 1) * 2], b[n / 2][(n & 1) * 2 + 1]);
+  if constexpr (NT == 2) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) ldmatrix4(b[n], along<STRIDE>(tile + term, n * 16, k));
+#pragma unroll
+    for (int n = 0; n < 8; ++n) mma(c[n], hi, b[n / 2][(n & 1) * 2], b[n / 2][(n & 1) * 2 + 1]);
+  }
+}
+// c[n] += a (16 rows of a tile from k), for all groups of eight of their elements.
+template <int NT, int NB, int STRIDE>
+__device__ __forceinline__ void across_rows(float (&c)[NB][4], const unsigned (&hi)[4], const unsigned (&lo)[4],
+                                            unsigned tile, unsigned term, int k) {
+#pragma unroll
+  for (int first = 0; first < NB; first += 8) {
+    unsigned b[4][4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) ldmatrix4_trans(b[n], across(tile, STRIDE, k, first * 8 + n * 16));
+#pragma unroll
+    for (int n = 0; n < 8; ++n) mma(c[first + n], hi, b[n / 2][(n & 1) * 2], b[n / 2][(n & 1) * 2 + 1]);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) mma(c[first + n], lo, b[n / 2][(n & 1) * 2], b[n / 2][(n & 1) * 2 + 1]);
+    if constexpr (NT == 2) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) ldmatrix4_trans(b[n], across(tile + term, STRIDE, k, first * 8 + n * 16));
+#pragma unroll
+      for (int n = 0; n < 8; ++n) mma(c[first + n], hi, b[n / 2][(n & 1) * 2], b[n / 2][(n & 1) * 2 + 1]);
+    }
+  }
+}
+// The same for a part of the elements from `first`, N groups of eight.
+template <int NT, int N, int STRIDE>
+__device__ __forceinline__ void part_across(float (&c)[N][4], const unsigned (&hi)[4], const unsigned (&lo)[4],
+                                            unsigned tile, unsigned term, int k, int first) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    unsigned b[N / 2][4];
+#pragma unroll
+    for (int n = 0; n < N / 2; ++n) ldmatrix4_trans(b[n], across(tile + t * term, STRIDE, k, first + n * 16));
+#pragma unroll
+    for (int n = 0; n < N; ++n) mma(c[n], hi, b[n / 2][(n & 1) * 2], b[n / 2][(n & 1) * 2 + 1]);
+    if (t == 0)
+#pragma unroll
+      for (int n = 0; n < N; ++n) mma(c[n], lo, b[n / 2][(n & 1) * 2], b[n / 2][(n & 1) * 2 + 1]);
+  }
+}
+// c[n] += a piece(n), n from FIRST to LAST - 1; a in one term where A1.
+template <int FIRST, int LAST, bool A1, typename F>
+__device__ __forceinline__ void by_pieces(float (&c)[8][4], const unsigned (&hi)[4], const unsigned (&lo)[4],
+                                          F&& piece) {
+#pragma unroll
+  for (int first = FIRST; first < LAST; first += 4) {
+    uint4 b[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      if (first + n < LAST) b[n] = piece(first + n);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      if (first + n < LAST) mma(c[first + n], hi, b[n].x, b[n].y);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      if (first + n < LAST) mma(c[first + n], hi, b[n].z, b[n].w);
+    if constexpr (!A1) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (first + n < LAST) mma(c[first + n], lo, b[n].x, b[n].y);
+    }
+  }
+}
+// Calls f with 0, 1, 2, 3 as constants.
+template <typename F>
+__device__ __forceinline__ void four(F&& f) {
+  f(std::integral_constant<int, 0>());
+  f(std::integral_constant<int, 1>());
+  f(std::integral_constant<int, 2>());
+  f(std::integral_constant<int, 3>());
 }
 
-// c += a b over one 16-deep piece: a in two terms, b in NB.
-template <int NB>
-__device__ __forceinline__ void mma_terms(float (&c)[4], const unsigned (&hi)[4],
-                                          const unsigned (&lo)[4], unsigned b0, unsigned b1,
-                                          unsigned l0, unsigned l1) {
-  mma(c, hi, b0, b1);
-  mma(c, lo, b0, b1);
-  if constexpr (NB == 2) mma(c, hi, l0, l1);
+// ---------------------------------------------------------------------------- several warps a group of columns
+// KS warps share 16 columns: each keeps an equal part of dk of the transposed state and works out
+// the chunk's rows in its 8 / KS groups of eight. What all of them need as first operands of the next products goes
+// through shared memory, split and in the registers' order.
+template <int KS>
+struct Team {
+  static constexpr int kRows = 8 / KS;  // groups of rows of a warp
+  int j;                                // the warp's place
+  // Group i of the warp: low and high numbers together, since the triangles grow with them.
+  __device__ __forceinline__ int rows(int i) const {
+    return 2 * KS * (i / 2) + (i & 1 ? 2 * KS - 1 - j : j);
+  }
+};
+template <int DK>
+struct Exchange {
+  uint4 state[DK / 16][2][32];  // [16 of dk][hi, lo]
+  uint4 first[4][2][32];        // [16 rows]
+  uint4 second[4][2][32];
+  uint4 third[4][2][32];
+};
+// One group of eight rows (a 16 x 8 result) as half of a first operand over 16 rows.
+__device__ __forceinline__ void put_half(uint4 (&at)[4][2][32], int n, const float (&x)[4]) {
+  const int lane = threadIdx.x & 31;
+  const Split a = split(x[0], x[1]), b = split(x[2], x[3]);
+  reinterpret_cast<uint2*>(&at[n / 2][0][lane])[n & 1] = make_uint2(a.hi, b.hi);
+  reinterpret_cast<uint2*>(&at[n / 2][1][lane])[n & 1] = make_uint2(a.lo, b.lo);
+}
+__device__ __forceinline__ void get_operand(unsigned (&hi)[4], unsigned (&lo)[4], const uint4 (&at)[2][32]) {
+  const int lane = threadIdx.x & 31;
+  const uint4 a = at[0][lane], b = at[1][lane];
+  hi[0] = a.x, hi[1] = a.y, hi[2] = a.z, hi[3] = a.w;
+  lo[0] = b.x, lo[1] = b.y, lo[2] = b.z, lo[3] = b.w;
+}
+// ldmatrix addresses of two groups of eight rows, n and m: as second operand over the rows' elements, and transposed as
+// two 16 x 8 results.
+template <int STRIDE>
+__device__ __forceinline__ unsigned along_two(unsigned tile, int n, int m, int k) {
+  const int lane = threadIdx.x & 31;
+  return tile + 2 * (((lane & 16 ? m : n) * 8 + (lane & 7)) * STRIDE + k + (lane & 8));
+}
+template <typename T>
+__device__ __forceinline__ void read_two(float (&x)[4], float (&y)[4], const T* v, int v_stride, int n, int m) {
+  const int lane = threadIdx.x & 31, g = lane / 4, t2 = (lane & 3) * 2;
+  if constexpr (sizeof(T) == 2) {
+    unsigned w[4];
+    ldmatrix4_trans(w, smem_addr(v + ((lane & 16 ? m : n) * 8 + (lane & 7)) * v_stride + (lane & 8)));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float2 a = to_f32(*reinterpret_cast<const typename Pair<T>::type*>(&w[j])),
+                   b = to_f32(*reinterpret_cast<const typename Pair<T>::type*>(&w[2 + j]));
+      x[2 * j] = a.x, x[2 * j + 1] = a.y, y[2 * j] = b.x, y[2 * j + 1] = b.y;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = to_f32(v[(n * 8 + t2 + (e & 1)) * v_stride + g + (e / 2) * 8]);
+      y[e] = to_f32(v[(m * 8 + t2 + (e & 1)) * v_stride + g + (e / 2) * 8]);
+    }
+  }
+}
+// Rounds two groups of eight rows through the warp's own rows and columns of a tile and stores those below
+// n_rows, `width` columns at most.
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_two(const float (&x)[4], const float (&y)[4], T* v, int v_stride, int n,
+                                          int m, T* to, int64_t ld, int n_rows, int width) {
+  const int lane = threadIdx.x & 31, g = lane / 4, t2 = (lane & 3) * 2;
+  __syncwarp();
+  if constexpr (sizeof(T) == 2) {
+    unsigned w[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const auto a = pair_from_f32<T>(make_float2(x[2 * j], x[2 * j + 1])),
+                 b = pair_from_f32<T>(make_float2(y[2 * j], y[2 * j + 1]));
+      w[j] = *reinterpret_cast<const unsigned*>(&a);
+      w[2 + j] = *reinterpret_cast<const unsigned*>(&b);
+    }
+    stmatrix4_trans(smem_addr(v + ((lane & 16 ? m : n) * 8 + (lane & 7)) * v_stride + (lane & 8)), w[0], w[1],
+                    w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[(n * 8 + t2 + (e & 1)) * v_stride + g + (e / 2) * 8] = from_f32<T>(x[e]);
+      v[(m * 8 + t2 + (e & 1)) * v_stride + g + (e / 2) * 8] = from_f32<T>(y[e]);
+    }
+  }
+  __syncwarp();
+  constexpr int kV = VEC ? 16 / static_cast<int>(sizeof(T)) : 1, kVecs = 16 / kV;
+#pragma unroll
+  for (int j = lane; j < 16 * kVecs; j += 32) {
+    const int r = j / kVecs, c = (j % kVecs) * kV, row = (r < 8 ? n : m) * 8 + (r & 7);
+    if (row >= n_rows || c >= width) continue;
+    if constexpr (VEC)
+      *reinterpret_cast<uint4*>(to + row * ld + c) = *reinterpret_cast<const uint4*>(v + row * v_stride + c);
+    else
+      to[row * ld + c] = v[row * v_stride + c];
+  }
+}
+constexpr int kMaxTeams = 2, kTeamStages = 2;
+template <typename T, int DK>
+constexpr int team_bytes(int teams) {
+  return kTeamStages * Stage<T, DK>::bytes(teams) + teams * static_cast<int>(sizeof(Exchange<DK>));
+}
+// How a chain's blocks are made up: teams of four warps (`teams` a block), or one warp a group of columns.
+struct Blocks {
+  int teams, warps;
+};
+// The least (turns of all SMs, one block each) x (a chunk's time in a block, 0.1 us, measured with dk = dv = 128 in BF16
+// where all blocks run at once): a team takes the chain's products apart, so that a chunk takes less than
+// half of one warp's time, but its warps exchange their parts, so that blocks of eight single warps do more in
+// all. FP32 and FP16 stages are not brought ahead by single warps.
+template <typename T, int DK>
+Blocks chain_blocks(const GdeltaRows<T>& p) {
+  const int groups = gdelta_groups(p.dv);
+  Blocks best{0, 1};
+  int64_t least = INT64_MAX;
+  auto offer = [&](int a_block, int time, Blocks b) {
+    const int64_t blocks = p.batch * p.heads_v * ((groups + a_block - 1) / a_block);
+    const int64_t cost = (blocks + kSms - 1) / kSms * time;
+    if (cost < least) least = cost, best = b;
+  };
+  const int slow = Terms<T>::n;
+  offer(1, 21, {1, 0});
+  if (groups > 1 && team_bytes<T, DK>(2) <= kMaxShared) offer(2, 27, {2, 0});
+  if (groups > 2) offer(4, 50 * slow, {0, 4});
+  if (groups > 4) offer(8, 69 * slow, {0, 8});
+  return best;
+}
+// The warps behind the teams bring the stages: `load` for each chunk in its order, two stages ahead at most.
+constexpr int kLoaders = 128;  // threads
+template <bool ASYNC, typename F>
+__device__ __forceinline__ void bring_stages(int64_t chunks, int stages, uint64_t* full, uint64_t* empty,
+                                             volatile int* failed, F&& load) {
+  for (int64_t i = 0; i < chunks; ++i) {
+    const int s = static_cast<int>(i % stages);
+    if (!wait_for(&empty[s], (i / stages & 1) ^ 1, failed)) return;
+    load(i, s);
+    if constexpr (ASYNC) {
+      arrive_behind_copies(&full[s]);
+    } else {
+      cp_async_wait_all();
+      barrier_arrive(&full[s]);
+    }
+  }
+  cp_async_wait_all();
+}
+__device__ __forceinline__ void team_sync(int team, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
 }
 
 }  // namespace

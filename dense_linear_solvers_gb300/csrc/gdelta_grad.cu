@@ -11,7 +11,8 @@
 // the last row's more by sum e beta k.E + f_last <G, S>; dg is db summed from the chunk's end.
 // The sums over dv run over groups of 16 columns, whose operands lie in the registers' order in global memory
 // and come by cp.async two groups ahead. Of the 64 x dk products a warp has all rows and an eighth of the
-// columns, of the 64 x 64 ones up to three of the 20 tiles of 16 x 8 on and below the diagonal. Value heads
+// columns, of the 64 x 64 ones one to four of the 20 tiles of 16 x 8 on and below the diagonal, those of the rows
+// whose operands it has at hand. Value heads
 // of one key head follow each other in the block, which adds them up in order in registers.
 #include "gdelta_grad.cuh"
 
@@ -20,14 +21,14 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kStages = 3;
-constexpr int kTiles = 20, kSlots = 3;  // tiles of the lower triangle, of a warp
+constexpr int kTiles = 20, kSlots = 4;  // tiles of the lower triangle, of a warp at most
 constexpr int kDs = 24;                 // row distance of D's 16 columns: 16-byte pieces, banks apart
 constexpr int kXs = kChunk + 8;
 
 template <int DK, int NT>
 struct GradStage {
-  uint4 state[DK / 8][32], solution[8][32];     // S, M
-  uint4 grad[DK / 8][32], solution_grad[8][32]; // G, dU
+  uint4 state[DK / 8][32], solution[4][2][32];      // S, M
+  uint4 grad[DK / 8][32], solution_grad[4][2][32];  // G, dU
   __nv_bfloat16 d[NT][kChunk][kDs];
 };
 
@@ -49,17 +50,8 @@ struct GradShared {
   Span span;
 };
 
-// Row block and column group of a tile.
-__device__ __forceinline__ void tile_at(int tile, int* m, int* n) {
-  *m = tile < 2 ? 0 : tile < 6 ? 1 : tile < 12 ? 2 : 3;
-  *n = tile - *m * (*m + 1);
-}
-// The first operand of 16 rows from two pieces of 8.
-__device__ __forceinline__ void rows_of_pieces(unsigned (&hi)[4], unsigned (&lo)[4], const uint4& a,
-                                               const uint4& b) {
-  hi[0] = a.x, hi[1] = b.x, hi[2] = a.y, hi[3] = b.y;
-  lo[0] = a.z, lo[1] = b.z, lo[2] = a.w, lo[3] = b.w;
-}
+// Number of a tile: row block m, column group n.
+__device__ __forceinline__ int tile_at(int m, int n) { return m * (m + 1) + n; }
 __device__ __forceinline__ float2 two(unsigned v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
@@ -68,11 +60,11 @@ __device__ __forceinline__ float dot_terms(unsigned ahi, unsigned alo, unsigned 
   return __fmaf_rn(__fadd_rn(a.x, c.x), __fadd_rn(b.x, d.x),
                    __fmul_rn(__fadd_rn(a.y, c.y), __fadd_rn(b.y, d.y)));
 }
-__device__ __forceinline__ void products3(float (&c)[4], const unsigned (&hi)[4], const unsigned (&lo)[4],
-                                          const uint4& b) {
-  mma(c, hi, b.x, b.y);
-  mma(c, hi, b.z, b.w);
-  mma(c, lo, b.x, b.y);
+__device__ __forceinline__ void get_rows(unsigned (&hi)[4], unsigned (&lo)[4], const uint4 (&at)[2][32]) {
+  const int lane = threadIdx.x & 31;
+  const uint4 a = at[0][lane], b = at[1][lane];
+  hi[0] = a.x, hi[1] = a.y, hi[2] = a.z, hi[3] = a.w;
+  lo[0] = b.x, lo[1] = b.y, lo[2] = b.z, lo[3] = b.w;
 }
 
 template <typename T, int DK, bool VEC>
@@ -92,39 +84,38 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(GdeltaRows<T> p, Gdel
   const Span span = sh.span;
   if (span.rows == 0) return;
   load_terms<T, DK, STRIDE, VEC>(&sh.q[0][0][0], p.q + span.row * p.ldq + kh * p.dk, p.ldq, span.rows,
-                                 p.dk);
+                                 p.dk, threadIdx.x, kThreads);
   load_terms<T, DK, STRIDE, VEC>(&sh.k[0][0][0], p.k + span.row * p.ldk + kh * p.dk, p.ldk, span.rows,
-                                 p.dk);
+                                 p.dk, threadIdx.x, kThreads);
   cp_async_commit();
   auto load = [&](int h, int w) {  // a group of 16 columns
     auto& st = sh.stage[w % kStages];
     const int64_t at = ((place * p.heads_v + h) * groups + w) * (kept_pieces(DK) * 32);
     constexpr int kPart = (NB + 8) * 32;
-    uint4* to = &st.state[0][0];
-    for (int j = threadIdx.x; j < 2 * kPart; j += kThreads)
-      cp_async_16(to + j, j < kPart ? g.forward + at + j : g.backward + at + j - kPart, 16);
+    uint4* to = &st.state[0][0] + threadIdx.x;
+    const uint4 *s = g.forward + at + threadIdx.x, *d = g.backward + at + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < kPart; j += kThreads) {
+      cp_async_16(to + j, s + j, 16);
+      cp_async_16(to + kPart + j, d + j, 16);
+    }
     load_terms<T, 16, kDs, VEC>(&st.d[0][0][0], g.dout + span.row * g.lddo + h * p.dv + w * 16, g.lddo,
-                                span.rows, p.dv - w * 16);
+                                span.rows, p.dv - w * 16, threadIdx.x, kThreads);
   };
   cp_async_wait_all();
   __syncthreads();
-  // q k and k k of the warp's tiles
-#pragma unroll
-  for (int s = 0; s < kSlots; ++s) {
-    const int tile = warp + s * kWarps;
-    if (tile >= kTiles) continue;
-    int m, n;
-    tile_at(tile, &m, &n);
+  // q k and k k of the warp's tiles: rows of block warp / 2, every other group of columns
+  const int rows16 = warp / 2, odd = warp & 1;
+  for (int s = 0; s <= rows16; ++s) {
     float qk[4] = {0.f, 0.f, 0.f, 0.f}, kk[4] = {0.f, 0.f, 0.f, 0.f};
     for (int d = 0; d < DK; d += 16) {
       unsigned a[NT][4], b[NT][4], c[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        ldmatrix4(a[t], across(smem_addr(&sh.q[t][0][0]), STRIDE, m * 16, d));
-        ldmatrix4(b[t], across(smem_addr(&sh.k[t][0][0]), STRIDE, m * 16, d));
-        ldmatrix4(c[t], along<STRIDE>(smem_addr(&sh.k[t][0][0]), n / 2 * 16, d));
+        ldmatrix4(a[t], across(smem_addr(&sh.q[t][0][0]), STRIDE, rows16 * 16, d));
+        ldmatrix4(b[t], across(smem_addr(&sh.k[t][0][0]), STRIDE, rows16 * 16, d));
+        ldmatrix4(c[t], along<STRIDE>(smem_addr(&sh.k[t][0][0]), s * 16, d));
       }
-      const bool odd = n & 1;
       mma(qk, a[0], odd ? c[0][2] : c[0][0], odd ? c[0][3] : c[0][1]);
       mma(kk, b[0], odd ? c[0][2] : c[0][0], odd ? c[0][3] : c[0][1]);
       if constexpr (NT == 2) {
@@ -187,37 +178,44 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(GdeltaRows<T> p, Gdel
       }
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        unsigned a[NT][4], hi[4], lo[4];
+        unsigned a[NT][4], hi[4], lo[4], mhi[4], mlo[4];
 #pragma unroll
         for (int t = 0; t < NT; ++t) ldmatrix4(a[t], across(d + t * (kChunk * kDs * 2), kDs, m * 16, 0));
-        rows_of_pieces(hi, lo, st.solution_grad[2 * m][lane], st.solution_grad[2 * m + 1][lane]);
+        get_rows(hi, lo, st.solution_grad[m]);
+        get_rows(mhi, mlo, st.solution[m]);
+        // the terms of one sum apart from each other: a product waits for its sum's last one
 #pragma unroll
         for (int j = 0; j < N8; ++j) {
           mma(P[m][j], a[0], S[j].x, S[j].y);
+          mma(R[m][j], hi, S[j].x, S[j].y);
+          mma(E[m][j], mhi, G[j].x, G[j].y);
+        }
+#pragma unroll
+        for (int j = 0; j < N8; ++j) {
           mma(P[m][j], a[0], S[j].z, S[j].w);
+          mma(R[m][j], hi, S[j].z, S[j].w);
+          mma(E[m][j], mhi, G[j].z, G[j].w);
+        }
+#pragma unroll
+        for (int j = 0; j < N8; ++j) {
           if constexpr (NT == 2) mma(P[m][j], a[1], S[j].x, S[j].y);
-          products3(R[m][j], hi, lo, S[j]);
+          mma(R[m][j], lo, S[j].x, S[j].y);
+          mma(E[m][j], mlo, G[j].x, G[j].y);
         }
-        rows_of_pieces(hi, lo, st.solution[2 * m][lane], st.solution[2 * m + 1][lane]);
+        if (m == rows16) {
 #pragma unroll
-        for (int j = 0; j < N8; ++j) products3(E[m][j], hi, lo, G[j]);
-      }
-#pragma unroll
-      for (int s = 0; s < kSlots; ++s) {
-        const int tile = warp + s * kWarps;
-        if (tile >= kTiles) continue;
-        int m, n;
-        tile_at(tile, &m, &n);
-        const uint4 b = st.solution[n][lane];
-        unsigned a[4], hi[4], lo[4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          ldmatrix4(a, across(d + t * (kChunk * kDs * 2), kDs, m * 16, 0));
-          mma(H[s], a, b.x, b.y);
-          if (t == 0) mma(H[s], a, b.z, b.w);
+          for (int s = 0; s <= m; ++s) {
+            const uint4 b = st.solution[s][0][lane], c = st.solution[s][1][lane];
+            const unsigned b0 = odd ? b.y : b.x, b1 = odd ? b.w : b.z, c0 = odd ? c.y : c.x,
+                           c1 = odd ? c.w : c.z;
+            mma(H[s], a[0], b0, b1);
+            mma(J[s], hi, b0, b1);
+            mma(H[s], a[0], c0, c1);
+            mma(J[s], hi, c0, c1);
+            if constexpr (NT == 2) mma(H[s], a[1], b0, b1);
+            mma(J[s], lo, b0, b1);
+          }
         }
-        rows_of_pieces(hi, lo, st.solution_grad[2 * m][lane], st.solution_grad[2 * m + 1][lane]);
-        products3(J[s], hi, lo, b);
       }
     }
 #pragma unroll
@@ -227,10 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(GdeltaRows<T> p, Gdel
     __syncthreads();  // the stages give way to x and w
 #pragma unroll
     for (int s = 0; s < kSlots; ++s) {
-      const int tile = warp + s * kWarps;
-      if (tile >= kTiles) continue;
-      int m, n;
-      tile_at(tile, &m, &n);
+      if (s > rows16) continue;
+      const int m = rows16, n = 2 * s + odd, tile = tile_at(m, n);
       const float4 q4 = sh.qk[s][threadIdx.x], k4 = sh.kk[s][threadIdx.x];
       const float qk[4] = {q4.x, q4.y, q4.z, q4.w}, kk[4] = {k4.x, k4.y, k4.z, k4.w};
       float x[4], w[4], sum[4];

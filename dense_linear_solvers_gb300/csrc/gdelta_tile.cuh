@@ -137,14 +137,14 @@ __device__ __forceinline__ Span chunk_at(const GdeltaRows<T>& p, int64_t place) 
 // ---------------------------------------------------------------------------- rows in shared memory
 // Brings `n` rows of `width` elements (row j at src + j ld) into a tile of 64 rows of COLS elements, row
 // distance STRIDE, as BF16 terms, one tile a term, zeros elsewhere. VEC: rows aligned to 16 bytes.
-// BF16 rows come by cp.async: commit and wait behind it.
+// BF16 rows come by cp.async: commit and wait behind it. By `threads` threads, this one number `thread`.
 template <typename T, int COLS, int STRIDE, bool VEC>
 __device__ __forceinline__ void load_terms(__nv_bfloat16* tile, const T* src, int64_t ld, int n,
-                                           int width) {
+                                           int width, int thread, int threads) {
   constexpr int kTerm = kChunk * STRIDE;
   if constexpr (VEC) {
     constexpr int kV = 16 / sizeof(T);
-    for (int j = threadIdx.x; j < kChunk * (COLS / kV); j += blockDim.x) {
+    for (int j = thread; j < kChunk * (COLS / kV); j += threads) {
       const int r = j / (COLS / kV), c = (j % (COLS / kV)) * kV;
       const int have = r < n ? min(max(width - c, 0), kV) : 0;  // width is a multiple of kV here
       const T* from = have ? src + r * ld + c : src;
@@ -164,7 +164,7 @@ __device__ __forceinline__ void load_terms(__nv_bfloat16* tile, const T* src, in
       }
     }
   } else {
-    for (int j = threadIdx.x; j < kChunk * COLS; j += blockDim.x) {
+    for (int j = thread; j < kChunk * COLS; j += threads) {
       const int r = j / COLS, c = j % COLS;
       __nv_bfloat16* at = tile + r * STRIDE + c;
       const bool have = r < n && c < width;
@@ -183,18 +183,18 @@ __device__ __forceinline__ void load_terms(__nv_bfloat16* tile, const T* src, in
 // The same, as stored: `cols` elements a row.
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_rows(T* tile, int stride, int cols, const T* src, int64_t ld,
-                                          int n, int width) {
+                                          int n, int width, int thread, int threads) {
   if constexpr (VEC) {
     constexpr int kV = 16 / sizeof(T);
     const int vecs = cols / kV;
-    for (int j = threadIdx.x; j < kChunk * vecs; j += blockDim.x) {
+    for (int j = thread; j < kChunk * vecs; j += threads) {
       const int r = j / vecs, c = (j % vecs) * kV;
       const int have = r < n ? min(max(width - c, 0), kV) : 0;
       cp_async_16(tile + r * stride + c, have ? src + r * ld + c : src,
                   have * static_cast<int>(sizeof(T)));
     }
   } else {
-    for (int j = threadIdx.x; j < kChunk * cols; j += blockDim.x) {
+    for (int j = thread; j < kChunk * cols; j += threads) {
       const int r = j / cols, c = j % cols;
       tile[r * stride + c] = r < n && c < width ? src[r * ld + c] : from_f32<T>(0.f);
     }
@@ -223,7 +223,7 @@ struct Prepared {
   uint4 inverse[kPieces][32];
   uint4 mixing[kPieces][32];
   float front[kChunk], beta[kChunk], back[kChunk];
-  float sum_hi[kChunk], sum_lo[kChunk];  // the running sum of the log decays
+  float sum_hi[kChunk], sum_lo[kChunk];  // the running sum of the log decays, in units of log 2
 };
 static_assert(sizeof(Prepared) % 16 == 0, "copied in pieces of 16 bytes");
 // Where a piece of the lower triangle is: columns (2 pair + half) * 8 .. + 7, which are rows of the matrix, depth
@@ -235,13 +235,20 @@ __host__ __device__ constexpr int upper_piece(int pair, int half, int k) {
   return pair * (9 - pair) + half * (4 - pair) + k - pair;
 }
 
-// e^(b_r - b_i) from the sums' two parts.
+constexpr double kLog2 = 1.4426950408889634;  // 1 / log 2
+// 2^v, within two units in the last place; 0 below 2^-126.
+__device__ __forceinline__ float power_of_two(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// e^(b_r - b_i) from the sums' two parts, in units of log 2.
 __device__ __forceinline__ float decay_between(const float* hi, const float* lo, int r, int i) {
-  return expf(__fadd_rn(__fsub_rn(hi[r], hi[i]), __fsub_rn(lo[r], lo[i])));
+  return power_of_two(__fadd_rn(__fsub_rn(hi[r], hi[i]), __fsub_rn(lo[r], lo[i])));
 }
 
-// What the chains leave for the gradients of a chunk, by value head and 16 columns of dv: a state (or its gradient) and 64
-// rows, both as second operands of products over dv, in pieces of 8 columns and 16 deep as above.
+// What the chains leave for the gradients of a chunk, by value head and 16 columns of dv: a state (or its
+// gradient) as second operand of products over dv, in pieces as above, and 64 rows as first operand of such.
 __host__ __device__ constexpr int gdelta_groups(int dv) { return (dv + 15) / 16; }
 constexpr int gdelta_deep(int dk) { return dk <= 64 ? 64 : 128; }   // dk as the kernels pad it
 __host__ __device__ constexpr int64_t kept_pieces(int deep) { return deep / 8 + kChunk / 8; }

@@ -16,6 +16,7 @@
 
 #include <cuda.h>
 
+#include "barrier.cuh"
 #include "cluster.cuh"
 #include "common.cuh"
 #include "grec_math.cuh"
@@ -47,48 +48,12 @@ struct Problem {
   int64_t ldsa, ldsw, ldy;
 };
 
-// ---------------------------------------------------------------------------- barriers, copies
-constexpr long long kPatience = 4000000000ll;  // clocks, about two seconds
-
-__device__ __forceinline__ unsigned addr(const void* p) {
-  return static_cast<unsigned>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void barrier_init(uint64_t* b, int count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(addr(b)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void barrier_arrive(uint64_t* b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr(b)) : "memory");
-}
-__device__ __forceinline__ void barrier_expect(uint64_t* b, int bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(addr(b)), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ bool barrier_passed(uint64_t* b, unsigned parity) {
-  unsigned done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done) : "r"(addr(b)), "r"(parity) : "memory");
-  return done;
-}
-// False where the wait ran out, here or (`failed`) elsewhere in the block.
-__device__ __forceinline__ bool wait_for(uint64_t* b, unsigned parity, volatile int* failed) {
-  if (barrier_passed(b, parity)) return true;
-  const long long start = clock64();
-  while (!barrier_passed(b, parity)) {
-    if (*failed) return false;
-    if (clock64() - start > kPatience) {
-      *failed = 1;
-      return false;
-    }
-  }
-  return true;
-}
+// ---------------------------------------------------------------------------- copies
 __device__ __forceinline__ void copy_tile(void* to, const CUtensorMap* map, int x, int y, uint64_t* b) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3}], [%4];" ::"r"(addr(to)),
-      "l"(map), "r"(x), "r"(y), "r"(addr(b))
+      "[%1, {%2, %3}], [%4];" ::"r"(smem_address(to)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_address(b))
       : "memory");
 }
 
@@ -113,7 +78,7 @@ __device__ __forceinline__ void product(unsigned result, uint64_t a, uint64_t b,
 }
 __device__ __forceinline__ void commit(uint64_t* b) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   addr(b)) : "memory");
+                   smem_address(b)) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void read_columns(unsigned at, float (&v)[N]);
@@ -155,7 +120,7 @@ gemm_q8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   __shared__ uint64_t full[C::kStages], empty[C::kStages], ready[C::kResults], taken[C::kResults];
   __shared__ unsigned columns;
   __shared__ volatile int failed;
-  unsigned char* stages = raw + (1024 - (addr(raw) & 1023)) % 1024;
+  unsigned char* stages = raw + (1024 - (smem_address(raw) & 1023)) % 1024;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int split = cluster_size(), rank = cluster_rank();
   const int features = static_cast<int>((p.n + kBlock - 1) / kBlock);
@@ -168,10 +133,10 @@ gemm_q8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     failed = 0;
     for (int s = 0; s < C::kStages; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], 1);
     for (int r = 0; r < C::kResults; ++r) barrier_init(&ready[r], 1), barrier_init(&taken[r], kSumWarps);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    barriers_ready();
   }
   if (warp == kSumWarps) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(addr(&columns)),
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_address(&columns)),
                  "n"(C::kColumns) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -214,7 +179,7 @@ gemm_q8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                      wait_for(&full[s], (it / C::kStages) & 1, &failed)))
             break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const unsigned at = addr(stages + s * C::kStage);
+          const unsigned at = smem_address(stages + s * C::kStage);
 #pragma unroll
           for (int k = 0; k < kBlock; k += 32)
             product(memory + r * TOKENS, operand_at(at + k), operand_at(at + kBlock * kBlock + k),
@@ -297,7 +262,7 @@ gemm_q8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     cluster_sync();
     const int64_t tile = blockIdx.x / split;
     const int64_t f0 = tile % features * kBlock, t0 = tile / features * TOKENS;
-    const unsigned part = addr(stages);
+    const unsigned part = smem_address(stages);
     for (int j = rank * kThreads + threadIdx.x; j < TOKENS * kBlock; j += split * kThreads) {
       const int64_t t = t0 + j / kBlock, f = f0 + j % kBlock;
       if (t >= p.m || f >= p.n) continue;
