@@ -1,7 +1,7 @@
 // Matrix product of 8-bit operands under block scales (bs_gemm_q8):
 //   y[t][f] = sum over blocks b of 128 of  sa[t][b] sw[f / 128][b] sum over k in b of a[t][k] w[f][k].
 //
-// tcgen05.mma (e4m3, FP32 sums in tensor memory) takes the features as its 128 rows and TOKENS tokens as its
+// For few tokens tcgen05.mma (e4m3, FP32 sums in tensor memory) takes the features as its 128 rows and TOKENS tokens as its
 // columns: a tile's 128 features share one weight scale a block, one token costs 16 columns at
 // least instead of 128 rows, and a lane of the result is a feature, so that a warp's stores of one token are
 // contiguous. Each block of 128 is a result of its own (four instructions of depth 32), which eight warps
@@ -34,11 +34,11 @@ constexpr int kMaxSplit = 8;
 template <int TOKENS>
 struct Config {
   static constexpr int kStage = (kBlock + TOKENS) * kBlock;  // bytes of both operands' block
-  static constexpr int kStages = TOKENS == 256 ? 4 : TOKENS == 128 ? 6 : 8;
-  static constexpr int kResults = TOKENS == 256 ? 2 : 4;     // results in tensor memory
+  static constexpr int kStages = TOKENS == 128 ? 6 : 8;
+  static constexpr int kResults = 4;                         // results in tensor memory
   static constexpr int kColumns = TOKENS * kResults < 32 ? 32 : TOKENS * kResults;
   static constexpr int kOwn = TOKENS / 2;                    // columns of a summing thread
-  static constexpr int kPiece = kOwn < 32 ? kOwn : TOKENS == 256 ? 16 : 32;       // columns read at once
+  static constexpr int kPiece = kOwn < 32 ? kOwn : 32;       // columns read at once
   static constexpr int kShared = kStages * kStage + 1024;    // the stages start on 1024 bytes
 };
 
@@ -54,6 +54,16 @@ __device__ __forceinline__ void copy_tile(void* to, const CUtensorMap* map, int 
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
       "[%1, {%2, %3}], [%4];" ::"r"(smem_address(to)),
       "l"(map), "r"(x), "r"(y), "r"(smem_address(b))
+      : "memory");
+}
+
+// Into the same place of every block of a cluster that `mask` names, counted by each one's barrier.
+__device__ __forceinline__ void copy_tile_to(void* to, const CUtensorMap* map, int x, int y, uint64_t* b,
+                                             unsigned mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_address(to)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_address(b)), "h"(static_cast<unsigned short>(mask))
       : "memory");
 }
 
@@ -79,6 +89,12 @@ __device__ __forceinline__ void product(unsigned result, uint64_t a, uint64_t b,
 __device__ __forceinline__ void commit(uint64_t* b) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_address(b)) : "memory");
+}
+// The same at the barriers of every block that `mask` names.
+__device__ __forceinline__ void commit_to(uint64_t* b, unsigned mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_address(b)), "h"(static_cast<unsigned short>(mask)) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void read_columns(unsigned at, float (&v)[N]);
@@ -285,6 +301,176 @@ gemm_q8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(memory), "n"(C::kColumns));
 }
 
+// ---------------------------------------------------------------------------- many tokens
+// The same product with the tokens as the tensor core's rows and FEATURES features as its columns: a thread's token has
+// one scale a block for all of the thread's columns, so that scaling and adding takes one instruction for two
+// results and no shared memory; sixteen warps have a quarter of the columns each. Blocks of a cluster have neighbouring tokens and the same
+// features: each brings an equal part of the weights' tile for all of them, since one block alone asks the second cache
+// level for 48 KB a block of k, more than it gives to all SMs at once (16,384 x 8,192 x 4,096: 1,075 us).
+constexpr int kRowWarps = 16;
+constexpr int kRowThreads = (kRowWarps + 2) * 32;
+
+template <int FEATURES>
+struct RowConfig {
+  static constexpr int kStage = (kBlock + FEATURES) * kBlock;
+  static constexpr int kStages = FEATURES == 256 ? 4 : 6;
+  static constexpr int kResults = 512 / FEATURES;
+  static constexpr int kOwn = FEATURES / 4;  // columns of a summing thread
+  static constexpr int kShared = kStages * kStage + 1024;
+};
+
+template <typename T, int FEATURES>
+__global__ void __launch_bounds__(kRowThreads, 1)
+gemm_q8_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                    Problem p, T* __restrict__ y, bool vectors) {
+  using C = RowConfig<FEATURES>;
+  extern __shared__ unsigned char raw[];
+  __shared__ uint64_t full[C::kStages], empty[C::kStages], ready[C::kResults], taken[C::kResults];
+  __shared__ unsigned columns;
+  __shared__ volatile int failed;
+  unsigned char* stages = raw + (1024 - (smem_address(raw) & 1023)) % 1024;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int across = static_cast<int>((p.n + FEATURES - 1) / FEATURES);
+  // a cluster takes `size` tiles of tokens at a time
+  const int size = cluster_size(), rank = cluster_rank();
+  const int64_t tiles = across * ((p.m + kBlock * size - 1) / (kBlock * size));
+  const int64_t turn = gridDim.x / size;
+  const unsigned all = (1u << size) - 1;
+  const int blocks = static_cast<int>((p.k + kBlock - 1) / kBlock);
+
+  if (threadIdx.x == 0) {
+    failed = 0;
+    for (int s = 0; s < C::kStages; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], size);
+    for (int r = 0; r < C::kResults; ++r) barrier_init(&ready[r], 1), barrier_init(&taken[r], kRowWarps);
+    barriers_ready();
+  }
+  if (warp == kRowWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_address(&columns)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const unsigned memory = columns;
+  cluster_publish();
+  cluster_sync();  // every block's barriers are set up
+
+  if (warp == kRowWarps) {
+    if (lane == 0) {  // copies
+      unsigned it = 0;
+      bool ok = true;
+      for (int64_t tile = blockIdx.x / size; ok && tile < tiles; tile += turn) {
+        const int f0 = static_cast<int>(tile % across) * FEATURES;
+        const int t0 = static_cast<int>(tile / across * size + rank) * kBlock;
+        for (int b = 0; b < blocks; ++b, ++it) {
+          const unsigned s = it % C::kStages;
+          if (!(ok = wait_for(&empty[s], ((it / C::kStages) & 1) ^ 1, &failed))) break;
+          barrier_expect(&full[s], C::kStage);
+          unsigned char* at = stages + s * C::kStage;
+          copy_tile(at, &map_a, b * kBlock, t0, &full[s]);
+          const int part = FEATURES / size * rank;  // rows of the weights' tile
+          copy_tile_to(at + (kBlock + part) * kBlock, &map_w, b * kBlock, f0 + part, &full[s], all);
+        }
+      }
+      // nothing may be in flight when the block ends
+      for (unsigned back = it > C::kStages ? it - C::kStages : 0; back < it; ++back)
+        for (int n = 0; n < 1000000 && !barrier_passed(&full[back % C::kStages], (back / C::kStages) & 1);
+             ++n) {
+        }
+    }
+  } else if (warp == kRowWarps + 1) {
+    if (lane == 0) {  // products
+      unsigned it = 0;
+      bool ok = true;
+      for (int64_t tile = blockIdx.x / size; ok && tile < tiles; tile += turn)
+        for (int b = 0; b < blocks; ++b, ++it) {
+          const unsigned s = it % C::kStages, r = it % C::kResults;
+          if (!(ok = wait_for(&taken[r], ((it / C::kResults) & 1) ^ 1, &failed) &&
+                     wait_for(&full[s], (it / C::kStages) & 1, &failed)))
+            break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const unsigned at = smem_address(stages + s * C::kStage);
+#pragma unroll
+          for (int k = 0; k < kBlock; k += 32)
+            product(memory + r * FEATURES, operand_at(at + k), operand_at(at + kBlock * kBlock + k),
+                    instruction(FEATURES), k > 0);
+          commit_to(&empty[s], all);
+          commit(&ready[r]);
+        }
+      for (int n = 0; it > 0 && n < 1000000; ++n)  // none may be in flight when the block ends
+        if (barrier_passed(&ready[(it - 1) % C::kResults], ((it - 1) / C::kResults) & 1)) break;
+    }
+  } else {
+    // warp w: lanes (tokens) 32 (w % 4) .., columns (features) of quarter w / 4
+    const int quarter = warp / 4 * C::kOwn;
+    const unsigned at = memory + (static_cast<unsigned>(warp % 4 * 32) << 16) + quarter;
+    unsigned it = 0;
+    bool ok = true;
+    for (int64_t tile = blockIdx.x / size; tile < tiles; tile += turn) {
+      const int64_t f0 = tile % across * FEATURES + quarter;
+      const int64_t token = (tile / across * size + rank) * kBlock + warp % 4 * 32 + lane;
+      const bool there = token < p.m;
+      const float* sa = p.sa + token * p.ldsa;
+      // columns behind n lie in the last group of features, or in none: their sums are zeros either way
+      const float* sw = p.sw + min(f0, p.n - 1) / kBlock * p.ldsw;
+      float2 sum[C::kOwn / 2];
+#pragma unroll
+      for (int j = 0; j < C::kOwn / 2; ++j) sum[j] = make_float2(0.f, 0.f);
+      float next_a = there ? sa[0] : 0.f, next_w = sw[0];
+      for (int b = 0; b < blocks; ++b, ++it) {
+        const float f = __fmul_rn(next_a, next_w);
+        if (b + 1 < blocks) {
+          next_a = there ? sa[b + 1] : 0.f;
+          next_w = sw[b + 1];
+        }
+        const unsigned r = it % C::kResults;
+        ok = __all_sync(0xFFFFFFFFu, ok && wait_for(&ready[r], (it / C::kResults) & 1, &failed));
+        if (!ok) continue;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+        for (int c = 0; c < C::kOwn; c += 16) {
+          float v[16];
+          read_columns<16>(at + r * FEATURES + c, v);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          if (c + 16 == C::kOwn) {  // read to the end: the next result may come
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) barrier_arrive(&taken[r]);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; j += 2)
+            sum[(c + j) / 2] = fma2(make_float2(v[j], v[j + 1]), both(f), sum[(c + j) / 2]);
+        }
+      }
+      if (!there) continue;
+      T* to = y + token * p.ldy + f0;
+      const float bad = __int_as_float(0x7FC00000);
+      constexpr int kV = 16 / static_cast<int>(sizeof(T));
+      if (vectors && ok) {
+#pragma unroll
+        for (int j = 0; j < C::kOwn; j += kV) {
+          alignas(16) T w[kV];
+#pragma unroll
+          for (int e = 0; e < kV; e += 2)
+            *reinterpret_cast<typename Pair<T>::type*>(w + e) = pair_from_f32<T>(sum[(j + e) / 2]);
+          if (f0 + j < p.n) *reinterpret_cast<uint4*>(to + j) = *reinterpret_cast<const uint4*>(w);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < C::kOwn; ++j)
+          if (f0 + j < p.n) to[j] = from_f32<T>(!ok ? bad : j & 1 ? sum[j / 2].y : sum[j / 2].x);
+      }
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  cluster_sync();  // no block ends while others copy into it or arrive at its barriers
+  if (warp == kRowWarps)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(memory));
+}
+
 // ---------------------------------------------------------------------------- launch
 using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
@@ -318,6 +504,13 @@ cudaError_t tile_map(Encode encode, CUtensorMap* map, const uint8_t* base, int64
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// A tile's blocks of k over a cluster while that leaves no SM with two parts, nor a part without two blocks.
+int split_of(int64_t tiles, int64_t blocks) {
+  int split = 1;
+  while (2 * split <= kMaxSplit && tiles * 2 * split <= kSms && blocks >= 4 * split) split *= 2;
+  return split;
+}
+
 template <typename T, int TOKENS>
 cudaError_t run(Encode encode, const GemmQ8<T>& g, cudaStream_t stream) {
   using C = Config<TOKENS>;
@@ -330,15 +523,40 @@ cudaError_t run(Encode encode, const GemmQ8<T>& g, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t tiles = (g.n + kBlock - 1) / kBlock * ((g.m + TOKENS - 1) / TOKENS);
   const int64_t blocks = (g.k + kBlock - 1) / kBlock;
-  // a tile's blocks of k over a cluster while that leaves no SM with two parts, nor a part without two blocks
-  int split = 1;
-  while (2 * split <= kMaxSplit && tiles * 2 * split <= kSms && blocks >= 4 * split) split *= 2;
+  const int split = split_of(tiles, blocks);
   const int64_t grid = split > 1 ? tiles * split : std::min<int64_t>(tiles, kSms);
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t config = cluster_config(&attr, dim3(static_cast<unsigned>(grid)), kThreads,
                                                    C::kShared, split, stream);
   return cudaLaunchKernelEx(&config, kernel, w, a,
                             Problem{g.m, g.n, g.k, g.sa, g.sw, g.ldsa, g.ldsw, g.ldy}, g.y);
+}
+
+template <typename T, int FEATURES>
+cudaError_t run_rows(Encode encode, const GemmQ8<T>& g, cudaStream_t stream) {
+  using C = RowConfig<FEATURES>;
+  auto* kernel = gemm_q8_rows_kernel<T, FEATURES>;
+  static HeldClusters known;
+  Held held;
+  cudaError_t e = known.of(kernel, kRowThreads, C::kShared, &held);
+  if (e != cudaSuccess) return e;
+  const int64_t across = (g.n + FEATURES - 1) / FEATURES, along = (g.m + kBlock - 1) / kBlock;
+  // Clusters as large as the GPU is still filled with, four at most.
+  int size = 1;
+  while (size < 4 && along % (2 * size) == 0 && across * along >= 2 * size * held.clusters[2 * size]) size *= 2;
+  CUtensorMap w, a;
+  e = tile_map(encode, &w, g.w, g.n, g.k, g.ldw, FEATURES / size);
+  if (e == cudaSuccess) e = tile_map(encode, &a, g.a, g.m, g.k, g.lda, kBlock);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = across * ((along + size - 1) / size);
+  const bool vectors = ((reinterpret_cast<uintptr_t>(g.y) | static_cast<uintptr_t>(g.ldy * sizeof(T)) |
+                         static_cast<uintptr_t>(g.n * sizeof(T))) & 15) == 0;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t config =
+      cluster_config(&attr, dim3(static_cast<unsigned>(std::min<int64_t>(tiles, held.clusters[size]) * size)),
+                     kRowThreads, C::kShared, size, stream);
+  return cudaLaunchKernelEx(&config, kernel, a, w, Problem{g.m, g.n, g.k, g.sa, g.sw, g.ldsa, g.ldsw, g.ldy},
+                            g.y, vectors);
 }
 
 // y = 0: no block of k.
@@ -362,17 +580,23 @@ cudaError_t launch_gemm_q8(const GemmQ8<T>& g, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (g.m <= 16) return run<T, 16>(encode, g, stream);
   if (g.m <= 32) return run<T, 32>(encode, g, stream);
-  if (g.m <= 64) return run<T, 64>(encode, g, stream);
-  // The least (turns of all SMs) x (a tile's time): its products take 2 cycles a token and block, its copies
-  // not less than 250 cycles a block, its start and end about 3000.
-  const int64_t features = (g.n + kBlock - 1) / kBlock, blocks = (g.k + kBlock - 1) / kBlock;
-  auto cost = [&](int tokens) {
-    const int64_t tiles = features * ((g.m + tokens - 1) / tokens);
-    return (tiles + kSms - 1) / kSms * (blocks * std::max(2 * tokens, 250) + 3000);
+  // The least (turns of all SMs) x (a tile's time: its blocks of k, and its start and end, about 3000 cycles).
+  const int64_t blocks = (g.k + kBlock - 1) / kBlock;
+  auto cost = [&](int64_t tiles, int cycles, bool splits) {
+    const int split = splits ? split_of(tiles, blocks) : 1;
+    return (tiles * split + kSms - 1) / kSms * ((blocks + split - 1) / split * cycles + 3000);
   };
-  const int64_t c64 = cost(64), c128 = cost(128), c256 = cost(256);
-  if (c256 <= c128 && c256 <= c64) return run<T, 256>(encode, g, stream);
-  return c128 <= c64 ? run<T, 128>(encode, g, stream) : run<T, 64>(encode, g, stream);
+  auto tiles = [&](int features, int tokens) {
+    return (g.n + features - 1) / features * ((g.m + tokens - 1) / tokens);
+  };
+  const int64_t costs[] = {cost(tiles(kBlock, 64), 600, true), cost(tiles(kBlock, 128), 1100, true),
+                           cost(tiles(128, kBlock), 350, false), cost(tiles(256, kBlock), 600, false)};
+  switch (std::min_element(costs, costs + 4) - costs) {
+    case 0: return run<T, 64>(encode, g, stream);
+    case 1: return run<T, 128>(encode, g, stream);
+    case 2: return run_rows<T, 128>(encode, g, stream);
+    default: return run_rows<T, 256>(encode, g, stream);
+  }
 }
 template cudaError_t launch_gemm_q8(const GemmQ8<float>&, cudaStream_t);
 template cudaError_t launch_gemm_q8(const GemmQ8<__nv_bfloat16>&, cudaStream_t);
