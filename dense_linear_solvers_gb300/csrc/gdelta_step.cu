@@ -11,12 +11,11 @@
 namespace bsolve {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kMaxDk = 128;
 
 // V columns a thread, LANES threads a row of the block's columns.
-template <typename T, int V, int LANES>
-__global__ void __launch_bounds__(kWarps * 32)
+template <typename T, int V, int LANES, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, 1024 / (kWarps * 32))
 step_kernel(GdeltaRows<T> p, float* state, int64_t num_slots, const int32_t* slots, T* o, int64_t ldo,
             int slices) {
   constexpr int COLS = V * LANES, ROWS = 32 / LANES, N = kMaxDk / (kWarps * ROWS);
@@ -126,11 +125,11 @@ step_kernel(GdeltaRows<T> p, float* state, int64_t num_slots, const int32_t* slo
     for (int e = 0; e < V; ++e) to[c + e] = from_f32<T>(y[e]);
 }
 
-template <typename T, int V, int LANES>
+template <typename T, int V, int LANES, int kWarps>
 cudaError_t step(const GdeltaRows<T>& p, float* state, int64_t num_slots, const int32_t* slots, T* o,
                  int64_t ldo, cudaStream_t stream) {
   const int slices = (p.dv + V * LANES - 1) / (V * LANES);
-  step_kernel<T, V, LANES><<<static_cast<unsigned>(p.batch * p.heads_v * slices), kWarps * 32, 0, stream>>>(
+  step_kernel<T, V, LANES, kWarps><<<static_cast<unsigned>(p.batch * p.heads_v * slices), kWarps * 32, 0, stream>>>(
       p, state, num_slots, slots, o, ldo, slices);
   return cudaGetLastError();
 }
@@ -141,10 +140,10 @@ template <typename T>
 cudaError_t launch_gdelta_step(const GdeltaRows<T>& p, float* state, int64_t num_slots,
                                const int32_t* slots, T* o, int64_t ldo, cudaStream_t stream) {
   if (p.dv % 4 != 0 || (reinterpret_cast<uintptr_t>(state) & 15) != 0)
-    return step<T, 1, 32>(p, state, num_slots, slots, o, ldo, stream);
+    return step<T, 1, 32, 8>(p, state, num_slots, slots, o, ldo, stream);
   if (p.batch * p.heads_v * ((p.dv + 127) / 128) >= 4 * kSms)
-    return step<T, 4, 32>(p, state, num_slots, slots, o, ldo, stream);
-  return step<T, 4, 8>(p, state, num_slots, slots, o, ldo, stream);
+    return step<T, 4, 32, 16>(p, state, num_slots, slots, o, ldo, stream);
+  return step<T, 4, 8, 8>(p, state, num_slots, slots, o, ldo, stream);
 }
 template cudaError_t launch_gdelta_step(const GdeltaRows<float>&, float*, int64_t, const int32_t*,
                                         float*, int64_t, cudaStream_t);

@@ -142,39 +142,59 @@ template <typename T, int COLS, int STRIDE, bool VEC>
 __device__ __forceinline__ void load_terms(__nv_bfloat16* tile, const T* src, int64_t ld, int n,
                                            int width, int thread, int threads) {
   constexpr int kTerm = kChunk * STRIDE;
-  if constexpr (VEC) {
-    constexpr int kV = 16 / sizeof(T);
-    for (int j = thread; j < kChunk * (COLS / kV); j += threads) {
-      const int r = j / (COLS / kV), c = (j % (COLS / kV)) * kV;
+  // where they have to be split, or are not aligned, several loads are asked for before the first is used
+  if constexpr (VEC && Terms<T>::n == 1) {
+    constexpr int kV = 16 / sizeof(T), kVecs = COLS / kV;
+    for (int j = thread; j < kChunk * kVecs; j += threads) {
+      const int r = j / kVecs, c = (j % kVecs) * kV;
       const int have = r < n ? min(max(width - c, 0), kV) : 0;  // width is a multiple of kV here
-      const T* from = have ? src + r * ld + c : src;
-      __nv_bfloat16* at = tile + r * STRIDE + c;
-      if constexpr (Terms<T>::n == 1) {
-        cp_async_16(at, from, have * static_cast<int>(sizeof(T)));
-      } else {
-        alignas(16) T v[kV];
-        *reinterpret_cast<uint4*>(v) = have ? *reinterpret_cast<const uint4*>(from)
-                                            : make_uint4(0, 0, 0, 0);
+      cp_async_16(tile + r * STRIDE + c, have ? src + r * ld + c : src, have * static_cast<int>(sizeof(T)));
+    }
+  } else if constexpr (VEC) {
+    constexpr int kV = 16 / sizeof(T), kVecs = COLS / kV, kAtOnce = 4;
+    for (int first = thread; first < kChunk * kVecs; first += kAtOnce * threads) {
+      uint4 v[kAtOnce];
 #pragma unroll
-        for (int e = 0; e < kV; e += 2) {
-          const Split s = split(to_f32(v[e]), to_f32(v[e + 1]));
-          *reinterpret_cast<unsigned*>(at + e) = s.hi;
-          *reinterpret_cast<unsigned*>(at + kTerm + e) = s.lo;
+      for (int a = 0; a < kAtOnce; ++a) {
+        const int j = first + a * threads, r = j / kVecs, c = (j % kVecs) * kV;
+        v[a] = j < kChunk * kVecs && r < n && c < width ? *reinterpret_cast<const uint4*>(src + r * ld + c)
+                                                        : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) {
+        const int j = first + a * threads;
+        if (j >= kChunk * kVecs) break;
+        unsigned* at = reinterpret_cast<unsigned*>(tile + j / kVecs * STRIDE + (j % kVecs) * kV);
+        const auto* pairs = reinterpret_cast<const typename Pair<T>::type*>(&v[a]);
+#pragma unroll
+        for (int e = 0; e < kV / 2; ++e) {
+          const float2 f = to_f32(pairs[e]);
+          const Split s = split(f.x, f.y);
+          at[e] = s.hi;
+          at[kTerm / 2 + e] = s.lo;
         }
       }
     }
   } else {
-    for (int j = thread; j < kChunk * COLS; j += threads) {
-      const int r = j / COLS, c = j % COLS;
-      __nv_bfloat16* at = tile + r * STRIDE + c;
-      const bool have = r < n && c < width;
-      if constexpr (Terms<T>::n == 1) {
-        *at = have ? src[r * ld + c] : __float2bfloat16_rn(0.f);
-      } else {
-        const float x = have ? to_f32(src[r * ld + c]) : 0.f;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-        *at = hi;
-        at[kTerm] = __float2bfloat16_rn(__fsub_rn(x, __bfloat162float(hi)));
+    constexpr int kPairs = COLS / 2, kAtOnce = 8;
+    for (int first = thread; first < kChunk * kPairs; first += kAtOnce * threads) {
+      float2 v[kAtOnce];
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) {
+        const int j = first + a * threads, r = j / kPairs, c = (j % kPairs) * 2;
+        const bool row = j < kChunk * kPairs && r < n;
+        const T* from = src + r * ld + c;
+        v[a].x = row && c < width ? to_f32(from[0]) : 0.f;
+        v[a].y = row && c + 1 < width ? to_f32(from[1]) : 0.f;
+      }
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) {
+        const int j = first + a * threads;
+        if (j >= kChunk * kPairs) break;
+        unsigned* at = reinterpret_cast<unsigned*>(tile + j / kPairs * STRIDE + (j % kPairs) * 2);
+        const Split s = split(v[a].x, v[a].y);
+        at[0] = s.hi;  // a BF16 number itself
+        if constexpr (Terms<T>::n == 2) at[kTerm / 2] = s.lo;
       }
     }
   }
@@ -194,9 +214,19 @@ __device__ __forceinline__ void load_rows(T* tile, int stride, int cols, const T
                   have * static_cast<int>(sizeof(T)));
     }
   } else {
-    for (int j = thread; j < kChunk * cols; j += threads) {
-      const int r = j / cols, c = j % cols;
-      tile[r * stride + c] = r < n && c < width ? src[r * ld + c] : from_f32<T>(0.f);
+    constexpr int kAtOnce = 8;
+    for (int first = thread; first < kChunk * cols; first += kAtOnce * threads) {
+      T v[kAtOnce];
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) {
+        const int j = first + a * threads, r = j / cols, c = j % cols;
+        v[a] = r < n && c < width ? src[r * ld + c] : from_f32<T>(0.f);
+      }
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) {
+        const int j = first + a * threads;
+        if (j < kChunk * cols) tile[j / cols * stride + j % cols] = v[a];
+      }
     }
   }
 }

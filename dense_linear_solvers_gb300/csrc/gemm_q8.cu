@@ -57,16 +57,6 @@ __device__ __forceinline__ void copy_tile(void* to, const CUtensorMap* map, int 
       : "memory");
 }
 
-// Into the same place of every block of a cluster that `mask` names, counted by each one's barrier.
-__device__ __forceinline__ void copy_tile_to(void* to, const CUtensorMap* map, int x, int y, uint64_t* b,
-                                             unsigned mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
-      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_address(to)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_address(b)), "h"(static_cast<unsigned short>(mask))
-      : "memory");
-}
-
 // ---------------------------------------------------------------------------- tensor memory
 // A tile of rows of 128 bytes in shared memory as TMA's 128-byte swizzle leaves it: eight rows (1024 bytes)
 // a group.
@@ -89,12 +79,6 @@ __device__ __forceinline__ void product(unsigned result, uint64_t a, uint64_t b,
 __device__ __forceinline__ void commit(uint64_t* b) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_address(b)) : "memory");
-}
-// The same at the barriers of every block that `mask` names.
-__device__ __forceinline__ void commit_to(uint64_t* b, unsigned mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_address(b)), "h"(static_cast<unsigned short>(mask)) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void read_columns(unsigned at, float (&v)[N]);
@@ -304,9 +288,11 @@ gemm_q8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
 // ---------------------------------------------------------------------------- many tokens
 // The same product with the tokens as the tensor core's rows and FEATURES features as its columns: a thread's token has
 // one scale a block for all of the thread's columns, so that scaling and adding takes one instruction for two
-// results and no shared memory; sixteen warps have a quarter of the columns each. Blocks of a cluster have neighbouring tokens and the same
-// features: each brings an equal part of the weights' tile for all of them, since one block alone asks the second cache
-// level for 48 KB a block of k, more than it gives to all SMs at once (16,384 x 8,192 x 4,096: 1,075 us).
+// results and no shared memory; sixteen warps have a quarter of the columns each. 16,384 x 8,192 x 4,096: 616 us (1.79
+// PFLOP/s). Left out in turn, the sums take 108 us of it and three quarters of the products as much; the copies alone, 48 KB a
+// block of k and SM, need 422. Shared between the blocks of a cluster (multicast) they gain nothing: an SM takes in no
+// more; two SMs on one tile of 256 x 256 (cta_group::2) would take in two thirds, but wait longer for each other
+// (1.04 ms).
 constexpr int kRowWarps = 16;
 constexpr int kRowThreads = (kRowWarps + 2) * 32;
 
@@ -331,16 +317,12 @@ gemm_q8_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
   unsigned char* stages = raw + (1024 - (smem_address(raw) & 1023)) % 1024;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int across = static_cast<int>((p.n + FEATURES - 1) / FEATURES);
-  // a cluster takes `size` tiles of tokens at a time
-  const int size = cluster_size(), rank = cluster_rank();
-  const int64_t tiles = across * ((p.m + kBlock * size - 1) / (kBlock * size));
-  const int64_t turn = gridDim.x / size;
-  const unsigned all = (1u << size) - 1;
+  const int64_t tiles = across * ((p.m + kBlock - 1) / kBlock);
   const int blocks = static_cast<int>((p.k + kBlock - 1) / kBlock);
 
   if (threadIdx.x == 0) {
     failed = 0;
-    for (int s = 0; s < C::kStages; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], size);
+    for (int s = 0; s < C::kStages; ++s) barrier_init(&full[s], 1), barrier_init(&empty[s], 1);
     for (int r = 0; r < C::kResults; ++r) barrier_init(&ready[r], 1), barrier_init(&taken[r], kRowWarps);
     barriers_ready();
   }
@@ -353,24 +335,21 @@ gemm_q8_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const unsigned memory = columns;
-  cluster_publish();
-  cluster_sync();  // every block's barriers are set up
 
   if (warp == kRowWarps) {
     if (lane == 0) {  // copies
       unsigned it = 0;
       bool ok = true;
-      for (int64_t tile = blockIdx.x / size; ok && tile < tiles; tile += turn) {
+      for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
         const int f0 = static_cast<int>(tile % across) * FEATURES;
-        const int t0 = static_cast<int>(tile / across * size + rank) * kBlock;
+        const int t0 = static_cast<int>(tile / across) * kBlock;
         for (int b = 0; b < blocks; ++b, ++it) {
           const unsigned s = it % C::kStages;
           if (!(ok = wait_for(&empty[s], ((it / C::kStages) & 1) ^ 1, &failed))) break;
           barrier_expect(&full[s], C::kStage);
           unsigned char* at = stages + s * C::kStage;
           copy_tile(at, &map_a, b * kBlock, t0, &full[s]);
-          const int part = FEATURES / size * rank;  // rows of the weights' tile
-          copy_tile_to(at + (kBlock + part) * kBlock, &map_w, b * kBlock, f0 + part, &full[s], all);
+          copy_tile(at + kBlock * kBlock, &map_w, b * kBlock, f0, &full[s]);
         }
       }
       // nothing may be in flight when the block ends
@@ -383,7 +362,7 @@ gemm_q8_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     if (lane == 0) {  // products
       unsigned it = 0;
       bool ok = true;
-      for (int64_t tile = blockIdx.x / size; ok && tile < tiles; tile += turn)
+      for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x)
         for (int b = 0; b < blocks; ++b, ++it) {
           const unsigned s = it % C::kStages, r = it % C::kResults;
           if (!(ok = wait_for(&taken[r], ((it / C::kResults) & 1) ^ 1, &failed) &&
@@ -395,7 +374,7 @@ gemm_q8_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
           for (int k = 0; k < kBlock; k += 32)
             product(memory + r * FEATURES, operand_at(at + k), operand_at(at + kBlock * kBlock + k),
                     instruction(FEATURES), k > 0);
-          commit_to(&empty[s], all);
+          commit(&empty[s]);
           commit(&ready[r]);
         }
       for (int n = 0; it > 0 && n < 1000000; ++n)  // none may be in flight when the block ends
@@ -407,21 +386,23 @@ gemm_q8_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     const unsigned at = memory + (static_cast<unsigned>(warp % 4 * 32) << 16) + quarter;
     unsigned it = 0;
     bool ok = true;
-    for (int64_t tile = blockIdx.x / size; tile < tiles; tile += turn) {
-      const int64_t f0 = tile % across * FEATURES + quarter;
-      const int64_t token = (tile / across * size + rank) * kBlock + warp % 4 * 32 + lane;
-      const bool there = token < p.m;
-      const float* sa = p.sa + token * p.ldsa;
-      // columns behind n lie in the last group of features, or in none: their sums are zeros either way
-      const float* sw = p.sw + min(f0, p.n - 1) / kBlock * p.ldsw;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+      // (worked out again behind the loop, which has no registers for them)
+      const float *sa, *sw;
+      {
+        const int64_t f0 = tile % across * FEATURES + quarter, token = tile / across * kBlock + warp % 4 * 32 + lane;
+        // a token behind m: its operands are zeros; columns behind n: zeros either way
+        sa = p.sa + min(token, p.m - 1) * p.ldsa;
+        sw = p.sw + min(f0, p.n - 1) / kBlock * p.ldsw;
+      }
       float2 sum[C::kOwn / 2];
 #pragma unroll
       for (int j = 0; j < C::kOwn / 2; ++j) sum[j] = make_float2(0.f, 0.f);
-      float next_a = there ? sa[0] : 0.f, next_w = sw[0];
+      float next_a = sa[0], next_w = sw[0];
       for (int b = 0; b < blocks; ++b, ++it) {
         const float f = __fmul_rn(next_a, next_w);
         if (b + 1 < blocks) {
-          next_a = there ? sa[b + 1] : 0.f;
+          next_a = sa[b + 1];
           next_w = sw[b + 1];
         }
         const unsigned r = it % C::kResults;
@@ -443,7 +424,8 @@ gemm_q8_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             sum[(c + j) / 2] = fma2(make_float2(v[j], v[j + 1]), both(f), sum[(c + j) / 2]);
         }
       }
-      if (!there) continue;
+      const int64_t f0 = tile % across * FEATURES + quarter, token = tile / across * kBlock + warp % 4 * 32 + lane;
+      if (token >= p.m) continue;
       T* to = y + token * p.ldy + f0;
       const float bad = __int_as_float(0x7FC00000);
       constexpr int kV = 16 / static_cast<int>(sizeof(T));
@@ -466,7 +448,6 @@ gemm_q8_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  cluster_sync();  // no block ends while others copy into it or arrive at its barriers
   if (warp == kRowWarps)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(memory));
 }
@@ -535,28 +516,19 @@ cudaError_t run(Encode encode, const GemmQ8<T>& g, cudaStream_t stream) {
 template <typename T, int FEATURES>
 cudaError_t run_rows(Encode encode, const GemmQ8<T>& g, cudaStream_t stream) {
   using C = RowConfig<FEATURES>;
-  auto* kernel = gemm_q8_rows_kernel<T, FEATURES>;
-  static HeldClusters known;
-  Held held;
-  cudaError_t e = known.of(kernel, kRowThreads, C::kShared, &held);
-  if (e != cudaSuccess) return e;
-  const int64_t across = (g.n + FEATURES - 1) / FEATURES, along = (g.m + kBlock - 1) / kBlock;
-  // Clusters as large as the GPU is still filled with, four at most.
-  int size = 1;
-  while (size < 4 && along % (2 * size) == 0 && across * along >= 2 * size * held.clusters[2 * size]) size *= 2;
   CUtensorMap w, a;
-  e = tile_map(encode, &w, g.w, g.n, g.k, g.ldw, FEATURES / size);
+  cudaError_t e = tile_map(encode, &w, g.w, g.n, g.k, g.ldw, FEATURES);
   if (e == cudaSuccess) e = tile_map(encode, &a, g.a, g.m, g.k, g.lda, kBlock);
+  auto* kernel = gemm_q8_rows_kernel<T, FEATURES>;
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kShared);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = across * ((along + size - 1) / size);
+  const int64_t tiles = (g.n + FEATURES - 1) / FEATURES * ((g.m + kBlock - 1) / kBlock);
   const bool vectors = ((reinterpret_cast<uintptr_t>(g.y) | static_cast<uintptr_t>(g.ldy * sizeof(T)) |
                          static_cast<uintptr_t>(g.n * sizeof(T))) & 15) == 0;
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t config =
-      cluster_config(&attr, dim3(static_cast<unsigned>(std::min<int64_t>(tiles, held.clusters[size]) * size)),
-                     kRowThreads, C::kShared, size, stream);
-  return cudaLaunchKernelEx(&config, kernel, a, w, Problem{g.m, g.n, g.k, g.sa, g.sw, g.ldsa, g.ldsw, g.ldy},
-                            g.y, vectors);
+  kernel<<<static_cast<unsigned>(std::min<int64_t>(tiles, kSms)), kRowThreads, C::kShared, stream>>>(
+      a, w, Problem{g.m, g.n, g.k, g.sa, g.sw, g.ldsa, g.ldsw, g.ldy}, g.y, vectors);
+  return cudaGetLastError();
 }
 
 // y = 0: no block of k.
@@ -590,7 +562,7 @@ cudaError_t launch_gemm_q8(const GemmQ8<T>& g, cudaStream_t stream) {
     return (g.n + features - 1) / features * ((g.m + tokens - 1) / tokens);
   };
   const int64_t costs[] = {cost(tiles(kBlock, 64), 600, true), cost(tiles(kBlock, 128), 1100, true),
-                           cost(tiles(128, kBlock), 350, false), cost(tiles(256, kBlock), 600, false)};
+                           cost(tiles(128, kBlock), 900, false), cost(tiles(256, kBlock), 1300, false)};
   switch (std::min_element(costs, costs + 4) - costs) {
     case 0: return run<T, 64>(encode, g, stream);
     case 1: return run<T, 128>(encode, g, stream);
