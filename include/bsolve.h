@@ -1,7 +1,7 @@
 /*
  * bsolve.h -- C ABI of libbsolve.so: batched solution of many independent small dense
  * linear systems A x = b on one GPU (sm_103a), and the row operators of recurrent layers
- * (bs_grec, bs_gnorm: their own sections below).
+ * (bs_grec, bs_gnorm, bs_gemm_q8, bs_gdelta: their own sections below).
  *
  * Every entry point solves `batch` independent systems in one asynchronous launch (two
  * when a factor and a solve run apart: a fused call with more than 8 right-hand sides,
@@ -21,7 +21,8 @@
  *
  * Errors are reported synchronously, before anything is launched:
  *   BS_ERR_INVALID_ARG  null pointer, negative size, a base address not 16-byte aligned
- *                       (bs_grec and bs_gnorm calls: not aligned to its elements), or two
+ *                       (the row operators': not aligned to its elements, or as their
+ *                       sections say), or two
  *                       operands of the call whose byte ranges overlap;
  *   BS_ERR_UNSUPPORTED  a shape, dtype, layout or fill with no kernel instance (there is
  *                       no CPU fallback: the caller chooses another path);
@@ -53,8 +54,7 @@ typedef enum {
   BS_ERR_CUDA = 3
 } bs_status;
 
-/* The solvers take BS_FP32 and BS_FP64; the bs_grec and bs_gnorm calls BS_FP32, BS_BF16 and
- * BS_FP16. */
+/* The solvers take BS_FP32 and BS_FP64; the row operators BS_FP32, BS_BF16 and BS_FP16. */
 typedef enum { BS_FP32 = 0, BS_FP64 = 1, BS_BF16 = 2, BS_FP16 = 3 } bs_dtype;
 
 /* Element (r, c) of an n x m operand lives at r*m + c (row-major) or c*n + r
