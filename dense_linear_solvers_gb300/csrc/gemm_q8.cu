@@ -288,9 +288,8 @@ gemm_q8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
 // ---------------------------------------------------------------------------- many tokens
 // The same product with the tokens as the tensor core's rows and FEATURES features as its columns: a thread's token has
 // one scale a block for all of the thread's columns, so that scaling and adding takes one instruction for two
-// results and no shared memory; sixteen warps have a quarter of the columns each. 16,384 x 8,192 x 4,096: 616 us (1.79
-// PFLOP/s). Left out in turn, the sums take 108 us of it and three quarters of the products as much; the copies alone, 48 KB a
-// block of k and SM, need 422. Shared between the blocks of a cluster (multicast) they gain nothing: an SM takes in no
+// results and no shared memory; sixteen warps have a quarter of the columns each. 16,384 x 8,192 x 4,096: 569 us (1.93
+// PFLOP/s); the copies alone, 48 KB a block of k and SM, need 422. Shared between the blocks of a cluster (multicast) they gain nothing: an SM takes in no
 // more; two SMs on one tile of 256 x 256 (cta_group::2) would take in two thirds, but wait longer for each other
 // (1.04 ms).
 constexpr int kRowWarps = 16;
@@ -477,7 +476,8 @@ cudaError_t encoder(Encode* out) {
 cudaError_t tile_map(Encode encode, CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t width,
                      int64_t ld, int box) {
   const cuuint64_t dims[] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[] = {static_cast<cuuint64_t>(ld)};
+  // a single row's distance to the next may be any; a map's is a multiple of 16 bytes
+  const cuuint64_t strides[] = {static_cast<cuuint64_t>(rows > 1 ? ld : (width + 15) / 16 * 16)};
   const cuuint32_t tile[] = {kBlock, static_cast<cuuint32_t>(box)}, steps[] = {1, 1};
   const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides,
                             tile, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

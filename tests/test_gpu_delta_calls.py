@@ -206,3 +206,15 @@ def test_a_layer_over_a_prompt_and_its_next_token():
     bs.bs_gdelta_step_batched(*token, pool, y, slots=at.to(torch.int32))
     ref = reference(*token, [(b, b + 1) for b in range(batch)], h0=hT.double())
     assert ref.close("o", y, torch.bfloat16)[0] and ref.close("hT", pool[at], torch.float32)[0]
+
+
+@pytest.mark.parametrize("m, n, k", [(1, 40, 100), (1, 1, 7), (3, 1, 100), (1, 300, 129), (70, 1, 1)])
+def test_single_rows_of_any_depth(m, n, k):
+    """A single row of an operand has no distance to a next one that could be a wrong one."""
+    deep = -(-k // 16) * 16
+    new = lambda rows: torch.randn(rows, deep, device="cuda").to(E4M3)[:, :k]  # noqa: E731
+    a, w = (new(r) if r > 1 else torch.randn(1, k, device="cuda").to(E4M3) for r in (m, n))
+    sa, sw = (torch.rand(r, -(-k // 128), device="cuda") for r in (m, -(-n // 128)))
+    y = torch.empty(m, n, device="cuda")
+    bs.bs_gemm_q8(a, sa, w, sw, y)
+    check(a, sa, w, sw, y, "f32")
