@@ -12,7 +12,9 @@
 // The sums over dv run over groups of 16 columns, whose operands lie in the registers' order in global memory
 // and come by cp.async two groups ahead. Of the 64 x dk products a warp has all rows and an eighth of the
 // columns, of the 64 x 64 ones one to four of the 20 tiles of 16 x 8 on and below the diagonal, those of the rows
-// whose operands it has at hand. Value heads
+// whose operands it has at hand. 8 x 2,048 rows of 16 heads 128 x 128, BF16: 445 us, two thirds of it the groups of columns, whose
+// products alone would take two thirds of that (with each head's first columns asked for only behind the last head, and db
+// summed in 64 bits, 531). Value heads
 // of one key head follow each other in the block, which adds them up in order in registers.
 #include "gdelta_grad.cuh"
 
@@ -32,6 +34,10 @@ struct GradStage {
   __nv_bfloat16 d[NT][kChunk][kDs];
 };
 
+struct HeadRows {
+  float front[kChunk], back[kChunk], beta[kChunk], sum_hi[kChunk], sum_lo[kChunk];
+};
+
 template <int DK, int NT>
 struct GradShared {
   __nv_bfloat16 q[NT][kChunk][DK + 8];
@@ -39,11 +45,12 @@ struct GradShared {
   union {
     GradStage<DK, NT> stage[kStages];
     struct {
+      GradStage<DK, NT> ahead[2];  // the next head's first columns come meanwhile
       __nv_bfloat16 x[2][kChunk][kXs], w[2][kChunk][kXs];  // two terms each
     } mix;
   };
   float4 qk[kSlots][kThreads], kk[kSlots][kThreads];  // of the warps' tiles
-  float front[kChunk], back[kChunk], beta[kChunk], sum_hi[kChunk], sum_lo[kChunk];
+  HeadRows rows[2];  // of a head and the next one
   float dots[3][kWarps][kChunk];  // q.P, k.Q', k.E by the warps' columns
   float row_part[kTiles][16], col_part[kTiles][8];
   float product[kWarps];          // <G, S>
@@ -102,10 +109,28 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(GdeltaRows<T> p, Gdel
     load_terms<T, 16, kDs, VEC>(&st.d[0][0][0], g.dout + span.row * g.lddo + h * p.dv + w * 16, g.lddo,
                                 span.rows, p.dv - w * 16, threadIdx.x, kThreads);
   };
-  cp_async_wait_all();
+  auto begin = [&](int h) {  // a head's numbers and its first columns
+    const Prepared& own = g.prepared[place * p.heads_v + h];
+    HeadRows& to = sh.rows[h & 1];
+    if (threadIdx.x < kChunk / 4) {
+      const int r = threadIdx.x * 4;
+      cp_async_16(&to.front[r], &own.front[r], 16);
+      cp_async_16(&to.back[r], &own.back[r], 16);
+      cp_async_16(&to.beta[r], &own.beta[r], 16);
+      cp_async_16(&to.sum_hi[r], &own.sum_hi[r], 16);
+      cp_async_16(&to.sum_lo[r], &own.sum_lo[r], 16);
+    }
+    load(h, 0);
+    cp_async_commit();
+    if (groups > 1) load(h, 1);
+    cp_async_commit();
+  };
+  begin(kh * group);
+  cp_async_wait_group<2>();
   __syncthreads();
-  // q k and k k of the warp's tiles: rows of block warp / 2, every other group of columns
-  const int rows16 = warp / 2, odd = warp & 1;
+  // q k and k k of the warp's tiles: a block of 16 rows, every other group of columns. The two warps of a scheduler
+  // (w and w + 4) have five tiles together.
+  const int rows16 = warp < 4 ? warp / 2 : 3 - (warp - 4) / 2, odd = warp & 1;
   for (int s = 0; s <= rows16; ++s) {
     float qk[4] = {0.f, 0.f, 0.f, 0.f}, kk[4] = {0.f, 0.f, 0.f, 0.f};
     for (int d = 0; d < DK; d += 16) {
@@ -138,17 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(GdeltaRows<T> p, Gdel
       for (int e = 0; e < 4; ++e) dq[m][j][e] = dk[m][j][e] = 0.f;
 
   for (int h = kh * group; h < (kh + 1) * group; ++h) {
-    const Prepared& own = g.prepared[place * p.heads_v + h];
-    __syncthreads();  // the last head's numbers and terms are used
-    load(h, 0);
-    cp_async_commit();
-    if (groups > 1) load(h, 1);
-    cp_async_commit();
-    if (threadIdx.x < kChunk) {
-      const int r = threadIdx.x;
-      sh.front[r] = own.front[r], sh.back[r] = own.back[r], sh.beta[r] = own.beta[r];
-      sh.sum_hi[r] = own.sum_hi[r], sh.sum_lo[r] = own.sum_lo[r];
-    }
+    const HeadRows& own = sh.rows[h & 1];
     float P[4][N8][4], R[4][N8][4], E[4][N8][4], H[kSlots][4], J[kSlots][4], product = 0.f;
 #pragma unroll
     for (int m = 0; m < 4; ++m)
@@ -222,7 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(GdeltaRows<T> p, Gdel
     for (int o = 16; o; o /= 2) product += __shfl_xor_sync(0xFFFFFFFFu, product, o);
     if (lane == 0) sh.product[warp] = product;
     cp_async_wait_all();
-    __syncthreads();  // the stages give way to x and w
+    __syncthreads();  // the last stage gives way to x and w
+    if (h + 1 < (kh + 1) * group) begin(h + 1);
 #pragma unroll
     for (int s = 0; s < kSlots; ++s) {
       if (s > rows16) continue;
@@ -233,10 +249,10 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(GdeltaRows<T> p, Gdel
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = m * 16 + gr + (e / 2) * 8, i = n * 8 + t2 + (e & 1);
-        const float decay = i <= r ? decay_between(sh.sum_hi, sh.sum_lo, r, i) : 0.f;
-        const float b = __fmul_rn(decay, sh.beta[i]);
+        const float decay = i <= r ? decay_between(own.sum_hi, own.sum_lo, r, i) : 0.f;
+        const float b = __fmul_rn(decay, own.beta[i]);
         x[e] = i <= r ? __fmul_rn(__fmul_rn(p.scale, b), H[s][e]) : 0.f;
-        w[e] = i < r ? -__fmul_rn(__fmul_rn(sh.beta[r], b), J[s][e]) : 0.f;
+        w[e] = i < r ? -__fmul_rn(__fmul_rn(own.beta[r], b), J[s][e]) : 0.f;
         sum[e] = i <= r ? __fmaf_rn(x[e], qk[e], __fmul_rn(w[e], kk[e])) : 0.f;
         if (i == r && r < span.rows) g.dbeta[(span.row + r) * g.lddbeta + h] = J[s][e];
       }
@@ -264,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(GdeltaRows<T> p, Gdel
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int r = m * 16 + gr + half * 8;
-        const float f = sh.front[r], bf = __fmul_rn(sh.beta[r], f), eb = __fmul_rn(sh.back[r], sh.beta[r]);
+        const float f = own.front[r], bf = __fmul_rn(own.beta[r], f), eb = __fmul_rn(own.back[r], own.beta[r]);
         float v[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < N8; ++j) {
@@ -338,42 +354,40 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(GdeltaRows<T> p, Gdel
     }
     // dg: two rows a lane
     if (warp == 0) {
-      double db[2], tail[2];
+      float db[2], tail[2];  // their terms' errors are far above FP32's
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 2 * lane + e, m = r / 16, n = r / 8;
-        double sum = 0.0;
+        float sum = 0.f;
         for (int j = 0; j < 2 * m + 2; ++j) sum += sh.row_part[m * (m + 1) + j][r % 16];
         for (int j = m; j < 4; ++j) sum -= sh.col_part[j * (j + 1) + n][r % 8];
         float v[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int x = 0; x < 3; ++x)
           for (int j = 0; j < kWarps; ++j) v[x] += sh.dots[x][j][r];
-        const float f = sh.front[r], b = sh.beta[r];
-        tail[e] = static_cast<double>(__fmul_rn(__fmul_rn(sh.back[r], b), v[2]));
-        db[e] = sum + static_cast<double>(__fmul_rn(__fmul_rn(p.scale, f), v[0])) -
-                static_cast<double>(__fmul_rn(__fmul_rn(b, f), v[1])) - tail[e];
+        const float f = own.front[r], b = own.beta[r];
+        tail[e] = __fmul_rn(__fmul_rn(own.back[r], b), v[2]);
+        db[e] = sum + __fmul_rn(__fmul_rn(p.scale, f), v[0]) - __fmul_rn(__fmul_rn(b, f), v[1]) - tail[e];
       }
-      double whole = tail[0] + tail[1];
+      float whole = tail[0] + tail[1];
 #pragma unroll
       for (int o = 16; o; o /= 2) whole += __shfl_xor_sync(0xFFFFFFFFu, whole, o);
       float states = 0.f;
       for (int j = 0; j < kWarps; ++j) states += sh.product[j];
-      whole += static_cast<double>(__fmul_rn(sh.front[kChunk - 1], states));
+      whole += __fmul_rn(own.front[kChunk - 1], states);
       // sums from the chunk's end
       db[0] += db[1];
-      double run = db[0];
+      float run = db[0];
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
-        const double above = __shfl_down_sync(0xFFFFFFFFu, run, o);
+        const float above = __shfl_down_sync(0xFFFFFFFFu, run, o);
         if (lane + o < 32) run += above;
       }
-      const double behind = run - db[0] + whole;
+      const float behind = run - db[0] + whole;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 2 * lane + e;
-        if (r < span.rows)
-          g.dg[(span.row + r) * g.lddg + h] = static_cast<float>(behind + db[e]);
+        if (r < span.rows) g.dg[(span.row + r) * g.lddg + h] = behind + db[e];
       }
     }
   }
