@@ -11,7 +11,7 @@
 // shared memory for the block's warps. Bound by the chain: few warps (255 registers a thread), each waiting for its
 // own products. 8 x 2,048 rows of 16 heads 128 x 128, BF16: 279 us, the tensor pipe busy for 45%, schedulers issue on
 // 28% of the cycles. Where there are too few columns for that many warps, teams of four warps take 16 columns (see
-// gdelta_chain.cuh): one sequence of 32,768 rows of 16 heads, the whole call, 4.34 to 1.21 ms.
+// gdelta_chain.cuh): one sequence of 32,768 rows of 16 heads, the whole call, 4.34 to 0.95 ms.
 #include "gdelta_chain.cuh"
 
 namespace bsolve {
@@ -181,16 +181,16 @@ chain_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
 
 // The same chain by teams of KS warps a group of 16 columns, `teams` groups a block.
 template <typename T, int DK, bool VEC, int KS>
-__global__ void __launch_bounds__(kMaxTeams * 32 * KS + kLoaders, 1)
+__global__ void __launch_bounds__(kMaxTeams<T, DK> * 32 * KS + kLoaders<T, DK>, 1)
 team_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
   using St = Stage<T, DK>;
-  constexpr int STAGES = kTeamStages, NT = Terms<T>::n, NB = DK / 8, STRIDE = St::kStride, OWN = NB / KS, ROWS = Team<KS>::kRows;
+  constexpr int STAGES = kTeamStages<T, DK>, NT = Terms<T>::n, NB = DK / 8, STRIDE = St::kStride, OWN = NB / KS, ROWS = Team<KS>::kRows;
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ int64_t scratch[kSortedBatch + 1];
   __shared__ uint64_t full[STAGES], empty[STAGES];
   __shared__ volatile int failed;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, t2 = (lane & 3) * 2;
-  const int team = warp / KS, teams = (blockDim.x - kLoaders) / (32 * KS);
+  const int team = warp / KS, teams = (blockDim.x - kLoaders<T, DK>) / (32 * KS);
   const Team<KS> mine{warp % KS};
   const int v_stride = St::v_stride(teams), stage_bytes = St::bytes(teams);
   auto& x = reinterpret_cast<Exchange<DK>*>(raw + STAGES * stage_bytes)[team];
@@ -207,7 +207,7 @@ team_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
   if (threadIdx.x == 0) {
     failed = 0;
     for (int s = 0; s < STAGES; ++s) {
-      barrier_init(&full[s], kLoaders);
+      barrier_init(&full[s], kLoaders<T, DK>);
       barrier_init(&empty[s], teams * KS);
     }
     barriers_ready();
@@ -218,7 +218,7 @@ team_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
       const int64_t c = i;
       load_stage<T, DK, VEC>(raw + s * stage_bytes, p, p.v, p.ldv,
                              out.prepared + (at.chunk + c) * p.heads_v + at.h, start + c * kChunk, rows_of(c),
-                             at.kh, at.h, at.col, teams * 16, v_stride, threadIdx.x - teams * KS * 32, kLoaders);
+                             at.kh, at.h, at.col, teams * 16, v_stride, threadIdx.x - teams * KS * 32, kLoaders<T, DK>);
     });
     return;
   }
@@ -385,7 +385,7 @@ cudaError_t chain(const GdeltaRows<T>& p, const ChainOut<T>& out, cudaStream_t s
     auto* kernel = team_kernel<T, DK, VEC, 4>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(p.batch * p.heads_v * slices), teams * 128 + kLoaders, shared, stream>>>(p, out,
+    kernel<<<static_cast<unsigned>(p.batch * p.heads_v * slices), teams * 128 + kLoaders<T, DK>, shared, stream>>>(p, out,
                                                                                                 slices);
     return cudaGetLastError();
   }

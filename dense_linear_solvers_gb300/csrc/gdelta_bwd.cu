@@ -174,16 +174,16 @@ back_kernel(GdeltaRows<T> p, Back<T> out, int slices) {
 
 // The same chain by teams of KS warps a group of 16 columns, as in the forward pass.
 template <typename T, int DK, bool VEC, int KS>
-__global__ void __launch_bounds__(kMaxTeams * 32 * KS + kLoaders, 1)
+__global__ void __launch_bounds__(kMaxTeams<T, DK> * 32 * KS + kLoaders<T, DK>, 1)
 team_back_kernel(GdeltaRows<T> p, Back<T> out, int slices) {
   using St = Stage<T, DK>;
-  constexpr int STAGES = kTeamStages, NT = Terms<T>::n, NB = DK / 8, STRIDE = St::kStride, OWN = NB / KS, ROWS = Team<KS>::kRows;
+  constexpr int STAGES = kTeamStages<T, DK>, NT = Terms<T>::n, NB = DK / 8, STRIDE = St::kStride, OWN = NB / KS, ROWS = Team<KS>::kRows;
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ int64_t scratch[kSortedBatch + 1];
   __shared__ uint64_t full[STAGES], empty[STAGES];
   __shared__ volatile int failed;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, t2 = (lane & 3) * 2;
-  const int team = warp / KS, teams = (blockDim.x - kLoaders) / (32 * KS);
+  const int team = warp / KS, teams = (blockDim.x - kLoaders<T, DK>) / (32 * KS);
   const Team<KS> mine{warp % KS};
   const int v_stride = St::v_stride(teams), stage_bytes = St::bytes(teams);
   auto& x = reinterpret_cast<Exchange<DK>*>(raw + STAGES * stage_bytes)[team];
@@ -200,7 +200,7 @@ team_back_kernel(GdeltaRows<T> p, Back<T> out, int slices) {
   if (threadIdx.x == 0) {
     failed = 0;
     for (int s = 0; s < STAGES; ++s) {
-      barrier_init(&full[s], kLoaders);
+      barrier_init(&full[s], kLoaders<T, DK>);
       barrier_init(&empty[s], teams * KS);
     }
     barriers_ready();
@@ -211,7 +211,7 @@ team_back_kernel(GdeltaRows<T> p, Back<T> out, int slices) {
       const int64_t c = chunks - 1 - i;
       load_stage<T, DK, VEC>(raw + s * stage_bytes, p, out.dout, out.lddo,
                              out.prepared + (at.chunk + c) * p.heads_v + at.h, start + c * kChunk, rows_of(c),
-                             at.kh, at.h, at.col, teams * 16, v_stride, threadIdx.x - teams * KS * 32, kLoaders);
+                             at.kh, at.h, at.col, teams * 16, v_stride, threadIdx.x - teams * KS * 32, kLoaders<T, DK>);
     });
     return;
   }
@@ -379,7 +379,7 @@ cudaError_t chain(const GdeltaRows<T>& p, const Back<T>& out, cudaStream_t strea
     auto* kernel = team_back_kernel<T, DK, VEC, 4>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(p.batch * p.heads_v * slices), teams * 128 + kLoaders, shared, stream>>>(p, out,
+    kernel<<<static_cast<unsigned>(p.batch * p.heads_v * slices), teams * 128 + kLoaders<T, DK>, shared, stream>>>(p, out,
                                                                                                 slices);
     return cudaGetLastError();
   }

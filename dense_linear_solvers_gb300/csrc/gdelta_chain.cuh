@@ -434,11 +434,22 @@ __device__ __forceinline__ void store_two(const float (&x)[4], const float (&y)[
       to[row * ld + c] = v[row * v_stride + c];
   }
 }
-constexpr int kMaxTeams = 2, kTeamStages = 2;
+// A block's stages: three where two teams' fit (32,768 BF16 rows of 16 heads 128 x 128, the whole call: 1,072 to 950
+// us). Four more warps for O, which the next chunk does not wait for, gained nothing beside them.
+template <typename T, int DK>
+constexpr int kTeamStages =
+    3 * Stage<T, DK>::bytes(2) + 2 * static_cast<int>(sizeof(Exchange<DK>)) <= kMaxShared ? 3 : 2;
 template <typename T, int DK>
 constexpr int team_bytes(int teams) {
-  return kTeamStages * Stage<T, DK>::bytes(teams) + teams * static_cast<int>(sizeof(Exchange<DK>));
+  return kTeamStages<T, DK> * Stage<T, DK>::bytes(teams) + teams * static_cast<int>(sizeof(Exchange<DK>));
 }
+// Teams of a block at most, and the threads behind them that bring the stages: the same registers a thread are left
+// where one team's stages are all that fits, and its rows have to be split on their way (3 x 1,023 unaligned FP32 rows of
+// 5 heads 93 x 77: 105 us with 128 such threads, 82 with 256).
+template <typename T, int DK>
+constexpr int kMaxTeams = team_bytes<T, DK>(2) <= kMaxShared ? 2 : 1;
+template <typename T, int DK>
+constexpr int kLoaders = kMaxTeams<T, DK> == 2 ? 128 : 256;
 // How a chain's blocks are made up: teams of four warps (`teams` a block), or one warp a group of columns.
 struct Blocks {
   int teams, warps;
@@ -459,13 +470,12 @@ Blocks chain_blocks(const GdeltaRows<T>& p) {
   };
   const int slow = Terms<T>::n;
   offer(1, 21, {1, 0});
-  if (groups > 1 && team_bytes<T, DK>(2) <= kMaxShared) offer(2, 27, {2, 0});
+  if (groups > 1 && kMaxTeams<T, DK> == 2) offer(2, 27, {2, 0});
   if (groups > 2) offer(4, 50 * slow, {0, 4});
   if (groups > 4) offer(8, 69 * slow, {0, 8});
   return best;
 }
 // The warps behind the teams bring the stages: `load` for each chunk in its order, two stages ahead at most.
-constexpr int kLoaders = 128;  // threads
 template <bool ASYNC, typename F>
 __device__ __forceinline__ void bring_stages(int64_t chunks, int stages, uint64_t* full, uint64_t* empty,
                                              volatile int* failed, F&& load) {

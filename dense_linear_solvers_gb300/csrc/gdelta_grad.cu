@@ -12,7 +12,7 @@
 // The sums over dv run over groups of 16 columns, whose operands lie in the registers' order in global memory
 // and come by cp.async two groups ahead. Of the 64 x dk products a warp has all rows and an eighth of the
 // columns, of the 64 x 64 ones one to four of the 20 tiles of 16 x 8 on and below the diagonal, those of the rows
-// whose operands it has at hand. 8 x 2,048 rows of 16 heads 128 x 128, BF16: 445 us, two thirds of it the groups of columns, whose
+// whose operands it has at hand. 8 x 2,048 rows of 16 heads 128 x 128, BF16: 445 us, more than half of it the groups of columns, whose
 // products alone would take two thirds of that (with each head's first columns asked for only behind the last head, and db
 // summed in 64 bits, 531). Value heads
 // of one key head follow each other in the block, which adds them up in order in registers.
