@@ -371,26 +371,7 @@ team_back_kernel(GdeltaRows<T> p, Back<T> out, int slices) {
 
 template <typename T, int DK, bool VEC>
 cudaError_t chain(const GdeltaRows<T>& p, const Back<T>& out, cudaStream_t stream) {
-  constexpr int STAGES = Terms<T>::n == 1 ? 2 : 1;
-  const Blocks blocks = chain_blocks<T, DK>(p);
-  if (const int teams = blocks.teams) {
-    const int slices = (gdelta_groups(p.dv) + teams - 1) / teams;
-    const int shared = team_bytes<T, DK>(teams);
-    auto* kernel = team_back_kernel<T, DK, VEC, 4>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
-    if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(p.batch * p.heads_v * slices), teams * 128 + kLoaders<T, DK>, shared, stream>>>(p, out,
-                                                                                                slices);
-    return cudaGetLastError();
-  }
-  const int warps = blocks.warps, slices = (gdelta_groups(p.dv) + warps - 1) / warps;
-  const int shared = STAGES * Stage<T, DK>::bytes(warps);
-  auto* kernel = back_kernel<T, DK, VEC, STAGES>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
-  if (e != cudaSuccess) return e;
-  kernel<<<static_cast<unsigned>(p.batch * p.heads_v * slices), warps * 32, shared, stream>>>(p, out,
-                                                                                             slices);
-  return cudaGetLastError();
+  return launch_chain<T, DK>(team_back_kernel<T, DK, VEC, 4>, back_kernel<T, DK, VEC, kWarpStages<T>>, p, out, stream);
 }
 
 }  // namespace

@@ -47,6 +47,10 @@ __device__ __forceinline__ void load_stage(unsigned char* stage, const GdeltaRow
     cp_async_16(own + j, reinterpret_cast<const uint4*>(prepared) + j, 16);
 }
 
+// Stages of a block of single warps: FP32 and FP16 rows are split on their way, none is brought ahead.
+template <typename T>
+constexpr int kWarpStages = Terms<T>::n == 1 ? 2 : 1;
+
 // Whether a stage comes by bulk copies (rows that need no other form): a row an instruction instead of 16
 // bytes (16,384 rows of 16 heads 128 x 128: forward chain 286 to 279 us, backward 269 to 251).
 template <typename T, bool VEC>
@@ -474,6 +478,23 @@ Blocks chain_blocks(const GdeltaRows<T>& p) {
   if (groups > 2) offer(4, 50 * slow, {0, 4});
   if (groups > 4) offer(8, 69 * slow, {0, 8});
   return best;
+}
+// Launches a chain in the blocks that chain_blocks() gives, by its kernel for teams or the one for single warps. The
+// limit of shared memory belongs to the kernel and the device, not to a host thread: it is the kernel's
+// largest, since a call that set its own size could lower it between another thread's setting and launch.
+template <typename T, int DK, typename Out>
+cudaError_t launch_chain(void (*by_teams)(GdeltaRows<T>, Out, int), void (*by_warps)(GdeltaRows<T>, Out, int),
+                         const GdeltaRows<T>& p, const Out& out, cudaStream_t stream) {
+  const auto [teams, warps] = chain_blocks<T, DK>(p);
+  auto* kernel = teams ? by_teams : by_warps;
+  const int groups = teams ? teams : warps, slices = (gdelta_groups(p.dv) + groups - 1) / groups;
+  const int threads = teams ? teams * 128 + kLoaders<T, DK> : warps * 32;
+  const int shared = teams ? team_bytes<T, DK>(teams) : kWarpStages<T> * Stage<T, DK>::bytes(warps);
+  const int most = teams ? team_bytes<T, DK>(kMaxTeams<T, DK>) : kWarpStages<T> * Stage<T, DK>::bytes(kMaxWarps);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e != cudaSuccess) return e;
+  kernel<<<static_cast<unsigned>(p.batch * p.heads_v * slices), threads, shared, stream>>>(p, out, slices);
+  return cudaGetLastError();
 }
 // The warps behind the teams bring the stages: `load` for each chunk in its order, two stages ahead at most.
 template <bool ASYNC, typename F>
