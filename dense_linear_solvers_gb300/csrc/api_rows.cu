@@ -313,8 +313,10 @@ bs_status bs_gemm_q8(bs_dtype dtype, int64_t m, int64_t n, int64_t k, const uint
   if (m == 0 || n == 0) return BS_OK;
   const int64_t es = element_size(dtype);
   if (!y || (k > 0 && (!a || !sa || !w || !sw))) return BS_ERR_INVALID_ARG;
-  if (!aligned(a, 16) || !aligned(w, 16) || (m > 1 && lda % 16) || (n > 1 && ldw % 16) ||
-      !aligned(sa, 4) || !aligned(sw, 4) || !aligned(y, es))
+  if (!aligned(y, es)) return BS_ERR_INVALID_ARG;
+  // (with k == 0 the other operands are not read)
+  if (k > 0 && (!aligned(a, 16) || !aligned(w, 16) || (m > 1 && lda % 16) || (n > 1 && ldw % 16) ||
+                !aligned(sa, 4) || !aligned(sw, 4)))
     return BS_ERR_INVALID_ARG;
   if (!apart({{y, m, n * es, ldy * es}}, {{a, m, k, lda}, {sa, m, blocks * 4, ldsa * 4}, {w, n, k, ldw},
                                           {sw, groups, blocks * 4, ldsw * 4}}))

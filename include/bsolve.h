@@ -505,9 +505,10 @@ BS_API bs_status bs_gnorm_q8_batched(bs_dtype dtype, int64_t rows, int width, co
  *       one for each 128 x 128 block;
  *   y   m rows of n elements of dtype (BS_FP32, BS_BF16, BS_FP16), ldy apart.
  * The products of a block of 128 are summed on the tensor cores in FP32, the blocks in FP32 after their
- * scales, in an order that the sizes fix; y is rounded once. a and w are 16-byte aligned, lda (of
- * more than one row) and ldw multiples of 16 bytes; scales and y aligned to their elements. Inputs
- * may overlap each other, y no operand. k == 0 gives y = 0; m == 0 or n == 0 launches nothing. NaN
+ * scales, in an order that the sizes fix; y is rounded once. a and w are 16-byte aligned, lda and ldw
+ * (of more than one row) multiples of 16 bytes; scales and y aligned to their elements. Inputs
+ * may overlap each other, y no operand. k == 0 gives y = 0 and reads nothing (a, sa, w and sw of any
+ * alignment, or null); m == 0 or n == 0 launches nothing. NaN
  * and infinite scales stay in their row of a, or in the columns of y that a block of w reaches.
  * Supported: m <= 2^30, n, k and every ld <= 2^21.
  */

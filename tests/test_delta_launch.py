@@ -164,3 +164,18 @@ out["notes"] = notes()
             limits.setdefault(name, set()).add(int(value))
     assert any("team_kernel" in n for n in limits) and any("chain_kernel" in n for n in limits)
     assert {n: v for n, v in limits.items() if len(v) > 1} == {}
+
+
+def test_a_product_of_no_depth(stand_in):
+    """Rows of no element may lie at any distance and on any address: nothing of them is read."""
+    got = child(stand_in, """
+f = lib.bs_gemm_q8
+empty = dict(k=0, lda=1, ldw=1, ldsa=0, ldsw=0)
+out["taken"] = [call(f, PRODUCT, **empty), call(f, PRODUCT, **empty, a=None, sa=None, w=None, sw=None),
+                call(f, PRODUCT, **empty, a=FAR[0] + 3, sa=FAR[1] + 1, w=FAR[2] + 5, sw=FAR[3] + 2)]
+out["kernels"] = [n[1].split("::")[-1].split("<")[0] for n in notes() if n[0] == "launch"]
+out["refused"] = [call(f, PRODUCT, **empty, y=None), call(f, PRODUCT, lda=257), call(f, PRODUCT, ldw=257),
+                  call(f, PRODUCT, k=1, lda=1, ldw=1, ldsa=1, ldsw=1)]
+""")
+    assert got["taken"] == [0] * 3 and got["refused"] == [1] * 4
+    assert got["kernels"] == ["zero_kernel"] * 3
