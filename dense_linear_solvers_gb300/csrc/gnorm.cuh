@@ -120,13 +120,23 @@ enum Mode : int { kFull = 0, kAligned = 1, kAny = 2 };
 // maxima of the numbers' bits, which order them and keep a NaN.
 constexpr int kScaled = 128;  // elements under one scale
 
-struct Scale {
+__device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ float scale_of(unsigned top) {
+  return __fdiv_rn(__uint_as_float(max(top, __float_as_uint(0x1p-100f))), 448.f);
+}
+// Quotients by the scale that is stored: a product with the rounded inverse alone would put values near the middle of
+// two e4m3 numbers on the other side. The product is corrected once by its remainder (Markstein's method), two
+// instructions for two numbers (16,384 x 4,096 BF16, all operands: 109.6 us, 107.8 without, 122.2 with __fdiv_rn).
+struct Divisor {
   float s, inverse;
 };
-__device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-__device__ __forceinline__ Scale scale_of(unsigned top) {
-  const float m = __uint_as_float(max(top, __float_as_uint(0x1p-100f)));
-  return {__fdiv_rn(m, 448.f), __fdiv_rn(448.f, m)};
+// (an infinite scale: the inverse is 0, and with 0 for the scale the remainder of a finite number is none of NaN)
+__device__ __forceinline__ Divisor divisor(float s) {
+  return {s == __int_as_float(0x7F800000) ? 0.f : s, __fdiv_rn(1.f, s)};
+}
+__device__ __forceinline__ float2 quotient(float2 v, const Divisor& by) {
+  const float2 q = v * both(by.inverse), rest = fma2(q, both(-by.s), v);
+  return fma2(rest, both(by.inverse), q);
 }
 __device__ __forceinline__ unsigned as_e4m3(float2 v) {
   return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
@@ -160,16 +170,16 @@ struct Quantise {
             top = max(top, max(magnitude(v[i][k][e].x), magnitude(v[i][k][e].y)));
 #pragma unroll
           for (int m = 1; m < kLanes; m *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-          const Scale s = scale_of(top);
+          const float s = scale_of(top);
+          const Divisor by = divisor(s);
           const int at = (k * THREADS + t) * VE;
           if (row0 + i >= rows || at >= width) continue;
           const unsigned row = row0 + i;
-          if (at % kScaled == 0) out.s[row * out.lds + at / kScaled] = s.s;
+          if (at % kScaled == 0) out.s[row * out.lds + at / kScaled] = s;
           unsigned w[H / 2];
 #pragma unroll
           for (int e = 0; e < H; e += 2)
-            w[e / 2] = as_e4m3(v[i][k][e] * both(s.inverse)) |
-                       as_e4m3(v[i][k][e + 1] * both(s.inverse)) << 16;
+            w[e / 2] = as_e4m3(quotient(v[i][k][e], by)) | as_e4m3(quotient(v[i][k][e + 1], by)) << 16;
           uint8_t* to = out.q + row * out.ldq + at;
           if (MODE == kFull || at + VE <= width) {
             if constexpr (H == 4) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
@@ -203,9 +213,9 @@ struct Quantise {
             const float x = e & 1 ? v[i][k][e / 2].y : v[i][k][e / 2].x;
             const int c = row_element<VE, THREADS, false>(t, k, e);
             if (c >= width) continue;
-            const Scale s = scale_of(tops[i * kBlocks + c / kScaled]);
-            out.q[row * out.ldq + c] = static_cast<uint8_t>(as_e4m3(make_float2(x * s.inverse, 0.f)));
-            if (c % kScaled == 0) out.s[row * out.lds + c / kScaled] = s.s;
+            const float s = scale_of(tops[i * kBlocks + c / kScaled]);
+            out.q[row * out.ldq + c] = static_cast<uint8_t>(as_e4m3(make_float2(__fdiv_rn(x, s), 0.f)));
+            if (c % kScaled == 0) out.s[row * out.lds + c / kScaled] = s;
           }
       }
       meet();
@@ -782,14 +792,14 @@ gnorm_long_kernel(GnormRows<T> p, T* __restrict__ y, int64_t ldy, T* __restrict_
           if (p.w_pre) v[j] *= r2 * p.w_pre[c];
           top = max(top, magnitude(v[j]));
         }
-        const Scale s = scale_of(__reduce_max_sync(0xFFFFFFFFu, top));
-        if (lane == 0) bytes8.s[row * bytes8.lds + block] = s.s;
+        const float s = scale_of(__reduce_max_sync(0xFFFFFFFFu, top));
+        if (lane == 0) bytes8.s[row * bytes8.lds + block] = s;
 #pragma unroll
         for (int j = 0; j < kScaled / 32; ++j) {
           const int c = block * kScaled + j * 32 + lane;
           if (c < p.width)
             bytes8.q[row * bytes8.ldq + c] =
-                static_cast<uint8_t>(as_e4m3(make_float2(v[j] * s.inverse, 0.f)));
+                static_cast<uint8_t>(as_e4m3(make_float2(__fdiv_rn(v[j], s), 0.f)));
         }
       }
     } else {

@@ -483,7 +483,8 @@ BS_API size_t bs_gnorm_backward_workspace(int width, int64_t rows);
  * is given q holds u, else y (before its rounding to dtype; all of z, x, w_post, scale, w_pre and y are
  * optional). With v that value and B the 128-element block of a row that it belongs to (the
  * last one of a row may be shorter),
- *   scales[B] = max(max_B |v|, 2^-100) / 448,   q = v / scales[B] rounded to e4m3 (to nearest even).
+ *   scales[B] = max(max_B |v|, 2^-100) / 448,   q = v / scales[B] rounded to e4m3 (to nearest even),
+ * both quotients taken in FP32.
  *   q       rows of `width` e4m3 numbers (1 sign, 4 exponent, 3 fraction bits, largest 448), ldq
  *           bytes apart;
  *   scales  rows of ceil(width / 128) FP32 numbers, lds apart.

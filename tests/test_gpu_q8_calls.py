@@ -19,3 +19,65 @@ def test_a_product_of_no_depth(m, n):
     y = torch.full((m, n + 3), 7.0, device="cuda")
     bs.bs_gemm_q8(a, sa, w, sw, y[:, 1:n + 1])
     assert bool((y[:, 1:n + 1] == 0).all()) and bool((y[:, :1] == 7).all()) and bool((y[:, n + 1:] == 7).all())
+
+
+def near_ties(rows, width, seed):
+    """Values that lie on midpoints of two e4m3 numbers times their block's scale, and one to three steps of
+    FP32 beside them."""
+    gen = torch.Generator().manual_seed(seed)
+    blocks = -(-width // 128)
+    top = 0.5 + torch.rand(rows, blocks, 1, generator=gen)
+    # halfway between two numbers of three fraction bits, from the subnormal ones up to 240
+    exponent = torch.randint(-7, 7, (rows, blocks, 128), generator=gen)
+    fraction = torch.randint(0, 8, (rows, blocks, 128), generator=gen) + 0.5
+    unit = torch.exp2(exponent.clamp_min(-6).float() - 3)
+    middle = unit * (fraction + 8 * (exponent > -7))
+    v = middle * (top / 448)
+    for _ in range(3):  # up or down a step, or not
+        to = torch.randint(-1, 2, v.shape, generator=gen).float()
+        v = torch.where(to == 0, v, torch.nextafter(v, to * torch.inf))
+    v = torch.where(torch.rand(v.shape, generator=gen) < 0.5, v, -v)
+    v[..., 0] = top[..., 0]
+    return v.flatten(1)[:, :width].contiguous()
+
+
+@pytest.mark.parametrize("rows, width, pad", [(300, 128, 0), (40, 4096, 0), (64, 1000, 0), (300, 129, 1), (9, 2051, 1),
+                                              (2, 20008, 0)])
+def test_numbers_are_quotients(rows, width, pad):
+    """scales = max / 448 and q = v / scales, both divisions of FP32, q then to nearest even: to the bit, for
+    rows that take vectors, that take elements, and that are longer than a block of threads holds."""
+    v = near_ties(rows, width, seed=rows + width)
+    wide = torch.zeros(rows, width + 2 * pad)
+    wide[:, pad:pad + width] = v
+    f = wide.cuda()[:, pad:pad + width]
+    blocks = -(-width // 128)
+    full = torch.zeros(rows, blocks * 128)
+    full[:, :width] = v
+    full = full.unflatten(1, (blocks, 128))
+    s = full.abs().amax(2) / torch.full((rows, blocks), 448.0)
+    want = (full / s[..., None]).flatten(1)[:, :width].to(E4M3)
+    q, scales = torch.empty(rows, width, device="cuda").to(E4M3), torch.empty(rows, blocks, device="cuda")
+    bs.bs_gnorm_q8_batched(f, q, scales)
+    assert torch.equal(scales.cpu(), s)
+    assert int((q.cpu().view(torch.uint8) != want.view(torch.uint8)).sum()) == 0
+
+
+@pytest.mark.parametrize("width, pad", [(256, 0), (256, 1), (70000 // 4, 0)])
+def test_numbers_of_blocks_that_are_not_finite(width, pad):
+    """Under an infinite scale a finite number is 0 and an infinity no number; under no number everything is none.
+    The largest and smallest finite blocks keep their quotients."""
+    wide = torch.randn(4, width + 2 * pad, device="cuda")
+    f = wide[:, pad:pad + width]
+    f[0, 3], f[1, 7] = float("inf"), float("nan")
+    f[2] *= 2.0 ** 124
+    f[3] *= 2.0 ** -98
+    f[2].clamp_(-3e38, 3e38)
+    blocks = -(-width // 128)
+    q, s = torch.empty(4, width, device="cuda").to(E4M3), torch.empty(4, blocks, device="cuda")
+    bs.bs_gnorm_q8_batched(f, q, s)
+    got, first = q.cpu().float(), min(width, 128)
+    assert s[0, 0] == float("inf") and bool(s[1, 0].isnan())
+    assert bool(got[0, 3].isnan()) and bool((got[0, :3] == 0).all()) and bool((got[0, 4:first] == 0).all())
+    assert bool(got[1, :first].isnan().all()) and bool(got[:2, 128:].isfinite().all())
+    v, by = f.cpu()[2:], s.cpu()[2:].repeat_interleave(128, 1)[:, :width]
+    assert torch.equal(got[2:], (v / by).to(E4M3).float())
