@@ -458,10 +458,16 @@ constexpr int kLoaders = kMaxTeams<T, DK> == 2 ? 128 : 256;
 struct Blocks {
   int teams, warps;
 };
+// Whether blocks of single warps are ever the better ones: for rows that are split on their way only where a block holds
+// no two teams (below).
+template <typename T, int DK>
+constexpr bool kByWarps = Terms<T>::n == 1 || kMaxTeams<T, DK> == 1;
 // The least (turns of all SMs, one block each) x (a chunk's time in a block, 0.1 us, measured with dk = dv = 128 in BF16
 // where all blocks run at once): a team takes the chain's products apart, so that a chunk takes less than
 // half of one warp's time, but its warps exchange their parts, so that blocks of eight single warps do more in
-// all. FP32 and FP16 stages are not brought ahead by single warps.
+// all. FP32 and FP16 stages are not brought ahead by single warps, which is taken as their time again: four (100) are
+// then never better than two blocks of two teams (54) or four of one (84), eight (138) never better than four of two
+// (108), but may be than eight of one (168).
 template <typename T, int DK>
 Blocks chain_blocks(const GdeltaRows<T>& p) {
   const int groups = gdelta_groups(p.dv);
@@ -472,14 +478,15 @@ Blocks chain_blocks(const GdeltaRows<T>& p) {
     const int64_t cost = (blocks + kSms - 1) / kSms * time;
     if (cost < least) least = cost, best = b;
   };
-  const int slow = Terms<T>::n;
+  constexpr bool kSplit = Terms<T>::n == 2;
   offer(1, 21, {1, 0});
   if (groups > 1 && kMaxTeams<T, DK> == 2) offer(2, 27, {2, 0});
-  if (groups > 2) offer(4, 50 * slow, {0, 4});
-  if (groups > 4) offer(8, 69 * slow, {0, 8});
+  if (groups > 2 && !kSplit) offer(4, 50, {0, 4});
+  if (groups > 4 && kByWarps<T, DK>) offer(8, kSplit ? 138 : 69, {0, 8});
   return best;
 }
-// Launches a chain in the blocks that chain_blocks() gives, by its kernel for teams or the one for single warps. The
+// Launches a chain in the blocks that chain_blocks() gives, by its kernel for teams or the one for single warps (null
+// where none are ever chosen). The
 // limit of shared memory belongs to the kernel and the device, not to a host thread: it is the kernel's
 // largest, since a call that set its own size could lower it between another thread's setting and launch.
 template <typename T, int DK, typename Out>

@@ -40,6 +40,12 @@ static cudaError_t launched(const void* f, dim3 grid, dim3 block, size_t shared,
 }
 static int encode(...) { return 0; }
 extern "C" {
+const char* stand_in_names() {
+  static std::string out;
+  for (const auto& n : names)
+    if (n.second.find("bsolve") != std::string::npos) out += name_of(n.first) + "\n";
+  return out.c_str();
+}
 const char* stand_in_notes() { static std::string out; out.swap(notes); notes.clear(); return out.c_str(); }
 void __cudaRegisterFunction(void** module, const char* host, char* fun, const char* device, int limit, uint3* tid,
                             uint3* bid, dim3* block, dim3* grid, int* warp) {
@@ -79,7 +85,7 @@ cudaError_t __cudaLaunchKernel(void* f, dim3 grid, dim3 block, void**, size_t sh
 CHILD = r"""
 import ctypes, json, sys
 fake = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)
-fake.stand_in_notes.restype = ctypes.c_char_p
+fake.stand_in_notes.restype = fake.stand_in_names.restype = ctypes.c_char_p
 sys.path.insert(0, sys.argv[2])
 import dense_linear_solvers_gb300 as bs
 from tests.test_delta_host import BACKWARD, FORWARD, PRODUCT, call
@@ -179,3 +185,20 @@ out["refused"] = [call(f, PRODUCT, **empty, y=None), call(f, PRODUCT, lda=257), 
 """)
     assert got["taken"] == [0] * 3 and got["refused"] == [1] * 4
     assert got["kernels"] == ["zero_kernel"] * 3
+
+
+def test_every_compiled_chain_can_be_chosen(stand_in):
+    got = child(stand_in, """
+for kind in TYPES:
+    for dk in (64, 128):
+        for hv in (1, 40, 128, 300):
+            for dv in (8, 24, 64, 128, 256):
+                for pad in (0, 3):
+                    assert forward(kind, 1, 100, 1, hv, dk, dv, pad) == 0
+                    assert backward(kind, 1, 100, 1, hv, dk, dv, pad) == 0
+out["launched"] = sorted({n[1] for n in notes() if n[0] == "launch"})
+out["compiled"] = fake.stand_in_names().decode().splitlines()
+""")
+    chains = {n for n in got["compiled"] if any(k in n for k in ("chain_kernel<", "team_kernel<", "back_kernel<"))}
+    assert len(chains) == 2 * (12 + 8)  # teams: three types, two depths, aligned or not; single warps: four less
+    assert chains == {n for n in got["launched"] if n in chains}
