@@ -9,6 +9,7 @@ import sys
 import pytest
 
 from dense_linear_solvers_gb300 import _build
+from tests.delta_forms import CHAINS, PACKED, PRODUCTS
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -202,3 +203,54 @@ out["compiled"] = fake.stand_in_names().decode().splitlines()
     chains = {n for n in got["compiled"] if any(k in n for k in ("chain_kernel<", "team_kernel<", "back_kernel<"))}
     assert len(chains) == 2 * (12 + 8)  # teams: three types, two depths, aligned or not; single warps: four less
     assert chains == {n for n in got["launched"] if n in chains}
+
+
+def block_of(note):
+    """How a chain's launch is made up, and 1 where its kernel takes aligned rows only."""
+    name, threads = note[1], int(note[3])
+    kernel, args = name.split("::")[-1][:-1].split("<")
+    kind, deep, vec, last = args.split(", ")[-4:]
+    if kernel.startswith("team"):
+        loaders = 128 if deep == "64" or "bfloat16" in name else 256
+        return f"{(threads - loaders) // 128} teams", vec == "true"
+    return f"{threads // 32} warps", vec == "true"
+
+
+def test_the_shapes_of_the_tests_reach_their_chains(stand_in):
+    """Both passes take the form that the GPU's tests are there for, and all forms are among them, aligned and not."""
+    got = child(stand_in, """
+from tests.delta_forms import CHAINS, CUTS, PACKED
+shapes = [s for s, _ in CHAINS] + [(kind, 5, CUTS[-1] // 5, *rest, 0) for kind, *rest in PACKED]
+out["notes"] = []
+for shape in shapes:
+    assert forward(*shape) == 0 and backward(*shape) == 0
+    out["notes"].append([n for n in notes() if n[0] == "launch"])
+""")
+    forms = [f for _, f in CHAINS] + ["8 warps"] * len(PACKED)
+    seen = set()
+    for (shape, form, notes) in zip([s for s, _ in CHAINS] + PACKED, forms, got["notes"]):
+        chains = [n for n in notes if any(k in n[1] for k in ("chain_kernel<", "team_kernel<", "back_kernel<"))]
+        assert len(chains) == 2
+        for n in chains:
+            block, vec = block_of(n)
+            assert block == form, (shape, block)
+            seen.add((n[1].split("::")[-1], block))
+    kernels = {k for k, _ in seen}
+    for kind in ("float", "__half", "__nv_bfloat16"):
+        for vec in ("true", "false"):
+            for kernel in ("chain_kernel", "back_kernel"):
+                assert f"{kernel}<{kind}, 128, {vec}, {2 if 'bf' in kind else 1}>" in kernels
+
+
+def test_the_shapes_of_the_tests_reach_their_products(stand_in):
+    got = child(stand_in, """
+from tests.delta_forms import PRODUCTS
+for (m, n, k, ld), _ in PRODUCTS:
+    wide = -(-k // 16) * 16
+    assert call(lib.bs_gemm_q8, PRODUCT, m=m, n=n, k=k, a=FAR[0], lda=wide, sa=FAR[1], ldsa=-(-k // 128), w=FAR[2],
+                ldw=wide, sw=FAR[3], ldsw=-(-k // 128), y=FAR[4], ldy=n + 2 * ld) == 0
+out["notes"] = [n for n in notes() if n[0] == "launch"]
+""")
+    for (shape, form), (_, name, _, _, _, cluster) in zip(PRODUCTS, got["notes"]):
+        kernel, args = name.split("::")[-1][:-1].split("<")
+        assert f"{kernel} {args.split(', ')[-1]} {cluster}" == form, (shape, name, cluster)
