@@ -81,3 +81,37 @@ def test_numbers_of_blocks_that_are_not_finite(width, pad):
     assert bool(got[1, :first].isnan().all()) and bool(got[:2, 128:].isfinite().all())
     v, by = f.cpu()[2:], s.cpu()[2:].repeat_interleave(128, 1)[:, :width]
     assert torch.equal(got[2:], (v / by).to(E4M3).float())
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows, width, front, ld", [
+    (5, 299, 16, 336), (9, 300, 32, 352), (3, 37, 16, 64), (700, 131, 16, 160), (2, 4093, 16, 4128),  # 16-byte rows
+    (6, 130, 3, 139), (3, 2050, 1, 2053),                                                           # any rows
+    (2, 17001, 16, 17040)])                                                                         # long ones
+def test_norms_write_their_rows_only(kind, rows, width, front, ld):
+    """y, the numbers and the scales as windows of matrices that keep what they held on both sides, among them rows
+    that end inside a vector of 16 bytes."""
+    gen = torch.Generator("cuda").manual_seed(width)
+    blocks = -(-width // 128)
+
+    def window(like, n, at, total, fill):
+        wide = torch.full((rows, total), fill, device="cuda").to(like)
+        return wide, wide[:, at:at + n]
+
+    f, x = (torch.randn(rows, ld, generator=gen, device="cuda").to(kind)[:, front:front + width] for _ in range(2))
+    w = 1 + 0.1 * torch.randn(width, generator=gen, device="cuda")
+    held_y, y = window(kind, width, front, ld, 7.0)
+    held_q, q = window(torch.uint8, width, front, ld, 99)
+    held_s, s = window(torch.float32, blocks, 2, blocks + 5, 7.0)
+    q = q.view(E4M3)
+    bs.bs_gnorm_q8_batched(f, q, s, y=y, x=x, w_pre=w)
+    for held, n, at, fill in ((held_y, width, front, 7), (held_q, width, front, 99), (held_s, blocks, 2, 7)):
+        assert bool((held[:, :at] == fill).all()) and bool((held[:, at + n:] == fill).all())
+    # and right ones: half a step of e4m3 (or half its smallest number) around values whose sums and products in FP32
+    # are off by far less than 2^-18 of themselves
+    v = f.double() + x.double()
+    assert bool(((y.double() - v).abs() <= torch.finfo(kind).eps / 2 * v.abs() + 2.0 ** -23 * v.abs()).all())
+    v = v * torch.rsqrt((v ** 2).mean(1, keepdim=True) + 1e-6) * w.double()
+    by = s.double().repeat_interleave(128, 1)[:, :width]
+    far = (q.float().double() * by - v).abs()
+    assert bool((far <= (2.0 ** -4 + 2.0 ** -17) * v.abs() + 2.0 ** -10 * by).all())
