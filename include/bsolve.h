@@ -510,7 +510,9 @@ BS_API bs_status bs_gnorm_q8_batched(bs_dtype dtype, int64_t rows, int width, co
  * (of more than one row) multiples of 16 bytes; scales and y aligned to their elements. Inputs
  * may overlap each other, y no operand. k == 0 gives y = 0 and reads nothing (a, sa, w and sw of any
  * alignment, or null); m == 0 or n == 0 launches nothing. NaN
- * and infinite scales stay in their row of a, or in the columns of y that a block of w reaches.
+ * and infinite scales stay in their row of a, or in the columns of y that a block of w reaches. The
+ * product of two scales is taken in FP32 and has to be a number of its normal range (2^-126 to 2^128): below
+ * it loses bits, above it is infinite.
  * Supported: m <= 2^30, n, k and every ld <= 2^21.
  */
 BS_API bs_status bs_gemm_q8(bs_dtype dtype, int64_t m, int64_t n, int64_t k, const uint8_t* a,
