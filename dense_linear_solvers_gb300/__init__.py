@@ -708,7 +708,8 @@ def bs_gnorm_backward_batched(f, dy, df, work=None, z=None, x=None, w_post=None,
 def bs_gnorm_q8_batched(f, q, scales, y=None, z=None, x=None, w_post=None, scale=None, w_pre=None,
                         eps: float = 1e-6, gate: int = BS_GATE_SILU, stream=None) -> None:
     """bs_gnorm_batched with its last value, u where w_pre is given, else y, in 8 bits (see bsolve.h):
-    q, float8_e4m3fn of f's shape, and scales, float32, one for each 128 elements of a row."""
+    q, float8_e4m3fn of f's shape, and scales, float32, one for each 128 elements of a row. bs_gemm_q8 takes
+    rows of q a multiple of 16 bytes apart."""
     st = _rows().gnorm_q8(f, q, scales, y, z, x, w_post, scale, w_pre, eps, gate,
                           _row_stream(stream, f))
     if st:
@@ -718,7 +719,9 @@ def bs_gnorm_q8_batched(f, q, scales, y=None, z=None, x=None, w_post=None, scale
 def bs_gemm_q8(a, sa, w, sw, y, stream=None) -> None:
     """y <- a w^T of 8-bit operands under block scales (see bsolve.h). a: (rows, k) or (batch, length, k)
     float8_e4m3fn, sa: its scales as bs_gnorm_q8_batched leaves them; w: (n, k) float8_e4m3fn, sw:
-    (ceil(n / 128), ceil(k / 128)) float32; y: (..., n) float32, bfloat16 or float16."""
+    (ceil(n / 128), ceil(k / 128)) float32; y: (..., n) float32, bfloat16 or float16. The rows of a and of w
+    lie a multiple of 16 bytes apart: for another k they are columns of a wider tensor, such as
+    torch.empty(rows, -(-k // 16) * 16, dtype=torch.float8_e4m3fn, device="cuda")[:, :k]."""
     st = _rows().gemm_q8(a, sa, w, sw, y, _row_stream(stream, y))
     if st:
         _check(st, "bs_gemm_q8")

@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <stdexcept>
 #include <string>
+#include <tuple>
 #include <vector>
 
 #include <ATen/core/Tensor.h>
@@ -372,6 +373,10 @@ PyObject* gemm_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
               sa = row_of(a[1], "sa", l, at::kFloat, beside(l.shape, blocks)),
               rw = row_of(a[2], "w", l, at::kFloat8_e4m3fn, own),
               sw = row_of(a[3], "sw", l, at::kFloat, groups);
+    // the rows of a contiguous tensor of another width than a multiple of 16 do not lie so
+    for (auto [r, rows, name] : {std::tuple(&ra, l.rows(), "a"), std::tuple(&rw, own[0], "w")})
+      if (k > 0 && rows > 1 && r->ld % 16)
+        value_error(std::string(name) + ": rows " + std::to_string(r->ld) + " bytes apart, a multiple of 16 expected");
     return enter(l, bs_gemm_q8, l.code, l.rows(), l.width, k, static_cast<const uint8_t*>(ra.p), ra.ld,
                  static_cast<const float*>(sa.p), sa.ld, static_cast<const uint8_t*>(rw.p), rw.ld,
                  static_cast<const float*>(sw.p), sw.ld, y.p, y.ld, handle(a[5]));

@@ -115,3 +115,20 @@ def test_norms_write_their_rows_only(kind, rows, width, front, ld):
     by = s.double().repeat_interleave(128, 1)[:, :width]
     far = (q.float().double() * by - v).abs()
     assert bool((far <= (2.0 ** -4 + 2.0 ** -17) * v.abs() + 2.0 ** -10 * by).all())
+
+
+def test_rows_of_an_odd_width():
+    """A contiguous tensor's are refused with the reason; columns of a wider one are taken, straight from the norm."""
+    width, n = 1000, 40
+    f, w = torch.randn(9, width, device="cuda"), torch.randn(n, 1008, device="cuda").to(E4M3)[:, :width]
+    s, sw, y = torch.empty(9, 8, device="cuda"), torch.ones(1, 8, device="cuda"), torch.empty(9, n, device="cuda")
+    q = torch.empty(9, width, device="cuda").to(E4M3)
+    with pytest.raises(ValueError, match="a: rows 1000 bytes apart"):
+        bs.bs_gemm_q8(q, s, w, sw, y)
+    wide = torch.empty(9, -(-width // 16) * 16, dtype=E4M3, device="cuda")[:, :width]
+    with pytest.raises(ValueError, match="w: rows 1000 bytes apart"):
+        bs.bs_gemm_q8(wide, s, w.float().contiguous().to(E4M3), sw, y)
+    bs.bs_gnorm_q8_batched(f, wide, s)
+    bs.bs_gemm_q8(wide, s, w, sw, y)
+    want = (wide.float().double() * s.double().repeat_interleave(128, 1)[:, :width]) @ w.float().double().T
+    assert float((y - want).norm() / want.norm()) <= 2.0 ** -20  # a few FP32 roundings of independent terms
