@@ -371,9 +371,7 @@ team_back_kernel(GdeltaRows<T> p, Back<T> out, int slices) {
 
 template <typename T, int DK, bool VEC>
 cudaError_t chain(const GdeltaRows<T>& p, const Back<T>& out, cudaStream_t stream) {
-  void (*by_warps)(GdeltaRows<T>, Back<T>, int) = nullptr;
-  if constexpr (kByWarps<T, DK>) by_warps = back_kernel<T, DK, VEC, kWarpStages<T>>;
-  return launch_chain<T, DK>(team_back_kernel<T, DK, VEC, 4>, by_warps, p, out, stream);
+  return launch_chain<T, DK>(team_back_kernel<T, DK, VEC, 4>, back_kernel<T, DK, VEC, kWarpStages<T>>, p, out, stream);
 }
 
 }  // namespace

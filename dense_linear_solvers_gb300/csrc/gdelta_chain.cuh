@@ -458,35 +458,41 @@ constexpr int kLoaders = kMaxTeams<T, DK> == 2 ? 128 : 256;
 struct Blocks {
   int teams, warps;
 };
-// Whether blocks of single warps are ever the better ones: for rows that are split on their way only where a block holds
-// no two teams (below).
+// A chunk's time in a block, 0.01 us, where every SM has one: of one team and of two, of four single warps and of eight. The
+// mean of both passes over aligned rows of 152 heads, each with as many columns as the block has (BF16 heads of 128: forward
+// 1.64, 2.49, 5.38 and 6.88 us, backward 1.95, 2.85, 6.14 and 7.79). 0: not there, or never the best (four warps in BF16:
+// two blocks of two teams take less).
+struct ChunkTimes {
+  int teams[2], warps[2];
+};
 template <typename T, int DK>
-constexpr bool kByWarps = Terms<T>::n == 1 || kMaxTeams<T, DK> == 1;
-// The least (turns of all SMs, one block each) x (a chunk's time in a block, 0.1 us, measured with dk = dv = 128 in BF16
-// where all blocks run at once): a team takes the chain's products apart, so that a chunk takes less than
-// half of one warp's time, but its warps exchange their parts, so that blocks of eight single warps do more in
-// all. FP32 and FP16 stages are not brought ahead by single warps, which is taken as their time again: four (100) are
-// then never better than two blocks of two teams (54) or four of one (84), eight (138) never better than four of two
-// (108), but may be than eight of one (168).
+constexpr ChunkTimes kChunkTimes =
+    Terms<T>::n == 1 ? (DK == 64 ? ChunkTimes{{154, 217}, {0, 569}} : ChunkTimes{{180, 267}, {0, 733}})
+    : sizeof(T) == 2 ? (DK == 64 ? ChunkTimes{{311, 358}, {638, 886}} : ChunkTimes{{320, 0}, {971, 1180}})
+                     : (DK == 64 ? ChunkTimes{{460, 503}, {973, 1018}} : ChunkTimes{{467, 0}, {1648, 1562}});
+// The least (turns of all SMs, one block each) x (a chunk's time): a team takes the chain's products apart, so that a
+// chunk takes less than half of one warp's time, but its warps exchange their parts, so that blocks of eight single warps
+// do more in all.
 template <typename T, int DK>
 Blocks chain_blocks(const GdeltaRows<T>& p) {
+  constexpr ChunkTimes kTimes = kChunkTimes<T, DK>;
+  static_assert((kTimes.teams[1] != 0) == (kMaxTeams<T, DK> == 2), "a time for every block that fits");
   const int groups = gdelta_groups(p.dv);
   Blocks best{0, 1};
   int64_t least = INT64_MAX;
   auto offer = [&](int a_block, int time, Blocks b) {
+    if (time == 0) return;
     const int64_t blocks = p.batch * p.heads_v * ((groups + a_block - 1) / a_block);
     const int64_t cost = (blocks + kSms - 1) / kSms * time;
     if (cost < least) least = cost, best = b;
   };
-  constexpr bool kSplit = Terms<T>::n == 2;
-  offer(1, 21, {1, 0});
-  if (groups > 1 && kMaxTeams<T, DK> == 2) offer(2, 27, {2, 0});
-  if (groups > 2 && !kSplit) offer(4, 50, {0, 4});
-  if (groups > 4 && kByWarps<T, DK>) offer(8, kSplit ? 138 : 69, {0, 8});
+  offer(1, kTimes.teams[0], {1, 0});
+  if (groups > 1) offer(2, kTimes.teams[1], {2, 0});
+  if (groups > 2) offer(4, kTimes.warps[0], {0, 4});
+  if (groups > 4) offer(8, kTimes.warps[1], {0, 8});
   return best;
 }
-// Launches a chain in the blocks that chain_blocks() gives, by its kernel for teams or the one for single warps (null
-// where none are ever chosen). The
+// Launches a chain in the blocks that chain_blocks() gives, by its kernel for teams or the one for single warps. The
 // limit of shared memory belongs to the kernel and the device, not to a host thread: it is the kernel's
 // largest, since a call that set its own size could lower it between another thread's setting and launch.
 template <typename T, int DK, typename Out>

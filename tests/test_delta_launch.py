@@ -201,7 +201,7 @@ out["launched"] = sorted({n[1] for n in notes() if n[0] == "launch"})
 out["compiled"] = fake.stand_in_names().decode().splitlines()
 """)
     chains = {n for n in got["compiled"] if any(k in n for k in ("chain_kernel<", "team_kernel<", "back_kernel<"))}
-    assert len(chains) == 2 * (12 + 8)  # teams: three types, two depths, aligned or not; single warps: four less
+    assert len(chains) == 2 * (12 + 12)  # teams and single warps: three types, two depths, aligned or not
     assert chains == {n for n in got["launched"] if n in chains}
 
 
@@ -248,9 +248,10 @@ from tests.delta_forms import PRODUCTS
 for (m, n, k, ld), _ in PRODUCTS:
     wide = -(-k // 16) * 16
     assert call(lib.bs_gemm_q8, PRODUCT, m=m, n=n, k=k, a=FAR[0], lda=wide, sa=FAR[1], ldsa=-(-k // 128), w=FAR[2],
-                ldw=wide, sw=FAR[3], ldsw=-(-k // 128), y=FAR[4], ldy=n + 2 * ld) == 0
+                ldw=wide, sw=FAR[3], ldsw=-(-k // 128), y=FAR[4] + 2 * ld, ldy=n + 2 * ld) == 0
 out["notes"] = [n for n in notes() if n[0] == "launch"]
 """)
+    assert len(got["notes"]) == len(PRODUCTS)
     for (shape, form), (_, name, _, _, _, cluster) in zip(PRODUCTS, got["notes"]):
         kernel, args = name.split("::")[-1][:-1].split("<")
         assert f"{kernel} {args.split(', ')[-1]} {cluster}" == form, (shape, name, cluster)
