@@ -288,7 +288,7 @@ gemm_q8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
 // ---------------------------------------------------------------------------- many tokens
 // The same product with the tokens as the tensor core's rows and FEATURES features as its columns: a thread's token has
 // one scale a block for all of the thread's columns, so that scaling and adding takes one instruction for two
-// results and no shared memory; sixteen warps have a quarter of the columns each. 16,384 x 8,192 x 4,096: 569 us (1.93
+// results and no shared memory; sixteen warps have a quarter of the columns each. Rows of y take 16 bytes at once. 16,384 x 8,192 x 4,096: 569 us (1.93
 // PFLOP/s); the copies alone, 48 KB a block of k and SM, need 422. Shared between the blocks of a cluster (multicast) they gain nothing: an SM takes in no
 // more; two SMs on one tile of 256 x 256 (cta_group::2) would take in two thirds, but wait longer for each other
 // (1.04 ms).
@@ -307,7 +307,7 @@ struct RowConfig {
 template <typename T, int FEATURES>
 __global__ void __launch_bounds__(kRowThreads, 1)
 gemm_q8_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
-                    Problem p, T* __restrict__ y, bool vectors) {
+                    Problem p, T* __restrict__ y) {
   using C = RowConfig<FEATURES>;
   extern __shared__ unsigned char raw[];
   __shared__ uint64_t full[C::kStages], empty[C::kStages], ready[C::kResults], taken[C::kResults];
@@ -428,19 +428,13 @@ gemm_q8_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
       T* to = y + token * p.ldy + f0;
       const float bad = __int_as_float(0x7FC00000);
       constexpr int kV = 16 / static_cast<int>(sizeof(T));
-      if (vectors && ok) {
 #pragma unroll
-        for (int j = 0; j < C::kOwn; j += kV) {
-          alignas(16) T w[kV];
+      for (int j = 0; j < C::kOwn; j += kV) {
+        alignas(16) T w[kV];
 #pragma unroll
-          for (int e = 0; e < kV; e += 2)
-            *reinterpret_cast<typename Pair<T>::type*>(w + e) = pair_from_f32<T>(sum[(j + e) / 2]);
-          if (f0 + j < p.n) *reinterpret_cast<uint4*>(to + j) = *reinterpret_cast<const uint4*>(w);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < C::kOwn; ++j)
-          if (f0 + j < p.n) to[j] = from_f32<T>(!ok ? bad : j & 1 ? sum[j / 2].y : sum[j / 2].x);
+        for (int e = 0; e < kV; e += 2)
+          *reinterpret_cast<typename Pair<T>::type*>(w + e) = pair_from_f32<T>(ok ? sum[(j + e) / 2] : both(bad));
+        if (f0 + j < p.n) *reinterpret_cast<uint4*>(to + j) = *reinterpret_cast<const uint4*>(w);
       }
     }
   }
@@ -524,10 +518,8 @@ cudaError_t run_rows(Encode encode, const GemmQ8<T>& g, cudaStream_t stream) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kShared);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (g.n + FEATURES - 1) / FEATURES * ((g.m + kBlock - 1) / kBlock);
-  const bool vectors = ((reinterpret_cast<uintptr_t>(g.y) | static_cast<uintptr_t>(g.ldy * sizeof(T)) |
-                         static_cast<uintptr_t>(g.n * sizeof(T))) & 15) == 0;
   kernel<<<static_cast<unsigned>(std::min<int64_t>(tiles, kSms)), kRowThreads, C::kShared, stream>>>(
-      a, w, Problem{g.m, g.n, g.k, g.sa, g.sw, g.ldsa, g.ldsw, g.ldy}, g.y, vectors);
+      a, w, Problem{g.m, g.n, g.k, g.sa, g.sw, g.ldsa, g.ldsw, g.ldy}, g.y);
   return cudaGetLastError();
 }
 
@@ -552,18 +544,22 @@ cudaError_t launch_gemm_q8(const GemmQ8<T>& g, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (g.m <= 16) return run<T, 16>(encode, g, stream);
   if (g.m <= 32) return run<T, 32>(encode, g, stream);
-  // The least (turns of all SMs) x (a tile's time: its blocks of k, and its start and end, about 3000 cycles).
+  // The least (turns of all SMs) x (a tile's time: its blocks of k, and its start and end), in cycles, from 4,096 x 4,096 x
+  // 512 and 16,384 x 8,192 x 4,096 in BF16 (64 tokens 49 and 1,535 us, 128 tokens 39 and 917, rows by 128 features 25 and
+  // 769, by 256 features 27 and 565). Rows of y that do not take 16 bytes at once are for the kernel whose lanes are
+  // features: a row kernel's lanes would store elements of 32 rows (4,096 x 4,095 x 512: 128 tokens 40 us, rows 146
+  // and 157; 16,384 x 8,191 x 4,096: 919, 1,802 and 1,590).
   const int64_t blocks = (g.k + kBlock - 1) / kBlock;
-  auto cost = [&](int64_t tiles, int cycles, bool splits) {
+  auto cost = [&](int features, int tokens, int block, int ends, bool splits) {
+    const int64_t tiles = (g.n + features - 1) / features * ((g.m + tokens - 1) / tokens);
     const int split = splits ? split_of(tiles, blocks) : 1;
-    return (tiles * split + kSms - 1) / kSms * ((blocks + split - 1) / split * cycles + 3000);
+    return (tiles * split + kSms - 1) / kSms * ((blocks + split - 1) / split * block + ends);
   };
-  auto tiles = [&](int features, int tokens) {
-    return (g.n + features - 1) / features * ((g.m + tokens - 1) / tokens);
-  };
-  const int64_t costs[] = {cost(tiles(kBlock, 64), 600, true), cost(tiles(kBlock, 128), 1100, true),
-                           cost(tiles(128, kBlock), 900, false), cost(tiles(256, kBlock), 1300, false)};
-  switch (std::min_element(costs, costs + 4) - costs) {
+  const int64_t costs[] = {cost(kBlock, 64, 725, 3800, true), cost(kBlock, 128, 770, 7600, true),
+                           cost(128, kBlock, 725, 3900, false), cost(256, kBlock, 960, 9200, false)};
+  const bool vectors = ((reinterpret_cast<uintptr_t>(g.y) | static_cast<uintptr_t>(g.ldy * sizeof(T)) |
+                         static_cast<uintptr_t>(g.n * sizeof(T))) & 15) == 0;
+  switch (std::min_element(costs, costs + (vectors ? 4 : 2)) - costs) {
     case 0: return run<T, 64>(encode, g, stream);
     case 1: return run<T, 128>(encode, g, stream);
     case 2: return run_rows<T, 128>(encode, g, stream);

@@ -34,12 +34,15 @@ PACKED = [("bf16", 15, 30, 128, 128), ("bf16", 30, 30, 93, 77), ("f32", 15, 30, 
 
 # tokens, features, depth, elements beside y's rows; the kernel, its columns and the blocks that share a tile
 PRODUCTS = [
-    ((4485, 1301, 300, 0), "gemm_q8_rows_kernel 256 1"),    # more tiles than SMs, rows of an odd length
-    ((2311, 2008, 208, 0), "gemm_q8_rows_kernel 256 1"),    # stores of 16 bytes, tiles that end inside a quarter
-    ((2500, 2048, 256, 1), "gemm_q8_rows_kernel 256 1"),    # whole tiles on rows that are not aligned
-    ((20000, 3, 130, 0), "gemm_q8_rows_kernel 128 1"),      # more tiles than SMs, few columns
-    ((1001, 2001, 640, 1), "gemm_q8_rows_kernel 128 1"),
+    ((4001, 2056, 1043, 0), "gemm_q8_rows_kernel 256 1"),   # more tiles than SMs, the last of few columns or tokens
+    ((16384, 512, 1100, 8), "gemm_q8_rows_kernel 256 1"),
     ((1000, 2008, 640, 0), "gemm_q8_rows_kernel 128 1"),
+    ((2311, 2008, 208, 8), "gemm_q8_rows_kernel 128 1"),
+    ((20000, 8, 130, 0), "gemm_q8_rows_kernel 128 1"),
+    ((4485, 1301, 300, 0), "gemm_q8_kernel 128 1"),         # rows that do not take 16 bytes at once
+    ((1001, 2001, 640, 1), "gemm_q8_kernel 128 1"),
+    ((2500, 2048, 256, 1), "gemm_q8_kernel 64 1"),
+    ((20000, 3, 130, 0), "gemm_q8_kernel 64 1"),
     ((65, 4456, 9099, 0), "gemm_q8_kernel 128 4"),
     ((1335, 506, 2578, 1), "gemm_q8_kernel 128 2"),
     ((300, 257, 2000, 2), "gemm_q8_kernel 64 8"),
