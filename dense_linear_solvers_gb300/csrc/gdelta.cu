@@ -11,7 +11,7 @@
 // shared memory for the block's warps. Bound by the chain: few warps (255 registers a thread), each waiting for its
 // own products. 8 x 2,048 rows of 16 heads 128 x 128, BF16: 279 us, the tensor pipe busy for 45%, schedulers issue on
 // 28% of the cycles. Where there are too few columns for that many warps, teams of four warps take 16 columns (see
-// gdelta_chain.cuh): one sequence of 32,768 rows of 16 heads, the whole call, 4.34 to 0.95 ms.
+// gdelta_chain.cuh): one sequence of 32,768 rows of 16 heads, the whole call, 4.34 to 0.94 ms.
 #include "gdelta_chain.cuh"
 
 namespace bsolve {
@@ -89,7 +89,7 @@ chain_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
     __syncthreads();
     if (mine) {
       unsigned char* stage = raw + (c % STAGES) * stage_bytes;
-      const unsigned q = smem_addr(stage), k = q + St::kQk;
+      const unsigned q = smem_address(stage), k = q + St::kQk;
       T* v = reinterpret_cast<T*>(stage + 2 * St::kQk) + warp * 16;
       const auto& own = *reinterpret_cast<const Prepared*>(stage + 2 * St::kQk +
                                                            kChunk * v_stride * sizeof(T));
@@ -184,7 +184,8 @@ template <typename T, int DK, bool VEC, int KS>
 __global__ void __launch_bounds__(kMaxTeams<T, DK> * 32 * KS + kLoaders<T, DK>, 1)
 team_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
   using St = Stage<T, DK>;
-  constexpr int STAGES = kTeamStages<T, DK>, NT = Terms<T>::n, NB = DK / 8, STRIDE = St::kStride, OWN = NB / KS, ROWS = Team<KS>::kRows;
+  constexpr int STAGES = kTeamStages<T, DK>, NT = Terms<T>::n, NB = DK / 8, STRIDE = St::kStride;
+  constexpr int OWN = NB / KS, ROWS = Team<KS>::kRows;
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ int64_t scratch[kSortedBatch + 1];
   __shared__ uint64_t full[STAGES], empty[STAGES];
@@ -214,8 +215,7 @@ team_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
   }
   __syncthreads();
   if (warp >= teams * KS) {
-    bring_stages<VEC && NT == 1>(chunks, STAGES, full, empty, &failed, [&](int64_t i, int s) {
-      const int64_t c = i;
+    bring_stages<VEC && NT == 1>(chunks, STAGES, full, empty, &failed, [&](int64_t c, int s) {
       load_stage<T, DK, VEC>(raw + s * stage_bytes, p, p.v, p.ldv,
                              out.prepared + (at.chunk + c) * p.heads_v + at.h, start + c * kChunk, rows_of(c),
                              at.kh, at.h, at.col, teams * 16, v_stride, threadIdx.x - teams * KS * 32, kLoaders<T, DK>);
@@ -241,7 +241,7 @@ team_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
     team_sync(team, KS * 32);
     if (active) {
       unsigned char* stage = raw + s * stage_bytes;
-      const unsigned q = smem_addr(stage), k = q + St::kQk;
+      const unsigned q = smem_address(stage), k = q + St::kQk;
       T* v = reinterpret_cast<T*>(stage + 2 * St::kQk) + team * 16;
       const auto& own = *reinterpret_cast<const Prepared*>(stage + 2 * St::kQk +
                                                            kChunk * v_stride * sizeof(T));

@@ -88,7 +88,7 @@ back_kernel(GdeltaRows<T> p, Back<T> out, int slices) {
     __syncthreads();
     if (mine) {
       unsigned char* stage = raw + (c % STAGES) * stage_bytes;
-      const unsigned q = smem_addr(stage), k = q + St::kQk;
+      const unsigned q = smem_address(stage), k = q + St::kQk;
       T* d = reinterpret_cast<T*>(stage + 2 * St::kQk) + warp * 16;
       const auto& own = *reinterpret_cast<const Prepared*>(stage + 2 * St::kQk +
                                                            kChunk * v_stride * sizeof(T));
@@ -177,7 +177,8 @@ template <typename T, int DK, bool VEC, int KS>
 __global__ void __launch_bounds__(kMaxTeams<T, DK> * 32 * KS + kLoaders<T, DK>, 1)
 team_back_kernel(GdeltaRows<T> p, Back<T> out, int slices) {
   using St = Stage<T, DK>;
-  constexpr int STAGES = kTeamStages<T, DK>, NT = Terms<T>::n, NB = DK / 8, STRIDE = St::kStride, OWN = NB / KS, ROWS = Team<KS>::kRows;
+  constexpr int STAGES = kTeamStages<T, DK>, NT = Terms<T>::n, NB = DK / 8, STRIDE = St::kStride;
+  constexpr int OWN = NB / KS, ROWS = Team<KS>::kRows;
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ int64_t scratch[kSortedBatch + 1];
   __shared__ uint64_t full[STAGES], empty[STAGES];
@@ -234,7 +235,7 @@ team_back_kernel(GdeltaRows<T> p, Back<T> out, int slices) {
     team_sync(team, KS * 32);
     if (active) {
       unsigned char* stage = raw + s * stage_bytes;
-      const unsigned q = smem_addr(stage), k = q + St::kQk;
+      const unsigned q = smem_address(stage), k = q + St::kQk;
       T* d = reinterpret_cast<T*>(stage + 2 * St::kQk) + team * 16;
       const auto& own = *reinterpret_cast<const Prepared*>(stage + 2 * St::kQk +
                                                            kChunk * v_stride * sizeof(T));

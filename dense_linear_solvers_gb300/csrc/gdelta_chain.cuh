@@ -14,7 +14,8 @@ namespace {
 constexpr int kMaxWarps = 8;
 constexpr int kMaxShared = 230000;  // bytes of dynamic shared memory, beside what the kernels declare
 
-// Tiles of one stage for a block of `warps` warps: q, k as terms, v (or a gradient of its shape) as stored, the prepared chunk.
+// Tiles of one stage for a block of `warps` warps: q, k as terms, v (or a gradient of its shape) as stored, the
+// prepared chunk.
 template <typename T, int DK>
 struct Stage {
   static constexpr int kStride = DK + 8;
@@ -103,7 +104,7 @@ __device__ __forceinline__ void read_transposed(float (&x)[2][4], const T* v, in
   const int lane = threadIdx.x & 31, g = lane / 4, t2 = (lane & 3) * 2;
   if constexpr (sizeof(T) == 2) {
     unsigned w[4];
-    ldmatrix4_trans(w, smem_addr(v + (n * 8 + (lane & 7) + ((lane & 16) >> 1)) * v_stride + (lane & 8)));
+    ldmatrix4_trans(w, smem_address(v + (n * 8 + (lane & 7) + ((lane & 16) >> 1)) * v_stride + (lane & 8)));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = to_f32(*reinterpret_cast<const typename Pair<T>::type*>(&w[j]));
@@ -136,7 +137,7 @@ __device__ __forceinline__ void store_transposed(const float (&O)[8][4], T* v, i
                                                        O[n + j / 2][(j & 1) * 2 + 1]));
         w[j] = *reinterpret_cast<const unsigned*>(&pair);
       }
-      stmatrix4_trans(smem_addr(v + (n * 8 + (lane & 7) + ((lane & 16) >> 1)) * v_stride + (lane & 8)),
+      stmatrix4_trans(smem_address(v + (n * 8 + (lane & 7) + ((lane & 16) >> 1)) * v_stride + (lane & 8)),
                       w[0], w[1], w[2], w[3]);
     }
   } else {
@@ -386,7 +387,7 @@ __device__ __forceinline__ void read_two(float (&x)[4], float (&y)[4], const T* 
   const int lane = threadIdx.x & 31, g = lane / 4, t2 = (lane & 3) * 2;
   if constexpr (sizeof(T) == 2) {
     unsigned w[4];
-    ldmatrix4_trans(w, smem_addr(v + ((lane & 16 ? m : n) * 8 + (lane & 7)) * v_stride + (lane & 8)));
+    ldmatrix4_trans(w, smem_address(v + ((lane & 16 ? m : n) * 8 + (lane & 7)) * v_stride + (lane & 8)));
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const float2 a = to_f32(*reinterpret_cast<const typename Pair<T>::type*>(&w[j])),
@@ -417,7 +418,7 @@ __device__ __forceinline__ void store_two(const float (&x)[4], const float (&y)[
       w[j] = *reinterpret_cast<const unsigned*>(&a);
       w[2 + j] = *reinterpret_cast<const unsigned*>(&b);
     }
-    stmatrix4_trans(smem_addr(v + ((lane & 16 ? m : n) * 8 + (lane & 7)) * v_stride + (lane & 8)), w[0], w[1],
+    stmatrix4_trans(smem_address(v + ((lane & 16 ? m : n) * 8 + (lane & 7)) * v_stride + (lane & 8)), w[0], w[1],
                     w[2], w[3]);
   } else {
 #pragma unroll
@@ -438,7 +439,7 @@ __device__ __forceinline__ void store_two(const float (&x)[4], const float (&y)[
       to[row * ld + c] = v[row * v_stride + c];
   }
 }
-// A block's stages: three where two teams' fit (32,768 BF16 rows of 16 heads 128 x 128, the whole call: 1,072 to 950
+// A block's stages: three where two teams' fit (32,768 BF16 rows of 16 heads 128 x 128, the whole call: 1,072 to 940
 // us). Four more warps for O, which the next chunk does not wait for, gained nothing beside them.
 template <typename T, int DK>
 constexpr int kTeamStages =
@@ -458,10 +459,10 @@ constexpr int kLoaders = kMaxTeams<T, DK> == 2 ? 128 : 256;
 struct Blocks {
   int teams, warps;
 };
-// A chunk's time in a block, 0.01 us, where every SM has one: of one team and of two, of four single warps and of eight. The
-// mean of both passes over aligned rows of 152 heads, each with as many columns as the block has (BF16 heads of 128: forward
-// 1.64, 2.49, 5.38 and 6.88 us, backward 1.95, 2.85, 6.14 and 7.79). 0: not there, or never the best (four warps in BF16:
-// two blocks of two teams take less).
+// A chunk's time in a block, 0.01 us, where every SM has one: of one team and of two, of four single warps and of eight.
+// The mean of both passes over aligned rows of 152 heads, each with as many columns as the block has (BF16 heads of 128:
+// forward 1.64, 2.49, 5.38 and 6.88 us, backward 1.95, 2.85, 6.14 and 7.79). 0: not there, or never the best (four
+// warps in BF16: two blocks of two teams take less).
 struct ChunkTimes {
   int teams[2], warps[2];
 };

@@ -12,10 +12,10 @@
 // The sums over dv run over groups of 16 columns, whose operands lie in the registers' order in global memory
 // and come by cp.async two groups ahead. Of the 64 x dk products a warp has all rows and an eighth of the
 // columns, of the 64 x 64 ones one to four of the 20 tiles of 16 x 8 on and below the diagonal, those of the rows
-// whose operands it has at hand. 8 x 2,048 rows of 16 heads 128 x 128, BF16: 445 us, more than half of it the groups of columns, whose
-// products alone would take two thirds of that (with each head's first columns asked for only behind the last head, and db
-// summed in 64 bits, 531). Value heads
-// of one key head follow each other in the block, which adds them up in order in registers.
+// whose operands it has at hand. 8 x 2,048 rows of 16 heads 128 x 128, BF16: 445 us, more than half of it the groups
+// of columns, whose products alone would take two thirds of that (with each head's first columns asked for only behind
+// the last head, and db summed in 64 bits, 531). Value heads of one key head follow each other in the block, which adds
+// them up in order in registers.
 #include "gdelta_grad.cuh"
 
 namespace bsolve {
@@ -137,9 +137,9 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(GdeltaRows<T> p, Gdel
       unsigned a[NT][4], b[NT][4], c[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        ldmatrix4(a[t], across(smem_addr(&sh.q[t][0][0]), STRIDE, rows16 * 16, d));
-        ldmatrix4(b[t], across(smem_addr(&sh.k[t][0][0]), STRIDE, rows16 * 16, d));
-        ldmatrix4(c[t], along<STRIDE>(smem_addr(&sh.k[t][0][0]), s * 16, d));
+        ldmatrix4(a[t], across(smem_address(&sh.q[t][0][0]), STRIDE, rows16 * 16, d));
+        ldmatrix4(b[t], across(smem_address(&sh.k[t][0][0]), STRIDE, rows16 * 16, d));
+        ldmatrix4(c[t], along<STRIDE>(smem_address(&sh.k[t][0][0]), s * 16, d));
       }
       mma(qk, a[0], odd ? c[0][2] : c[0][0], odd ? c[0][3] : c[0][1]);
       mma(kk, b[0], odd ? c[0][2] : c[0][0], odd ? c[0][3] : c[0][1]);
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(GdeltaRows<T> p, Gdel
       if (w + 2 < groups) load(h, w + 2);
       cp_async_commit();
       const auto& st = sh.stage[w % kStages];
-      const unsigned d = smem_addr(&st.d[0][0][0]);
+      const unsigned d = smem_address(&st.d[0][0][0]);
       uint4 S[N8], G[N8];
 #pragma unroll
       for (int j = 0; j < N8; ++j) {
@@ -312,15 +312,15 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(GdeltaRows<T> p, Gdel
       }
     __syncthreads();
     // x K, x^T Q + (w + w^T) K
-    const unsigned x_at = smem_addr(&sh.mix.x[0][0][0]), w_at = smem_addr(&sh.mix.w[0][0][0]);
+    const unsigned x_at = smem_address(&sh.mix.x[0][0][0]), w_at = smem_address(&sh.mix.w[0][0][0]);
     constexpr unsigned kTerm = kChunk * kXs * 2;
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       unsigned q[NT][4], k[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        ldmatrix4_trans(q[t], across(smem_addr(&sh.q[t][0][0]), STRIDE, kb * 16, warp * N8 * 8));
-        ldmatrix4_trans(k[t], across(smem_addr(&sh.k[t][0][0]), STRIDE, kb * 16, warp * N8 * 8));
+        ldmatrix4_trans(q[t], across(smem_address(&sh.q[t][0][0]), STRIDE, kb * 16, warp * N8 * 8));
+        ldmatrix4_trans(k[t], across(smem_address(&sh.k[t][0][0]), STRIDE, kb * 16, warp * N8 * 8));
       }
       auto add = [&](float (&c)[N8][4], const unsigned (&hi)[4], const unsigned (&lo)[4],
                      const unsigned (&b)[NT][4]) {

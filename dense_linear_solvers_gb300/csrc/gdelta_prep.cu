@@ -142,7 +142,7 @@ prepare_kernel(GdeltaRows<T> p, Prepared* out) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) kk[j][e] = qk[j][e] = 0.f;
   {
-    const unsigned q = smem_addr(&sh.in.q[0][0][0]), k = smem_addr(&sh.in.k[0][0][0]);
+    const unsigned q = smem_address(&sh.in.q[0][0][0]), k = smem_address(&sh.in.k[0][0][0]);
     for (int d = 0; d < DK; d += 16) {
       unsigned a[NT][4], c[NT][4];
 #pragma unroll

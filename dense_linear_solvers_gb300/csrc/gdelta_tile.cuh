@@ -13,6 +13,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "barrier.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "row_types.cuh"
@@ -31,9 +32,6 @@ template <>
 struct Terms<__nv_bfloat16> { static constexpr int n = 1; };
 
 // ---------------------------------------------------------------------------- products
-__device__ __forceinline__ unsigned smem_addr(const void* p) {
-  return static_cast<unsigned>(__cvta_generic_to_shared(p));
-}
 __device__ __forceinline__ void mma(float (&c)[4], const unsigned (&a)[4], unsigned b0, unsigned b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -245,9 +243,9 @@ __device__ __forceinline__ unsigned across(unsigned tile, int stride, int k, int
 }
 
 // ---------------------------------------------------------------------------- prepared chunks
-// What a chunk's chain needs of each value head, made from q, k, g, beta alone: the inverse and the mixing matrix, lower triangular, as second operands in
-// registers' order (20 pieces of 8 columns and 16 deep, hi and lo, 16 bytes a lane), and by row
-// the decay from the chunk's start, beta, the decay to its end, and the log decays' sum.
+// What a chunk's chain needs of each value head, made from q, k, g, beta alone: the inverse and the mixing matrix,
+// lower triangular, as second operands in registers' order (20 pieces of 8 columns and 16 deep, hi and lo, 16 bytes
+// a lane), and by row the decay from the chunk's start, beta, the decay to its end, and the log decays' sum.
 constexpr int kPieces = 20;
 struct Prepared {
   uint4 inverse[kPieces][32];

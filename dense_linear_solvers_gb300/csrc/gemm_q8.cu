@@ -1,8 +1,8 @@
 // Matrix product of 8-bit operands under block scales (bs_gemm_q8):
 //   y[t][f] = sum over blocks b of 128 of  sa[t][b] sw[f / 128][b] sum over k in b of a[t][k] w[f][k].
 //
-// For few tokens tcgen05.mma (e4m3, FP32 sums in tensor memory) takes the features as its 128 rows and TOKENS tokens as its
-// columns: a tile's 128 features share one weight scale a block, one token costs 16 columns at
+// For few tokens tcgen05.mma (e4m3, FP32 sums in tensor memory) takes the features as its 128 rows and TOKENS tokens as
+// its columns: a tile's 128 features share one weight scale a block, one token costs 16 columns at
 // least instead of 128 rows, and a lane of the result is a feature, so that a warp's stores of one token are
 // contiguous. Each block of 128 is a result of its own (four instructions of depth 32), which eight warps
 // read back, multiply by its two scales and add up in FP32 registers while the next ones are computed
@@ -288,10 +288,10 @@ gemm_q8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
 // ---------------------------------------------------------------------------- many tokens
 // The same product with the tokens as the tensor core's rows and FEATURES features as its columns: a thread's token has
 // one scale a block for all of the thread's columns, so that scaling and adding takes one instruction for two
-// results and no shared memory; sixteen warps have a quarter of the columns each. Rows of y take 16 bytes at once. 16,384 x 8,192 x 4,096: 569 us (1.93
-// PFLOP/s); the copies alone, 48 KB a block of k and SM, need 422. Shared between the blocks of a cluster (multicast) they gain nothing: an SM takes in no
-// more; two SMs on one tile of 256 x 256 (cta_group::2) would take in two thirds, but wait longer for each other
-// (1.04 ms).
+// results and no shared memory; sixteen warps have a quarter of the columns each. Rows of y take 16 bytes at once.
+// 16,384 x 8,192 x 4,096: 565 to 585 us (1.88 to 1.95 PFLOP/s); the copies alone, 48 KB a block of k and SM, need 422.
+// Shared between the blocks of a cluster (multicast) they gain nothing: an SM takes in no more; two SMs on one tile of
+// 256 x 256 (cta_group::2) would take in two thirds, but wait longer for each other (1.04 ms).
 constexpr int kRowWarps = 16;
 constexpr int kRowThreads = (kRowWarps + 2) * 32;
 
@@ -544,11 +544,12 @@ cudaError_t launch_gemm_q8(const GemmQ8<T>& g, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (g.m <= 16) return run<T, 16>(encode, g, stream);
   if (g.m <= 32) return run<T, 32>(encode, g, stream);
-  // The least (turns of all SMs) x (a tile's time: its blocks of k, and its start and end), in cycles, from 4,096 x 4,096 x
-  // 512 and 16,384 x 8,192 x 4,096 in BF16 (64 tokens 49 and 1,535 us, 128 tokens 39 and 917, rows by 128 features 25 and
-  // 769, by 256 features 27 and 565). Rows of y that do not take 16 bytes at once are for the kernel whose lanes are
-  // features: a row kernel's lanes would store elements of 32 rows (4,096 x 4,095 x 512: 128 tokens 40 us, rows 146
-  // and 157; 16,384 x 8,191 x 4,096: 919, 1,802 and 1,590).
+  // The least (turns of all SMs) x (a tile's time: its blocks of k, and its start and end), in cycles, from 4,096 x 4,096
+  // x 512 and 16,384 x 8,192 x 4,096 in BF16 (64 tokens 49 and 1,535 us, 128 tokens 39 and 917, rows by 128 features
+  // 25 and 769, by 256 features 27 and 565; on 40 drawn sizes the choice is the best one or within 13%, but for a few
+  // of 7 to 11 us). Rows of y that do not take 16 bytes at once are for the kernel whose lanes are features: a row
+  // kernel's lanes would store elements of 32 rows (4,096 x 4,095 x 512: 128 tokens 40 us, rows 146 and 157;
+  // 16,384 x 8,191 x 4,096: 919, 1,802 and 1,590).
   const int64_t blocks = (g.k + kBlock - 1) / kBlock;
   auto cost = [&](int features, int tokens, int block, int ends, bool splits) {
     const int64_t tiles = (g.n + features - 1) / features * ((g.m + tokens - 1) / tokens);

@@ -1,5 +1,5 @@
-// The row operators' calls (bs_grec, bs_gnorm, bs_gemm_q8 and bs_gdelta calls of bsolve.h) from Python: reads devices, types,
-// shapes, row distances and pointers from torch tensors, checks them against each other and calls the
+// The row operators' calls (bs_grec, bs_gnorm, bs_gemm_q8 and bs_gdelta calls of bsolve.h) from Python: reads
+// devices, types, shapes, row distances and pointers from torch tensors, checks them against each other and calls the
 // C ABI. A call costs about 3 us with its launch; reading as much tensor by tensor in Python
 // takes 5 us warm and twice that between a program's other work, more than a small call's kernel.
 #include <Python.h>
