@@ -2,6 +2,7 @@
 // columns of them, its state in registers.
 #pragma once
 
+#include <cmath>
 #include <type_traits>
 
 #include "barrier.cuh"
@@ -459,47 +460,71 @@ constexpr int kLoaders = kMaxTeams<T, DK> == 2 ? 128 : 256;
 struct Blocks {
   int teams, warps;
 };
-// A chunk's time in a block, 0.01 us, where every SM has one: of one team and of two, of four single warps and of eight.
-// The mean of both passes over aligned rows of 152 heads, each with as many columns as the block has (BF16 heads of 128:
-// forward 1.64, 2.49, 5.38 and 6.88 us, backward 1.95, 2.85, 6.14 and 7.79). 0: not there, or never the best (four
-// warps in BF16: two blocks of two teams take less).
+// A chunk's time in a block, 0.01 us, where every SM has one: of one team and of two; of four single warps, and with two such
+// blocks on an SM; of eight. Measured over 2,048 and 4,096 rows of 152 or 304 heads with as many columns as the block has, the
+// mean of both passes (BF16, 128: forward 1.6, 2.4, 5.3 and 6.8 us). 0: does not fit. ALIGNED: rows that come in pieces of
+// 16 bytes; others come by elements.
 struct ChunkTimes {
-  int teams[2], warps[2];
+  int teams[2], four[2], eight;
 };
-template <typename T, int DK>
-constexpr ChunkTimes kChunkTimes =
-    Terms<T>::n == 1 ? (DK == 64 ? ChunkTimes{{154, 217}, {0, 569}} : ChunkTimes{{180, 267}, {0, 733}})
-    : sizeof(T) == 2 ? (DK == 64 ? ChunkTimes{{311, 358}, {638, 886}} : ChunkTimes{{320, 0}, {971, 1180}})
-                     : (DK == 64 ? ChunkTimes{{460, 503}, {973, 1018}} : ChunkTimes{{467, 0}, {1648, 1562}});
-// The least (turns of all SMs, one block each) x (a chunk's time): a team takes the chain's products apart, so that a
-// chunk takes less than half of one warp's time, but its warps exchange their parts, so that blocks of eight single warps
-// do more in all.
-template <typename T, int DK>
+template <typename T, int DK, bool ALIGNED>
+constexpr ChunkTimes chunk_times() {
+  constexpr bool kLong = DK == 128;
+  if constexpr (Terms<T>::n == 1) {
+    if (ALIGNED) return kLong ? ChunkTimes{{170, 256}, {568, 0}, 719} : ChunkTimes{{147, 204}, {449, 566}, 557};
+    return kLong ? ChunkTimes{{1462, 1564}, {2151, 0}, 1776} : ChunkTimes{{823, 923}, {1422, 1594}, 1307};
+  } else if constexpr (sizeof(T) == 2) {
+    if (ALIGNED) return kLong ? ChunkTimes{{310, 0}, {963, 1143}, 1172} : ChunkTimes{{299, 345}, {630, 776}, 877};
+    return kLong ? ChunkTimes{{864, 0}, {2467, 2684}, 2169} : ChunkTimes{{839, 945}, {1555, 1741}, 1484};
+  } else {
+    if (ALIGNED) return kLong ? ChunkTimes{{457, 0}, {1645, 1843}, 1556} : ChunkTimes{{451, 491}, {966, 1135}, 1010};
+    return kLong ? ChunkTimes{{578, 0}, {1882, 2160}, 1925} : ChunkTimes{{554, 688}, {1325, 1504}, 1416};
+  }
+}
+constexpr int kTurnTime = 400;  // what a turn costs beside its chunks
+// The least time. Equal sequences run in turns of what the GPU holds, a turn as long as its blocks. Uneven ones fill each
+// other's gaps, but the longest, about 1 + ln(batch) times the average where they were cut at random, cannot take less
+// than its own chunks. A team takes the chain's products apart, so that a chunk takes less than half of one warp's
+// time, but its warps exchange their parts, so that blocks of eight single warps do more in all.
+template <typename T, int DK, bool ALIGNED>
 Blocks chain_blocks(const GdeltaRows<T>& p) {
-  constexpr ChunkTimes kTimes = kChunkTimes<T, DK>;
+  constexpr ChunkTimes kTimes = chunk_times<T, DK, ALIGNED>();
   static_assert((kTimes.teams[1] != 0) == (kMaxTeams<T, DK> == 2), "a time for every block that fits");
   const int groups = gdelta_groups(p.dv);
-  Blocks best{0, 1};
-  int64_t least = INT64_MAX;
-  auto offer = [&](int a_block, int time, Blocks b) {
-    if (time == 0) return;
-    const int64_t blocks = p.batch * p.heads_v * ((groups + a_block - 1) / a_block);
-    const int64_t cost = (blocks + kSms - 1) / kSms * time;
-    if (cost < least) least = cost, best = b;
+  const double average = std::fmax(1.0, static_cast<double>(p.rows) / (static_cast<double>(p.batch) * kChunk));
+  const double chunks = p.offsets ? average : std::ceil(average);
+  Blocks best{1, 0};
+  double least = 0;
+  // blocks of so many groups, `one` a chunk with one of them on an SM, `two` with two (0: there is no room)
+  auto offer = [&](int a_block, int one, int two, Blocks b) {
+    if (one == 0) return;
+    const double blocks = static_cast<double>(p.batch * p.heads_v * ((groups + a_block - 1) / a_block));
+    const double held = two ? 2.0 * kSms : kSms;
+    auto turn = [&](int time) { return chunks * time + kTurnTime; };
+    double cost;
+    if (p.offsets) {
+      const int time = two && blocks > kSms ? two : one;
+      cost = std::fmax(blocks / (time == one ? kSms : held) * turn(time),
+                       chunks * (1.0 + std::log(static_cast<double>(p.batch))) * time);
+    } else {
+      const double turns = std::floor(blocks / held), rest = blocks - turns * held;
+      cost = turns * turn(two ? two : one) + (rest > kSms ? turn(two) : rest > 0 ? turn(one) : 0);
+    }
+    if (least == 0 || cost < least) least = cost, best = b;
   };
-  offer(1, kTimes.teams[0], {1, 0});
-  if (groups > 1) offer(2, kTimes.teams[1], {2, 0});
-  if (groups > 2) offer(4, kTimes.warps[0], {0, 4});
-  if (groups > 4) offer(8, kTimes.warps[1], {0, 8});
+  offer(1, kTimes.teams[0], 0, {1, 0});
+  if (groups > 1) offer(2, kTimes.teams[1], 0, {2, 0});
+  if (groups > 2) offer(4, kTimes.four[0], kTimes.four[1], {0, 4});
+  if (groups > 4) offer(8, kTimes.eight, 0, {0, 8});
   return best;
 }
 // Launches a chain in the blocks that chain_blocks() gives, by its kernel for teams or the one for single warps. The
 // limit of shared memory belongs to the kernel and the device, not to a host thread: it is the kernel's
 // largest, since a call that set its own size could lower it between another thread's setting and launch.
-template <typename T, int DK, typename Out>
+template <typename T, int DK, bool ALIGNED, typename Out>
 cudaError_t launch_chain(void (*by_teams)(GdeltaRows<T>, Out, int), void (*by_warps)(GdeltaRows<T>, Out, int),
                          const GdeltaRows<T>& p, const Out& out, cudaStream_t stream) {
-  const auto [teams, warps] = chain_blocks<T, DK>(p);
+  const auto [teams, warps] = chain_blocks<T, DK, ALIGNED>(p);
   auto* kernel = teams ? by_teams : by_warps;
   const int groups = teams ? teams : warps, slices = (gdelta_groups(p.dv) + groups - 1) / groups;
   const int threads = teams ? teams * 128 + kLoaders<T, DK> : warps * 32;

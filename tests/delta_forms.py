@@ -9,8 +9,8 @@ CHAINS = [
     (("bf16", 2, 130, 64, 64, 93, 77, 0), "8 warps"),     # no row but the first aligned
     (("bf16", 1, 100, 50, 150, 64, 300, 8), "8 warps"),   # few columns for the last block
     (("bf16", 1, 70, 32, 128, 60, 125, 3), "8 warps"),
-    (("f16", 2, 150, 64, 64, 128, 128, 0), "8 warps"),
-    (("f16", 2, 65, 32, 64, 104, 120, 16), "8 warps"),
+    (("f16", 2, 150, 64, 64, 128, 128, 0), "4 warps"),
+    (("f16", 2, 65, 32, 64, 104, 120, 16), "4 warps"),
     (("f16", 1, 130, 64, 128, 127, 113, 1), "8 warps"),
     (("f16", 2, 66, 32, 64, 64, 120, 8), "8 warps"),
     (("f16", 2, 128, 64, 64, 64, 64, 0), "4 warps"),
@@ -21,9 +21,12 @@ CHAINS = [
     (("f32", 1, 66, 64, 128, 61, 124, 2), "8 warps"),
     (("f32", 2, 129, 64, 64, 60, 64, 4), "4 warps"),
     (("f32", 1, 70, 128, 128, 128, 50, 0), "4 warps"),
+    (("bf16", 8, 66, 30, 60, 64, 64, 0), "4 warps"),      # two blocks on an SM
     (("bf16", 2, 130, 15, 30, 128, 64, 0), "2 teams"),
-    (("bf16", 2, 128, 64, 64, 64, 64, 0), "2 teams"),
-    (("bf16", 2, 70, 32, 64, 50, 61, 3), "2 teams"),
+    (("bf16", 2, 130, 15, 30, 64, 64, 0), "2 teams"),
+    (("bf16", 2, 70, 30, 30, 50, 50, 3), "2 teams"),
+    (("bf16", 2, 128, 64, 64, 64, 64, 0), "4 warps"),
+    (("bf16", 2, 70, 32, 64, 50, 61, 3), "4 warps"),
     (("f16", 2, 130, 30, 30, 64, 64, 0), "2 teams"),
     (("f32", 2, 130, 15, 30, 60, 64, 0), "2 teams"),
     (("f32", 1, 190, 2, 4, 128, 128, 0), "1 teams"),

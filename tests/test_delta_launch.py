@@ -194,7 +194,7 @@ for kind in TYPES:
     for dk in (64, 128):
         for hv in (1, 40, 128, 300):
             for dv in (8, 24, 64, 128, 256):
-                for pad in (0, 3):
+                for pad in (0, 3):  # aligned rows and others
                     assert forward(kind, 1, 100, 1, hv, dk, dv, pad) == 0
                     assert backward(kind, 1, 100, 1, hv, dk, dv, pad) == 0
 out["launched"] = sorted({n[1] for n in notes() if n[0] == "launch"})
@@ -220,10 +220,10 @@ def test_the_shapes_of_the_tests_reach_their_chains(stand_in):
     """Both passes take the form that the GPU's tests are there for, and all forms are among them, aligned and not."""
     got = child(stand_in, """
 from tests.delta_forms import CHAINS, CUTS, PACKED
-shapes = [s for s, _ in CHAINS] + [(kind, 5, CUTS[-1] // 5, *rest, 0) for kind, *rest in PACKED]
+shapes = [(s, False) for s, _ in CHAINS] + [((kind, 5, CUTS[-1] // 5, *rest, 0), True) for kind, *rest in PACKED]
 out["notes"] = []
-for shape in shapes:
-    assert forward(*shape) == 0 and backward(*shape) == 0
+for shape, packed in shapes:
+    assert forward(*shape, packed=packed) == 0 and backward(*shape, packed=packed) == 0
     out["notes"].append([n for n in notes() if n[0] == "launch"])
 """)
     forms = [f for _, f in CHAINS] + ["8 warps"] * len(PACKED)
