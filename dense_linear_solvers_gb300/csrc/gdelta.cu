@@ -377,7 +377,8 @@ team_kernel(GdeltaRows<T> p, ChainOut<T> out, int slices) {
 
 template <typename T, int DK, bool VEC>
 cudaError_t chain(const GdeltaRows<T>& p, const ChainOut<T>& out, cudaStream_t stream) {
-  return launch_chain<T, DK, VEC>(team_kernel<T, DK, VEC, 4>, chain_kernel<T, DK, VEC, kWarpStages<T>>, p, out, stream);
+  return launch_chain<T, DK, VEC>(team_kernel<T, DK, VEC, 4>, chain_kernel<T, DK, VEC, kWarpStages<T>>, p, out,
+                                  stream);
 }
 
 }  // namespace

@@ -372,7 +372,8 @@ team_back_kernel(GdeltaRows<T> p, Back<T> out, int slices) {
 
 template <typename T, int DK, bool VEC>
 cudaError_t chain(const GdeltaRows<T>& p, const Back<T>& out, cudaStream_t stream) {
-  return launch_chain<T, DK, VEC>(team_back_kernel<T, DK, VEC, 4>, back_kernel<T, DK, VEC, kWarpStages<T>>, p, out, stream);
+  return launch_chain<T, DK, VEC>(team_back_kernel<T, DK, VEC, 4>, back_kernel<T, DK, VEC, kWarpStages<T>>, p, out,
+                                  stream);
 }
 
 }  // namespace

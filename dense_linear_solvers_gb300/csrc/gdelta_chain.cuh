@@ -460,10 +460,10 @@ constexpr int kLoaders = kMaxTeams<T, DK> == 2 ? 128 : 256;
 struct Blocks {
   int teams, warps;
 };
-// A chunk's time in a block, 0.01 us, where every SM has one: of one team and of two; of four single warps, and with two such
-// blocks on an SM; of eight. Measured over 2,048 and 4,096 rows of 152 or 304 heads with as many columns as the block has, the
-// mean of both passes (BF16, 128: forward 1.6, 2.4, 5.3 and 6.8 us). 0: does not fit. ALIGNED: rows that come in pieces of
-// 16 bytes; others come by elements.
+// A chunk's time in a block, 0.01 us, where every SM has one: of one team and of two; of four single warps, and with two
+// such blocks on an SM; of eight. Measured over 2,048 and 4,096 rows of 152 or 304 heads with as many columns as the
+// block has, the mean of both passes (BF16, 128: forward 1.6, 2.4, 5.3 and 6.8 us). 0: does not fit. ALIGNED: rows
+// that come in pieces of 16 bytes; others come by elements.
 struct ChunkTimes {
   int teams[2], four[2], eight;
 };
@@ -481,9 +481,9 @@ constexpr ChunkTimes chunk_times() {
     return kLong ? ChunkTimes{{578, 0}, {1882, 2160}, 1925} : ChunkTimes{{554, 688}, {1325, 1504}, 1416};
   }
 }
-constexpr int kTurnTime = 400;  // what a turn costs beside its chunks
-// The least time. Equal sequences run in turns of what the GPU holds, a turn as long as its blocks. Uneven ones fill each
-// other's gaps, but the longest, about 1 + ln(batch) times the average where they were cut at random, cannot take less
+constexpr int kTurnTime = 400;  // what a turn costs beside its chunks: the same runs, extended to none
+// The least time. Equal sequences run in turns of what the GPU holds, a turn as long as its blocks. Uneven ones fill
+// each other's gaps, but the longest, about 1 + ln(batch) times the average where they were cut at random, cannot take less
 // than its own chunks. A team takes the chain's products apart, so that a chunk takes less than half of one warp's
 // time, but its warps exchange their parts, so that blocks of eight single warps do more in all.
 template <typename T, int DK, bool ALIGNED>

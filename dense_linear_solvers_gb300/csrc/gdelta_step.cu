@@ -6,7 +6,7 @@
 // HBM for a batch, by latency for one sequence. A block has all dk rows of some columns of one head's state: 128
 // columns by sixteen warps where that gives every SM several blocks, else 32 by eight. 200 rows of 32 heads 128 x 128:
 // 140 us (6.0 TB/s of the states' one read and one write, 89% of a copy's rate; 128 columns by eight warps 176);
-// one row 7 to 9 us, a call of torch and a launch.
+// one row 6 to 9 us, a call of torch and a launch.
 #include "gdelta_tile.cuh"
 
 namespace bsolve {

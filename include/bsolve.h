@@ -506,7 +506,7 @@ BS_API bs_status bs_gnorm_q8_batched(bs_dtype dtype, int64_t rows, int width, co
  *       one for each 128 x 128 block;
  *   y   m rows of n elements of dtype (BS_FP32, BS_BF16, BS_FP16), ldy apart.
  * The products of a block of 128 are summed on the tensor cores in FP32, the blocks in FP32 after their
- * scales, in an order that the sizes fix; y is rounded once. a and w are 16-byte aligned, lda and ldw
+ * scales, in an order that the sizes and y's alignment fix; y is rounded once. a and w are 16-byte aligned, lda and ldw
  * (of more than one row) multiples of 16 bytes; scales and y aligned to their elements. Inputs
  * may overlap each other, y no operand. k == 0 gives y = 0 and reads nothing (a, sa, w and sw of any
  * alignment, or null); m == 0 or n == 0 launches nothing. NaN
@@ -570,7 +570,7 @@ BS_API bs_status bs_gemm_q8(bs_dtype dtype, int64_t m, int64_t n, int64_t k, con
  *          batch then). Row j with a slot outside 0 .. num_slots - 1 changes no state and gets
  *          o = 0. Two rows with one slot: unspecified states.
  * batch == 0: nothing is launched.
- * Results do not depend on the stream or the run: no atomics, a fixed order of every sum.
+ * Results do not depend on the stream or the run: no atomics, an order of every sum that sizes and alignment fix.
  * Supported: 1 <= dk <= 128, 1 <= dv <= 1024, heads_v <= 65535, batch * heads_v <= 2^24,
  * rows <= 2^30, ld <= 2^21, scale finite. The queries return 0 for invalid sizes.
  */
